@@ -378,6 +378,167 @@ int q2k_mmq_q8_1(const void* W, int64_t N, int64_t K, const void* xq, int64_t m,
 int dense_gemm_bf16(const uint16_t* x, int64_t m, int64_t K, int64_t ldx, const uint16_t* W,
                     int64_t N, float* y, int64_t ldy, q2k_stream_t stream);
 
+/* ---- the rest of a decode layer: cache, attention, norms, route ----------
+ *
+ * The five calls below stand between the products above, so that a layer
+ * runs without leaving the device: norms around each block, the paged K/V
+ * cache with its bookkeeping, its writer and its reader, and the route of
+ * the experts (moe_v41/init.rs, `moe_v41_route_select`; attn_v41/decode.rs,
+ * `q_kv_projections` and `attend_and_project`, name the steps).
+ *
+ * The cache: K and V are bf16 arrays of pages, page p at p * page_stride
+ * elements, each page [Hkv, page_size, D] contiguous.  page_size is a power
+ * of two, 16..1024; page_stride >= Hkv * page_size * D and a multiple of 8
+ * (2 * Hkv * page_size * D, say, when K and V pages alternate in one
+ * buffer).  Slot s is row s % page_size of page s / page_size.  A request's
+ * token at position p lies in page block_table[r, p / page_size]. */
+
+/* Element types of arguments that take more than one. */
+enum q2k_type {
+    Q2K_F32 = 0,
+    Q2K_BF16 = 1
+};
+
+/* A step's cache bookkeeping from the requests' lengths, on the device.
+ *   ctx_lens     int32 [n_req]: tokens each request has in the cache
+ *   new_lens     int32 [n_req]: tokens it adds in this step (0 allowed)
+ *   free_pages   int32 [n_free]: ids of unused pages, taken in order
+ *   free_head    int32 [1], nullable (then 0): entries already taken
+ *   block_table  int32 [n_req, max_pages], rows ld_table apart, row r's
+ *                first ceil(ctx/page_size) entries in use; the entries of
+ *                pages that the new tokens open are written, the others left
+ *   cu_q         int32 [n_req + 1]: sums of new_lens, 0 first
+ *   seq_lens     int32 [n_req]: ctx_lens + new_lens
+ *   positions, token_req, slot_map   int32 [max_tokens]: position, request
+ *                and slot of each new token, request by request; entries
+ *                past the last token are -1 (a captured step of fixed size
+ *                can be padded)
+ *   free_head_out  int32 [1]: free_head + pages taken (may not be
+ *                free_head itself: a repeated call then gives the same)
+ *   err_flag     int32, nullable; bits OR'ed in: 1 = the pool ran out
+ *                (those pages and their slots are -1), 2 = a request
+ *                outgrew its table row (its later slots are -1), 4 = a
+ *                negative length or head (read as 0), 8 = more than
+ *                max_tokens tokens (cu_q and the token arrays are cut)
+ * 1 <= n_req <= 16384, 0 <= max_tokens <= 2^30, page_size a power of two
+ * 16..1024.  One launch. */
+int kv_page_plan(const int32_t* ctx_lens, const int32_t* new_lens, int64_t n_req, int64_t page_size,
+                 const int32_t* free_pages, int64_t n_free, const int32_t* free_head, int32_t* block_table,
+                 int64_t max_pages, int64_t ld_table, int32_t* cu_q, int32_t* seq_lens, int32_t* positions, int32_t* token_req,
+                 int32_t* slot_map, int64_t max_tokens, int32_t* free_head_out, int32_t* err_flag,
+                 q2k_stream_t stream);
+
+/* Rotary positions with up to three axes, and the store into the cache.
+ *   q, k, v      x_type (Q2K_F32, as the projections write, or Q2K_BF16):
+ *                token t's head h at t * ld + h * D; Hq heads in q, Hkv in
+ *                k and v.  q and q_out may both be NULL (store only).
+ *   positions    int32 [n_axes, T]
+ *   sections     HOST int32 [n_axes]: rotary pairs of each axis, in order
+ *                (time, height, width); they add up to rot / 2
+ *   inv_freq     fp32 [rot / 2]
+ *   interleaved  0: pair i is values i and i + rot/2; 1: 2i and 2i + 1
+ *   slot_map     int32 [T]; a token with a negative slot is not stored
+ *   q_out        bf16, token t's head h at t * ld_qo + h * D
+ * Pair i of a q or k head turns by fp32(position) * inv_freq[i] (one fp32
+ * product): (a, b) -> (a cos - b sin, b cos + a sin) in fp32, rounded once
+ * to bf16; values rot..D-1, and v, are rounded only.
+ *   err_flag     int32, nullable: set to 1 when a slot is past the cache
+ *                (that token is not stored)
+ * 1 <= D <= 512, rot even, 0 <= rot <= D, n_axes 1..3,
+ * n_pages * page_size <= 2^31.  Slots must differ.  One launch; rows on
+ * 16-byte boundaries with D and rot multiples of 16 go 16 values a thread,
+ * others value by value with the same result. */
+int kv_rope_store(const void* q, int64_t ld_q, const void* k, int64_t ld_k, const void* v, int64_t ld_v, int x_type,
+                  int64_t T, int64_t Hq, int64_t Hkv, int64_t D, const int32_t* positions, int64_t n_axes,
+                  const int32_t* sections, const float* inv_freq, int64_t rot, int interleaved,
+                  const int32_t* slot_map, uint16_t* q_out, int64_t ld_qo, uint16_t* k_cache, uint16_t* v_cache,
+                  int64_t n_pages, int64_t page_size, int64_t page_stride, int32_t* err_flag, q2k_stream_t stream);
+
+/* Workspace bytes kv_attention_bf16 needs (0 for a bad shape). */
+size_t kv_attention_workspace_bytes(int64_t T, int64_t Hq, int64_t Hkv, int64_t D);
+
+/* Attention of new tokens, one or many per request, over the paged cache
+ * that already holds them.
+ *   q            bf16, token t's head h at t * ld_q + h * D, 16-byte
+ *                aligned, ld_q % 8 == 0; request r owns tokens cu_q[r] ..
+ *                cu_q[r+1] - 1 (tokens past cu_q[n_req] are not written)
+ *   block_table  int32 [n_req, max_pages], rows ld_table apart
+ *   seq_lens     int32 [n_req]: tokens in the cache, the new ones last:
+ *                new token i of n sits at position p = seq_len - n + i and
+ *                sees positions max(0, p - window + 1) .. p (window 0: all)
+ *   scale        > 0; the scores are scale * q.k
+ *   out          bf16, token t's head h at t * ld_o + h * D
+ *   lse          fp32 [T, Hq], nullable: ln of the sum of e^score
+ * Query head h reads kv head h / (Hq / Hkv).  A row that sees no key (p < 0)
+ * gives zeros and lse -inf.  Keys outside a row's range may hold anything in
+ * K; V rows that no row of a request's tile can see may too (they are never
+ * multiplied), so an uninitialised page is safe.  Table entries outside
+ * [0, n_pages), and positions past max_pages pages, read as zeros and set
+ * bit 1 of the device error word.
+ * Softmax statistics and sums are fp32; the probabilities enter the second
+ * product as bf16.  K and V values are read once per 2 * floor(128 / (Hq /
+ * Hkv)) new tokens of a request.
+ * D a multiple of 16, 16..128; Hq / Hkv 1..128; caches 16-byte aligned.
+ * workspace: kv_attention_workspace_bytes(T, Hq, Hkv, D) bytes, 16-byte
+ * aligned.  Results repeat bit for bit.  Two launches. */
+int kv_attention_bf16(const uint16_t* q, int64_t ld_q, int64_t T, int64_t Hq, int64_t Hkv, int64_t D,
+                      const uint16_t* k_cache, const uint16_t* v_cache, int64_t n_pages, int64_t page_size,
+                      int64_t page_stride, const int32_t* block_table, int64_t max_pages, int64_t ld_table,
+                      const int32_t* cu_q, const int32_t* seq_lens, int64_t n_req, float scale, int64_t window,
+                      uint16_t* out, int64_t ld_o, float* lse, void* workspace, size_t workspace_bytes, q2k_stream_t stream);
+
+/* The norms around a block, with its gate and residual scale, in one pass:
+ *   u = y                                   (no y: u = 0)
+ *   u = u / rms(u) * post_w                 (with post_w)
+ *   u = u * gate                            (with gate)
+ *   h = residual + alpha * u                -> residual_out
+ *   n = h / rms(h) * pre_w                  -> out (bf16), out_q8 (q8_1)
+ * rms(z) = sqrt(mean(z^2) + eps); fp32 throughout, each result rounded once
+ * (n comes from the unrounded h).
+ *   y, gate       y_type, rows ld_y / ld_gate apart; ld_gate 0: one row for
+ *                 every token.  y NULL needs post_w and gate NULL.
+ *   residual      stream_type, rows ld_res apart; residual_out likewise,
+ *                 ld_ro apart, nullable, may be residual itself
+ *   post_w, pre_w fp32 [dim], post_w nullable
+ *   out           bf16 rows ld_out apart, nullable with out_q8
+ *   out_q8        q8_1 rows of n, nullable (dim % 32 == 0): equal to
+ *                 q8_1_quantize_rows(out) bit for bit
+ * 0 <= T, 1 <= dim <= 32768, eps >= 0, alpha finite.  One launch. */
+int norm_gate_residual(const void* y, int y_type, int64_t ld_y, const float* post_w, const void* gate,
+                       int64_t ld_gate, const void* residual, int stream_type, int64_t ld_res, float alpha,
+                       const float* pre_w, float eps, int64_t T, int64_t dim, void* residual_out, int64_t ld_ro,
+                       uint16_t* out, int64_t ld_out, void* out_q8, q2k_stream_t stream);
+
+enum q2k_route_score {
+    Q2K_ROUTE_SOFTMAX = 0,
+    Q2K_ROUTE_SIGMOID = 1
+};
+
+/* Routing to experts (moe_v41/init.rs, `moe_v41_route_select`).
+ *   logits    fp32 or bf16 (type) [m, E], rows ld apart
+ *   bias      fp32 [E], nullable: added to the scores for the choice only
+ *   score     s = softmax(logits) over all E, or 1 / (1 + e^-logit)
+ *   n_group   groups of E / n_group experts in a row; with n_group > 1 a
+ *             group's score is the sum of its two largest s + bias (its
+ *             largest where it has one expert), and the choice is limited
+ *             to the topk_group best groups
+ *   topk      experts per token: the largest s + bias, ties to the lowest
+ *             index, in falling order
+ *   ids       int32 [m, topk]
+ *   weights   fp32 [m, topk]: s of the chosen, divided by their sum + 1e-20
+ *             when renorm, times scale
+ *   expert_ptrs  int64 device pointers [3, E] (gate, up, down), nullable;
+ *   ptrs_out     with it: [m, 3 * topk], each row the pointer table that
+ *             q2k_moe_m1 takes (gate of the chosen, then up, then down)
+ * A logit of NaN counts as -inf; -inf has score 0, and a row of nothing else
+ * gives experts by bias and weights 0.  The softmax sum carries its rounding
+ * error along, so the choice does not depend on the order of the sum.
+ * 1 <= E <= 1024, 1 <= topk <= 32, topk <= topk_group * E / n_group,
+ * n_group <= 32 and divides E, 0 <= m.  One launch. */
+int moe_route_topk(const void* logits, int type, int64_t m, int64_t E, int64_t ld, const float* bias, int score,
+                   int64_t n_group, int64_t topk_group, int64_t topk, int renorm, float scale, int32_t* ids,
+                   float* weights, const int64_t* expert_ptrs, int64_t* ptrs_out, q2k_stream_t stream);
+
 /* Human-readable name of a status code (static string). */
 const char* q2k_status_string(int status);
 

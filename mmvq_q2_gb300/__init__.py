@@ -11,6 +11,7 @@ activations as ``torch.bfloat16``; outputs are fp32 unless stated.
 """
 from __future__ import annotations
 
+import collections
 import ctypes
 import os
 import threading
@@ -30,6 +31,8 @@ EXPORTS = (
     "q2k_moe_m1_workspace_bytes", "q2k_moe_m1", "q2k_moe_m1_static_scratch", "dense_gemm_bf16", "q2k_status_string",
     "q2k_mmq_bf16", "q2k_mmq_q8_1_workspace_bytes", "q2k_mmq_q8_1",
     "q2k_last_cuda_error", "q2k_device_error",
+    "kv_page_plan", "kv_rope_store", "kv_attention_workspace_bytes", "kv_attention_bf16", "norm_gate_residual",
+    "moe_route_topk",
 )
 
 Q2K_OK = 0
@@ -90,6 +93,15 @@ def lib() -> ctypes.CDLL:
             "q2k_mmq_bf16": (I32, [P, I64, I64, P, I64, I64, P, I64, P]),
             "q2k_mmq_q8_1_workspace_bytes": (SZ, [I64, I64]),
             "q2k_mmq_q8_1": (I32, [P, I64, I64, P, I64, P, I64, P, SZ, P]),
+            "kv_page_plan": (I32, [P, P, I64, I64, P, I64, P, P, I64, I64, P, P, P, P, P, I64, P, P, P]),
+            "kv_rope_store": (I32, [P, I64, P, I64, P, I64, I32, I64, I64, I64, I64, P, I64, P, P, I64, I32, P, P, I64,
+                                    P, P, I64, I64, I64, P, P]),
+            "kv_attention_workspace_bytes": (SZ, [I64, I64, I64, I64]),
+            "kv_attention_bf16": (I32, [P, I64, I64, I64, I64, I64, P, P, I64, I64, I64, P, I64, I64, P, P, I64,
+                                        ctypes.c_float, I64, P, I64, P, P, SZ, P]),
+            "norm_gate_residual": (I32, [P, I32, I64, P, P, I64, P, I32, I64, ctypes.c_float, P, ctypes.c_float, I64, I64,
+                                         P, I64, P, I64, P, P]),
+            "moe_route_topk": (I32, [P, I32, I64, I64, I64, P, I32, I64, I64, I64, I32, ctypes.c_float, P, P, P, P, P]),
             "q2k_status_string": (ctypes.c_char_p, [I32]),
             "q2k_last_cuda_error": (I32, []),
             "q2k_device_error": (I32, [ctypes.POINTER(ctypes.c_int32), I32]),
@@ -377,6 +389,261 @@ def dense_gemm_bf16(x, W, out=None, stream=None):
         out = torch.empty((m, N), dtype=torch.float32, device=x.device)
     _call("dense_gemm_bf16", _ptr(x), m, K, x.stride(0), _ptr(W), N, _ptr(out), out.stride(0), _stream(stream))
     return out
+
+
+Q2K_F32 = 0
+Q2K_BF16 = 1
+_TYPES = {torch.float32: Q2K_F32, torch.bfloat16: Q2K_BF16}
+
+
+def _type(t, what):
+    try:
+        return _TYPES[t.dtype]
+    except KeyError:
+        raise TypeError(f"{what} must be fp32 or bf16, not {t.dtype}") from None
+
+
+def _typed(dtype, **ts):
+    for name, t in ts.items():
+        if t is not None and t.dtype != dtype:
+            raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
+
+
+def _dense(**ts):
+    for name, t in ts.items():
+        if t is not None and not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _heads(t, name):
+    """``[T, H, D]`` whose heads of a token lie back to back -> the stride between tokens."""
+    if t.dim() != 3 or t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != t.shape[2]):
+        raise ValueError(f"{name} must be [T, H, D] with the heads of a token back to back")
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1] * t.shape[2])
+
+
+def _cache(k_cache, v_cache):
+    """``[n_pages, Hkv, page_size, D]`` twice, pages dense, the pages themselves at any equal stride."""
+    n_pages, Hkv, page, D = k_cache.shape
+    if v_cache.shape != k_cache.shape or k_cache.stride() != v_cache.stride():
+        raise ValueError("k_cache and v_cache must have one shape and one set of strides")
+    if k_cache.stride()[1:] != (page * D, D, 1):
+        raise ValueError("a page of the cache must be contiguous [Hkv, page_size, D]")
+    return n_pages, Hkv, page, D, k_cache.stride(0) if n_pages > 1 else max(k_cache.stride(0), Hkv * page * D)
+
+
+def _table(t):
+    """Columns of a block table and the stride between its rows."""
+    return t.shape[1], t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+
+
+PagePlan = collections.namedtuple("PagePlan", "cu_q seq_lens positions token_req slot_map free_head")
+
+
+def kv_page_plan(ctx_lens, new_lens, page_size, free_pages, block_table, max_tokens, free_head=None, err_flag=None,
+                 out=None, stream=None):
+    """A step's cache bookkeeping from the requests' lengths (all int32):
+    opens pages for the new tokens in ``block_table [n_req, ld]`` (in place)
+    and returns ``PagePlan(cu_q [n_req+1], seq_lens [n_req], positions,
+    token_req, slot_map [max_tokens], free_head [1])``.  ``out``: a
+    ``PagePlan`` to write into."""
+    _need_cuda(ctx_lens, new_lens, free_pages, block_table, free_head, err_flag)
+    _typed(torch.int32, ctx_lens=ctx_lens, new_lens=new_lens, free_pages=free_pages, block_table=block_table,
+           free_head=free_head, err_flag=err_flag)
+    _dense(ctx_lens=ctx_lens, new_lens=new_lens, free_pages=free_pages)
+    n = ctx_lens.numel()
+    if new_lens.numel() != n or block_table.dim() != 2 or block_table.shape[0] != n or block_table.stride(1) != 1:
+        raise ValueError("one ctx_len, new_len and row of block_table per request")
+    if out is None:
+        # one allocation; the arrays start on 16-byte boundaries
+        n4, t4 = (n + 4) & ~3, (max_tokens + 3) & ~3
+        buf = torch.empty(2 * n4 + 3 * t4 + 1, dtype=torch.int32, device=ctx_lens.device)
+        sizes = (n + 1, n, max_tokens, max_tokens, max_tokens, 1)
+        starts = (0, n4, 2 * n4, 2 * n4 + t4, 2 * n4 + 2 * t4, 2 * n4 + 3 * t4)
+        out = PagePlan(*(buf[a:a + c] for a, c in zip(starts, sizes)))
+    else:
+        _need_cuda(*out)
+        _typed(torch.int32, **out._asdict())
+        _dense(**out._asdict())
+        if tuple(t.numel() for t in out) != (n + 1, n, max_tokens, max_tokens, max_tokens, 1):
+            raise ValueError("out does not fit n_req and max_tokens")
+    cols, ld = _table(block_table)
+    _call("kv_page_plan", _addr(ctx_lens), _addr(new_lens), n, page_size, _addr(free_pages), free_pages.numel(),
+          _addr(free_head), _addr(block_table), cols, ld, _addr(out.cu_q), _addr(out.seq_lens), _addr(out.positions),
+          _addr(out.token_req), _addr(out.slot_map), max_tokens, _addr(out.free_head), _addr(err_flag),
+          _stream(stream))
+    return out
+
+
+def kv_rope_store(q, k, v, positions, inv_freq, slot_map, k_cache, v_cache, sections=None, interleaved=False,
+                  q_out=None, err_flag=None, stream=None):
+    """Rotate ``q [T, Hq, D]`` and ``k [T, Hkv, D]`` (fp32 or bf16, token
+    stride allowed) by ``positions [T]`` or ``[n_axes, T]`` and store k and
+    ``v`` into the pages at ``slot_map``; returns bf16 ``q_out`` (None when q
+    is None).  ``sections``: rotary pairs of each axis."""
+    _need_cuda(q, k, v, positions, inv_freq, slot_map, k_cache, v_cache, q_out, err_flag)
+    x_type = _type(k, "k")
+    _typed(k.dtype, q=q, v=v)
+    _typed(torch.bfloat16, k_cache=k_cache, v_cache=v_cache, q_out=q_out)
+    _typed(torch.int32, positions=positions, slot_map=slot_map, err_flag=err_flag)
+    _typed(torch.float32, inv_freq=inv_freq)
+    _dense(positions=positions, inv_freq=inv_freq, slot_map=slot_map)
+    T, Hkv, D = k.shape
+    n_pages, Hc, page, Dc, page_stride = _cache(k_cache, v_cache)
+    n_axes = 1 if positions.dim() == 1 else positions.shape[0]
+    if v.shape != k.shape or (Hc, Dc) != (Hkv, D) or slot_map.numel() != T or positions.numel() != n_axes * T or \
+            (q is not None and (q.shape[0], q.shape[2]) != (T, D)):
+        raise ValueError("q, k, v, positions, slot_map and the cache do not fit one another")
+    if sections is None:
+        sections = (inv_freq.numel(),)
+    if len(sections) != n_axes or n_axes > 3:
+        raise ValueError("one section per axis, three at most")
+    Hq = 0
+    if q is None:
+        if q_out is not None:
+            raise ValueError("q_out without q")
+    else:
+        Hq = q.shape[1]
+        if q_out is None:
+            q_out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=k.device)
+        elif q_out.shape != q.shape:
+            raise ValueError("q_out must have q's shape")
+    _call("kv_rope_store", _addr(q), 0 if q is None else _heads(q, "q"), _addr(k), _heads(k, "k"), _addr(v),
+          _heads(v, "v"), x_type, T, Hq, Hkv, D, _addr(positions), n_axes, (ctypes.c_int32 * 3)(*sections),
+          _addr(inv_freq), 2 * inv_freq.numel(), 1 if interleaved else 0, _addr(slot_map), _addr(q_out),
+          0 if q is None else _heads(q_out, "q_out"), _addr(k_cache), _addr(v_cache), n_pages, page, page_stride,
+          _addr(err_flag), _stream(stream))
+    return q_out
+
+
+def kv_attention_workspace_bytes(T, Hq, Hkv, D) -> int:
+    return lib().kv_attention_workspace_bytes(T, Hq, Hkv, D)
+
+
+def kv_attention_bf16(q, k_cache, v_cache, block_table, cu_q, seq_lens, scale=None, window=0, out=None, lse=None,
+                      want_lse=False, workspace=None, stream=None):
+    """Causal attention of the new tokens ``q [T, Hq, D]`` (bf16, requests
+    back to back, ``cu_q [n_req+1]``) over the cache, which holds
+    ``seq_lens [n_req]`` tokens of each request, the new ones last ->
+    (out bf16 ``[T, Hq, D]``, lse fp32 ``[T, Hq]`` or None).  ``scale``
+    defaults to ``D ** -0.5``; ``window`` 0 sees all earlier keys."""
+    _need_cuda(q, k_cache, v_cache, block_table, cu_q, seq_lens, out, lse, workspace)
+    _typed(torch.bfloat16, q=q, k_cache=k_cache, v_cache=v_cache, out=out)
+    _typed(torch.int32, block_table=block_table, cu_q=cu_q, seq_lens=seq_lens)
+    _typed(torch.float32, lse=lse)
+    _dense(cu_q=cu_q, seq_lens=seq_lens, lse=lse)
+    T, Hq, D = q.shape
+    n_pages, Hkv, page, Dc, page_stride = _cache(k_cache, v_cache)
+    n = seq_lens.numel()
+    if Dc != D or cu_q.numel() != n + 1 or block_table.dim() != 2 or block_table.shape[0] != n or \
+            (n and block_table.stride(1) != 1):
+        raise ValueError("q, the cache, block_table, cu_q and seq_lens do not fit one another")
+    if out is None:
+        out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=q.device)
+    elif out.shape != q.shape:
+        raise ValueError("out must have q's shape")
+    if lse is None:
+        if want_lse:
+            lse = torch.empty((T, Hq), dtype=torch.float32, device=q.device)
+    elif lse.shape != (T, Hq):
+        raise ValueError("lse must be [T, Hq]")
+    if workspace is None:
+        workspace = torch.empty(max(lib().kv_attention_workspace_bytes(T, Hq, Hkv, D), 16), dtype=torch.uint8,
+                                device=q.device)
+    cols, ld_table = _table(block_table)
+    _call("kv_attention_bf16", _addr(q), _heads(q, "q"), T, Hq, Hkv, D, _addr(k_cache), _addr(v_cache), n_pages, page,
+          page_stride, _addr(block_table), cols, ld_table, _addr(cu_q), _addr(seq_lens), n,
+          D ** -0.5 if scale is None else scale, window, _addr(out), _heads(out, "out"), _addr(lse),
+          _addr(workspace), workspace.numel(), _stream(stream))
+    return out, lse
+
+
+def norm_gate_residual(residual, pre_w, eps, y=None, post_w=None, gate=None, alpha=1.0, residual_out=None, out=None,
+                       want_q8=False, out_q8=None, stream=None):
+    """``h = residual + alpha * gate * (rms-normed, post_w-weighted) y`` and
+    ``n = rms-normed, pre_w-weighted h`` in one pass -> (h, n bf16), and the
+    q8_1 rows of n as a third with ``want_q8`` or ``out_q8``.  ``residual``
+    and ``y`` ``[T, dim]`` fp32 or bf16 (row stride allowed), ``gate``
+    ``[dim]`` or ``[T, dim]`` of y's type, weights fp32 ``[dim]``; without y,
+    h is the residual.  ``residual_out`` may be ``residual``."""
+    _need_cuda(residual, pre_w, y, post_w, gate, residual_out, out, out_q8)
+    T, dim = residual.shape
+    s_type = _type(residual, "residual")
+    y_type = Q2K_F32 if y is None else _type(y, "y")
+    _typed(residual.dtype, residual_out=residual_out)
+    _typed(torch.float32, pre_w=pre_w, post_w=post_w)
+    _typed(torch.bfloat16, out=out)
+    _dense(pre_w=pre_w, post_w=post_w, out_q8=out_q8)
+    if y is not None:
+        _typed(y.dtype, gate=gate)
+    if residual_out is None:
+        residual_out = torch.empty((T, dim), dtype=residual.dtype, device=residual.device)
+    if out is None:
+        out = torch.empty((T, dim), dtype=torch.bfloat16, device=residual.device)
+    for name, t in (("residual", residual), ("y", y), ("residual_out", residual_out), ("out", out)):
+        if t is not None and (t.shape != (T, dim) or t.stride(1) != 1):
+            raise ValueError(f"{name} must be [T, dim] with dense rows")
+    if pre_w.numel() != dim or (post_w is not None and post_w.numel() != dim):
+        raise ValueError("a weight must have dim values")
+    ld_gate = 0
+    if gate is not None:
+        if gate.shape[-1] != dim or gate.stride(-1) != 1 or (gate.dim() == 2 and gate.shape[0] not in (1, T)):
+            raise ValueError("gate must be [dim] or [T, dim] with dense rows")
+        if gate.dim() == 2 and gate.shape[0] == T and T > 1:
+            ld_gate = gate.stride(0)
+    if out_q8 is None:
+        if want_q8:
+            out_q8 = torch.empty((T, q8_1_row_bytes(dim)), dtype=torch.uint8, device=residual.device)
+    elif out_q8.numel() != T * q8_1_row_bytes(dim):
+        raise ValueError("out_q8 must hold T q8_1 rows")
+    _call("norm_gate_residual", _addr(y), y_type, _row(y, dim), _addr(post_w), _addr(gate), ld_gate, _addr(residual),
+          s_type, _row(residual, dim), alpha, _addr(pre_w), eps, T, dim, _addr(residual_out),
+          _row(residual_out, dim), _addr(out), _row(out, dim), _addr(out_q8), _stream(stream))
+    return (residual_out, out) if out_q8 is None else (residual_out, out, out_q8)
+
+
+def _row(t, dim):
+    """Stride between the rows of ``t`` (a single row has none of its own)."""
+    return 0 if t is None else t.stride(0) if t.shape[0] > 1 else max(t.stride(0), dim)
+
+
+ROUTE_SCORES = {"softmax": 0, "sigmoid": 1}
+
+
+def moe_route_topk(logits, topk, bias=None, score="softmax", n_group=1, topk_group=1, renorm=True, scale=1.0,
+                   expert_ptrs=None, ids=None, weights=None, ptrs=None, stream=None):
+    """Routing from ``logits [m, E]`` (fp32 or bf16, row stride allowed) ->
+    (ids int32 ``[m, topk]``, weights fp32 ``[m, topk]``), and with
+    ``expert_ptrs`` (int64 ``[3, E]``: gate, up and down addresses) the
+    pointer tables int64 ``[m, 3 * topk]`` that ``q2k_moe_m1`` takes."""
+    _need_cuda(logits, bias, expert_ptrs, ids, weights, ptrs)
+    if score not in ROUTE_SCORES:
+        raise ValueError(f"score must be one of {sorted(ROUTE_SCORES)}")
+    l_type = _type(logits, "logits")
+    _typed(torch.float32, bias=bias, weights=weights)
+    _typed(torch.int32, ids=ids)
+    _typed(torch.int64, expert_ptrs=expert_ptrs, ptrs=ptrs)
+    _dense(bias=bias, ids=ids, weights=weights, expert_ptrs=expert_ptrs, ptrs=ptrs)
+    m, E = logits.shape
+    if logits.stride(1) != 1 or (bias is not None and bias.numel() != E) or \
+            (expert_ptrs is not None and expert_ptrs.numel() != 3 * E):
+        raise ValueError("logits must be [m, E] with dense rows, bias [E], expert_ptrs [3, E]")
+    if ids is None:
+        ids = torch.empty((m, topk), dtype=torch.int32, device=logits.device)
+    if weights is None:
+        weights = torch.empty((m, topk), dtype=torch.float32, device=logits.device)
+    if ptrs is None and expert_ptrs is not None:
+        ptrs = torch.empty((m, 3 * topk), dtype=torch.int64, device=logits.device)
+    if ids.numel() != m * topk or weights.numel() != m * topk or (ptrs is not None and ptrs.numel() != 3 * m * topk):
+        raise ValueError("ids, weights and ptrs must hold topk (3 * topk) entries per token")
+    _call("moe_route_topk", _addr(logits), l_type, m, E, _row(logits, E), _addr(bias), ROUTE_SCORES[score], n_group,
+          topk_group, topk, 1 if renorm else 0, scale, _addr(ids), _addr(weights), _addr(expert_ptrs), _addr(ptrs),
+          _stream(stream))
+    return (ids, weights) if ptrs is None else (ids, weights, ptrs)
 
 
 def q2k_device_error(clear=True) -> int:

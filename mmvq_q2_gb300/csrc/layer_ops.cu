@@ -1,0 +1,479 @@
+// Between the products of a decode layer: the norms around a block fused
+// with its gate and residual scale, and the route of the experts
+// (include/q2k.h, norm_gate_residual and moe_route_topk).
+#include <algorithm>
+#include <cfloat>
+
+#include "q2k_common.cuh"
+#include "q2k_internal.h"
+#include "q2k_q8.cuh"
+
+namespace q2k {
+
+namespace {
+
+// ---- norm_gate_residual --------------------------------------------------------
+//
+// h = residual + alpha * gate * norm(y), n = norm(h): two sums over a row,
+// the second of values that need the first.  Bound by memory: a row stays in
+// registers (8 values a run, up to four runs a thread) from its one read to
+// its one write.
+
+struct NormArgs {
+    const void *y, *gate, *residual;
+    void *residual_out, *out_q8;
+    uint16_t* out;
+    const float *post_w, *pre_w;
+    int64_t ld_y, ld_gate, ld_res, ld_ro, ld_out, T;
+    float alpha, eps;
+    int dim, y_bf16, stream_bf16;
+};
+
+__device__ __forceinline__ float load1(const void* p, int64_t i, int bf16)
+{
+    return bf16 ? bf16_bits_f(static_cast<const uint16_t*>(p)[i]) : static_cast<const float*>(p)[i];
+}
+
+__device__ __forceinline__ void load8(const void* p, int64_t i, int bf16, float (&v)[8])
+{
+    if (bf16) {
+        const uint4 u = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + i);
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            v[2 * j] = __uint_as_float(w[j] << 16);
+            v[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
+        }
+    } else {
+        const float4* f = reinterpret_cast<const float4*>(static_cast<const float*>(p) + i);
+        const float4 a = f[0], b = f[1];
+        v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+    }
+}
+
+__device__ __forceinline__ uint32_t bf16_pair(float lo, float hi)
+{
+    return (uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(lo)) |
+           ((uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(hi)) << 16);
+}
+
+__device__ __forceinline__ void store8(void* p, int64_t i, int bf16, const float (&v)[8])
+{
+    if (bf16)
+        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p) + i) =
+            make_uint4(bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3]), bf16_pair(v[4], v[5]), bf16_pair(v[6], v[7]));
+    else {
+        float4* f = reinterpret_cast<float4*>(static_cast<float*>(p) + i);
+        f[0] = make_float4(v[0], v[1], v[2], v[3]);
+        f[1] = make_float4(v[4], v[5], v[6], v[7]);
+    }
+}
+
+// Sum over the block, the same bits in every thread (fixed order).
+__device__ __forceinline__ float block_sum(float v, float* part)
+{
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1)
+        v += __shfl_xor_sync(0xffffffffu, v, o);
+    const int nw = (int)(blockDim.x >> 5);
+    if (nw == 1)
+        return v;
+    if ((threadIdx.x & 31) == 0)
+        part[threadIdx.x >> 5] = v;
+    __syncthreads();
+    float s = (int)(threadIdx.x & 31) < nw ? part[threadIdx.x & 31] : 0.f;
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1)
+        s += __shfl_xor_sync(0xffffffffu, s, o);
+    return s;
+}
+
+// The q8_1 rows of the bf16 row in shared memory.
+__device__ __forceinline__ void encode_row(const uint16_t* n_row, int dim, uint8_t* out)
+{
+    for (int i0 = 0; i0 < dim; i0 += 4 * (int)blockDim.x) {
+        const int i = i0 + 4 * (int)threadIdx.x;
+        const bool live = i < dim;
+        float v[4] = {0.f, 0.f, 0.f, 0.f};
+        if (live) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                v[j] = bf16_bits_f(n_row[i + j]);
+        }
+        q8_1_encode_group(v, out + (i / kQ8Values) * kQ8Bytes, (int)threadIdx.x & 7, live);
+    }
+}
+
+// 8 values a thread; rows and pointers on 16-byte boundaries.
+constexpr int kNormVecDim = 8 * 1024;
+
+__global__ void __launch_bounds__(1024) norm_vec_kernel(const NormArgs a)
+{
+    extern __shared__ __align__(16) uint16_t n_row[];  // with out_q8: the bf16 row
+    __shared__ float part[2][32];
+    pdl_launch_dependents();
+    pdl_wait();
+    const int64_t t = blockIdx.x;
+    const int i = (int)threadIdx.x * 8;
+    const bool live = i < a.dim;
+    float h[8], u[8], g[8], w[8];
+    if (live) {
+        load8(a.residual, t * a.ld_res + i, a.stream_bf16, h);
+        if (a.y)
+            load8(a.y, t * a.ld_y + i, a.y_bf16, u);
+        if (a.gate)
+            load8(a.gate, t * a.ld_gate + i, a.y_bf16, g);
+        if (a.post_w)
+            load8(a.post_w, i, 0, w);
+    }
+    if (a.post_w) {
+        float s = 0.f;
+        if (live) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                s = fmaf(u[j], u[j], s);
+        }
+        const float inv = 1.0f / sqrtf(block_sum(s, part[0]) / (float)a.dim + a.eps);
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            u[j] = u[j] * inv * w[j];
+    }
+    if (a.gate) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            u[j] *= g[j];
+    }
+    float s = 0.f;
+    if (live) {
+        if (a.y) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                h[j] = fmaf(a.alpha, u[j], h[j]);
+        }
+        load8(a.pre_w, i, 0, w);
+        if (a.residual_out)
+            store8(a.residual_out, t * a.ld_ro + i, a.stream_bf16, h);
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            s = fmaf(h[j], h[j], s);
+    }
+    if (!a.out && !a.out_q8)
+        return;
+    const float inv = 1.0f / sqrtf(block_sum(s, part[1]) / (float)a.dim + a.eps);
+    if (live) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            h[j] = h[j] * inv * w[j];
+        if (a.out)
+            store8(a.out, t * a.ld_out + i, 1, h);
+        if (a.out_q8)
+            store8(n_row, i, 1, h);
+    }
+    if (a.out_q8) {
+        __syncthreads();
+        encode_row(n_row, a.dim, static_cast<uint8_t*>(a.out_q8) + t * (a.dim / kQ8Values) * kQ8Bytes);
+    }
+}
+
+// Any dim, stride and alignment: the row waits in shared memory as fp32.
+__global__ void __launch_bounds__(256) norm_any_kernel(const NormArgs a)
+{
+    extern __shared__ float smem[];
+    float* part = smem;          // [2][32]
+    float* row = smem + 64;      // [dim]
+    pdl_launch_dependents();
+    pdl_wait();
+    const int64_t t = blockIdx.x;
+    float inv = 1.f;
+    if (a.post_w) {
+        float s = 0.f;
+        for (int i = (int)threadIdx.x; i < a.dim; i += (int)blockDim.x) {
+            const float v = load1(a.y, t * a.ld_y + i, a.y_bf16);
+            s = fmaf(v, v, s);
+        }
+        inv = 1.0f / sqrtf(block_sum(s, part) / (float)a.dim + a.eps);
+    }
+    float s = 0.f;
+    for (int i = (int)threadIdx.x; i < a.dim; i += (int)blockDim.x) {
+        float h = load1(a.residual, t * a.ld_res + i, a.stream_bf16);
+        if (a.y) {
+            float u = load1(a.y, t * a.ld_y + i, a.y_bf16);
+            if (a.post_w)
+                u = u * inv * a.post_w[i];
+            if (a.gate)
+                u *= load1(a.gate, t * a.ld_gate + i, a.y_bf16);
+            h = fmaf(a.alpha, u, h);
+        }
+        row[i] = h;
+        if (a.residual_out) {
+            if (a.stream_bf16)
+                static_cast<uint16_t*>(a.residual_out)[t * a.ld_ro + i] = __bfloat16_as_ushort(__float2bfloat16_rn(h));
+            else
+                static_cast<float*>(a.residual_out)[t * a.ld_ro + i] = h;
+        }
+        s = fmaf(h, h, s);
+    }
+    if (!a.out && !a.out_q8)
+        return;
+    inv = 1.0f / sqrtf(block_sum(s, part + 32) / (float)a.dim + a.eps);
+    uint16_t* n_row = reinterpret_cast<uint16_t*>(row + a.dim);
+    for (int i = (int)threadIdx.x; i < a.dim; i += (int)blockDim.x) {
+        const uint16_t n = __bfloat16_as_ushort(__float2bfloat16_rn(row[i] * inv * a.pre_w[i]));
+        if (a.out)
+            a.out[t * a.ld_out + i] = n;
+        if (a.out_q8)
+            n_row[i] = n;
+    }
+    if (a.out_q8) {
+        __syncthreads();
+        encode_row(n_row, a.dim, static_cast<uint8_t*>(a.out_q8) + t * (a.dim / kQ8Values) * kQ8Bytes);
+    }
+}
+
+// ---- moe_route_topk ------------------------------------------------------------
+//
+// One warp a token, expert e in lane e % 32: the scores stay in registers.
+// The choice works on whole numbers that order like the floats, so that a
+// maximum over the warp is one redux instruction and a tie falls to the
+// lowest index exactly.
+
+struct RouteArgs {
+    const void* logits;
+    const float* bias;
+    int32_t* ids;
+    float* weights;
+    const int64_t* expert_ptrs;
+    int64_t* ptrs_out;
+    int64_t m, ld;
+    int E, bf16, sigmoid, n_group, topk_group, topk, renorm;
+    float scale;
+};
+
+// Orders like the float; NaN below -inf, 0 is left for "taken".
+__device__ __forceinline__ uint32_t order_key(float v)
+{
+    const uint32_t b = __float_as_uint(v + 0.f);  // -0 becomes 0
+    if (v != v)
+        return 1u;
+    return b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+
+__device__ __forceinline__ float key_value(uint32_t k)
+{
+    return __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k);
+}
+
+// s += v, with what the rounding loses kept in lo (the two-sum identity).
+__device__ __forceinline__ void add_exact(float& hi, float& lo, float v)
+{
+    const float s = __fadd_rn(hi, v), b = __fadd_rn(s, -hi);
+    lo = __fadd_rn(lo, __fadd_rn(__fadd_rn(hi, -__fadd_rn(s, -b)), __fadd_rn(v, -b)));
+    hi = s;
+}
+
+template <int NE>
+__global__ void __launch_bounds__(128) moe_route_kernel(const RouteArgs a)
+{
+    pdl_launch_dependents();
+    pdl_wait();
+    const int lane = threadIdx.x & 31;
+    const int64_t t = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
+    if (t >= a.m)
+        return;
+    float s[NE];
+    uint32_t key[NE];
+    float top = -FLT_MAX;
+#pragma unroll
+    for (int j = 0; j < NE; ++j) {
+        const int e = j * 32 + lane;
+        float x = e < a.E ? (a.bf16 ? bf16_bits_f(static_cast<const uint16_t*>(a.logits)[t * a.ld + e])
+                                    : static_cast<const float*>(a.logits)[t * a.ld + e])
+                          : -INFINITY;
+        // fminf and fmaxf return the other argument for a NaN
+        x = x != x ? -INFINITY : fminf(x, FLT_MAX);
+        s[j] = x;
+        top = fmaxf(top, x);
+    }
+    if (a.sigmoid) {
+#pragma unroll
+        for (int j = 0; j < NE; ++j)
+            s[j] = __fdiv_rn(1.0f, 1.0f + expf(-s[j]));
+    } else {
+        top = key_value(__reduce_max_sync(0xffffffffu, order_key(top)));
+        float hi = 0.f, lo = 0.f;
+#pragma unroll
+        for (int j = 0; j < NE; ++j) {
+            s[j] = expf(s[j] - top);
+            add_exact(hi, lo, s[j]);
+        }
+#pragma unroll
+        for (int o = 16; o >= 1; o >>= 1) {
+            const float h2 = __shfl_xor_sync(0xffffffffu, hi, o), l2 = __shfl_xor_sync(0xffffffffu, lo, o);
+            lo = __fadd_rn(lo, l2);
+            add_exact(hi, lo, h2);
+        }
+        const float sum = __shfl_sync(0xffffffffu, __fadd_rn(hi, lo), 0);
+#pragma unroll
+        for (int j = 0; j < NE; ++j)
+            s[j] = sum > 0.f ? __fdiv_rn(s[j], sum) : 0.f;
+    }
+#pragma unroll
+    for (int j = 0; j < NE; ++j) {
+        const int e = j * 32 + lane;
+        key[j] = e < a.E ? order_key(a.bias ? __fadd_rn(s[j], a.bias[e]) : s[j]) : 0u;
+    }
+    if (a.n_group > 1) {
+        const int size = a.E / a.n_group;
+        uint32_t gkey = 0;  // lane g: group g's score
+        for (int g = 0; g < a.n_group; ++g) {
+            uint32_t k1 = 0, k2 = 0;
+#pragma unroll
+            for (int j = 0; j < NE; ++j) {
+                const int e = j * 32 + lane - g * size;
+                if (e >= 0 && e < size) {
+                    const uint32_t k = key[j];
+                    k2 = max(k2, min(k1, k));
+                    k1 = max(k1, k);
+                }
+            }
+            const uint32_t b1 = __reduce_max_sync(0xffffffffu, k1);
+            float score = key_value(b1);
+            if (size > 1) {
+                // the first lane that holds the largest gives its next one
+                const uint32_t has = __ballot_sync(0xffffffffu, k1 == b1);
+                if (lane == __ffs(has) - 1)
+                    k1 = k2;
+                score += key_value(__reduce_max_sync(0xffffffffu, k1));
+            }
+            if (lane == g)
+                gkey = order_key(score);
+        }
+        uint32_t kept = 0;
+        for (int i = 0; i < a.topk_group; ++i) {
+            const uint32_t best = __reduce_max_sync(0xffffffffu, gkey);
+            const int g = __ffs(__ballot_sync(0xffffffffu, gkey == best)) - 1;
+            kept |= 1u << g;
+            if (lane == g)
+                gkey = 0;
+        }
+#pragma unroll
+        for (int j = 0; j < NE; ++j) {
+            const int e = j * 32 + lane;
+            if (e < a.E && !(kept >> (e / size) & 1u))
+                key[j] = 0;
+        }
+    }
+    float w = 0.f;  // lane i: weight and expert of choice i
+    int id = 0;
+    for (int i = 0; i < a.topk; ++i) {
+        uint32_t k = 0;
+#pragma unroll
+        for (int j = 0; j < NE; ++j)
+            k = max(k, key[j]);
+        const uint32_t best = __reduce_max_sync(0xffffffffu, k);
+        uint32_t e = 0xffffffffu;
+#pragma unroll
+        for (int j = NE - 1; j >= 0; --j)
+            if (key[j] == best)
+                e = j * 32 + lane;
+        e = __reduce_min_sync(0xffffffffu, e);
+        float v = 0.f;
+#pragma unroll
+        for (int j = 0; j < NE; ++j)
+            if (e == (uint32_t)(j * 32 + lane)) {
+                v = s[j];
+                key[j] = 0;
+            }
+        v = __shfl_sync(0xffffffffu, v, (int)(e & 31u));
+        if (lane == i) {
+            w = v;
+            id = (int)e;
+        }
+    }
+    if (a.renorm) {
+        float sum = w;
+#pragma unroll
+        for (int o = 16; o >= 1; o >>= 1)
+            sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        w = w / (sum + 1e-20f);
+    }
+    if (lane < a.topk) {
+        a.ids[t * a.topk + lane] = id;
+        a.weights[t * a.topk + lane] = w * a.scale;
+        if (a.ptrs_out) {
+#pragma unroll
+            for (int i = 0; i < 3; ++i)
+                a.ptrs_out[(t * 3 + i) * a.topk + lane] = a.expert_ptrs[(int64_t)i * a.E + id];
+        }
+    }
+}
+
+bool on16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+}  // namespace
+
+cudaError_t launch_norm_gate_residual(const NormProblem& p, cudaStream_t s)
+{
+    NormArgs a{};
+    a.y = p.y;
+    a.gate = p.gate;
+    a.residual = p.residual;
+    a.residual_out = p.residual_out;
+    a.out_q8 = p.out_q8;
+    a.out = p.out;
+    a.post_w = p.post_w;
+    a.pre_w = p.pre_w;
+    a.ld_y = p.ld_y;
+    a.ld_gate = p.ld_gate;
+    a.ld_res = p.ld_res;
+    a.ld_ro = p.ld_ro;
+    a.ld_out = p.ld_out;
+    a.T = p.T;
+    a.alpha = p.alpha;
+    a.eps = p.eps;
+    a.dim = (int)p.dim;
+    a.y_bf16 = p.y_bf16;
+    a.stream_bf16 = p.stream_bf16;
+    const int y16 = p.y_bf16 ? 8 : 4, s16 = p.stream_bf16 ? 8 : 4;  // elements of 16 bytes
+    const bool vec = a.dim % 8 == 0 && on16(a.y) && on16(a.gate) && on16(a.residual) && on16(a.residual_out) &&
+                     on16(a.out) && on16(a.post_w) && on16(a.pre_w) && (!a.y || a.ld_y % y16 == 0) &&
+                     a.ld_gate % y16 == 0 && a.ld_res % s16 == 0 && (!a.residual_out || a.ld_ro % s16 == 0) &&
+                     (!a.out || a.ld_out % 8 == 0);
+    if (!vec || a.dim > kNormVecDim) {
+        static std::atomic<unsigned long long> smem_devs{0};
+        cudaError_t e = allow_max_smem(norm_any_kernel, smem_devs);
+        if (e != cudaSuccess)
+            return e;
+        return launch_pdl(norm_any_kernel, dim3((unsigned)a.T), dim3(256),
+                          (size_t)(64 + a.dim) * sizeof(float) + (a.out_q8 ? (size_t)a.dim * 2 : 0), s, a);
+    }
+    const int threads = (a.dim / 8 + 31) / 32 * 32;
+    return launch_pdl(norm_vec_kernel, dim3((unsigned)a.T), dim3(threads), a.out_q8 ? (size_t)a.dim * 2 : 0, s, a);
+}
+
+cudaError_t launch_moe_route(const RouteProblem& p, cudaStream_t s)
+{
+    RouteArgs a{};
+    a.logits = p.logits;
+    a.bias = p.bias;
+    a.ids = p.ids;
+    a.weights = p.weights;
+    a.expert_ptrs = p.expert_ptrs;
+    a.ptrs_out = p.ptrs_out;
+    a.m = p.m;
+    a.ld = p.ld;
+    a.E = (int)p.E;
+    a.bf16 = p.bf16;
+    a.sigmoid = p.sigmoid;
+    a.n_group = p.n_group;
+    a.topk_group = p.topk_group;
+    a.topk = p.topk;
+    a.renorm = p.renorm;
+    a.scale = p.scale;
+    const int ne = (a.E + 31) / 32;
+    auto* kernel = ne <= 1 ? moe_route_kernel<1> : ne <= 2 ? moe_route_kernel<2> : ne <= 4 ? moe_route_kernel<4>
+                 : ne <= 8 ? moe_route_kernel<8> : ne <= 16 ? moe_route_kernel<16> : moe_route_kernel<32>;
+    return launch_pdl(kernel, dim3((unsigned)((p.m + 3) / 4)), dim3(128), 0, s, a);
+}
+
+}  // namespace q2k

@@ -81,6 +81,24 @@ int finish(cudaError_t e) { return e == cudaSuccess ? Q2K_OK : fail_cuda(e); }
 // Largest K the library accepts (weights rows up to 1 MiB of blocks).
 constexpr int64_t kMaxK = 1 << 20;
 
+// Cache slots are int32.
+constexpr int64_t kMaxSlots = (int64_t)1 << 31;
+
+bool type_ok(int t) { return t == Q2K_F32 || t == Q2K_BF16; }
+
+bool page_size_ok(int64_t p) { return p >= 16 && p <= 1024 && (p & (p - 1)) == 0; }
+
+bool cache_ok(int64_t n_pages, int64_t page_size, int64_t page_stride, int64_t Hkv, int64_t D)
+{
+    return page_size_ok(page_size) && n_pages >= 1 && n_pages <= kMaxSlots / page_size &&
+           page_stride >= Hkv * page_size * D && page_stride % 8 == 0 && page_stride < ((int64_t)1 << 36);
+}
+
+bool attn_heads_ok(int64_t Hq, int64_t Hkv, int64_t D)
+{
+    return Hkv >= 1 && Hkv <= 4096 && Hq >= Hkv && Hq % Hkv == 0 && Hq / Hkv <= 128 && D >= 16 && D <= 128 && D % 16 == 0;
+}
+
 }  // namespace
 
 extern "C" {
@@ -126,7 +144,7 @@ int q2k_device_error(int32_t* host_out, int clear)
 {
     if (!host_out)
         return Q2K_ERR_NULL_ARG;
-    int32_t a = 0, b = 0, c = 0, d = 0, q = 0, o = 0, mq = 0, q3t = 0;
+    int32_t a = 0, b = 0, c = 0, d = 0, q = 0, o = 0, mq = 0, q3t = 0, at = 0;
     cudaError_t e = mv_error_word(&a, clear != 0);
     if (e == cudaSuccess)
         e = m1_error_word(&o, clear != 0);
@@ -142,9 +160,11 @@ int q2k_device_error(int32_t* host_out, int clear)
         e = q3_error_word(&q, clear != 0);
     if (e == cudaSuccess)
         e = q3mt_error_word(&q3t, clear != 0);
+    if (e == cudaSuccess)
+        e = attn_error_word(&at, clear != 0);
     if (e != cudaSuccess)
         return fail_cuda(e);
-    *host_out = a | b | c | d | q | o | mq | q3t;
+    *host_out = a | b | c | d | q | o | mq | q3t | at;
     return Q2K_OK;
 }
 
@@ -649,6 +669,248 @@ int dense_gemm_bf16(const uint16_t* x, int64_t m, int64_t K, int64_t ldx, const 
     if (st != Q2K_OK)
         return st;
     return finish(launch_dense_gemm(x, m, K, ldx, W, N, y, ldy, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int kv_page_plan(const int32_t* ctx_lens, const int32_t* new_lens, int64_t n_req, int64_t page_size,
+                 const int32_t* free_pages, int64_t n_free, const int32_t* free_head, int32_t* block_table,
+                 int64_t max_pages, int64_t ld_table, int32_t* cu_q, int32_t* seq_lens, int32_t* positions, int32_t* token_req,
+                 int32_t* slot_map, int64_t max_tokens, int32_t* free_head_out, int32_t* err_flag,
+                 q2k_stream_t stream)
+{
+    if (!ctx_lens || !new_lens || (n_free > 0 && !free_pages) || !block_table || !cu_q || !seq_lens ||
+        (max_tokens > 0 && (!positions || !token_req || !slot_map)) || !free_head_out)
+        return Q2K_ERR_NULL_ARG;
+    if (n_req < 1 || n_req > 16384 || !page_size_ok(page_size) || n_free < 0 || n_free > kMaxSlots || max_pages < 1 ||
+        max_pages > kMaxSlots || ld_table < max_pages || max_tokens < 0 || max_tokens > (1 << 30) || free_head == free_head_out)
+        return Q2K_ERR_BAD_SHAPE;
+    if (!aligned(ctx_lens, 4) || !aligned(new_lens, 4) || !aligned(free_pages, 4) || !aligned(free_head, 4) ||
+        !aligned(block_table, 4) || !aligned(cu_q, 4) || !aligned(seq_lens, 4) || !aligned(positions, 4) ||
+        !aligned(token_req, 4) || !aligned(slot_map, 4) || !aligned(free_head_out, 4) || !aligned(err_flag, 4))
+        return Q2K_ERR_MISALIGNED;
+    int st = check_device();
+    if (st != Q2K_OK)
+        return st;
+    PagePlan p{};
+    p.ctx_lens = ctx_lens;
+    p.new_lens = new_lens;
+    p.n_req = n_req;
+    p.page_size = page_size;
+    p.free_pages = free_pages;
+    p.n_free = n_free;
+    p.free_head = free_head;
+    p.block_table = block_table;
+    p.max_pages = max_pages;
+    p.ld_table = ld_table;
+    p.cu_q = cu_q;
+    p.seq_lens = seq_lens;
+    p.positions = positions;
+    p.token_req = token_req;
+    p.slot_map = slot_map;
+    p.max_tokens = max_tokens;
+    p.free_head_out = free_head_out;
+    p.err_flag = err_flag;
+    return finish(launch_kv_page_plan(p, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int kv_rope_store(const void* q, int64_t ld_q, const void* k, int64_t ld_k, const void* v, int64_t ld_v, int x_type,
+                  int64_t T, int64_t Hq, int64_t Hkv, int64_t D, const int32_t* positions, int64_t n_axes,
+                  const int32_t* sections, const float* inv_freq, int64_t rot, int interleaved,
+                  const int32_t* slot_map, uint16_t* q_out, int64_t ld_qo, uint16_t* k_cache, uint16_t* v_cache,
+                  int64_t n_pages, int64_t page_size, int64_t page_stride, int32_t* err_flag, q2k_stream_t stream)
+{
+    if (!sections || (!q) != (!q_out) ||
+        (T > 0 && (!k || !v || !slot_map || !k_cache || !v_cache || (rot > 0 && (!positions || !inv_freq)))))
+        return Q2K_ERR_NULL_ARG;
+    if (!type_ok(x_type) || T < 0 || T > (1 << 30) || Hkv < 1 || Hkv > 4096 || (q && (Hq < 1 || Hq > 4096)) || D < 1 ||
+        D > 512 || rot < 0 || rot > D || rot % 2 || n_axes < 1 || n_axes > 3 || (interleaved != 0 && interleaved != 1) ||
+        ld_k < Hkv * D || ld_v < Hkv * D || (q && (ld_q < Hq * D || ld_qo < Hq * D)) ||
+        !cache_ok(n_pages, page_size, page_stride, Hkv, D))
+        return Q2K_ERR_BAD_SHAPE;
+    int64_t pairs = 0;
+    for (int64_t i = 0; i < n_axes; ++i) {
+        if (sections[i] < 0)
+            return Q2K_ERR_BAD_SHAPE;
+        pairs += sections[i];
+    }
+    if (pairs != rot / 2)
+        return Q2K_ERR_BAD_SHAPE;
+    const uintptr_t es = x_type == Q2K_BF16 ? 2 : 4;
+    if (!aligned(q, es) || !aligned(k, es) || !aligned(v, es) || !aligned(positions, 4) || !aligned(inv_freq, 4) ||
+        !aligned(slot_map, 4) || !aligned(q_out, 2) || !aligned(k_cache, 2) || !aligned(v_cache, 2) ||
+        !aligned(err_flag, 4))
+        return Q2K_ERR_MISALIGNED;
+    int st = check_device();
+    if (st != Q2K_OK)
+        return st;
+    if (T == 0)
+        return Q2K_OK;
+    RopeStore p{};
+    p.q = q;
+    p.k = k;
+    p.v = v;
+    p.ld_q = ld_q;
+    p.ld_k = ld_k;
+    p.ld_v = ld_v;
+    p.x_bf16 = x_type == Q2K_BF16;
+    p.T = T;
+    p.Hq = Hq;
+    p.Hkv = Hkv;
+    p.D = D;
+    p.positions = positions;
+    for (int64_t i = 0; i < n_axes; ++i)
+        p.sections[i] = sections[i];
+    p.inv_freq = inv_freq;
+    p.rot = rot;
+    p.interleaved = interleaved;
+    p.slot_map = slot_map;
+    p.q_out = q_out;
+    p.ld_qo = ld_qo;
+    p.k_cache = k_cache;
+    p.v_cache = v_cache;
+    p.n_pages = n_pages;
+    p.page_size = page_size;
+    p.page_stride = page_stride;
+    p.err_flag = err_flag;
+    return finish(launch_kv_rope_store(p, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+size_t kv_attention_workspace_bytes(int64_t T, int64_t Hq, int64_t Hkv, int64_t D)
+{
+    if (T < 0 || T > (1 << 24) || !attn_heads_ok(Hq, Hkv, D))
+        return 0;
+    return kv_attention_workspace(T, Hq, Hkv, D);
+}
+
+int kv_attention_bf16(const uint16_t* q, int64_t ld_q, int64_t T, int64_t Hq, int64_t Hkv, int64_t D,
+                      const uint16_t* k_cache, const uint16_t* v_cache, int64_t n_pages, int64_t page_size,
+                      int64_t page_stride, const int32_t* block_table, int64_t max_pages, int64_t ld_table,
+                      const int32_t* cu_q, const int32_t* seq_lens, int64_t n_req, float scale, int64_t window,
+                      uint16_t* out, int64_t ld_o, float* lse, void* workspace, size_t workspace_bytes, q2k_stream_t stream)
+{
+    if ((T != 0 && (!q || !out || !k_cache || !v_cache)) || (T != 0 && n_req != 0 && (!block_table || !cu_q || !seq_lens)))
+        return Q2K_ERR_NULL_ARG;
+    if (T < 0 || T > (1 << 24) || !attn_heads_ok(Hq, Hkv, D) || ld_q < Hq * D || ld_q % 8 || ld_o < Hq * D ||
+        !cache_ok(n_pages, page_size, page_stride, Hkv, D) || max_pages < 1 || max_pages > kMaxSlots || ld_table < max_pages || n_req < 0 ||
+        n_req > 16384 || !(scale > 0.f) || scale > 3.0e38f || window < 0)
+        return Q2K_ERR_BAD_SHAPE;
+    if (T != 0 && (!workspace || workspace_bytes < kv_attention_workspace_bytes(T, Hq, Hkv, D)))
+        return Q2K_ERR_WORKSPACE;
+    if (!aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(block_table, 4) ||
+        !aligned(cu_q, 4) || !aligned(seq_lens, 4) || !aligned(out, 2) || !aligned(lse, 4) || !aligned(workspace, 16))
+        return Q2K_ERR_MISALIGNED;
+    int st = check_device();
+    if (st != Q2K_OK)
+        return st;
+    if (T == 0 || n_req == 0)
+        return Q2K_OK;
+    AttnProblem p{};
+    p.q = q;
+    p.ld_q = ld_q;
+    p.T = T;
+    p.Hq = Hq;
+    p.Hkv = Hkv;
+    p.D = D;
+    p.k_cache = k_cache;
+    p.v_cache = v_cache;
+    p.n_pages = n_pages;
+    p.page_size = page_size;
+    p.page_stride = page_stride;
+    p.block_table = block_table;
+    p.max_pages = max_pages;
+    p.ld_table = ld_table;
+    p.cu_q = cu_q;
+    p.seq_lens = seq_lens;
+    p.n_req = n_req;
+    p.scale = scale;
+    p.window = window;
+    p.out = out;
+    p.ld_o = ld_o;
+    p.lse = lse;
+    p.workspace = workspace;
+    return finish(launch_kv_attention(p, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int norm_gate_residual(const void* y, int y_type, int64_t ld_y, const float* post_w, const void* gate,
+                       int64_t ld_gate, const void* residual, int stream_type, int64_t ld_res, float alpha,
+                       const float* pre_w, float eps, int64_t T, int64_t dim, void* residual_out, int64_t ld_ro,
+                       uint16_t* out, int64_t ld_out, void* out_q8, q2k_stream_t stream)
+{
+    if (T != 0 && (!residual || !pre_w || (!out && !out_q8 && !residual_out) || (!y && (post_w || gate))))
+        return Q2K_ERR_NULL_ARG;
+    if (!type_ok(y_type) || !type_ok(stream_type) || T < 0 || T > (1 << 30) || dim < 1 || dim > 32768 ||
+        (y && ld_y < dim) || (gate && ld_gate != 0 && ld_gate < dim) || ld_res < dim ||
+        (residual_out && ld_ro < dim) || (out && ld_out < dim) || (out_q8 && dim % kQ8Values) || !(eps >= 0.f) ||
+        eps > 3.0e38f || !(alpha >= -3.0e38f && alpha <= 3.0e38f))
+        return Q2K_ERR_BAD_SHAPE;
+    const uintptr_t ys = y_type == Q2K_BF16 ? 2 : 4, ss = stream_type == Q2K_BF16 ? 2 : 4;
+    if (!aligned(y, ys) || !aligned(gate, ys) || !aligned(post_w, 4) || !aligned(pre_w, 4) || !aligned(residual, ss) ||
+        !aligned(residual_out, ss) || !aligned(out, 2) || !aligned(out_q8, 4))
+        return Q2K_ERR_MISALIGNED;
+    int st = check_device();
+    if (st != Q2K_OK)
+        return st;
+    if (T == 0)
+        return Q2K_OK;
+    NormProblem p{};
+    p.y = y;
+    p.y_bf16 = y_type == Q2K_BF16;
+    p.ld_y = ld_y;
+    p.post_w = post_w;
+    p.gate = gate;
+    p.ld_gate = ld_gate;
+    p.residual = residual;
+    p.stream_bf16 = stream_type == Q2K_BF16;
+    p.ld_res = ld_res;
+    p.alpha = alpha;
+    p.pre_w = pre_w;
+    p.eps = eps;
+    p.T = T;
+    p.dim = dim;
+    p.residual_out = residual_out;
+    p.ld_ro = ld_ro;
+    p.out = out;
+    p.ld_out = ld_out;
+    p.out_q8 = out_q8;
+    return finish(launch_norm_gate_residual(p, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int moe_route_topk(const void* logits, int type, int64_t m, int64_t E, int64_t ld, const float* bias, int score,
+                   int64_t n_group, int64_t topk_group, int64_t topk, int renorm, float scale, int32_t* ids,
+                   float* weights, const int64_t* expert_ptrs, int64_t* ptrs_out, q2k_stream_t stream)
+{
+    if (m != 0 && (!logits || !ids || !weights || (!expert_ptrs) != (!ptrs_out)))
+        return Q2K_ERR_NULL_ARG;
+    if (!type_ok(type) || m < 0 || m > (1 << 30) || E < 1 || E > 1024 || ld < E ||
+        (score != Q2K_ROUTE_SOFTMAX && score != Q2K_ROUTE_SIGMOID) || n_group < 1 || n_group > 32 || E % n_group ||
+        topk_group < 1 || topk_group > n_group || topk < 1 || topk > 32 || topk > topk_group * (E / n_group) ||
+        (renorm != 0 && renorm != 1) || !(scale >= -3.0e38f && scale <= 3.0e38f))
+        return Q2K_ERR_BAD_SHAPE;
+    if (!aligned(logits, type == Q2K_BF16 ? 2 : 4) || !aligned(bias, 4) || !aligned(ids, 4) || !aligned(weights, 4) ||
+        !aligned(expert_ptrs, 8) || !aligned(ptrs_out, 8))
+        return Q2K_ERR_MISALIGNED;
+    int st = check_device();
+    if (st != Q2K_OK)
+        return st;
+    if (m == 0)
+        return Q2K_OK;
+    RouteProblem p{};
+    p.logits = logits;
+    p.bf16 = type == Q2K_BF16;
+    p.m = m;
+    p.E = E;
+    p.ld = ld;
+    p.bias = bias;
+    p.sigmoid = score == Q2K_ROUTE_SIGMOID;
+    p.n_group = (int)n_group;
+    p.topk_group = (int)topk_group;
+    p.topk = (int)topk;
+    p.renorm = renorm;
+    p.scale = scale;
+    p.ids = ids;
+    p.weights = weights;
+    p.expert_ptrs = expert_ptrs;
+    p.ptrs_out = ptrs_out;
+    return finish(launch_moe_route(p, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

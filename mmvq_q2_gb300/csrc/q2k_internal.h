@@ -150,6 +150,100 @@ constexpr int kQ3MtMinTokens = 3;
 bool q3mt_supported(const Q3Problem& p);
 cudaError_t launch_q3k_mt(const Q3Problem& p, cudaStream_t s);
 
+// The paged cache's bookkeeping and writer (kv_page.cu; q2k.h, kv_page_plan
+// and kv_rope_store).
+struct PagePlan {
+    const int32_t *ctx_lens, *new_lens;
+    int64_t n_req, page_size;
+    const int32_t* free_pages;
+    int64_t n_free;
+    const int32_t* free_head;
+    int32_t* block_table;
+    int64_t max_pages, ld_table;
+    int32_t *cu_q, *seq_lens, *positions, *token_req, *slot_map;
+    int64_t max_tokens;
+    int32_t *free_head_out, *err_flag;
+};
+cudaError_t launch_kv_page_plan(const PagePlan& p, cudaStream_t s);
+
+struct RopeStore {
+    const void *q, *k, *v;
+    int64_t ld_q, ld_k, ld_v;
+    int x_bf16;
+    int64_t T, Hq, Hkv, D;
+    const int32_t* positions;
+    int sections[3];  // pairs of each axis, 0 where there is none
+    const float* inv_freq;
+    int64_t rot;
+    int interleaved;
+    const int32_t* slot_map;
+    uint16_t* q_out;
+    int64_t ld_qo;
+    uint16_t *k_cache, *v_cache;
+    int64_t n_pages, page_size, page_stride;
+    int32_t* err_flag;
+};
+cudaError_t launch_kv_rope_store(const RopeStore& p, cudaStream_t s);
+
+// Attention over the paged cache (kv_attn.cu; q2k.h, kv_attention_bf16).
+struct AttnProblem {
+    const uint16_t* q;
+    int64_t ld_q, T, Hq, Hkv, D;
+    const uint16_t *k_cache, *v_cache;
+    int64_t n_pages, page_size, page_stride;
+    const int32_t* block_table;
+    int64_t max_pages, ld_table;
+    const int32_t *cu_q, *seq_lens;
+    int64_t n_req;
+    float scale;
+    int64_t window;
+    uint16_t* out;
+    int64_t ld_o;
+    float* lse;
+    void* workspace;
+};
+size_t kv_attention_workspace(int64_t T, int64_t Hq, int64_t Hkv, int64_t D);
+cudaError_t launch_kv_attention(const AttnProblem& p, cudaStream_t s);
+
+// The norms around a block and the route of the experts (layer_ops.cu;
+// q2k.h, norm_gate_residual and moe_route_topk).
+struct NormProblem {
+    const void* y;
+    int y_bf16;
+    int64_t ld_y;
+    const float* post_w;
+    const void* gate;
+    int64_t ld_gate;
+    const void* residual;
+    int stream_bf16;
+    int64_t ld_res;
+    float alpha;
+    const float* pre_w;
+    float eps;
+    int64_t T, dim;
+    void* residual_out;
+    int64_t ld_ro;
+    uint16_t* out;
+    int64_t ld_out;
+    void* out_q8;
+};
+cudaError_t launch_norm_gate_residual(const NormProblem& p, cudaStream_t s);
+
+struct RouteProblem {
+    const void* logits;
+    int bf16;
+    int64_t m, E, ld;
+    const float* bias;
+    int sigmoid;
+    int n_group, topk_group, topk, renorm;
+    float scale;
+    int32_t* ids;
+    float* weights;
+    const int64_t* expert_ptrs;
+    int64_t* ptrs_out;
+};
+cudaError_t launch_moe_route(const RouteProblem& p, cudaStream_t s);
+
 // Read (and optionally clear) this translation unit's device error word.
 cudaError_t mv_error_word(int32_t* out, bool clear);
 cudaError_t m1_error_word(int32_t* out, bool clear);
@@ -159,5 +253,6 @@ cudaError_t mt_error_word(int32_t* out, bool clear);
 cudaError_t umma_error_word(int32_t* out, bool clear);
 cudaError_t q3_error_word(int32_t* out, bool clear);
 cudaError_t q3mt_error_word(int32_t* out, bool clear);
+cudaError_t attn_error_word(int32_t* out, bool clear);
 
 }  // namespace q2k
