@@ -1,10 +1,58 @@
 // Attention of new tokens over the paged cache (include/q2k.h,
-// kv_attention_bf16).
+// kv_attention_bf16) on the 5th-generation tensor cores.
+//
+//   S = Q K^T,  P = 2^(c S - c m),  O = P V / l,   c = scale * log2(e)
+//
+// with the running maximum m and sum l of each row: one pass over the keys.
+//
+// Rows.  The query heads of one kv head read the same keys, so a row is a
+// (token, head) pair: g = Hq / Hkv heads of floor(128 / g) tokens fill a
+// tile of 128 rows, from one new token (g rows) to long prompts.
+//
+// Work.  An item is a request's block of two row tiles on one kv head, its
+// unit a tile of 128 keys.  Every CTA (one per SM) sums the units of all
+// requests from the lengths on the device and takes an equal run of them,
+// wherever it starts and ends: a long decode is split over the whole GPU,
+// a batch of ragged ones and causal prompts balance, and the host needs to
+// know no length.  An item that one CTA finishes is written at once; the
+// pieces of a split one go to the workspace, and a second launch joins them
+// in a fixed order.
+//
+// One CTA, twelve warps:
+//   warp 0       copies Q, K and V tiles (64 values of D by 128 rows, 128-byte
+//                swizzle) into shared memory, a TMA box per page;
+//   warp 1       issues the MMAs: S into tensor memory, and O += P V with P
+//                read from tensor memory (in S's place) and V as it lies;
+//   warps 4..7   softmax of stream 0, one row a thread,
+//   warps 8..11  of stream 1.
+// Two streams, so that the tensor cores work for one while the other's
+// softmax runs: the two row tiles of a block over the same keys, or, where
+// a block has a single tile (decode), every other key tile of it, merged at
+// the item's end.
+//
+// O is rescaled in tensor memory only when a row's maximum has grown by more
+// than 2^8 since the last time: P stays below 2^8, where bf16 and the fp32
+// sums hold it as well as below 1, and the division by l makes the result
+// the same.
+//
+// Rows of V that no row of the block may see (past the sequence's end, or
+// before a window) are cleared in shared memory: a probability of zero
+// times what an unused slot holds could be NaN.  Table entries that are not
+// needed are never read; what is not needed of a tile is filled with zeros
+// by reading past the cache.
+//
+// Every wait is bounded: on a timeout the kernel sets its error word, lets
+// the copies in flight land, frees its tensor memory and returns.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
 #include <algorithm>
 #include <cmath>
+#include <mutex>
 
 #include "q2k_common.cuh"
 #include "q2k_internal.h"
+#include "q2k_umma.cuh"
 
 namespace q2k {
 
@@ -12,130 +60,974 @@ __device__ int g_attn_error = 0;
 
 namespace {
 
-constexpr int kErrBadPage = 2;
+constexpr int kErrBadPage = 2, kErrSetup = 4;
+constexpr int kThreads = 384;
+constexpr int kMaxCtas = 160;
+constexpr int kRows = 128;                  // rows of a tile, keys of a tile
+constexpr int kHalfBytes = kRows * 128;     // 128 rows of 64 values
+constexpr int kMaxStages = 12;
+constexpr float kGrow = 8.0f;               // log2 of how far a row's P may pass 1
 
 struct AttnArgs {
-    const uint16_t *q, *k, *v;
     uint16_t* out;
     float* lse;
     const int32_t *table, *cu_q, *seq_lens;
-    int64_t ld_q, ld_o, ld_table, max_pages, n_pages, page_stride;
+    int64_t ld_o, ld_table, max_pages, n_pages;
     int T, Hq, Hkv, D, n_req, shift, window;
-    float scale;
+    int g, tq;         // query heads of a kv head, tokens of a row tile
+    int nst;           // ring stages
+    int row_cap;       // rows of a piece in the workspace
+    float c;           // scale * log2(e)
+    int vec_out;       // out on 16-byte boundaries
+    int4* heads;       // [2 * gridDim.x] pieces: {kind, r, h, j}
+    float* part_o;     // [2 * gridDim.x][row_cap][D]
+    float2* part_ml;   // [2 * gridDim.x][row_cap] maximum (times c) and sum
 };
 
-// One warp a (token, head): 32 keys at a time, a key's score in each lane,
-// then the lanes share the values' columns.  Running maximum and sum.
-__global__ void __launch_bounds__(128) kv_attn_kernel(const AttnArgs a)
+// Kinds of pieces: first and last key tile of the item, or not.
+constexpr int kNone = 0, kPiece = 1, kFirst = 2, kLast = 4;
+
+// ---- the work ------------------------------------------------------------------
+
+struct Request {
+    int t0, n, base;  // first token, new tokens, position of the first
+};
+
+__device__ __forceinline__ Request load_request(const AttnArgs& a, int r)
 {
-    __shared__ float q_s[4][128];
+    Request q;
+    q.t0 = min(max(a.cu_q[r], 0), a.T);
+    q.n = min(max(a.cu_q[r + 1], q.t0), a.T) - q.t0;
+    q.base = min(max(a.seq_lens[r], 0), 1 << 30) - q.n;
+    return q;
+}
+
+__device__ __forceinline__ int blocks_of(const AttnArgs& a, const Request& q) { return (q.n + 2 * a.tq - 1) / (2 * a.tq); }
+
+// First key that a row at position p sees.
+__device__ __forceinline__ int first_key(const AttnArgs& a, int p) { return a.window > 0 ? max(0, p - a.window + 1) : 0; }
+
+// Key tiles [lo, hi] that tokens i0..i1-1 of a request see (one, wholly
+// masked, where they see nothing).
+__device__ __forceinline__ void key_tiles(const AttnArgs& a, const Request& q, int i0, int i1, int& lo, int& hi)
+{
+    lo = first_key(a, q.base + i0) / kRows;
+    hi = max(q.base + i1 - 1, 0) / kRows;
+    lo = min(lo, hi);
+}
+
+__device__ __forceinline__ int tiles_of(const AttnArgs& a, const Request& q, int j)
+{
+    int lo, hi;
+    key_tiles(a, q, j * 2 * a.tq, min(q.n, (j + 1) * 2 * a.tq), lo, hi);
+    return hi - lo + 1;
+}
+
+// One item, or the part of it that lies in this CTA's run of units.
+struct Item {
+    int r, h, j;
+    Request q;
+    int i0, i1;      // tokens of the request
+    int k0, k1;      // this CTA's key tiles [k0, k1)
+    int lo, hi;      // the item's key tiles
+    bool two;        // two row tiles (else one, its key tiles dealt to both streams)
+    int steps;       // two * (k1 - k0), or k1 - k0
+
+    __device__ __forceinline__ int tile(int u) const { return k0 + (two ? u >> 1 : u); }
+    // Whether step u has anything to do: a row tile may see fewer keys than its block.
+    __device__ __forceinline__ bool active(const AttnArgs& a, int u) const
+    {
+        if (!two)
+            return true;
+        int l, x;
+        const int s = u & 1;
+        key_tiles(a, q, s ? i0 + a.tq : i0, s ? i1 : i0 + a.tq, l, x);
+        const int k = tile(u);
+        return k >= l && k <= x;
+    }
+    __device__ __forceinline__ int kind() const
+    {
+        return kPiece | (k0 == lo ? kFirst : 0) | (k1 == hi + 1 ? kLast : 0);
+    }
+};
+
+// Where a CTA's run starts: item (r, h, j), key tile lo + off, and its units.
+struct Start {
+    int r, h, j, off;
+    int64_t units;
+};
+
+struct Walk {
+    int r, h, j, off;
+    int64_t left;
+    Request q;
+
+    __device__ __forceinline__ Walk(const AttnArgs& a, const Start& s) : r(s.r), h(s.h), j(s.j), off(s.off), left(s.units)
+    {
+        q = load_request(a, r);
+    }
+    // The next item of the run; false when it is done.
+    __device__ __forceinline__ bool next(const AttnArgs& a, Item& it)
+    {
+        if (left <= 0)
+            return false;
+        it.r = r;
+        it.h = h;
+        it.j = j;
+        it.q = q;
+        it.i0 = j * 2 * a.tq;
+        it.i1 = min(q.n, it.i0 + 2 * a.tq);
+        key_tiles(a, q, it.i0, it.i1, it.lo, it.hi);
+        it.k0 = it.lo + off;
+        it.k1 = (int)min((int64_t)it.hi + 1, it.k0 + left);
+        it.two = it.i1 - it.i0 > a.tq;
+        it.steps = (it.k1 - it.k0) * (it.two ? 2 : 1);
+        left -= it.k1 - it.k0;
+        off = 0;
+        if (left > 0) {
+            if (++j >= blocks_of(a, q)) {
+                j = 0;
+                if (++h >= a.Hkv) {
+                    h = 0;
+                    do
+                        q = load_request(a, ++r);
+                    while (q.n == 0);
+                }
+            }
+        }
+        return true;
+    }
+};
+
+// All threads: the units before each request into sums[0..n_req] (shared
+// memory), with warp_sums as scratch.
+__device__ __forceinline__ void sum_units(const AttnArgs& a, int64_t* sums, int64_t* warp_sums)
+{
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int64_t base = 0;
+    for (int r0 = 0; r0 < a.n_req; r0 += kThreads) {
+        const int r = r0 + (int)threadIdx.x;
+        Request q{0, 0, 0};
+        if (r < a.n_req)
+            q = load_request(a, r);
+        const int nb = blocks_of(a, q);
+        int64_t units = 0;
+        if (nb <= 2)
+            for (int j = 0; j < nb; ++j)
+                units += tiles_of(a, q, j);
+        // many blocks: the warp shares them
+        for (uint32_t big = __ballot_sync(0xffffffffu, nb > 2); big; big &= big - 1) {
+            const int src = __ffs(big) - 1;
+            const Request b{__shfl_sync(0xffffffffu, q.t0, src), __shfl_sync(0xffffffffu, q.n, src),
+                            __shfl_sync(0xffffffffu, q.base, src)};
+            const int n = blocks_of(a, b);
+            int64_t mine = 0;
+            for (int j = lane; j < n; j += 32)
+                mine += tiles_of(a, b, j);
+#pragma unroll
+            for (int o = 16; o >= 1; o >>= 1)
+                mine += __shfl_xor_sync(0xffffffffu, mine, o);
+            if (lane == src)
+                units = mine;
+        }
+        units *= a.Hkv;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t v = __shfl_up_sync(0xffffffffu, units, o);
+            if (lane >= o)
+                units += v;
+        }
+        if (lane == 31)
+            warp_sums[warp] = units;
+        __syncthreads();
+        int64_t before = base;
+        for (int w = 0; w < kThreads / 32; ++w) {
+            if (w < warp)
+                before += warp_sums[w];
+            base += warp_sums[w];
+        }
+        if (r < a.n_req)
+            sums[r + 1] = before + units;
+        __syncthreads();
+    }
+    if (threadIdx.x == 0)
+        sums[0] = 0;
+    __syncthreads();
+}
+
+// One warp: the item and key tile of unit `at`.
+__device__ __forceinline__ void find_start(const AttnArgs& a, const int64_t* sums, int64_t at, Start& s)
+{
+    const int lane = threadIdx.x & 31;
+    int lo = 0, hi = a.n_req;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (sums[mid] <= at)
+            lo = mid;
+        else
+            hi = mid;
+    }
+    s.r = lo;
+    int64_t rem = at - sums[lo];
+    const int64_t per_head = (sums[lo + 1] - sums[lo]) / a.Hkv;
+    s.h = (int)(rem / per_head);
+    rem -= s.h * per_head;
+    const Request q = load_request(a, lo);
+    const int nb = blocks_of(a, q);
+    s.j = 0;
+    s.off = 0;
+    for (int j0 = 0; j0 < nb; j0 += 32) {
+        const int n = j0 + lane < nb ? tiles_of(a, q, j0 + lane) : 0;
+        int sum = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, sum, o);
+            if (lane >= o)
+                sum += v;
+        }
+        const uint32_t past = __ballot_sync(0xffffffffu, sum > rem);
+        if (past) {
+            const int src = __ffs(past) - 1;
+            s.j = j0 + src;
+            s.off = (int)(rem - __shfl_sync(0xffffffffu, sum - n, src));
+            return;
+        }
+        rem -= __shfl_sync(0xffffffffu, sum, 31);
+    }
+}
+
+// ---- PTX -----------------------------------------------------------------------
+
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
+            dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
+        : "memory");
+}
+
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, int w,
+                                            uint32_t bar)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
+        : "memory");
+}
+
+// Shared-memory matrix descriptor of V as it lies: rows of 64 values along N
+// (128 bytes, swizzled), K going down the rows.  Groups of 8 rows are 1024
+// bytes apart, the next 64 values of N one half tile.
+__device__ __forceinline__ uint64_t smem_desc_v(uint32_t addr)
+{
+    uint64_t d = 0;
+    d |= (uint64_t)((addr >> 4) & 0x3FFFu);
+    d |= (uint64_t)(kHalfBytes >> 4) << 16;
+    d |= (uint64_t)(1024 >> 4) << 32;
+    d |= (uint64_t)1 << 46;
+    d |= (uint64_t)2 << 61;
+    return d;
+}
+
+constexpr uint32_t kTransposeB = 1u << 16;
+
+// 32 fp32 columns of this warp's TMEM lanes into v[OFF..]; complete after tcgen05.wait::ld.
+template <int OFF, int N>
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&v)[N])
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
+        "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=f"(v[OFF + 0]), "=f"(v[OFF + 1]), "=f"(v[OFF + 2]), "=f"(v[OFF + 3]), "=f"(v[OFF + 4]), "=f"(v[OFF + 5]),
+          "=f"(v[OFF + 6]), "=f"(v[OFF + 7]), "=f"(v[OFF + 8]), "=f"(v[OFF + 9]), "=f"(v[OFF + 10]),
+          "=f"(v[OFF + 11]), "=f"(v[OFF + 12]), "=f"(v[OFF + 13]), "=f"(v[OFF + 14]), "=f"(v[OFF + 15]),
+          "=f"(v[OFF + 16]), "=f"(v[OFF + 17]), "=f"(v[OFF + 18]), "=f"(v[OFF + 19]), "=f"(v[OFF + 20]),
+          "=f"(v[OFF + 21]), "=f"(v[OFF + 22]), "=f"(v[OFF + 23]), "=f"(v[OFF + 24]), "=f"(v[OFF + 25]),
+          "=f"(v[OFF + 26]), "=f"(v[OFF + 27]), "=f"(v[OFF + 28]), "=f"(v[OFF + 29]), "=f"(v[OFF + 30]),
+          "=f"(v[OFF + 31])
+        : "r"(taddr));
+}
+
+__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16])
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
+            taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+
+__device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+
+__device__ __forceinline__ float exp2_approx(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
+{
+    uint32_t d;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+    return d;
+}
+
+// ---- the kernel ----------------------------------------------------------------
+
+struct Shared {
+    uint64_t q_full, q_empty, s_full[2], p_ready[2], o_done[2], traded, read;
+    uint64_t full[kMaxStages], empty[kMaxStages];
+    int64_t warp_sums[kThreads / 32];
+    Start start;
+    float2 ml[2][kRows];  // one-tile items: each stream's maximum (times c) and sum
+    uint32_t tmem;
+    int abort_flag;
+    int loads;            // stages filled, for the clean-up
+    int q_loads;
+};
+
+// Writes 16 values of a row of out.
+__device__ __forceinline__ void store_out16(uint16_t* dst, const float* v, float f, bool vec)
+{
+    if (vec) {
+        uint32_t w[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            w[i] = pack_bf16(v[2 * i] * f, v[2 * i + 1] * f);
+        reinterpret_cast<uint4*>(dst)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+        reinterpret_cast<uint4*>(dst)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            dst[i] = __bfloat16_as_ushort(__float2bfloat16_rn(v[i] * f));
+    }
+}
+
+__device__ __forceinline__ float lse_of(float mc, float l)
+{
+    return l > 0.f ? (mc + log2f(l)) * 0.6931471805599453f : -INFINITY;
+}
+
+template <int DB>  // halves of 64 values of D
+__global__ void __launch_bounds__(kThreads, 1)
+    kv_attn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
+                   const __grid_constant__ CUtensorMap tv)
+{
+    extern __shared__ __align__(1024) uint8_t smem[];  // two Q tiles, the ring, Shared
+    constexpr int kTile = DB * kHalfBytes;
+    pdl_launch_dependents();
+    Shared& sh = *reinterpret_cast<Shared*>(smem + (size_t)(2 + a.nst) * kTile);
+    const uint32_t q_smem = smem_u32(smem), ring = q_smem + 2 * kTile;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    volatile int* abort_flag = &sh.abort_flag;
+
+    if (smem_u32(smem) & 1023u) {  // the swizzle repeats every 1024 bytes
+        if (threadIdx.x == 0)
+            atomicOr(&g_attn_error, kErrSetup);
+        return;
+    }
+    if (threadIdx.x == 0) {
+        mbar_init(smem_u32(&sh.q_full), 1);
+        mbar_init(smem_u32(&sh.q_empty), 1);
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(smem_u32(&sh.s_full[s]), 1);
+            mbar_init(smem_u32(&sh.p_ready[s]), 4);
+            mbar_init(smem_u32(&sh.o_done[s]), 1);
+        }
+        mbar_init(smem_u32(&sh.traded), 8);
+        mbar_init(smem_u32(&sh.read), 8);
+        for (int s = 0; s < a.nst; ++s) {
+            mbar_init(smem_u32(&sh.full[s]), 1);
+            mbar_init(smem_u32(&sh.empty[s]), 1);
+        }
+        sh.abort_flag = 0;
+        sh.loads = sh.q_loads = 0;
+        fence_mbar_init();
+    }
+    pdl_wait();
+    // this CTA's run of units (the sums lie where the ring will be)
+    int64_t* sums = reinterpret_cast<int64_t*>(smem + 2 * kTile);
+    sum_units(a, sums, sh.warp_sums);
+    const int64_t total = sums[a.n_req];
+    const int64_t from = total * blockIdx.x / gridDim.x, to = total * (blockIdx.x + 1) / gridDim.x;
+    if (threadIdx.x < 2)
+        a.heads[2 * blockIdx.x + threadIdx.x] = make_int4(kNone, 0, 0, 0);
+    if (from == to)
+        return;
+    if (warp == 0) {
+        Start s;
+        find_start(a, sums, from, s);
+        s.units = to - from;
+        if (lane == 0)
+            sh.start = s;
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&sh.tmem)),
+                     "r"(512u)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the sums are read; copies may overwrite them
+    fence_before();
+    __syncthreads();
+    fence_after();
+    const uint32_t tmem = sh.tmem;
+
+    auto wait = [&](uint64_t& bar, uint32_t parity) {
+        if (mbar_wait_bounded(smem_u32(&bar), parity & 1u, abort_flag))
+            return true;
+        atomicOr(&g_attn_error, Q2K_ERR_BIT_WAIT_TIMEOUT);
+        *abort_flag = 1;
+        return false;
+    };
+    auto warp_wait = [&](uint64_t& bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(bar, parity)); };
+
+    Walk walk(a, sh.start);
+    Item it{};
+    if (warp == 0) {
+        // ---- copies ----
+        const int box_rows = min(1 << a.shift, kRows), boxes = kRows / box_rows;
+        int loads = 0, items = 0;
+        // the page that holds this lane's box of key tile k, or one past the cache where no row needs it
+        auto page_of = [&](int k) -> int {
+            const int key = k * kRows + lane * box_rows;
+            if (lane >= boxes || key > it.q.base + it.i1 - 1 || key + box_rows <= first_key(a, it.q.base + it.i0))
+                return (int)a.n_pages;
+            const int col = key >> a.shift;
+            const int page = col < a.max_pages ? a.table[it.r * a.ld_table + col] : -1;
+            if (page >= 0 && page < a.n_pages)
+                return page;
+            atomicOr(&g_attn_error, kErrBadPage);
+            return (int)a.n_pages;
+        };
+        auto load = [&](const CUtensorMap* map, int k, int page) {
+            const int s = loads % a.nst, use = loads / a.nst;
+            if (use > 0 && !warp_wait(sh.empty[s], (uint32_t)(use - 1)))
+                return false;
+            if (lane == 0) {
+                mbar_arrive_expect_tx(smem_u32(&sh.full[s]), kTile);
+                sh.loads = loads + 1;
+            }
+            __syncwarp();
+            if (lane < boxes) {
+                const uint32_t dst = ring + (uint32_t)s * kTile + (uint32_t)(lane * box_rows * 128);
+                const int row = (k * kRows + lane * box_rows) & ((1 << a.shift) - 1);
+#pragma unroll
+                for (int b = 0; b < DB; ++b)
+                    tma_load_4d(dst + b * kHalfBytes, map, b * 64, row, it.h, page, smem_u32(&sh.full[s]));
+            }
+            ++loads;
+            return true;
+        };
+        bool ok = true;
+        while (ok && walk.next(a, it)) {
+            if (items > 0 && !warp_wait(sh.q_empty, (uint32_t)(items - 1)))
+                break;
+            if (lane == 0) {
+                const int tiles = it.two ? 2 : 1;
+                mbar_arrive_expect_tx(smem_u32(&sh.q_full), (uint32_t)(tiles * DB * a.g * a.tq * 128));
+                sh.q_loads = items + 1;
+                for (int s = 0; s < tiles; ++s)
+#pragma unroll
+                    for (int b = 0; b < DB; ++b)
+                        tma_load_3d(q_smem + s * kTile + b * kHalfBytes, &tq, b * 64, it.h * a.g,
+                                    it.q.t0 + it.i0 + s * a.tq, smem_u32(&sh.q_full));
+            }
+            __syncwarp();
+            ++items;
+            // key tiles in the order of their first use: K(0) K(1) V(0) K(2) V(1) ...
+            const int n = it.k1 - it.k0, ahead = it.two ? 1 : 2;
+            int pages[2] = {page_of(it.k0), n > 1 ? page_of(it.k0 + 1) : 0};  // of tiles i, i + 1 (alternating)
+            ok = load(&tk, it.k0, pages[0]);
+            if (ahead == 2 && n > 1)
+                ok = ok && load(&tk, it.k0 + 1, pages[1]);
+            for (int i = 0; ok && i < n; ++i) {
+                const int k = it.k0 + i;
+                const int here = pages[i & 1];
+                if (i + 2 < n)
+                    pages[i & 1] = page_of(k + 2);
+                ok = load(&tv, k, here);
+                if (ok && i + ahead < n)
+                    ok = load(&tk, k + ahead, pages[(i + ahead) & 1]);
+            }
+        }
+    } else if (warp == 1) {
+        // ---- MMAs ----
+        const uint32_t idesc_s = instr_desc(kRows), idesc_o = instr_desc(a.D) | kTransposeB;
+        int loads = 0, items = 0, uses[2] = {0, 0};
+        bool ok = true;
+        while (ok && walk.next(a, it)) {
+            int k_stage = 0, v_stage = 0;
+            int done[2] = {0, 0};  // P V products of this item, by stream
+            const int v_lo = first_key(a, it.q.base + it.i0), v_hi = it.q.base + it.i1;
+            if (!warp_wait(sh.q_full, (uint32_t)items))
+                break;
+            ++items;
+            fence_after();
+            auto score = [&](int u) {  // S of step u
+                const int s = u & 1;
+                if (!it.two || s == 0) {
+                    k_stage = loads % a.nst;
+                    if (!warp_wait(sh.full[k_stage], (uint32_t)(loads / a.nst)))
+                        return false;
+                    ++loads;
+                    fence_after();
+                }
+                const uint32_t qa = q_smem + (it.two ? s * kTile : 0), kb = ring + (uint32_t)k_stage * kTile;
+                const bool act = it.active(a, u);
+                if (elect_one()) {
+                    if (act) {
+                        for (int k = 0; k < a.D / 16; ++k) {
+                            const uint32_t off = (uint32_t)((k >> 2) * kHalfBytes + (k & 3) * 32);
+                            umma_f16(tmem + s * 256, smem_desc_sw128(qa + off), smem_desc_sw128(kb + off), idesc_s, k > 0);
+                        }
+                        umma_commit(smem_u32(&sh.s_full[s]));
+                    }
+                    if (!it.two || s == 1)
+                        umma_commit(smem_u32(&sh.empty[k_stage]));
+                    if (u == it.steps - 1)
+                        umma_commit(smem_u32(&sh.q_empty));
+                }
+                __syncwarp();
+                return true;
+            };
+            ok = score(0) && (it.steps < 2 || score(1));
+            for (int u = 0; ok && u < it.steps; ++u) {
+                const int s = u & 1;
+                if (!it.two || s == 0) {
+                    v_stage = loads % a.nst;
+                    if (!(ok = warp_wait(sh.full[v_stage], (uint32_t)(loads / a.nst))))
+                        break;
+                    ++loads;
+                    // clear the rows that no row of the block sees
+                    const int z_lo = max(0, min(kRows, v_lo - it.tile(u) * kRows));
+                    const int z_hi = max(0, min(kRows, v_hi - it.tile(u) * kRows));
+                    if (z_lo > 0 || z_hi < kRows) {
+                        for (int i = lane; i < kRows * 8; i += 32) {
+                            const int row = i >> 3;
+                            if (row < z_lo || row >= z_hi) {
+                                uint8_t* p = smem + 2 * kTile + (size_t)v_stage * kTile + i * 16;
+#pragma unroll
+                                for (int b = 0; b < DB; ++b)
+                                    *reinterpret_cast<uint4*>(p + b * kHalfBytes) = make_uint4(0, 0, 0, 0);
+                            }
+                        }
+                        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                        __syncwarp();
+                    }
+                }
+                const bool act = it.active(a, u);
+                if (act) {
+                    if (!(ok = warp_wait(sh.p_ready[s], (uint32_t)uses[s])))
+                        break;
+                    ++uses[s];
+                }
+                fence_after();
+                if (elect_one()) {
+                    if (act) {
+                        const uint32_t vb = ring + (uint32_t)v_stage * kTile;
+#pragma unroll
+                        for (int k = 0; k < kRows / 16; ++k)
+                            umma_f16_tmem_a(tmem + s * 256 + 128, tmem + s * 256 + k * 8, smem_desc_v(vb + k * 2048),
+                                            idesc_o, done[s] > 0 || k > 0);
+                        umma_commit(smem_u32(&sh.o_done[s]));
+                    }
+                    if (!it.two || s == 1)
+                        umma_commit(smem_u32(&sh.empty[v_stage]));
+                }
+                __syncwarp();
+                done[s] += act;
+                if (u + 2 < it.steps)
+                    ok = score(u + 2);
+            }
+        }
+    } else if (warp >= 4) {
+        // ---- softmax ----
+        const int s = (warp - 4) >> 2, quarter = warp & 3, row = quarter * 32 + lane;
+        const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16), t_s = lanes + s * 256, t_o = t_s + 128;
+        int uses = 0, trades = 0;
+        bool ok = true;
+        while (ok && walk.next(a, it)) {
+            const int ti = row / a.g, head = row - ti * a.g;
+            const int i = it.i0 + ti + (it.two && s ? a.tq : 0);  // token of the request
+            const bool live = row < a.g * a.tq && i < it.i1;
+            const bool warp_live = __any_sync(0xffffffffu, live);
+            const int p = it.q.base + i;
+            const int k_max = live ? p : INT_MAX, k_min = live ? first_key(a, p) : 0;
+            float m = -INFINITY, l = 0.f;  // m: what P is relative to
+            int count = 0;
+            for (int u = s; ok && u < it.steps; u += 2) {
+                if (!it.active(a, u))
+                    continue;
+                if (!(ok = warp_wait(sh.s_full[s], (uint32_t)uses)))
+                    break;
+                fence_after();
+                if (warp_live) {
+                    float v[kRows];
+                    tmem_ld32<0>(t_s, v);
+                    tmem_ld32<32>(t_s + 32, v);
+                    tmem_ld32<64>(t_s + 64, v);
+                    tmem_ld32<96>(t_s + 96, v);
+                    tmem_wait_ld();
+                    const int key0 = it.tile(u) * kRows;
+                    if (__any_sync(0xffffffffu, key0 + kRows - 1 > k_max || key0 < k_min)) {
+                        const int hi = k_max - key0, lo = k_min - key0;
+#pragma unroll
+                        for (int x = 0; x < kRows; ++x)
+                            v[x] = x <= hi && x >= lo ? v[x] : -INFINITY;
+                    }
+                    float t4[4] = {v[0], v[1], v[2], v[3]};
+#pragma unroll
+                    for (int x = 4; x < kRows; ++x)
+                        t4[x & 3] = fmaxf(t4[x & 3], v[x]);
+                    const float top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
+                    const bool grow = (top - m) * a.c > kGrow;  // false for -inf - -inf
+                    if (__any_sync(0xffffffffu, grow)) {
+                        const float m_new = fmaxf(m, top);
+                        const float f = m_new == m ? 1.f : exp2_approx((m - m_new) * a.c);
+                        m = m_new;
+                        if (count > 0) {
+                            l *= f;
+                            // the last product into O must be done
+                            if (!(ok = warp_wait(sh.o_done[s], (uint32_t)(uses - 1))))
+                                break;
+                            fence_after();
+                            for (int x = 0; x < a.D; x += 16) {
+                                float o[16];
+                                uint32_t w[16];
+                                tmem_ld16(t_o + x, o);
+#pragma unroll
+                                for (int y = 0; y < 16; ++y)
+                                    w[y] = __float_as_uint(o[y] * f);
+                                tmem_st16(t_o + x, w);
+                            }
+                        }
+                    }
+                    const float mc = m == -INFINITY ? 0.f : m * a.c;
+                    float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int x = 0; x < kRows; x += 32) {
+                        uint32_t w[16];
+#pragma unroll
+                        for (int y = 0; y < 16; ++y) {
+                            const float e0 = exp2_approx(fmaf(v[x + 2 * y], a.c, -mc));
+                            const float e1 = exp2_approx(fmaf(v[x + 2 * y + 1], a.c, -mc));
+                            sum[(2 * y) & 3] += e0;
+                            sum[(2 * y + 1) & 3] += e1;
+                            w[y] = pack_bf16(e0, e1);
+                        }
+                        tmem_st16(t_s + x / 2, w);
+                    }
+                    l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                    tmem_wait_st();
+                }
+                ++uses;
+                ++count;
+                fence_before();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(smem_u32(&sh.p_ready[s]));
+            }
+            if (!ok)
+                break;
+            // ---- the item's result ----
+            if (count > 0 && !(ok = warp_wait(sh.o_done[s], (uint32_t)(uses - 1))))
+                break;
+            const int kind = it.kind();
+            const bool whole = (kind & kFirst) && (kind & kLast);
+            const int slot = 2 * blockIdx.x + ((kind & kFirst) ? 1 : 0);
+            if (!whole && warp == 4 && lane == 0)
+                a.heads[slot] = make_int4(kind, it.r, it.h, it.j);
+            const int64_t out_row = (int64_t)(it.q.t0 + i);
+            const int out_head = it.h * a.g + head;
+            uint16_t* dst = a.out + out_row * a.ld_o + (int64_t)out_head * a.D;
+            float mc = m == -INFINITY ? -INFINITY : m * a.c;
+            if (it.two) {
+                fence_after();
+                if (warp_live) {
+                    float* part = a.part_o + ((int64_t)slot * a.row_cap + s * kRows + row) * a.D;
+                    const float inv = l > 0.f ? 1.0f / l : 0.f;
+                    for (int x = 0; x < a.D; x += 16) {
+                        float o[16];
+                        if (count > 0)
+                            tmem_ld16(t_o + x, o);
+                        // a row without a key is zero, whatever O holds
+#pragma unroll
+                        for (int y = 0; y < 16; ++y)
+                            o[y] = l > 0.f ? o[y] : 0.f;
+                        if (live) {
+                            if (whole)
+                                store_out16(dst + x, o, inv, a.vec_out);
+                            else {
+#pragma unroll
+                                for (int y = 0; y < 16; y += 4)
+                                    *reinterpret_cast<float4*>(part + x + y) = make_float4(o[y], o[y + 1], o[y + 2], o[y + 3]);
+                            }
+                        }
+                    }
+                    if (live) {
+                        if (!whole)
+                            a.part_ml[(int64_t)slot * a.row_cap + s * kRows + row] = make_float2(mc, l);
+                        else if (a.lse)
+                            a.lse[out_row * a.Hq + out_head] = lse_of(mc, l);
+                    }
+                }
+                fence_before();
+            } else {
+                // both streams hold a part of the same rows: each joins half of the columns
+                sh.ml[s][row] = make_float2(mc, l);
+                fence_before();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(smem_u32(&sh.traded));
+                if (!(ok = warp_wait(sh.traded, (uint32_t)trades)))
+                    break;
+                fence_after();
+                if (warp_live) {
+                    const float2 e0 = sh.ml[0][row], e1 = sh.ml[1][row];
+                    const float top = fmaxf(e0.x, e1.x);
+                    const float f0 = e0.y > 0.f ? exp2_approx(e0.x - top) : 0.f;
+                    const float f1 = e1.y > 0.f ? exp2_approx(e1.x - top) : 0.f;
+                    const float sum = e0.y * f0 + e1.y * f1;
+                    const float inv = sum > 0.f ? 1.0f / sum : 0.f;
+                    float* part = a.part_o + ((int64_t)slot * a.row_cap + row) * a.D;
+                    for (int x = s * 16; x < a.D; x += 32) {
+                        float o0[16], o1[16];
+                        tmem_ld16(lanes + 128 + x, o0);
+                        tmem_ld16(lanes + 384 + x, o1);
+#pragma unroll
+                        for (int y = 0; y < 16; ++y)
+                            o0[y] = (f0 > 0.f ? o0[y] * f0 : 0.f) + (f1 > 0.f ? o1[y] * f1 : 0.f);
+                        if (live) {
+                            if (whole)
+                                store_out16(dst + x, o0, inv, a.vec_out);
+                            else {
+#pragma unroll
+                                for (int y = 0; y < 16; y += 4)
+                                    *reinterpret_cast<float4*>(part + x + y) =
+                                        make_float4(o0[y], o0[y + 1], o0[y + 2], o0[y + 3]);
+                            }
+                        }
+                    }
+                    if (live && s == 0) {
+                        if (!whole)
+                            a.part_ml[(int64_t)slot * a.row_cap + row] = make_float2(top, sum);
+                        else if (a.lse)
+                            a.lse[out_row * a.Hq + out_head] = lse_of(top, sum);
+                    }
+                }
+                // O and ml are free again once both streams have read them
+                fence_before();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(smem_u32(&sh.read));
+                if (!(ok = warp_wait(sh.read, (uint32_t)trades)))
+                    break;
+                ++trades;
+            }
+        }
+    }
+    fence_before();
+    __syncthreads();
+    if (*abort_flag && threadIdx.x == 0) {
+        // let the copies that were issued land before the CTA exits
+        for (int i = max(0, sh.loads - a.nst); i < sh.loads; ++i)
+            mbar_wait_bounded(smem_u32(&sh.full[i % a.nst]), (uint32_t)(i / a.nst) & 1u, nullptr);
+        if (sh.q_loads > 0)
+            mbar_wait_bounded(smem_u32(&sh.q_full), (uint32_t)(sh.q_loads - 1) & 1u, nullptr);
+    }
+    __syncthreads();
+    if (warp == 1)
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u) : "memory");
+}
+
+// Joins the pieces of split items: block x takes the item whose last piece
+// CTA x of the first launch wrote, a warp a row, pieces in the order of
+// their keys.
+constexpr int kJoinWarps = 8, kJoinY = 8;
+
+__global__ void __launch_bounds__(kJoinWarps * 32) kv_attn_join_kernel(const AttnArgs a)
+{
     pdl_launch_dependents();
     pdl_wait();
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int64_t row = (int64_t)blockIdx.x * 4 + warp;
-    if (row >= (int64_t)a.T * a.Hq)
+    const int last = (int)blockIdx.x, lane = threadIdx.x & 31;
+    const int4 head = a.heads[2 * last];
+    if (!(head.x & kLast))
         return;
-    const int t = (int)(row / a.Hq), head = (int)(row % a.Hq), kvh = head / (a.Hq / a.Hkv);
-    if (t >= a.cu_q[a.n_req])
-        return;
-    int r = 0, hi_r = a.n_req;
-    while (hi_r - r > 1) {
-        const int mid = (r + hi_r) / 2;
-        if (a.cu_q[mid] <= t)
-            r = mid;
-        else
-            hi_r = mid;
+    // the first piece is some CTA's second slot; CTAs without units lie between
+    int first = last;
+    while (first > 0) {
+        --first;
+        if (a.heads[2 * first + 1].x & kFirst)
+            break;
     }
-    const int p = a.seq_lens[r] - (a.cu_q[r + 1] - t);
-    const int lo = a.window > 0 ? max(0, p - a.window + 1) : 0;
-    for (int d = lane; d < a.D; d += 32)
-        q_s[warp][d] = bf16_bits_f(a.q[t * a.ld_q + (int64_t)head * a.D + d]) * a.scale;
-    __syncwarp();
-    float m = -INFINITY, l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
-    for (int j0 = lo; j0 <= p; j0 += 32) {
-        const int j = j0 + lane;
-        float s = -INFINITY;
-        int64_t at = -1;
-        if (j <= p) {
-            const int col = j >> a.shift;
-            const int page = col < a.max_pages ? a.table[r * a.ld_table + col] : -1;
-            s = 0.f;
-            if (page >= 0 && page < a.n_pages) {
-                at = page * a.page_stride + (((int64_t)kvh << a.shift) + (j & ((1 << a.shift) - 1))) * a.D;
-                for (int d = 0; d < a.D; ++d)
-                    s = fmaf(q_s[warp][d], bf16_bits_f(a.k[at + d]), s);
-            } else {
-                atomicOr(&g_attn_error, kErrBadPage);
+    const Request q = load_request(a, head.y);
+    const int i0 = head.w * 2 * a.tq, i1 = min(q.n, i0 + 2 * a.tq);
+    const bool two = i1 - i0 > a.tq;
+    const int rows = two ? 2 * kRows : kRows;
+    for (int row = (int)blockIdx.y * kJoinWarps + (threadIdx.x >> 5); row < rows; row += kJoinWarps * kJoinY) {
+        const int s = row >> 7, in = row & 127, ti = in / a.g;
+        const int i = i0 + s * a.tq + ti;
+        if (in >= a.g * a.tq || i >= i1)
+            continue;
+        float top = -INFINITY;
+        for (int c = first; c <= last; ++c) {
+            const int slot = 2 * c + (c == first);
+            if (a.heads[slot].x)
+                top = fmaxf(top, a.part_ml[(int64_t)slot * a.row_cap + row].x);
+        }
+        float sum = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
+        for (int c = first; c <= last; ++c) {
+            const int slot = 2 * c + (c == first);
+            if (!a.heads[slot].x)
+                continue;
+            const float2 ml = a.part_ml[(int64_t)slot * a.row_cap + row];
+            if (!(ml.y > 0.f))
+                continue;
+            const float f = exp2_approx(ml.x - top);
+            sum = fmaf(ml.y, f, sum);
+            const float* part = a.part_o + ((int64_t)slot * a.row_cap + row) * a.D;
+            if (lane * 4 < a.D) {
+                const float4 v = *reinterpret_cast<const float4*>(part + lane * 4);
+                o[0] = fmaf(v.x, f, o[0]);
+                o[1] = fmaf(v.y, f, o[1]);
+                o[2] = fmaf(v.z, f, o[2]);
+                o[3] = fmaf(v.w, f, o[3]);
             }
         }
-        float top = s;
+        const float inv = sum > 0.f ? 1.0f / sum : 0.f;
+        const int64_t t = q.t0 + i;
+        const int h = head.z * a.g + (in - ti * a.g);
+        if (lane * 4 < a.D) {
+            uint16_t* dst = a.out + t * a.ld_o + (int64_t)h * a.D + lane * 4;
 #pragma unroll
-        for (int i = 16; i >= 1; i >>= 1)
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, i));
-        const float mn = fmaxf(m, top);
-        const float shrink = expf(m - mn), e = expf(s - mn);
-        l *= shrink;
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
-            o[c] *= shrink;
-        m = mn;
-        float sum = e;
-#pragma unroll
-        for (int i = 16; i >= 1; i >>= 1)
-            sum += __shfl_xor_sync(0xffffffffu, sum, i);
-        l += sum;
-        for (int i = 0; i < 32 && j0 + i <= p; ++i) {
-            const float w = __shfl_sync(0xffffffffu, e, i);
-            const int64_t src = __shfl_sync(0xffffffffu, at, i);
-            if (src >= 0) {
-#pragma unroll
-                for (int c = 0; c < 4; ++c)
-                    if (c * 32 + lane < a.D)
-                        o[c] = fmaf(w, bf16_bits_f(a.v[src + c * 32 + lane]), o[c]);
-            }
+            for (int y = 0; y < 4; ++y)
+                dst[y] = __bfloat16_as_ushort(__float2bfloat16_rn(o[y] * inv));
         }
+        if (a.lse && lane == 0)
+            a.lse[t * a.Hq + h] = lse_of(top, sum);
     }
-    const float inv = l > 0.f ? 1.0f / l : 0.f;
-#pragma unroll
-    for (int c = 0; c < 4; ++c)
-        if (c * 32 + lane < a.D)
-            a.out[t * a.ld_o + (int64_t)head * a.D + c * 32 + lane] =
-                __bfloat16_as_ushort(__float2bfloat16_rn(o[c] * inv));
-    if (a.lse && lane == 0)
-        a.lse[(int64_t)t * a.Hq + head] = l > 0.f ? m + logf(l) : -INFINITY;
+}
+
+PFN_cuTensorMapEncodeTiled_v12000 encoder()
+{
+    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+    static std::once_flag once;
+    std::call_once(once, [] {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult q{};
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) ==
+                cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+    });
+    return fn;
+}
+
+bool encode(CUtensorMap* map, const void* base, int rank, const cuuint64_t* dims, const cuuint64_t* strides,
+            const cuuint32_t* box)
+{
+    PFN_cuTensorMapEncodeTiled_v12000 enc = encoder();
+    const cuuint32_t estr[4] = {1, 1, 1, 1};
+    return enc && enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)rank, const_cast<void*>(base), dims, strides, box,
+                      estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Workspace: piece headers, then sums and maxima, then rows of O.
+struct Layout {
+    int64_t row_cap;
+    size_t ml, o, bytes;
+};
+
+Layout layout_of(int64_t T, int64_t Hq, int64_t Hkv, int64_t D)
+{
+    const int64_t g = Hq / Hkv, tq = kRows / g;
+    Layout w{};
+    w.row_cap = T <= tq ? std::max<int64_t>(1, T * g) : 2 * kRows;
+    w.ml = (size_t)2 * kMaxCtas * sizeof(int4);
+    w.o = w.ml + ((size_t)2 * kMaxCtas * w.row_cap * sizeof(float2) + 15) / 16 * 16;
+    w.bytes = w.o + (size_t)2 * kMaxCtas * w.row_cap * D * sizeof(float);
+    return w;
+}
+
+template <int DB>
+cudaError_t launch_tc(AttnArgs& a, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, int grid,
+                      int smem_optin, cudaStream_t s)
+{
+    constexpr size_t tile = DB * kHalfBytes;
+    static std::atomic<unsigned long long> devs{0};
+    cudaError_t e = allow_max_smem(kv_attn_kernel<DB>, devs);
+    if (e != cudaSuccess)
+        return e;
+    a.nst = (int)std::min<size_t>(kMaxStages, ((size_t)smem_optin - sizeof(Shared)) / tile - 2);
+    if (a.nst < 3 || (size_t)a.nst * tile < ((size_t)a.n_req + 1) * sizeof(int64_t))
+        return cudaErrorInvalidConfiguration;
+    const size_t smem = (2 + (size_t)a.nst) * tile + sizeof(Shared);
+    if ((e = launch_pdl(kv_attn_kernel<DB>, dim3(grid), dim3(kThreads), smem, s, a, tq, tk, tv)) != cudaSuccess)
+        return e;
+    return launch_pdl(kv_attn_join_kernel, dim3(grid, kJoinY), dim3(kJoinWarps * 32), 0, s, a);
 }
 
 }  // namespace
 
-size_t kv_attention_workspace(int64_t, int64_t, int64_t, int64_t) { return 16; }
+size_t kv_attention_workspace(int64_t T, int64_t Hq, int64_t Hkv, int64_t D) { return layout_of(T, Hq, Hkv, D).bytes; }
 
 cudaError_t launch_kv_attention(const AttnProblem& p, cudaStream_t s)
 {
+    DeviceInfo di;
+    cudaError_t e = device_info(&di);
+    if (e != cudaSuccess)
+        return e;
     AttnArgs a{};
-    a.q = p.q;
-    a.k = p.k_cache;
-    a.v = p.v_cache;
     a.out = p.out;
     a.lse = p.lse;
     a.table = p.block_table;
     a.cu_q = p.cu_q;
     a.seq_lens = p.seq_lens;
-    a.ld_q = p.ld_q;
     a.ld_o = p.ld_o;
     a.max_pages = p.max_pages;
     a.ld_table = p.ld_table;
     a.n_pages = p.n_pages;
-    a.page_stride = p.page_stride;
     a.T = (int)p.T;
     a.Hq = (int)p.Hq;
     a.Hkv = (int)p.Hkv;
     a.D = (int)p.D;
     a.n_req = (int)p.n_req;
     a.window = (int)std::min<int64_t>(p.window, 0x7fffffff);
-    a.scale = p.scale;
     while ((1 << a.shift) < p.page_size)
         ++a.shift;
-    return launch_pdl(kv_attn_kernel, dim3((unsigned)((p.T * p.Hq + 3) / 4)), dim3(128), 0, s, a);
+    a.g = a.Hq / a.Hkv;
+    a.tq = kRows / a.g;
+    a.c = p.scale * 1.4426950408889634f;
+    a.vec_out = (reinterpret_cast<uintptr_t>(p.out) & 15u) == 0 && p.ld_o % 8 == 0;
+    const Layout w = layout_of(p.T, p.Hq, p.Hkv, p.D);
+    uint8_t* ws = static_cast<uint8_t*>(p.workspace);
+    a.row_cap = (int)w.row_cap;
+    a.heads = reinterpret_cast<int4*>(ws);
+    a.part_ml = reinterpret_cast<float2*>(ws + w.ml);
+    a.part_o = reinterpret_cast<float*>(ws + w.o);
+
+    CUtensorMap tq{}, tk{}, tv{};
+    const cuuint64_t qd[3] = {(cuuint64_t)p.D, (cuuint64_t)p.Hq, (cuuint64_t)p.T};
+    const cuuint64_t qs[2] = {(cuuint64_t)p.D * 2, (cuuint64_t)p.ld_q * 2};
+    const cuuint32_t qb[3] = {64, (cuuint32_t)a.g, (cuuint32_t)a.tq};
+    const cuuint64_t kd[4] = {(cuuint64_t)p.D, (cuuint64_t)p.page_size, (cuuint64_t)p.Hkv, (cuuint64_t)p.n_pages};
+    const cuuint64_t ks[3] = {(cuuint64_t)p.D * 2, (cuuint64_t)(p.page_size * p.D * 2), (cuuint64_t)p.page_stride * 2};
+    const cuuint32_t kb[4] = {64, (cuuint32_t)std::min<int64_t>(p.page_size, kRows), 1, 1};
+    if (!encode(&tq, p.q, 3, qd, qs, qb) || !encode(&tk, p.k_cache, 4, kd, ks, kb) ||
+        !encode(&tv, p.v_cache, 4, kd, ks, kb))
+        return cudaErrorInvalidValue;
+    const int grid = std::min(di.sm_count, kMaxCtas);
+    return p.D <= 64 ? launch_tc<1>(a, tq, tk, tv, grid, di.smem_optin, s)
+                     : launch_tc<2>(a, tq, tk, tv, grid, di.smem_optin, s);
 }
 
 cudaError_t attn_error_word(int32_t* out, bool clear)
