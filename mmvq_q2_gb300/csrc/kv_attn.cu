@@ -133,17 +133,19 @@ struct Item {
     bool two;        // two row tiles (else one, its key tiles dealt to both streams)
     int steps;       // two * (k1 - k0), or k1 - k0
 
-    __device__ __forceinline__ int tile(int u) const { return k0 + (two ? u >> 1 : u); }
-    // Whether step u has anything to do: a row tile may see fewer keys than its block.
-    __device__ __forceinline__ bool active(const AttnArgs& a, int u) const
+    __device__ __forceinline__ int tile(int u) const { return k0 + (two ? u >> 1 : u); }  // step u's key tile
+    // The key tiles of the run that stream s works on: of a block of two row
+    // tiles those that its own tile sees, else every other one.
+    __device__ __forceinline__ void span(const AttnArgs& a, int s, int& first, int& last) const
     {
-        if (!two)
-            return true;
-        int l, x;
-        const int s = u & 1;
-        key_tiles(a, q, s ? i0 + a.tq : i0, s ? i1 : i0 + a.tq, l, x);
-        const int k = tile(u);
-        return k >= l && k <= x;
+        first = k0;
+        last = k1 - 1;
+        if (two) {
+            int l, x;
+            key_tiles(a, q, s ? i0 + a.tq : i0, s ? i1 : i0 + a.tq, l, x);
+            first = max(first, l);
+            last = min(last, x);
+        }
     }
     __device__ __forceinline__ int kind() const
     {
@@ -296,6 +298,19 @@ __device__ __forceinline__ void find_start(const AttnArgs& a, const int64_t* sum
     }
 }
 
+// A place in the ring of stages and the parity of its use.
+struct Ring {
+    int s = 0;
+    uint32_t phase = 0;
+    __device__ __forceinline__ void next(int nst)
+    {
+        if (++s == nst) {
+            s = 0;
+            phase ^= 1u;
+        }
+    }
+};
+
 // ---- PTX -----------------------------------------------------------------------
 
 __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar)
@@ -362,6 +377,57 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
         : "memory");
 }
 
+// mbar_wait_bounded with its clock read only after many polls: here most
+// waits are short, and each lies on the path from one product to the next.
+__device__ __forceinline__ bool mbar_wait_short(uint32_t bar, uint32_t parity, const volatile int* abort_flag)
+{
+    uint64_t t0 = 0;
+    for (uint32_t it = 0;; ++it) {
+        if (mbar_try_wait(bar, parity))
+            return true;
+        if ((it & 63u) == 63u) {
+            if (*abort_flag)
+                return false;
+            const uint64_t t = global_timer_ns();
+            if (t0 == 0)
+                t0 = t;
+            else if (t - t0 > 2000000000ull)
+                return false;
+        }
+    }
+}
+
+template <int N>
+__device__ __forceinline__ void set_regs_down()
+{
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void set_regs_up()
+{
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+// Two fp32 operations an instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c)
+{
+    float2 d;
+    asm("{\n\t.reg .b64 a, b, c, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+        "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b)
+{
+    float2 d;
+    asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+        "add.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 
@@ -382,7 +448,7 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
 // ---- the kernel ----------------------------------------------------------------
 
 struct Shared {
-    uint64_t q_full, q_empty, s_full[2], p_ready[2], o_done[2], traded, read;
+    uint64_t q_full, q_empty, mma_done, s_full[2], p_ready[2], o_done[2], traded, read;
     uint64_t full[kMaxStages], empty[kMaxStages];
     int64_t warp_sums[kThreads / 32];
     Start start;
@@ -436,6 +502,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (threadIdx.x == 0) {
         mbar_init(smem_u32(&sh.q_full), 1);
         mbar_init(smem_u32(&sh.q_empty), 1);
+        mbar_init(smem_u32(&sh.mma_done), 1);
         for (int s = 0; s < 2; ++s) {
             mbar_init(smem_u32(&sh.s_full[s]), 1);
             mbar_init(smem_u32(&sh.p_ready[s]), 4);
@@ -481,7 +548,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tmem = sh.tmem;
 
     auto wait = [&](uint64_t& bar, uint32_t parity) {
-        if (mbar_wait_bounded(smem_u32(&bar), parity & 1u, abort_flag))
+        if (mbar_wait_short(smem_u32(&bar), parity & 1u, abort_flag))
             return true;
         atomicOr(&g_attn_error, Q2K_ERR_BIT_WAIT_TIMEOUT);
         *abort_flag = 1;
@@ -491,168 +558,203 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     Walk walk(a, sh.start);
     Item it{};
-    if (warp == 0) {
-        // ---- copies ----
-        const int box_rows = min(1 << a.shift, kRows), boxes = kRows / box_rows;
-        int loads = 0, items = 0;
-        // the page that holds this lane's box of key tile k, or one past the cache where no row needs it
-        auto page_of = [&](int k) -> int {
-            const int key = k * kRows + lane * box_rows;
-            if (lane >= boxes || key > it.q.base + it.i1 - 1 || key + box_rows <= first_key(a, it.q.base + it.i0))
+    // 384 threads started with 168 registers each: 4 warps give up 80, 8 take 40 more
+    if (warp < 4) {
+        set_regs_down<88>();
+        if (warp == 0) {
+            // ---- copies ----
+            const int box_rows = min(1 << a.shift, kRows), boxes = kRows / box_rows;
+            Ring at;
+            int loads = 0, items = 0;
+            // the page that holds this lane's box of key tile k, or one past the cache where no row needs it
+            auto page_of = [&](int k) -> int {
+                const int key = k * kRows + lane * box_rows;
+                if (lane >= boxes || key > it.q.base + it.i1 - 1 || key + box_rows <= first_key(a, it.q.base + it.i0))
+                    return (int)a.n_pages;
+                const int col = key >> a.shift;
+                const int page = col < a.max_pages ? a.table[it.r * a.ld_table + col] : -1;
+                if (page >= 0 && page < a.n_pages)
+                    return page;
+                atomicOr(&g_attn_error, kErrBadPage);
                 return (int)a.n_pages;
-            const int col = key >> a.shift;
-            const int page = col < a.max_pages ? a.table[it.r * a.ld_table + col] : -1;
-            if (page >= 0 && page < a.n_pages)
-                return page;
-            atomicOr(&g_attn_error, kErrBadPage);
-            return (int)a.n_pages;
-        };
-        auto load = [&](const CUtensorMap* map, int k, int page) {
-            const int s = loads % a.nst, use = loads / a.nst;
-            if (use > 0 && !warp_wait(sh.empty[s], (uint32_t)(use - 1)))
-                return false;
-            if (lane == 0) {
-                mbar_arrive_expect_tx(smem_u32(&sh.full[s]), kTile);
-                sh.loads = loads + 1;
-            }
-            __syncwarp();
-            if (lane < boxes) {
-                const uint32_t dst = ring + (uint32_t)s * kTile + (uint32_t)(lane * box_rows * 128);
-                const int row = (k * kRows + lane * box_rows) & ((1 << a.shift) - 1);
-#pragma unroll
-                for (int b = 0; b < DB; ++b)
-                    tma_load_4d(dst + b * kHalfBytes, map, b * 64, row, it.h, page, smem_u32(&sh.full[s]));
-            }
-            ++loads;
-            return true;
-        };
-        bool ok = true;
-        while (ok && walk.next(a, it)) {
-            if (items > 0 && !warp_wait(sh.q_empty, (uint32_t)(items - 1)))
-                break;
-            if (lane == 0) {
-                const int tiles = it.two ? 2 : 1;
-                mbar_arrive_expect_tx(smem_u32(&sh.q_full), (uint32_t)(tiles * DB * a.g * a.tq * 128));
-                sh.q_loads = items + 1;
-                for (int s = 0; s < tiles; ++s)
-#pragma unroll
-                    for (int b = 0; b < DB; ++b)
-                        tma_load_3d(q_smem + s * kTile + b * kHalfBytes, &tq, b * 64, it.h * a.g,
-                                    it.q.t0 + it.i0 + s * a.tq, smem_u32(&sh.q_full));
-            }
-            __syncwarp();
-            ++items;
-            // key tiles in the order of their first use: K(0) K(1) V(0) K(2) V(1) ...
-            const int n = it.k1 - it.k0, ahead = it.two ? 1 : 2;
-            int pages[2] = {page_of(it.k0), n > 1 ? page_of(it.k0 + 1) : 0};  // of tiles i, i + 1 (alternating)
-            ok = load(&tk, it.k0, pages[0]);
-            if (ahead == 2 && n > 1)
-                ok = ok && load(&tk, it.k0 + 1, pages[1]);
-            for (int i = 0; ok && i < n; ++i) {
-                const int k = it.k0 + i;
-                const int here = pages[i & 1];
-                if (i + 2 < n)
-                    pages[i & 1] = page_of(k + 2);
-                ok = load(&tv, k, here);
-                if (ok && i + ahead < n)
-                    ok = load(&tk, k + ahead, pages[(i + ahead) & 1]);
-            }
-        }
-    } else if (warp == 1) {
-        // ---- MMAs ----
-        const uint32_t idesc_s = instr_desc(kRows), idesc_o = instr_desc(a.D) | kTransposeB;
-        int loads = 0, items = 0, uses[2] = {0, 0};
-        bool ok = true;
-        while (ok && walk.next(a, it)) {
-            int k_stage = 0, v_stage = 0;
-            int done[2] = {0, 0};  // P V products of this item, by stream
-            const int v_lo = first_key(a, it.q.base + it.i0), v_hi = it.q.base + it.i1;
-            if (!warp_wait(sh.q_full, (uint32_t)items))
-                break;
-            ++items;
-            fence_after();
-            auto score = [&](int u) {  // S of step u
-                const int s = u & 1;
-                if (!it.two || s == 0) {
-                    k_stage = loads % a.nst;
-                    if (!warp_wait(sh.full[k_stage], (uint32_t)(loads / a.nst)))
-                        return false;
-                    ++loads;
-                    fence_after();
-                }
-                const uint32_t qa = q_smem + (it.two ? s * kTile : 0), kb = ring + (uint32_t)k_stage * kTile;
-                const bool act = it.active(a, u);
-                if (elect_one()) {
-                    if (act) {
-                        for (int k = 0; k < a.D / 16; ++k) {
-                            const uint32_t off = (uint32_t)((k >> 2) * kHalfBytes + (k & 3) * 32);
-                            umma_f16(tmem + s * 256, smem_desc_sw128(qa + off), smem_desc_sw128(kb + off), idesc_s, k > 0);
-                        }
-                        umma_commit(smem_u32(&sh.s_full[s]));
-                    }
-                    if (!it.two || s == 1)
-                        umma_commit(smem_u32(&sh.empty[k_stage]));
-                    if (u == it.steps - 1)
-                        umma_commit(smem_u32(&sh.q_empty));
+            };
+            auto load = [&](const CUtensorMap* map, int k, int page) {
+                const int s = at.s;
+                if (loads >= a.nst && !warp_wait(sh.empty[s], at.phase ^ 1u))
+                    return false;
+                ++loads;
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(smem_u32(&sh.full[s]), kTile);
+                    sh.loads = loads;
                 }
                 __syncwarp();
+                if (lane < boxes) {
+                    const uint32_t dst = ring + (uint32_t)s * kTile + (uint32_t)(lane * box_rows * 128);
+                    const int row = (k * kRows + lane * box_rows) & ((1 << a.shift) - 1);
+    #pragma unroll
+                    for (int b = 0; b < DB; ++b)
+                        tma_load_4d(dst + b * kHalfBytes, map, b * 64, row, it.h, page, smem_u32(&sh.full[s]));
+                }
+                at.next(a.nst);
                 return true;
             };
-            ok = score(0) && (it.steps < 2 || score(1));
-            for (int u = 0; ok && u < it.steps; ++u) {
-                const int s = u & 1;
-                if (!it.two || s == 0) {
-                    v_stage = loads % a.nst;
-                    if (!(ok = warp_wait(sh.full[v_stage], (uint32_t)(loads / a.nst))))
-                        break;
-                    ++loads;
-                    // clear the rows that no row of the block sees
-                    const int z_lo = max(0, min(kRows, v_lo - it.tile(u) * kRows));
-                    const int z_hi = max(0, min(kRows, v_hi - it.tile(u) * kRows));
-                    if (z_lo > 0 || z_hi < kRows) {
-                        for (int i = lane; i < kRows * 8; i += 32) {
-                            const int row = i >> 3;
-                            if (row < z_lo || row >= z_hi) {
-                                uint8_t* p = smem + 2 * kTile + (size_t)v_stage * kTile + i * 16;
-#pragma unroll
-                                for (int b = 0; b < DB; ++b)
-                                    *reinterpret_cast<uint4*>(p + b * kHalfBytes) = make_uint4(0, 0, 0, 0);
-                            }
-                        }
-                        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                        __syncwarp();
-                    }
-                }
-                const bool act = it.active(a, u);
-                if (act) {
-                    if (!(ok = warp_wait(sh.p_ready[s], (uint32_t)uses[s])))
-                        break;
-                    ++uses[s];
-                }
-                fence_after();
-                if (elect_one()) {
-                    if (act) {
-                        const uint32_t vb = ring + (uint32_t)v_stage * kTile;
-#pragma unroll
-                        for (int k = 0; k < kRows / 16; ++k)
-                            umma_f16_tmem_a(tmem + s * 256 + 128, tmem + s * 256 + k * 8, smem_desc_v(vb + k * 2048),
-                                            idesc_o, done[s] > 0 || k > 0);
-                        umma_commit(smem_u32(&sh.o_done[s]));
-                    }
-                    if (!it.two || s == 1)
-                        umma_commit(smem_u32(&sh.empty[v_stage]));
+            bool ok = true;
+            while (ok && walk.next(a, it)) {
+                if (items > 0 && !warp_wait(sh.q_empty, (uint32_t)(items - 1)))
+                    break;
+                if (lane == 0) {
+                    const int tiles = it.two ? 2 : 1;
+                    mbar_arrive_expect_tx(smem_u32(&sh.q_full), (uint32_t)(tiles * DB * a.g * a.tq * 128));
+                    sh.q_loads = items + 1;
+                    for (int s = 0; s < tiles; ++s)
+    #pragma unroll
+                        for (int b = 0; b < DB; ++b)
+                            tma_load_3d(q_smem + s * kTile + b * kHalfBytes, &tq, b * 64, it.h * a.g,
+                                        it.q.t0 + it.i0 + s * a.tq, smem_u32(&sh.q_full));
                 }
                 __syncwarp();
-                done[s] += act;
-                if (u + 2 < it.steps)
-                    ok = score(u + 2);
+                ++items;
+                // key tiles in the order of their first use: K(0) K(1) V(0) K(2) V(1) ...
+                const int n = it.k1 - it.k0, ahead = it.two ? 1 : 2;
+                int pages[2] = {page_of(it.k0), n > 1 ? page_of(it.k0 + 1) : 0};  // of tiles i, i + 1 (alternating)
+                ok = load(&tk, it.k0, pages[0]);
+                if (ahead == 2 && n > 1)
+                    ok = ok && load(&tk, it.k0 + 1, pages[1]);
+                for (int i = 0; ok && i < n; ++i) {
+                    const int k = it.k0 + i;
+                    const int here = pages[i & 1];
+                    if (i + 2 < n)
+                        pages[i & 1] = page_of(k + 2);
+                    ok = load(&tv, k, here);
+                    if (ok && i + ahead < n)
+                        ok = load(&tk, k + ahead, pages[(i + ahead) & 1]);
+                }
             }
+        } else if (warp == 1) {
+            // ---- MMAs ----
+            // The whole warp runs the loop and one elected lane issues, so
+            // that descriptors stay in warp-uniform registers; what a tile
+            // needs is worked out once per item and stage.  (With the loop in
+            // one lane, divisions for the stage and the span worked out per
+            // step, the issue took 140 cycles per MMA of 64.)
+            const uint32_t idesc_s = instr_desc(kRows), idesc_o = instr_desc(a.D) | kTransposeB;
+            const uint64_t q_desc = smem_desc_sw128(q_smem);
+            Ring at;
+            uint32_t q_phase = 0, p_phase = 0;  // p_phase: a bit a stream
+            bool ok = true;
+            while (ok && walk.next(a, it)) {
+                int f0, l0, f1, l1;
+                it.span(a, 0, f0, l0);
+                it.span(a, 1, f1, l1);
+                int k_stage = 0, v_stage = 0;
+                uint32_t begun = 0;  // a bit a stream: O holds a product of this item
+                const int v_lo = first_key(a, it.q.base + it.i0), v_hi = it.q.base + it.i1;
+                if (!(ok = warp_wait(sh.q_full, q_phase)))
+                    break;
+                q_phase ^= 1u;
+                fence_after();
+                auto active = [&](int u) {
+                    const int k = it.tile(u);
+                    return u & 1 ? k >= f1 && k <= l1 : k >= f0 && k <= l0;
+                };
+                auto score = [&](int u) {  // S of step u
+                    const int s = u & 1;
+                    if (!it.two || s == 0) {
+                        k_stage = at.s;
+                        if (!warp_wait(sh.full[k_stage], at.phase))
+                            return false;
+                        at.next(a.nst);
+                        fence_after();
+                    }
+                    if (active(u)) {
+                        const uint64_t qd = q_desc + (uint32_t)(it.two ? s * (kTile >> 4) : 0);
+                        const uint64_t kd = smem_desc_sw128(ring + (uint32_t)k_stage * kTile);
+                        const uint32_t d = tmem + s * 256;
+                        // columns past D are zero in both tiles
+#pragma unroll
+                        for (int k = 0; k < DB * 4; ++k) {
+                            const uint32_t off = (uint32_t)((k >> 2) * (kHalfBytes >> 4) + (k & 3) * 2);
+                            if (elect_one())
+                                umma_f16(d, qd + off, kd + off, idesc_s, k > 0);
+                        }
+                        if (elect_one())
+                            umma_commit(smem_u32(&sh.s_full[s]));
+                    }
+                    if (!it.two || s == 1) {
+                        if (elect_one())
+                            umma_commit(smem_u32(&sh.empty[k_stage]));
+                    }
+                    if (u == it.steps - 1) {
+                        if (elect_one())
+                            umma_commit(smem_u32(&sh.q_empty));
+                    }
+                    __syncwarp();
+                    return true;
+                };
+                ok = score(0) && (it.steps < 2 || score(1));
+                for (int u = 0; ok && u < it.steps; ++u) {
+                    const int s = u & 1;
+                    if (!it.two || s == 0) {
+                        v_stage = at.s;
+                        if (!(ok = warp_wait(sh.full[v_stage], at.phase)))
+                            break;
+                        at.next(a.nst);
+                        // clear the rows that no row of the block sees
+                        const int z_lo = max(0, min(kRows, v_lo - it.tile(u) * kRows));
+                        const int z_hi = max(0, min(kRows, v_hi - it.tile(u) * kRows));
+                        if (z_lo > 0 || z_hi < kRows) {
+                            for (int i = lane; i < kRows * 8; i += 32) {
+                                const int row = i >> 3;
+                                if (row < z_lo || row >= z_hi) {
+                                    uint8_t* p = smem + 2 * kTile + (size_t)v_stage * kTile + i * 16;
+#pragma unroll
+                                    for (int b = 0; b < DB; ++b)
+                                        *reinterpret_cast<uint4*>(p + b * kHalfBytes) = make_uint4(0, 0, 0, 0);
+                                }
+                            }
+                            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                            __syncwarp();
+                        }
+                    }
+                    if (active(u)) {
+                        if (!(ok = warp_wait(sh.p_ready[s], p_phase >> s)))
+                            break;
+                        p_phase ^= 1u << s;
+                        fence_after();
+                        const uint64_t vd = smem_desc_v(ring + (uint32_t)v_stage * kTile);
+                        const uint32_t d = tmem + s * 256;
+                        const bool more = begun >> s & 1u;
+#pragma unroll
+                        for (int k = 0; k < kRows / 16; ++k) {
+                            if (elect_one())
+                                umma_f16_tmem_a(d + 128, d + k * 8, vd + (uint32_t)(k * (2048 >> 4)), idesc_o, more || k > 0);
+                        }
+                        if (elect_one())
+                            umma_commit(smem_u32(&sh.o_done[s]));
+                        begun |= 1u << s;
+                    }
+                    if (!it.two || s == 1) {
+                        if (elect_one())
+                            umma_commit(smem_u32(&sh.empty[v_stage]));
+                    }
+                    __syncwarp();
+                    if (u + 2 < it.steps)
+                        ok = score(u + 2);
+                }
+            }
+            // every product and arrival has landed before the CTA can exit
+            if (elect_one())
+                umma_commit(smem_u32(&sh.mma_done));
+            __syncwarp();
+            mbar_wait_bounded(smem_u32(&sh.mma_done), 0u, nullptr);
+            __syncwarp();
         }
-    } else if (warp >= 4) {
+    } else {
+        set_regs_up<208>();
         // ---- softmax ----
         const int s = (warp - 4) >> 2, quarter = warp & 3, row = quarter * 32 + lane;
         const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16), t_s = lanes + s * 256, t_o = t_s + 128;
-        int uses = 0, trades = 0;
+        uint32_t phase = 0, trade = 0;
         bool ok = true;
         while (ok && walk.next(a, it)) {
             const int ti = row / a.g, head = row - ti * a.g;
@@ -663,10 +765,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int k_max = live ? p : INT_MAX, k_min = live ? first_key(a, p) : 0;
             float m = -INFINITY, l = 0.f;  // m: what P is relative to
             int count = 0;
-            for (int u = s; ok && u < it.steps; u += 2) {
-                if (!it.active(a, u))
-                    continue;
-                if (!(ok = warp_wait(sh.s_full[s], (uint32_t)uses)))
+            int k_first, k_last;
+            it.span(a, s, k_first, k_last);
+            const int stride = it.two ? 1 : 2;
+            for (int k = it.two ? k_first : k_first + s; k <= k_last; k += stride) {
+                if (!(ok = warp_wait(sh.s_full[s], phase)))
                     break;
                 fence_after();
                 if (warp_live) {
@@ -676,7 +779,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tmem_ld32<64>(t_s + 64, v);
                     tmem_ld32<96>(t_s + 96, v);
                     tmem_wait_ld();
-                    const int key0 = it.tile(u) * kRows;
+                    const int key0 = k * kRows;
                     if (__any_sync(0xffffffffu, key0 + kRows - 1 > k_max || key0 < k_min)) {
                         const int hi = k_max - key0, lo = k_min - key0;
 #pragma unroll
@@ -696,7 +799,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (count > 0) {
                             l *= f;
                             // the last product into O must be done
-                            if (!(ok = warp_wait(sh.o_done[s], (uint32_t)(uses - 1))))
+                            if (!(ok = warp_wait(sh.o_done[s], phase ^ 1u)))
                                 break;
                             fence_after();
                             for (int x = 0; x < a.D; x += 16) {
@@ -711,24 +814,26 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                     }
                     const float mc = m == -INFINITY ? 0.f : m * a.c;
-                    float sum[4] = {0.f, 0.f, 0.f, 0.f};
+                    const float2 c2 = make_float2(a.c, a.c), mc2 = make_float2(-mc, -mc);
+                    float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
                     for (int x = 0; x < kRows; x += 32) {
                         uint32_t w[16];
 #pragma unroll
                         for (int y = 0; y < 16; ++y) {
-                            const float e0 = exp2_approx(fmaf(v[x + 2 * y], a.c, -mc));
-                            const float e1 = exp2_approx(fmaf(v[x + 2 * y + 1], a.c, -mc));
-                            sum[(2 * y) & 3] += e0;
-                            sum[(2 * y + 1) & 3] += e1;
-                            w[y] = pack_bf16(e0, e1);
+                            float2 e = fma2(make_float2(v[x + 2 * y], v[x + 2 * y + 1]), c2, mc2);
+                            e.x = exp2_approx(e.x);
+                            e.y = exp2_approx(e.y);
+                            sum[y & 1] = add2(sum[y & 1], e);
+                            w[y] = pack_bf16(e.x, e.y);
                         }
                         tmem_st16(t_s + x / 2, w);
                     }
-                    l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                    sum[0] = add2(sum[0], sum[1]);
+                    l += sum[0].x + sum[0].y;
                     tmem_wait_st();
                 }
-                ++uses;
+                phase ^= 1u;
                 ++count;
                 fence_before();
                 __syncwarp();
@@ -738,7 +843,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!ok)
                 break;
             // ---- the item's result ----
-            if (count > 0 && !(ok = warp_wait(sh.o_done[s], (uint32_t)(uses - 1))))
+            if (count > 0 && !(ok = warp_wait(sh.o_done[s], phase ^ 1u)))
                 break;
             const int kind = it.kind();
             const bool whole = (kind & kFirst) && (kind & kLast);
@@ -787,7 +892,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __syncwarp();
                 if (lane == 0)
                     mbar_arrive(smem_u32(&sh.traded));
-                if (!(ok = warp_wait(sh.traded, (uint32_t)trades)))
+                if (!(ok = warp_wait(sh.traded, trade)))
                     break;
                 fence_after();
                 if (warp_live) {
@@ -828,9 +933,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __syncwarp();
                 if (lane == 0)
                     mbar_arrive(smem_u32(&sh.read));
-                if (!(ok = warp_wait(sh.read, (uint32_t)trades)))
+                if (!(ok = warp_wait(sh.read, trade)))
                     break;
-                ++trades;
+                trade ^= 1u;
             }
         }
     }
