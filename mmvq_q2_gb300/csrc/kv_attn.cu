@@ -21,8 +21,9 @@
 // One CTA, twelve warps:
 //   warp 0       copies Q, K and V tiles (64 values of D by 128 rows, 128-byte
 //                swizzle) into shared memory, a TMA box per page;
-//   warp 1       issues the MMAs: S into tensor memory, and O += P V with P
-//                read from tensor memory (in S's place) and V as it lies;
+//   warps 1, 2   issue the MMAs of streams 0 and 1: S into tensor memory, and
+//                O += P V with P read from tensor memory (in S's place) and V
+//                as it lies;
 //   warps 4..7   softmax of stream 0, one row a thread,
 //   warps 8..11  of stream 1.
 // Two streams, so that the tensor cores work for one while the other's
@@ -131,9 +132,7 @@ struct Item {
     int k0, k1;      // this CTA's key tiles [k0, k1)
     int lo, hi;      // the item's key tiles
     bool two;        // two row tiles (else one, its key tiles dealt to both streams)
-    int steps;       // two * (k1 - k0), or k1 - k0
 
-    __device__ __forceinline__ int tile(int u) const { return k0 + (two ? u >> 1 : u); }  // step u's key tile
     // The key tiles of the run that stream s works on: of a block of two row
     // tiles those that its own tile sees, else every other one.
     __device__ __forceinline__ void span(const AttnArgs& a, int s, int& first, int& last) const
@@ -183,7 +182,6 @@ struct Walk {
         it.k0 = it.lo + off;
         it.k1 = (int)min((int64_t)it.hi + 1, it.k0 + left);
         it.two = it.i1 - it.i0 > a.tq;
-        it.steps = (it.k1 - it.k0) * (it.two ? 2 : 1);
         left -= it.k1 - it.k0;
         off = 0;
         if (left > 0) {
@@ -302,13 +300,14 @@ __device__ __forceinline__ void find_start(const AttnArgs& a, const int64_t* sum
 struct Ring {
     int s = 0;
     uint32_t phase = 0;
-    __device__ __forceinline__ void next(int nst)
+    __device__ __forceinline__ void skip(int n, int nst)  // n <= nst
     {
-        if (++s == nst) {
-            s = 0;
+        if ((s += n) >= nst) {
+            s -= nst;
             phase ^= 1u;
         }
     }
+    __device__ __forceinline__ void next(int nst) { skip(1, nst); }
 };
 
 // ---- PTX -----------------------------------------------------------------------
@@ -431,6 +430,13 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b)
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 
+__device__ __forceinline__ float max3(float a, float b, float c)
+{
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
 __device__ __forceinline__ float exp2_approx(float x)
 {
     float y;
@@ -448,7 +454,7 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
 // ---- the kernel ----------------------------------------------------------------
 
 struct Shared {
-    uint64_t q_full, q_empty, mma_done, s_full[2], p_ready[2], o_done[2], traded, read;
+    uint64_t q_full, q_empty, mma_done, s_full[2], p_half[2], p_ready[2], o_done[2], traded, read;
     uint64_t full[kMaxStages], empty[kMaxStages];
     int64_t warp_sums[kThreads / 32];
     Start start;
@@ -501,10 +507,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (threadIdx.x == 0) {
         mbar_init(smem_u32(&sh.q_full), 1);
-        mbar_init(smem_u32(&sh.q_empty), 1);
-        mbar_init(smem_u32(&sh.mma_done), 1);
+        mbar_init(smem_u32(&sh.q_empty), 2);
+        mbar_init(smem_u32(&sh.mma_done), 2);
         for (int s = 0; s < 2; ++s) {
             mbar_init(smem_u32(&sh.s_full[s]), 1);
+            mbar_init(smem_u32(&sh.p_half[s]), 4);
             mbar_init(smem_u32(&sh.p_ready[s]), 4);
             mbar_init(smem_u32(&sh.o_done[s]), 1);
         }
@@ -512,7 +519,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(smem_u32(&sh.read), 8);
         for (int s = 0; s < a.nst; ++s) {
             mbar_init(smem_u32(&sh.full[s]), 1);
-            mbar_init(smem_u32(&sh.empty[s]), 1);
+            mbar_init(smem_u32(&sh.empty[s]), 2);
         }
         sh.abort_flag = 0;
         sh.loads = sh.q_loads = 0;
@@ -614,99 +621,90 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 __syncwarp();
                 ++items;
-                // key tiles in the order of their first use: K(0) K(1) V(0) K(2) V(1) ...
-                const int n = it.k1 - it.k0, ahead = it.two ? 1 : 2;
-                int pages[2] = {page_of(it.k0), n > 1 ? page_of(it.k0 + 1) : 0};  // of tiles i, i + 1 (alternating)
-                ok = load(&tk, it.k0, pages[0]);
-                if (ahead == 2 && n > 1)
-                    ok = ok && load(&tk, it.k0 + 1, pages[1]);
-                for (int i = 0; ok && i < n; ++i) {
-                    const int k = it.k0 + i;
-                    const int here = pages[i & 1];
-                    if (i + 2 < n)
-                        pages[i & 1] = page_of(k + 2);
-                    ok = load(&tv, k, here);
-                    if (ok && i + ahead < n)
-                        ok = load(&tk, k + ahead, pages[(i + ahead) & 1]);
+                // K and V of each key tile, with the pages of the next tile on their way
+                int here = page_of(it.k0);
+                for (int k = it.k0; ok && k < it.k1; ++k) {
+                    const int page = here;
+                    if (k + 1 < it.k1)
+                        here = page_of(k + 1);
+                    ok = load(&tk, k, page) && load(&tv, k, page);
                 }
             }
-        } else if (warp == 1) {
+        } else if (warp < 3) {
             // ---- MMAs ----
-            // The whole warp runs the loop and one elected lane issues, so
-            // that descriptors stay in warp-uniform registers; what a tile
-            // needs is worked out once per item and stage.  (With the loop in
-            // one lane, divisions for the stage and the span worked out per
-            // step, the issue took 140 cycles per MMA of 64.)
+            // Warp 1 issues for stream 0, warp 2 for stream 1: the issue from
+            // one warp (an MMA takes it 30 to 50 cycles, a wait or commit
+            // about as much) came to 2650 cycles per key tile of two row
+            // tiles, more than the 2048 that the tensor cores need.  The
+            // whole warp runs the loop and one elected lane issues, so that
+            // descriptors stay in warp-uniform registers.
+            const int s = warp - 1;
             const uint32_t idesc_s = instr_desc(kRows), idesc_o = instr_desc(a.D) | kTransposeB;
-            const uint64_t q_desc = smem_desc_sw128(q_smem);
-            Ring at;
-            uint32_t q_phase = 0, p_phase = 0;  // p_phase: a bit a stream
+            const uint32_t t_s = tmem + s * 256, t_o = t_s + 128;
+            Ring at;  // the place of the item's first K tile; its V tile lies behind it, and so on
+            uint32_t q_phase = 0, p_phase = 0;
             bool ok = true;
             while (ok && walk.next(a, it)) {
-                int f0, l0, f1, l1;
-                it.span(a, 0, f0, l0);
-                it.span(a, 1, f1, l1);
-                int k_stage = 0, v_stage = 0;
-                uint32_t begun = 0;  // a bit a stream: O holds a product of this item
-                const int v_lo = first_key(a, it.q.base + it.i0), v_hi = it.q.base + it.i1;
                 if (!(ok = warp_wait(sh.q_full, q_phase)))
                     break;
                 q_phase ^= 1u;
-                fence_after();
-                auto active = [&](int u) {
-                    const int k = it.tile(u);
-                    return u & 1 ? k >= f1 && k <= l1 : k >= f0 && k <= l0;
-                };
-                auto score = [&](int u) {  // S of step u
-                    const int s = u & 1;
-                    if (!it.two || s == 0) {
-                        k_stage = at.s;
-                        if (!warp_wait(sh.full[k_stage], at.phase))
-                            return false;
-                        at.next(a.nst);
-                        fence_after();
+                int first, last;
+                it.span(a, s, first, last);
+                const int v_lo = first_key(a, it.q.base + it.i0), v_hi = it.q.base + it.i1;
+                const uint64_t qd = smem_desc_sw128(q_smem + (it.two ? s * kTile : 0));
+                // both streams pass every tile of a block of two row tiles; of a
+                // block of one, this stream passes every other tile, alone
+                const int hop = it.two ? 1 : 2;
+                int k = it.two ? it.k0 : it.k0 + s;
+                Ring ks = at;  // K tile k's place
+                if (!it.two && s == 1)
+                    ks.skip(2, a.nst);
+                auto release = [&](int stage) {
+                    if (elect_one()) {
+                        umma_commit(smem_u32(&sh.empty[stage]));
+                        if (!it.two)  // for the other stream
+                            umma_commit(smem_u32(&sh.empty[stage]));
                     }
-                    if (active(u)) {
-                        const uint64_t qd = q_desc + (uint32_t)(it.two ? s * (kTile >> 4) : 0);
-                        const uint64_t kd = smem_desc_sw128(ring + (uint32_t)k_stage * kTile);
-                        const uint32_t d = tmem + s * 256;
+                };
+                auto score = [&]() {  // S of tile k
+                    if (!warp_wait(sh.full[ks.s], ks.phase))
+                        return false;
+                    fence_after();
+                    if (k >= first && k <= last) {
+                        const uint64_t kd = smem_desc_sw128(ring + (uint32_t)ks.s * kTile);
                         // columns past D are zero in both tiles
 #pragma unroll
-                        for (int k = 0; k < DB * 4; ++k) {
-                            const uint32_t off = (uint32_t)((k >> 2) * (kHalfBytes >> 4) + (k & 3) * 2);
+                        for (int x = 0; x < DB * 4; ++x) {
+                            const uint32_t off = (uint32_t)((x >> 2) * (kHalfBytes >> 4) + (x & 3) * 2);
                             if (elect_one())
-                                umma_f16(d, qd + off, kd + off, idesc_s, k > 0);
+                                umma_f16(t_s, qd + off, kd + off, idesc_s, x > 0);
                         }
                         if (elect_one())
                             umma_commit(smem_u32(&sh.s_full[s]));
                     }
-                    if (!it.two || s == 1) {
-                        if (elect_one())
-                            umma_commit(smem_u32(&sh.empty[k_stage]));
-                    }
-                    if (u == it.steps - 1) {
-                        if (elect_one())
-                            umma_commit(smem_u32(&sh.q_empty));
-                    }
-                    __syncwarp();
+                    release(ks.s);
                     return true;
                 };
-                ok = score(0) && (it.steps < 2 || score(1));
-                for (int u = 0; ok && u < it.steps; ++u) {
-                    const int s = u & 1;
-                    if (!it.two || s == 0) {
-                        v_stage = at.s;
-                        if (!(ok = warp_wait(sh.full[v_stage], at.phase)))
-                            break;
-                        at.next(a.nst);
-                        // clear the rows that no row of the block sees
-                        const int z_lo = max(0, min(kRows, v_lo - it.tile(u) * kRows));
-                        const int z_hi = max(0, min(kRows, v_hi - it.tile(u) * kRows));
+                bool begun = false;  // O holds a product of this item
+                if (k < it.k1)
+                    ok = score();
+                while (ok && k < it.k1) {
+                    Ring vs = ks;
+                    vs.next(a.nst);
+                    if (k + hop >= it.k1 && elect_one())
+                        umma_commit(smem_u32(&sh.q_empty));  // this was the last S of the item
+                    __syncwarp();
+                    if (!(ok = warp_wait(sh.full[vs.s], vs.phase)))
+                        break;
+                    if (k >= first && k <= last) {
+                        // clear the rows that no row of the block sees (the other stream may write the same zeros)
+                        const int z_lo = max(0, min(kRows, v_lo - k * kRows));
+                        const int z_hi = max(0, min(kRows, v_hi - k * kRows));
                         if (z_lo > 0 || z_hi < kRows) {
                             for (int i = lane; i < kRows * 8; i += 32) {
                                 const int row = i >> 3;
                                 if (row < z_lo || row >= z_hi) {
-                                    uint8_t* p = smem + 2 * kTile + (size_t)v_stage * kTile + i * 16;
+                                    uint8_t* p = smem + (size_t)(2 + vs.s) * kTile + i * 16;
 #pragma unroll
                                     for (int b = 0; b < DB; ++b)
                                         *reinterpret_cast<uint4*>(p + b * kHalfBytes) = make_uint4(0, 0, 0, 0);
@@ -715,32 +713,40 @@ __global__ void __launch_bounds__(kThreads, 1)
                             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                             __syncwarp();
                         }
-                    }
-                    if (active(u)) {
-                        if (!(ok = warp_wait(sh.p_ready[s], p_phase >> s)))
+                        const uint64_t vd = smem_desc_v(ring + (uint32_t)vs.s * kTile);
+                        if (!(ok = warp_wait(sh.p_half[s], p_phase)))
                             break;
-                        p_phase ^= 1u << s;
                         fence_after();
-                        const uint64_t vd = smem_desc_v(ring + (uint32_t)v_stage * kTile);
-                        const uint32_t d = tmem + s * 256;
-                        const bool more = begun >> s & 1u;
 #pragma unroll
-                        for (int k = 0; k < kRows / 16; ++k) {
+                        for (int x = 0; x < kRows / 32; ++x) {
                             if (elect_one())
-                                umma_f16_tmem_a(d + 128, d + k * 8, vd + (uint32_t)(k * (2048 >> 4)), idesc_o, more || k > 0);
+                                umma_f16_tmem_a(t_o, t_s + x * 8, vd + (uint32_t)(x * (2048 >> 4)), idesc_o, begun || x > 0);
                         }
-                        if (elect_one())
-                            umma_commit(smem_u32(&sh.o_done[s]));
-                        begun |= 1u << s;
+                        if (!(ok = warp_wait(sh.p_ready[s], p_phase)))
+                            break;
+                        p_phase ^= 1u;
+                        fence_after();
+#pragma unroll
+                        for (int x = kRows / 32; x < kRows / 16; ++x) {
+                            if (elect_one())
+                                umma_f16_tmem_a(t_o, t_s + x * 8, vd + (uint32_t)(x * (2048 >> 4)), idesc_o, true);
+                        }
+                        begun = true;
+                        if (k + hop > last && elect_one())
+                            umma_commit(smem_u32(&sh.o_done[s]));  // O is complete
+                        __syncwarp();
                     }
-                    if (!it.two || s == 1) {
-                        if (elect_one())
-                            umma_commit(smem_u32(&sh.empty[v_stage]));
-                    }
-                    __syncwarp();
-                    if (u + 2 < it.steps)
-                        ok = score(u + 2);
+                    release(vs.s);
+                    ks.skip(2 * hop, a.nst);
+                    k += hop;
+                    if (k < it.k1)
+                        ok = score();
                 }
+                if (it.k0 + (it.two ? 0 : s) >= it.k1 && lane == 0)
+                    mbar_arrive(smem_u32(&sh.q_empty));  // no tile of this item was this stream's
+                const int used = 2 * (it.k1 - it.k0), rounds = used / a.nst;
+                at.phase ^= (uint32_t)rounds & 1u;
+                at.skip(used - rounds * a.nst, a.nst);
             }
             // every product and arrival has landed before the CTA can exit
             if (elect_one())
@@ -754,7 +760,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ---- softmax ----
         const int s = (warp - 4) >> 2, quarter = warp & 3, row = quarter * 32 + lane;
         const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16), t_s = lanes + s * 256, t_o = t_s + 128;
-        uint32_t phase = 0, trade = 0;
+        uint32_t phase = 0, done = 0, trade = 0;
         bool ok = true;
         while (ok && walk.next(a, it)) {
             const int ti = row / a.g, head = row - ti * a.g;
@@ -788,20 +794,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     float t4[4] = {v[0], v[1], v[2], v[3]};
 #pragma unroll
-                    for (int x = 4; x < kRows; ++x)
-                        t4[x & 3] = fmaxf(t4[x & 3], v[x]);
-                    const float top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
+                    for (int x = 4; x + 8 <= kRows; x += 8) {
+#pragma unroll
+                        for (int y = 0; y < 4; ++y)
+                            t4[y] = max3(t4[y], v[x + y], v[x + 4 + y]);
+                    }
+                    const float top = max3(max3(t4[0], v[124], v[125]), max3(t4[1], v[126], v[127]), fmaxf(t4[2], t4[3]));
                     const bool grow = (top - m) * a.c > kGrow;  // false for -inf - -inf
                     if (__any_sync(0xffffffffu, grow)) {
                         const float m_new = fmaxf(m, top);
                         const float f = m_new == m ? 1.f : exp2_approx((m - m_new) * a.c);
                         m = m_new;
                         if (count > 0) {
+                            // S of this tile is complete, and with it the product into O issued before it
                             l *= f;
-                            // the last product into O must be done
-                            if (!(ok = warp_wait(sh.o_done[s], phase ^ 1u)))
-                                break;
-                            fence_after();
                             for (int x = 0; x < a.D; x += 16) {
                                 float o[16];
                                 uint32_t w[16];
@@ -815,36 +821,55 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     const float mc = m == -INFINITY ? 0.f : m * a.c;
                     const float2 c2 = make_float2(a.c, a.c), mc2 = make_float2(-mc, -mc);
-                    float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
                     for (int x = 0; x < kRows; x += 32) {
                         uint32_t w[16];
 #pragma unroll
                         for (int y = 0; y < 16; ++y) {
-                            float2 e = fma2(make_float2(v[x + 2 * y], v[x + 2 * y + 1]), c2, mc2);
-                            e.x = exp2_approx(e.x);
-                            e.y = exp2_approx(e.y);
-                            sum[y & 1] = add2(sum[y & 1], e);
-                            w[y] = pack_bf16(e.x, e.y);
+                            const float2 e = fma2(make_float2(v[x + 2 * y], v[x + 2 * y + 1]), c2, mc2);
+                            v[x + 2 * y] = exp2_approx(e.x);
+                            v[x + 2 * y + 1] = exp2_approx(e.y);
+                            w[y] = pack_bf16(v[x + 2 * y], v[x + 2 * y + 1]);
                         }
                         tmem_st16(t_s + x / 2, w);
+                        if (x == 32 || x == 96) {  // the product over these keys may start
+                            tmem_wait_st();
+                            fence_before();
+                            __syncwarp();
+                            if (lane == 0)
+                                mbar_arrive(smem_u32(x == 32 ? &sh.p_half[s] : &sh.p_ready[s]));
+                        }
                     }
-                    sum[0] = add2(sum[0], sum[1]);
+                    // the sum, off the path to the next product
+                    float2 sum[4] = {make_float2(v[0], v[1]), make_float2(v[2], v[3]), make_float2(v[4], v[5]),
+                                     make_float2(v[6], v[7])};
+#pragma unroll
+                    for (int x = 8; x < kRows; x += 8) {
+#pragma unroll
+                        for (int y = 0; y < 4; ++y)
+                            sum[y] = add2(sum[y], make_float2(v[x + 2 * y], v[x + 2 * y + 1]));
+                    }
+                    sum[0] = add2(add2(sum[0], sum[1]), add2(sum[2], sum[3]));
                     l += sum[0].x + sum[0].y;
-                    tmem_wait_st();
+                } else {
+                    fence_before();
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(smem_u32(&sh.p_half[s]));
+                        mbar_arrive(smem_u32(&sh.p_ready[s]));
+                    }
                 }
                 phase ^= 1u;
                 ++count;
-                fence_before();
-                __syncwarp();
-                if (lane == 0)
-                    mbar_arrive(smem_u32(&sh.p_ready[s]));
             }
             if (!ok)
                 break;
             // ---- the item's result ----
-            if (count > 0 && !(ok = warp_wait(sh.o_done[s], phase ^ 1u)))
-                break;
+            if (count > 0) {
+                if (!(ok = warp_wait(sh.o_done[s], done)))
+                    break;
+                done ^= 1u;
+            }
             const int kind = it.kind();
             const bool whole = (kind & kFirst) && (kind & kLast);
             const int slot = 2 * blockIdx.x + ((kind & kFirst) ? 1 : 0);
@@ -954,9 +979,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // Joins the pieces of split items: block x takes the item whose last piece
-// CTA x of the first launch wrote, a warp a row, pieces in the order of
-// their keys.
-constexpr int kJoinWarps = 8, kJoinY = 8;
+// CTA x of the first launch wrote, a warp a row, a lane a piece for the
+// weights and then four columns of every piece, in the order of their keys.
+// What bounds it is latency: few dependent loads, and those of the pieces
+// four at a time.
+constexpr int kJoinWarps = 8;
 
 __global__ void __launch_bounds__(kJoinWarps * 32) kv_attn_join_kernel(const AttnArgs a)
 {
@@ -966,55 +993,77 @@ __global__ void __launch_bounds__(kJoinWarps * 32) kv_attn_join_kernel(const Att
     const int4 head = a.heads[2 * last];
     if (!(head.x & kLast))
         return;
-    // the first piece is some CTA's second slot; CTAs without units lie between
-    int first = last;
-    while (first > 0) {
-        --first;
-        if (a.heads[2 * first + 1].x & kFirst)
+    // the first piece is some CTA's second slot; CTAs without units may lie between
+    int first = 0;
+    for (int c0 = last - 1; c0 >= 0; c0 -= 32) {
+        const int c = c0 - lane;
+        const uint32_t hit = __ballot_sync(0xffffffffu, c >= 0 && (a.heads[2 * max(c, 0) + 1].x & kFirst));
+        if (hit) {
+            first = c0 - (__ffs(hit) - 1);
             break;
+        }
     }
     const Request q = load_request(a, head.y);
     const int i0 = head.w * 2 * a.tq, i1 = min(q.n, i0 + 2 * a.tq);
-    const bool two = i1 - i0 > a.tq;
-    const int rows = two ? 2 * kRows : kRows;
-    for (int row = (int)blockIdx.y * kJoinWarps + (threadIdx.x >> 5); row < rows; row += kJoinWarps * kJoinY) {
+    const int rows = i1 - i0 > a.tq ? 2 * kRows : kRows;
+    for (int row = (int)blockIdx.y * kJoinWarps + (threadIdx.x >> 5); row < rows; row += kJoinWarps * (int)gridDim.y) {
         const int s = row >> 7, in = row & 127, ti = in / a.g;
         const int i = i0 + s * a.tq + ti;
         if (in >= a.g * a.tq || i >= i1)
             continue;
+        auto piece = [&](int c) {
+            const int slot = 2 * c + (c == first);
+            return c <= last && a.heads[slot].x ? a.part_ml[(int64_t)slot * a.row_cap + row] : make_float2(-INFINITY, 0.f);
+        };
         float top = -INFINITY;
-        for (int c = first; c <= last; ++c) {
-            const int slot = 2 * c + (c == first);
-            if (a.heads[slot].x)
-                top = fmaxf(top, a.part_ml[(int64_t)slot * a.row_cap + row].x);
-        }
-        float sum = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
-        for (int c = first; c <= last; ++c) {
-            const int slot = 2 * c + (c == first);
-            if (!a.heads[slot].x)
-                continue;
-            const float2 ml = a.part_ml[(int64_t)slot * a.row_cap + row];
-            if (!(ml.y > 0.f))
-                continue;
-            const float f = exp2_approx(ml.x - top);
+        for (int c0 = first; c0 <= last; c0 += 32)
+            top = fmaxf(top, piece(c0 + lane).x);
+#pragma unroll
+        for (int o = 16; o >= 1; o >>= 1)
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        float sum = 0.f, o4[4] = {0.f, 0.f, 0.f, 0.f};
+        for (int c0 = first; c0 <= last; c0 += 32) {
+            const float2 ml = piece(c0 + lane);
+            const float f = ml.y > 0.f ? exp2_approx(ml.x - top) : 0.f;
             sum = fmaf(ml.y, f, sum);
-            const float* part = a.part_o + ((int64_t)slot * a.row_cap + row) * a.D;
-            if (lane * 4 < a.D) {
-                const float4 v = *reinterpret_cast<const float4*>(part + lane * 4);
-                o[0] = fmaf(v.x, f, o[0]);
-                o[1] = fmaf(v.y, f, o[1]);
-                o[2] = fmaf(v.z, f, o[2]);
-                o[3] = fmaf(v.w, f, o[3]);
+            for (int i = 0; i < min(32, last - c0 + 1); i += 4) {
+                float w[4];
+                float4 v[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    w[j] = __shfl_sync(0xffffffffu, f, i + j);
+                    const int c = c0 + i + j;
+                    v[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (w[j] > 0.f && lane * 4 < a.D)
+                        v[j] = *reinterpret_cast<const float4*>(
+                            a.part_o + ((int64_t)(2 * c + (c == first)) * a.row_cap + row) * a.D + lane * 4);
+                }
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    o4[0] = fmaf(v[j].x, w[j], o4[0]);
+                    o4[1] = fmaf(v[j].y, w[j], o4[1]);
+                    o4[2] = fmaf(v[j].z, w[j], o4[2]);
+                    o4[3] = fmaf(v[j].w, w[j], o4[3]);
+                }
             }
         }
+#pragma unroll
+        for (int o = 16; o >= 1; o >>= 1)
+            sum += __shfl_xor_sync(0xffffffffu, sum, o);
         const float inv = sum > 0.f ? 1.0f / sum : 0.f;
         const int64_t t = q.t0 + i;
         const int h = head.z * a.g + (in - ti * a.g);
         if (lane * 4 < a.D) {
             uint16_t* dst = a.out + t * a.ld_o + (int64_t)h * a.D + lane * 4;
-#pragma unroll
-            for (int y = 0; y < 4; ++y)
-                dst[y] = __bfloat16_as_ushort(__float2bfloat16_rn(o[y] * inv));
+            const uint32_t lo = pack_bf16(o4[0] * inv, o4[1] * inv), hi = pack_bf16(o4[2] * inv, o4[3] * inv);
+            if (a.vec_out)
+                *reinterpret_cast<uint2*>(dst) = make_uint2(lo, hi);
+            else {
+                dst[0] = (uint16_t)lo;
+                dst[1] = (uint16_t)(lo >> 16);
+                dst[2] = (uint16_t)hi;
+                dst[3] = (uint16_t)(hi >> 16);
+            }
         }
         if (a.lse && lane == 0)
             a.lse[t * a.Hq + h] = lse_of(top, sum);
@@ -1078,7 +1127,8 @@ cudaError_t launch_tc(AttnArgs& a, const CUtensorMap& tq, const CUtensorMap& tk,
     const size_t smem = (2 + (size_t)a.nst) * tile + sizeof(Shared);
     if ((e = launch_pdl(kv_attn_kernel<DB>, dim3(grid), dim3(kThreads), smem, s, a, tq, tk, tv)) != cudaSuccess)
         return e;
-    return launch_pdl(kv_attn_join_kernel, dim3(grid, kJoinY), dim3(kJoinWarps * 32), 0, s, a);
+    const int y = std::min(16, (a.row_cap + kJoinWarps - 1) / kJoinWarps);
+    return launch_pdl(kv_attn_join_kernel, dim3(grid, y), dim3(kJoinWarps * 32), 0, s, a);
 }
 
 }  // namespace
