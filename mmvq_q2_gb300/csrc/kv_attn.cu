@@ -31,10 +31,12 @@
 // a block has a single tile (decode), every other key tile of it, merged at
 // the item's end.
 //
-// O is rescaled in tensor memory only when a row's maximum has grown by more
-// than 2^8 since the last time: P stays below 2^8, where bf16 and the fp32
-// sums hold it as well as below 1, and the division by l makes the result
-// the same.
+// P is relative to a reference that follows a row's maximum loosely: only
+// when a score has passed it by more than 8 (P above 2^8; bf16 and the fp32
+// sums hold large values as well as those below 1, and the division by l
+// makes the result the same) does the reference move, and O is rescaled in
+// tensor memory.  So the exponentials of a tile need not wait for its
+// maximum; a tile that would pass 2^64 is done again with the maximum first.
 //
 // Rows of V that no row of the block may see (past the sequence's end, or
 // before a window) are cleared in shared memory: a probability of zero
@@ -67,7 +69,8 @@ constexpr int kMaxCtas = 160;
 constexpr int kRows = 128;                  // rows of a tile, keys of a tile
 constexpr int kHalfBytes = kRows * 128;     // 128 rows of 64 values
 constexpr int kMaxStages = 12;
-constexpr float kGrow = 8.0f;               // log2 of how far a row's P may pass 1
+constexpr float kGrow = 8.0f;               // log2 of how far P may pass 1 before its reference moves
+constexpr float kRange = 64.0f;             // and of how far within one tile
 
 struct AttnArgs {
     uint16_t* out;
@@ -454,13 +457,13 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
 // ---- the kernel ----------------------------------------------------------------
 
 struct Shared {
-    uint64_t q_full, q_empty, mma_done, s_full[2], p_half[2], p_ready[2], o_done[2], traded, read;
+    uint64_t q_full, q_empty, mma_done, s_full[2], p_ready[2], o_done[2], traded, read;
     uint64_t full[kMaxStages], empty[kMaxStages];
     int64_t warp_sums[kThreads / 32];
     Start start;
     float2 ml[2][kRows];  // one-tile items: each stream's maximum (times c) and sum
     uint32_t tmem;
-    int abort_flag;
+    int abort_flag, turn;
     int loads;            // stages filled, for the clean-up
     int q_loads;
 };
@@ -511,7 +514,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(smem_u32(&sh.mma_done), 2);
         for (int s = 0; s < 2; ++s) {
             mbar_init(smem_u32(&sh.s_full[s]), 1);
-            mbar_init(smem_u32(&sh.p_half[s]), 4);
             mbar_init(smem_u32(&sh.p_ready[s]), 4);
             mbar_init(smem_u32(&sh.o_done[s]), 1);
         }
@@ -521,7 +523,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(smem_u32(&sh.full[s]), 1);
             mbar_init(smem_u32(&sh.empty[s]), 2);
         }
-        sh.abort_flag = 0;
+        sh.abort_flag = sh.turn = 0;
         sh.loads = sh.q_loads = 0;
         fence_mbar_init();
     }
@@ -685,6 +687,35 @@ __global__ void __launch_bounds__(kThreads, 1)
                     release(ks.s);
                     return true;
                 };
+                // Two row tiles: one stream's O += P V and its next S go to the
+                // tensor cores as one run.  Interleaved with the other's, both
+                // would end together, and both softmaxes would then run while
+                // the tensor cores wait.
+                bool mine = false;
+                auto take_turn = [&]() {
+                    bool got = true;
+                    if (lane == 0) {
+                        uint64_t t0 = 0;
+                        for (uint32_t n = 0; atomicCAS(&sh.turn, 0, 1) != 0; ++n) {
+                            if ((n & 63u) == 63u) {
+                                const uint64_t now = global_timer_ns();
+                                t0 = t0 ? t0 : now;
+                                if (*abort_flag || now - t0 > 2000000000ull) {
+                                    got = false;
+                                    break;
+                                }
+                            }
+                        }
+                    }
+                    mine = __all_sync(0xffffffffu, got);
+                    return mine;
+                };
+                auto end_turn = [&]() {
+                    __syncwarp();
+                    if (mine && lane == 0)
+                        atomicExch(&sh.turn, 0);
+                    mine = false;
+                };
                 bool begun = false;  // O holds a product of this item
                 if (k < it.k1)
                     ok = score();
@@ -714,22 +745,22 @@ __global__ void __launch_bounds__(kThreads, 1)
                             __syncwarp();
                         }
                         const uint64_t vd = smem_desc_v(ring + (uint32_t)vs.s * kTile);
-                        if (!(ok = warp_wait(sh.p_half[s], p_phase)))
-                            break;
-                        fence_after();
-#pragma unroll
-                        for (int x = 0; x < kRows / 32; ++x) {
-                            if (elect_one())
-                                umma_f16_tmem_a(t_o, t_s + x * 8, vd + (uint32_t)(x * (2048 >> 4)), idesc_o, begun || x > 0);
-                        }
                         if (!(ok = warp_wait(sh.p_ready[s], p_phase)))
                             break;
                         p_phase ^= 1u;
+                        if (it.two) {
+                            // nothing is waited for during a turn: the next K tile
+                            // may need a stage that the other stream has yet to free
+                            Ring ns = vs;
+                            ns.next(a.nst);
+                            if (!(ok = (k + 1 >= it.k1 || warp_wait(sh.full[ns.s], ns.phase)) && take_turn()))
+                                break;
+                        }
                         fence_after();
 #pragma unroll
-                        for (int x = kRows / 32; x < kRows / 16; ++x) {
+                        for (int x = 0; x < kRows / 16; ++x) {
                             if (elect_one())
-                                umma_f16_tmem_a(t_o, t_s + x * 8, vd + (uint32_t)(x * (2048 >> 4)), idesc_o, true);
+                                umma_f16_tmem_a(t_o, t_s + x * 8, vd + (uint32_t)(x * (2048 >> 4)), idesc_o, begun || x > 0);
                         }
                         begun = true;
                         if (k + hop > last && elect_one())
@@ -741,6 +772,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     k += hop;
                     if (k < it.k1)
                         ok = score();
+                    end_turn();
                 }
                 if (it.k0 + (it.two ? 0 : s) >= it.k1 && lane == 0)
                     mbar_arrive(smem_u32(&sh.q_empty));  // no tile of this item was this stream's
@@ -770,6 +802,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int p = it.q.base + i;
             const int k_max = live ? p : INT_MAX, k_min = live ? first_key(a, p) : 0;
             float m = -INFINITY, l = 0.f;  // m: what P is relative to
+            float m_next = -INFINITY;
+            bool pending = false;          // m_next takes over with the next tile
             int count = 0;
             int k_first, k_last;
             it.span(a, s, k_first, k_last);
@@ -780,33 +814,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                 fence_after();
                 if (warp_live) {
                     float v[kRows];
-                    tmem_ld32<0>(t_s, v);
-                    tmem_ld32<32>(t_s + 32, v);
-                    tmem_ld32<64>(t_s + 64, v);
-                    tmem_ld32<96>(t_s + 96, v);
-                    tmem_wait_ld();
-                    const int key0 = k * kRows;
-                    if (__any_sync(0xffffffffu, key0 + kRows - 1 > k_max || key0 < k_min)) {
-                        const int hi = k_max - key0, lo = k_min - key0;
-#pragma unroll
-                        for (int x = 0; x < kRows; ++x)
-                            v[x] = x <= hi && x >= lo ? v[x] : -INFINITY;
-                    }
-                    float t4[4] = {v[0], v[1], v[2], v[3]};
-#pragma unroll
-                    for (int x = 4; x + 8 <= kRows; x += 8) {
-#pragma unroll
-                        for (int y = 0; y < 4; ++y)
-                            t4[y] = max3(t4[y], v[x + y], v[x + 4 + y]);
-                    }
-                    const float top = max3(max3(t4[0], v[124], v[125]), max3(t4[1], v[126], v[127]), fmaxf(t4[2], t4[3]));
-                    const bool grow = (top - m) * a.c > kGrow;  // false for -inf - -inf
-                    if (__any_sync(0xffffffffu, grow)) {
-                        const float m_new = fmaxf(m, top);
+                    auto load_s = [&]() {
+                        tmem_ld32<0>(t_s, v);
+                        tmem_ld32<32>(t_s + 32, v);
+                        tmem_ld32<64>(t_s + 64, v);
+                        tmem_ld32<96>(t_s + 96, v);
+                        tmem_wait_ld();
+                    };
+                    // P against a new reference from here on.  S of this tile
+                    // is complete, and with it the product issued before it.
+                    auto move_to = [&](float m_new) {
                         const float f = m_new == m ? 1.f : exp2_approx((m - m_new) * a.c);
                         m = m_new;
                         if (count > 0) {
-                            // S of this tile is complete, and with it the product into O issued before it
                             l *= f;
                             for (int x = 0; x < a.D; x += 16) {
                                 float o[16];
@@ -818,47 +838,92 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 tmem_st16(t_o + x, w);
                             }
                         }
+                    };
+                    if (pending) {
+                        move_to(m_next);
+                        pending = false;
                     }
-                    const float mc = m == -INFINITY ? 0.f : m * a.c;
-                    const float2 c2 = make_float2(a.c, a.c), mc2 = make_float2(-mc, -mc);
+                    load_s();
+                    const int key0 = k * kRows;
+                    const bool edge = __any_sync(0xffffffffu, key0 + kRows - 1 > k_max || key0 < k_min);
+                    const float2 c2 = make_float2(a.c, a.c);
+                    float top = -INFINITY;
+                    bool redo = edge || count == 0;
+                    if (!redo) {
+                        // Against the reference as it stands, with the maximum
+                        // taken on the way: it only has to catch what passes
+                        // the range, and moves the reference for the next tile.
+                        const float mc = m == -INFINITY ? 0.f : m * a.c;
+                        const float2 mc2 = make_float2(-mc, -mc);
+                        float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+                        float t2[2] = {-INFINITY, -INFINITY};
+                        uint32_t w[kRows / 2];
 #pragma unroll
-                    for (int x = 0; x < kRows; x += 32) {
-                        uint32_t w[16];
-#pragma unroll
-                        for (int y = 0; y < 16; ++y) {
-                            const float2 e = fma2(make_float2(v[x + 2 * y], v[x + 2 * y + 1]), c2, mc2);
-                            v[x + 2 * y] = exp2_approx(e.x);
-                            v[x + 2 * y + 1] = exp2_approx(e.y);
-                            w[y] = pack_bf16(v[x + 2 * y], v[x + 2 * y + 1]);
+                        for (int y = 0; y < kRows / 2; ++y) {
+                            const float x0 = v[2 * y], x1 = v[2 * y + 1];
+                            t2[y & 1] = max3(t2[y & 1], x0, x1);
+                            float2 e = fma2(make_float2(x0, x1), c2, mc2);
+                            e.x = exp2_approx(e.x);
+                            e.y = exp2_approx(e.y);
+                            sum[y & 1] = add2(sum[y & 1], e);
+                            w[y] = pack_bf16(e.x, e.y);
                         }
-                        tmem_st16(t_s + x / 2, w);
-                        if (x == 32 || x == 96) {  // the product over these keys may start
-                            tmem_wait_st();
-                            fence_before();
-                            __syncwarp();
-                            if (lane == 0)
-                                mbar_arrive(smem_u32(x == 32 ? &sh.p_half[s] : &sh.p_ready[s]));
+                        top = fmaxf(t2[0], t2[1]);
+                        const float up = live ? (top - m) * a.c : 0.f;
+                        redo = __any_sync(0xffffffffu, up > kRange);
+                        if (!redo) {
+#pragma unroll
+                            for (int x = 0; x < 4; ++x)
+                                tmem_st16(t_s + x * 16, reinterpret_cast<const uint32_t(&)[16]>(w[x * 16]));
+                            sum[0] = add2(sum[0], sum[1]);
+                            l += sum[0].x + sum[0].y;
+                            pending = __any_sync(0xffffffffu, up > kGrow);
+                            m_next = fmaxf(m, top);
+                        } else
+                            load_s();
+                    }
+                    if (redo) {
+                        if (edge) {
+                            const int hi = k_max - key0, lo = k_min - key0;
+#pragma unroll
+                            for (int x = 0; x < kRows; ++x)
+                                v[x] = x <= hi && x >= lo ? v[x] : -INFINITY;
                         }
-                    }
-                    // the sum, off the path to the next product
-                    float2 sum[4] = {make_float2(v[0], v[1]), make_float2(v[2], v[3]), make_float2(v[4], v[5]),
-                                     make_float2(v[6], v[7])};
+                        float t4[4] = {v[0], v[1], v[2], v[3]};
 #pragma unroll
-                    for (int x = 8; x < kRows; x += 8) {
+                        for (int x = 4; x + 8 <= kRows; x += 8) {
 #pragma unroll
-                        for (int y = 0; y < 4; ++y)
-                            sum[y] = add2(sum[y], make_float2(v[x + 2 * y], v[x + 2 * y + 1]));
+                            for (int y = 0; y < 4; ++y)
+                                t4[y] = max3(t4[y], v[x + y], v[x + 4 + y]);
+                        }
+                        top = max3(max3(t4[0], v[124], v[125]), max3(t4[1], v[126], v[127]), fmaxf(t4[2], t4[3]));
+                        // false for -inf - -inf
+                        if (__any_sync(0xffffffffu, live && (top - m) * a.c > kGrow))
+                            move_to(fmaxf(m, top));
+                        const float mc = m == -INFINITY ? 0.f : m * a.c;
+                        const float2 mc2 = make_float2(-mc, -mc);
+                        float2 sum = make_float2(0.f, 0.f);
+#pragma unroll
+                        for (int x = 0; x < kRows; x += 32) {
+                            uint32_t w[16];
+#pragma unroll
+                            for (int y = 0; y < 16; ++y) {
+                                float2 e = fma2(make_float2(v[x + 2 * y], v[x + 2 * y + 1]), c2, mc2);
+                                e.x = exp2_approx(e.x);
+                                e.y = exp2_approx(e.y);
+                                sum = add2(sum, e);
+                                w[y] = pack_bf16(e.x, e.y);
+                            }
+                            tmem_st16(t_s + x / 2, w);
+                        }
+                        l += sum.x + sum.y;
                     }
-                    sum[0] = add2(add2(sum[0], sum[1]), add2(sum[2], sum[3]));
-                    l += sum[0].x + sum[0].y;
-                } else {
-                    fence_before();
-                    __syncwarp();
-                    if (lane == 0) {
-                        mbar_arrive(smem_u32(&sh.p_half[s]));
-                        mbar_arrive(smem_u32(&sh.p_ready[s]));
-                    }
+                    tmem_wait_st();
                 }
+                fence_before();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(smem_u32(&sh.p_ready[s]));
                 phase ^= 1u;
                 ++count;
             }
@@ -1122,7 +1187,7 @@ cudaError_t launch_tc(AttnArgs& a, const CUtensorMap& tq, const CUtensorMap& tk,
     if (e != cudaSuccess)
         return e;
     a.nst = (int)std::min<size_t>(kMaxStages, ((size_t)smem_optin - sizeof(Shared)) / tile - 2);
-    if (a.nst < 3 || (size_t)a.nst * tile < ((size_t)a.n_req + 1) * sizeof(int64_t))
+    if (a.nst < 5 || (size_t)a.nst * tile < ((size_t)a.n_req + 1) * sizeof(int64_t))
         return cudaErrorInvalidConfiguration;
     const size_t smem = (2 + (size_t)a.nst) * tile + sizeof(Shared);
     if ((e = launch_pdl(kv_attn_kernel<DB>, dim3(grid), dim3(kThreads), smem, s, a, tq, tk, tv)) != cudaSuccess)
