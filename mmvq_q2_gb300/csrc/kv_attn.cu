@@ -334,19 +334,36 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map
         : "memory");
 }
 
-// Shared-memory matrix descriptor of V as it lies: rows of 64 values along N
-// (128 bytes, swizzled), K going down the rows.  Groups of 8 rows are 1024
-// bytes apart, the next 64 values of N one half tile.
-__device__ __forceinline__ uint64_t smem_desc_v(uint32_t addr)
+// Shared-memory matrix descriptors, the address in the low word, the rest
+// here.  Q and K: rows of 64 values of D (128 bytes, swizzled), groups of 8
+// rows 1024 bytes apart.  V as it lies: the same rows are 64 values along N,
+// K going down them, and the next 64 values of N lie one half tile further.
+constexpr uint32_t kDescHi = (1024u >> 4) | 1u << 14 | 2u << 29;
+constexpr uint32_t kDescLoQK = 1u << 16, kDescLoV = (uint32_t)(kHalfBytes >> 4) << 16;
+
+__device__ __forceinline__ uint32_t desc_lo(uint32_t addr, uint32_t lo) { return (addr >> 4) | lo; }
+
+// The MMAs of q2k_umma.cuh with descriptors put together from words.
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool acc)
 {
-    uint64_t d = 0;
-    d |= (uint64_t)((addr >> 4) & 0x3FFFu);
-    d |= (uint64_t)(kHalfBytes >> 4) << 16;
-    d |= (uint64_t)(1024 >> 4) << 32;
-    d |= (uint64_t)1 << 46;
-    d |= (uint64_t)2 << 61;
-    return d;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 x, y;\n\tsetp.ne.b32 p, %5, 0;\n\tmov.b64 x, {%1, %4};\n\tmov.b64 y, {%2, %4};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "r"(idesc), "n"(kDescHi), "r"((uint32_t)acc)
+        : "memory");
 }
+
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a_tmem, uint32_t b, uint32_t idesc, bool acc)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 y;\n\tsetp.ne.b32 p, %5, 0;\n\tmov.b64 y, {%2, %4};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %3, p;\n\t}" ::"r"(d),
+        "r"(a_tmem), "r"(b), "r"(idesc), "n"(kDescHi), "r"((uint32_t)acc)
+        : "memory");
+}
+
+// The same value in every lane, known to the compiler as such.
+__device__ __forceinline__ uint32_t uniform(uint32_t v) { return __shfl_sync(0xffffffffu, v, 0); }
 
 constexpr uint32_t kTransposeB = 1u << 16;
 
@@ -642,7 +659,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             // descriptors stay in warp-uniform registers.
             const int s = warp - 1;
             const uint32_t idesc_s = instr_desc(kRows), idesc_o = instr_desc(a.D) | kTransposeB;
-            const uint32_t t_s = tmem + s * 256, t_o = t_s + 128;
+            const uint32_t t_s = uniform(tmem + s * 256), t_o = t_s + 128;
+            const uint32_t s_bar = uniform(smem_u32(&sh.s_full[s])), o_bar = uniform(smem_u32(&sh.o_done[s]));
             Ring at;  // the place of the item's first K tile; its V tile lies behind it, and so on
             uint32_t q_phase = 0, p_phase = 0;
             bool ok = true;
@@ -653,7 +671,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 int first, last;
                 it.span(a, s, first, last);
                 const int v_lo = first_key(a, it.q.base + it.i0), v_hi = it.q.base + it.i1;
-                const uint64_t qd = smem_desc_sw128(q_smem + (it.two ? s * kTile : 0));
+                const uint32_t qd = uniform(desc_lo(q_smem + (it.two ? s * kTile : 0), kDescLoQK));
                 // both streams pass every tile of a block of two row tiles; of a
                 // block of one, this stream passes every other tile, alone
                 const int hop = it.two ? 1 : 2;
@@ -661,30 +679,29 @@ __global__ void __launch_bounds__(kThreads, 1)
                 Ring ks = at;  // K tile k's place
                 if (!it.two && s == 1)
                     ks.skip(2, a.nst);
-                auto release = [&](int stage) {
-                    if (elect_one()) {
-                        umma_commit(smem_u32(&sh.empty[stage]));
-                        if (!it.two)  // for the other stream
-                            umma_commit(smem_u32(&sh.empty[stage]));
-                    }
-                };
-                auto score = [&]() {  // S of tile k
+                const bool alone = !it.two;  // then the stage is released for the other stream too
+                auto score = [&]() {         // S of tile k
                     if (!warp_wait(sh.full[ks.s], ks.phase))
                         return false;
                     fence_after();
-                    if (k >= first && k <= last) {
-                        const uint64_t kd = smem_desc_sw128(ring + (uint32_t)ks.s * kTile);
-                        // columns past D are zero in both tiles
+                    const bool act = k >= first && k <= last;
+                    const uint32_t kd = uniform(desc_lo(ring + (uint32_t)ks.s * kTile, kDescLoQK));
+                    const uint32_t bar = uniform(smem_u32(&sh.empty[ks.s]));
+                    if (elect_one()) {
+                        if (act) {
+                            // columns past D are zero in both tiles
 #pragma unroll
-                        for (int x = 0; x < DB * 4; ++x) {
-                            const uint32_t off = (uint32_t)((x >> 2) * (kHalfBytes >> 4) + (x & 3) * 2);
-                            if (elect_one())
-                                umma_f16(t_s, qd + off, kd + off, idesc_s, x > 0);
+                            for (int x = 0; x < DB * 4; ++x) {
+                                const uint32_t off = (uint32_t)((x >> 2) * (kHalfBytes >> 4) + (x & 3) * 2);
+                                mma_ss(t_s, qd + off, kd + off, idesc_s, x > 0);
+                            }
+                            umma_commit(s_bar);
                         }
-                        if (elect_one())
-                            umma_commit(smem_u32(&sh.s_full[s]));
+                        umma_commit(bar);
+                        if (alone)
+                            umma_commit(bar);
                     }
-                    release(ks.s);
+                    __syncwarp();
                     return true;
                 };
                 // Two row tiles: one stream's O += P V and its next S go to the
@@ -727,7 +744,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     __syncwarp();
                     if (!(ok = warp_wait(sh.full[vs.s], vs.phase)))
                         break;
-                    if (k >= first && k <= last) {
+                    const bool act = k >= first && k <= last;
+                    if (act) {
                         // clear the rows that no row of the block sees (the other stream may write the same zeros)
                         const int z_lo = max(0, min(kRows, v_lo - k * kRows));
                         const int z_hi = max(0, min(kRows, v_hi - k * kRows));
@@ -744,7 +762,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                             __syncwarp();
                         }
-                        const uint64_t vd = smem_desc_v(ring + (uint32_t)vs.s * kTile);
                         if (!(ok = warp_wait(sh.p_ready[s], p_phase)))
                             break;
                         p_phase ^= 1u;
@@ -757,17 +774,23 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 break;
                         }
                         fence_after();
-#pragma unroll
-                        for (int x = 0; x < kRows / 16; ++x) {
-                            if (elect_one())
-                                umma_f16_tmem_a(t_o, t_s + x * 8, vd + (uint32_t)(x * (2048 >> 4)), idesc_o, begun || x > 0);
-                        }
-                        begun = true;
-                        if (k + hop > last && elect_one())
-                            umma_commit(smem_u32(&sh.o_done[s]));  // O is complete
-                        __syncwarp();
                     }
-                    release(vs.s);
+                    const uint32_t vd = uniform(desc_lo(ring + (uint32_t)vs.s * kTile, kDescLoV));
+                    const uint32_t bar = uniform(smem_u32(&sh.empty[vs.s]));
+                    if (elect_one()) {
+                        if (act) {
+#pragma unroll
+                            for (int x = 0; x < kRows / 16; ++x)
+                                mma_ts(t_o, t_s + x * 8, vd + (uint32_t)(x * (2048 >> 4)), idesc_o, begun || x > 0);
+                            if (k + hop > last)
+                                umma_commit(o_bar);  // O is complete
+                        }
+                        umma_commit(bar);
+                        if (alone)
+                            umma_commit(bar);
+                    }
+                    __syncwarp();
+                    begun |= act;
                     ks.skip(2 * hop, a.nst);
                     k += hop;
                     if (k < it.k1)
