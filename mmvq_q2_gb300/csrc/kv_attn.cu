@@ -70,6 +70,7 @@ constexpr int kRows = 128;                  // rows of a tile, keys of a tile
 constexpr int kHalfBytes = kRows * 128;     // 128 rows of 64 values
 constexpr int kMaxStages = 12;
 constexpr float kGrow = 8.0f;               // log2 of how far P may pass 1 before its reference moves
+constexpr int kTurnMmas = 2;                // MMAs of S within a turn
 constexpr float kRange = 64.0f;             // and of how far within one tile
 
 struct AttnArgs {
@@ -82,7 +83,7 @@ struct AttnArgs {
     int nst;           // ring stages
     int row_cap;       // rows of a piece in the workspace
     float c;           // scale * log2(e)
-    int vec_out;       // out on 16-byte boundaries
+    int out_align;     // of the rows of out: 32, 16 or 2 bytes
     int4* heads;       // [2 * gridDim.x] pieces: {kind, r, h, j}
     float* part_o;     // [2 * gridDim.x][row_cap][D]
     float2* part_ml;   // [2 * gridDim.x][row_cap] maximum (times c) and sum
@@ -162,13 +163,14 @@ struct Start {
 };
 
 struct Walk {
-    int r, h, j, off;
+    int r, h, j, off, blocks;
     int64_t left;
     Request q;
 
     __device__ __forceinline__ Walk(const AttnArgs& a, const Start& s) : r(s.r), h(s.h), j(s.j), off(s.off), left(s.units)
     {
         q = load_request(a, r);
+        blocks = blocks_of(a, q);
     }
     // The next item of the run; false when it is done.
     __device__ __forceinline__ bool next(const AttnArgs& a, Item& it)
@@ -188,13 +190,14 @@ struct Walk {
         left -= it.k1 - it.k0;
         off = 0;
         if (left > 0) {
-            if (++j >= blocks_of(a, q)) {
+            if (++j >= blocks) {
                 j = 0;
                 if (++h >= a.Hkv) {
                     h = 0;
                     do
                         q = load_request(a, ++r);
                     while (q.n == 0);
+                    blocks = blocks_of(a, q);
                 }
             }
         }
@@ -485,16 +488,40 @@ struct Shared {
     int q_loads;
 };
 
-// Writes 16 values of a row of out.
-__device__ __forceinline__ void store_out16(uint16_t* dst, const float* v, float f, bool vec)
+__device__ __forceinline__ void store_32b(void* dst, const uint32_t (&w)[8])
 {
-    if (vec) {
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(dst), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+                 "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+}
+
+// 16 fp32 values of a row of a piece.
+__device__ __forceinline__ void store_part16(float* dst, const float* v)
+{
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        uint32_t w[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            w[i] = __float_as_uint(v[8 * h + i]);
+        store_32b(dst + 8 * h, w);
+    }
+}
+
+// 16 values of a row of out, a sector in one store where it is aligned.
+__device__ __forceinline__ void store_out16(uint16_t* dst, const float* v, float f, int align)
+{
+    if (align >= 16) {
         uint32_t w[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i)
             w[i] = pack_bf16(v[2 * i] * f, v[2 * i + 1] * f);
-        reinterpret_cast<uint4*>(dst)[0] = make_uint4(w[0], w[1], w[2], w[3]);
-        reinterpret_cast<uint4*>(dst)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+        if (align >= 32) {
+            store_32b(dst, w);
+        } else {
+            reinterpret_cast<uint4*>(dst)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+            reinterpret_cast<uint4*>(dst)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+        }
     } else {
 #pragma unroll
         for (int i = 0; i < 16; ++i)
@@ -679,35 +706,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 Ring ks = at;  // K tile k's place
                 if (!it.two && s == 1)
                     ks.skip(2, a.nst);
-                const bool alone = !it.two;  // then the stage is released for the other stream too
-                auto score = [&]() {         // S of tile k
-                    if (!warp_wait(sh.full[ks.s], ks.phase))
-                        return false;
-                    fence_after();
-                    const bool act = k >= first && k <= last;
-                    const uint32_t kd = uniform(desc_lo(ring + (uint32_t)ks.s * kTile, kDescLoQK));
-                    const uint32_t bar = uniform(smem_u32(&sh.empty[ks.s]));
-                    if (elect_one()) {
-                        if (act) {
-                            // columns past D are zero in both tiles
-#pragma unroll
-                            for (int x = 0; x < DB * 4; ++x) {
-                                const uint32_t off = (uint32_t)((x >> 2) * (kHalfBytes >> 4) + (x & 3) * 2);
-                                mma_ss(t_s, qd + off, kd + off, idesc_s, x > 0);
-                            }
-                            umma_commit(s_bar);
-                        }
-                        umma_commit(bar);
-                        if (alone)
-                            umma_commit(bar);
-                    }
-                    __syncwarp();
-                    return true;
-                };
-                // Two row tiles: one stream's O += P V and its next S go to the
-                // tensor cores as one run.  Interleaved with the other's, both
-                // would end together, and both softmaxes would then run while
-                // the tensor cores wait.
+                // Two row tiles: a stream takes a turn for its O += P V and the
+                // first MMAs of its next S.  Without turns the streams' products
+                // interleave and end together, both softmaxes then run at once
+                // and the tensor cores wait; with the whole of S in the turn
+                // they wait for its hand-over (8192 new tokens over 4096:
+                // 972 us without, 930 us with all of S, 883 us with two MMAs).
                 bool mine = false;
                 auto take_turn = [&]() {
                     bool got = true;
@@ -732,6 +736,33 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (mine && lane == 0)
                         atomicExch(&sh.turn, 0);
                     mine = false;
+                };
+                const bool alone = !it.two;  // then the stage is released for the other stream too
+                auto score = [&]() {         // S of tile k
+                    if (!warp_wait(sh.full[ks.s], ks.phase))
+                        return false;
+                    fence_after();
+                    const bool act = k >= first && k <= last;
+                    const uint32_t kd = uniform(desc_lo(ring + (uint32_t)ks.s * kTile, kDescLoQK));
+                    const uint32_t bar = uniform(smem_u32(&sh.empty[ks.s]));
+                    if (elect_one()) {
+                        if (act) {
+                            // columns past D are zero in both tiles
+#pragma unroll
+                            for (int x = 0; x < DB * 4; ++x) {
+                                const uint32_t off = (uint32_t)((x >> 2) * (kHalfBytes >> 4) + (x & 3) * 2);
+                                if (x == kTurnMmas && mine)
+                                    atomicExch(&sh.turn, 0);
+                                mma_ss(t_s, qd + off, kd + off, idesc_s, x > 0);
+                            }
+                            umma_commit(s_bar);
+                        }
+                        umma_commit(bar);
+                        if (alone)
+                            umma_commit(bar);
+                    }
+                    __syncwarp();
+                    return true;
                 };
                 bool begun = false;  // O holds a product of this item
                 if (k < it.k1)
@@ -795,7 +826,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     k += hop;
                     if (k < it.k1)
                         ok = score();
-                    end_turn();
+                    if (!(k < it.k1 && k >= first && k <= last))
+                        end_turn();  // no S to end it
+                    mine = false;
                 }
                 if (it.k0 + (it.two ? 0 : s) >= it.k1 && lane == 0)
                     mbar_arrive(smem_u32(&sh.q_empty));  // no tile of this item was this stream's
@@ -816,8 +849,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int s = (warp - 4) >> 2, quarter = warp & 3, row = quarter * 32 + lane;
         const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16), t_s = lanes + s * 256, t_o = t_s + 128;
         uint32_t phase = 0, done = 0, trade = 0;
-        bool ok = true;
-        while (ok && walk.next(a, it)) {
+        bool ok = true, more = walk.next(a, it);
+        while (ok && more) {
             const int ti = row / a.g, head = row - ti * a.g;
             const int i = it.i0 + ti + (it.two && s ? a.tq : 0);  // token of the request
             const bool live = row < a.g * a.tq && i < it.i1;
@@ -953,11 +986,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!ok)
                 break;
             // ---- the item's result ----
-            if (count > 0) {
-                if (!(ok = warp_wait(sh.o_done[s], done)))
-                    break;
-                done ^= 1u;
-            }
+            // (what the next item is gets worked out while the last product runs)
+            const bool two = it.two;
             const int kind = it.kind();
             const bool whole = (kind & kFirst) && (kind & kLast);
             const int slot = 2 * blockIdx.x + ((kind & kFirst) ? 1 : 0);
@@ -966,40 +996,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int64_t out_row = (int64_t)(it.q.t0 + i);
             const int out_head = it.h * a.g + head;
             uint16_t* dst = a.out + out_row * a.ld_o + (int64_t)out_head * a.D;
-            float mc = m == -INFINITY ? -INFINITY : m * a.c;
-            if (it.two) {
-                fence_after();
-                if (warp_live) {
-                    float* part = a.part_o + ((int64_t)slot * a.row_cap + s * kRows + row) * a.D;
-                    const float inv = l > 0.f ? 1.0f / l : 0.f;
-                    for (int x = 0; x < a.D; x += 16) {
-                        float o[16];
-                        if (count > 0)
-                            tmem_ld16(t_o + x, o);
-                        // a row without a key is zero, whatever O holds
-#pragma unroll
-                        for (int y = 0; y < 16; ++y)
-                            o[y] = l > 0.f ? o[y] : 0.f;
-                        if (live) {
-                            if (whole)
-                                store_out16(dst + x, o, inv, a.vec_out);
-                            else {
-#pragma unroll
-                                for (int y = 0; y < 16; y += 4)
-                                    *reinterpret_cast<float4*>(part + x + y) = make_float4(o[y], o[y + 1], o[y + 2], o[y + 3]);
-                            }
-                        }
-                    }
-                    if (live) {
-                        if (!whole)
-                            a.part_ml[(int64_t)slot * a.row_cap + s * kRows + row] = make_float2(mc, l);
-                        else if (a.lse)
-                            a.lse[out_row * a.Hq + out_head] = lse_of(mc, l);
-                    }
-                }
-                fence_before();
-            } else {
-                // both streams hold a part of the same rows: each joins half of the columns
+            float* part = a.part_o + ((int64_t)slot * a.row_cap + (two ? s * kRows : 0) + row) * a.D;
+            const float mc = m == -INFINITY ? -INFINITY : m * a.c;
+            more = walk.next(a, it);
+            if (count > 0) {
+                if (!(ok = warp_wait(sh.o_done[s], done)))
+                    break;
+                done ^= 1u;
+            }
+            float f0 = 1.f, f1 = 0.f, top = mc, sum = l;
+            if (!two) {
+                // both streams hold a part of the same rows: each joins every other 32 columns
                 sh.ml[s][row] = make_float2(mc, l);
                 fence_before();
                 __syncwarp();
@@ -1007,42 +1014,54 @@ __global__ void __launch_bounds__(kThreads, 1)
                     mbar_arrive(smem_u32(&sh.traded));
                 if (!(ok = warp_wait(sh.traded, trade)))
                     break;
-                fence_after();
-                if (warp_live) {
-                    const float2 e0 = sh.ml[0][row], e1 = sh.ml[1][row];
-                    const float top = fmaxf(e0.x, e1.x);
-                    const float f0 = e0.y > 0.f ? exp2_approx(e0.x - top) : 0.f;
-                    const float f1 = e1.y > 0.f ? exp2_approx(e1.x - top) : 0.f;
-                    const float sum = e0.y * f0 + e1.y * f1;
-                    const float inv = sum > 0.f ? 1.0f / sum : 0.f;
-                    float* part = a.part_o + ((int64_t)slot * a.row_cap + row) * a.D;
-                    for (int x = s * 16; x < a.D; x += 32) {
-                        float o0[16], o1[16];
-                        tmem_ld16(lanes + 128 + x, o0);
-                        tmem_ld16(lanes + 384 + x, o1);
+                const float2 e0 = sh.ml[0][row], e1 = sh.ml[1][row];
+                top = fmaxf(e0.x, e1.x);
+                f0 = e0.y > 0.f ? exp2_approx(e0.x - top) : 0.f;
+                f1 = e1.y > 0.f ? exp2_approx(e1.x - top) : 0.f;
+                sum = e0.y * f0 + e1.y * f1;
+            } else if (!(l > 0.f)) {
+                f0 = 0.f;  // a row without a key is zero, whatever O holds
+            }
+            fence_after();
+            if (warp_live) {
+                const float inv = whole ? (sum > 0.f ? 1.0f / sum : 0.f) : 1.f;
+                for (int x = two ? 0 : s * 32; x < a.D; x += two ? 32 : 64) {
+                    float o[32];
+                    tmem_ld32<0>((two ? t_o : lanes + 128) + x, o);
+                    if (!two) {
+                        float o1[32];
+                        tmem_ld32<0>(lanes + 384 + x, o1);
+                        tmem_wait_ld();
 #pragma unroll
-                        for (int y = 0; y < 16; ++y)
-                            o0[y] = (f0 > 0.f ? o0[y] * f0 : 0.f) + (f1 > 0.f ? o1[y] * f1 : 0.f);
-                        if (live) {
-                            if (whole)
-                                store_out16(dst + x, o0, inv, a.vec_out);
-                            else {
+                        for (int y = 0; y < 32; ++y)
+                            o[y] = (f0 > 0.f ? o[y] * f0 : 0.f) + (f1 > 0.f ? o1[y] * f1 : 0.f);
+                    } else {
+                        tmem_wait_ld();
 #pragma unroll
-                                for (int y = 0; y < 16; y += 4)
-                                    *reinterpret_cast<float4*>(part + x + y) =
-                                        make_float4(o0[y], o0[y + 1], o0[y + 2], o0[y + 3]);
-                            }
-                        }
+                        for (int y = 0; y < 32; ++y)
+                            o[y] = f0 > 0.f ? o[y] : 0.f;
                     }
-                    if (live && s == 0) {
-                        if (!whole)
-                            a.part_ml[(int64_t)slot * a.row_cap + row] = make_float2(top, sum);
-                        else if (a.lse)
-                            a.lse[out_row * a.Hq + out_head] = lse_of(top, sum);
+                    if (live) {
+#pragma unroll
+                        for (int y = 0; y < 32; y += 16)
+                            if (x + y < a.D) {
+                                if (whole)
+                                    store_out16(dst + x + y, o + y, inv, a.out_align);
+                                else
+                                    store_part16(part + x + y, o + y);
+                            }
                     }
                 }
+                if (live && (two || s == 0)) {
+                    if (!whole)
+                        a.part_ml[(int64_t)slot * a.row_cap + (two ? s * kRows : 0) + row] = make_float2(top, sum);
+                    else if (a.lse)
+                        a.lse[out_row * a.Hq + out_head] = lse_of(top, sum);
+                }
+            }
+            fence_before();
+            if (!two) {
                 // O and ml are free again once both streams have read them
-                fence_before();
                 __syncwarp();
                 if (lane == 0)
                     mbar_arrive(smem_u32(&sh.read));
@@ -1144,7 +1163,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) kv_attn_join_kernel(const Att
         if (lane * 4 < a.D) {
             uint16_t* dst = a.out + t * a.ld_o + (int64_t)h * a.D + lane * 4;
             const uint32_t lo = pack_bf16(o4[0] * inv, o4[1] * inv), hi = pack_bf16(o4[2] * inv, o4[3] * inv);
-            if (a.vec_out)
+            if (a.out_align >= 16)
                 *reinterpret_cast<uint2*>(dst) = make_uint2(lo, hi);
             else {
                 dst[0] = (uint16_t)lo;
@@ -1195,7 +1214,7 @@ Layout layout_of(int64_t T, int64_t Hq, int64_t Hkv, int64_t D)
     Layout w{};
     w.row_cap = T <= tq ? std::max<int64_t>(1, T * g) : 2 * kRows;
     w.ml = (size_t)2 * kMaxCtas * sizeof(int4);
-    w.o = w.ml + ((size_t)2 * kMaxCtas * w.row_cap * sizeof(float2) + 15) / 16 * 16;
+    w.o = w.ml + ((size_t)2 * kMaxCtas * w.row_cap * sizeof(float2) + 31) / 32 * 32;
     w.bytes = w.o + (size_t)2 * kMaxCtas * w.row_cap * D * sizeof(float);
     return w;
 }
@@ -1250,7 +1269,8 @@ cudaError_t launch_kv_attention(const AttnProblem& p, cudaStream_t s)
     a.g = a.Hq / a.Hkv;
     a.tq = kRows / a.g;
     a.c = p.scale * 1.4426950408889634f;
-    a.vec_out = (reinterpret_cast<uintptr_t>(p.out) & 15u) == 0 && p.ld_o % 8 == 0;
+    const uintptr_t out_bits = reinterpret_cast<uintptr_t>(p.out) | (uintptr_t)(p.ld_o * 2);
+    a.out_align = out_bits % 32 == 0 ? 32 : out_bits % 16 == 0 ? 16 : 2;
     const Layout w = layout_of(p.T, p.Hq, p.Hkv, p.D);
     uint8_t* ws = static_cast<uint8_t*>(p.workspace);
     a.row_cap = (int)w.row_cap;

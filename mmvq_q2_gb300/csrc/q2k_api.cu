@@ -796,7 +796,7 @@ int kv_attention_bf16(const uint16_t* q, int64_t ld_q, int64_t T, int64_t Hq, in
     if (T != 0 && (!workspace || workspace_bytes < kv_attention_workspace_bytes(T, Hq, Hkv, D)))
         return Q2K_ERR_WORKSPACE;
     if (!aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(block_table, 4) ||
-        !aligned(cu_q, 4) || !aligned(seq_lens, 4) || !aligned(out, 2) || !aligned(lse, 4) || !aligned(workspace, 16))
+        !aligned(cu_q, 4) || !aligned(seq_lens, 4) || !aligned(out, 2) || !aligned(lse, 4) || !aligned(workspace, 32))
         return Q2K_ERR_MISALIGNED;
     int st = check_device();
     if (st != Q2K_OK)

@@ -81,7 +81,7 @@ def test_attention_refusals(L):
         ({17: math.nan}, SHAPE), ({17: math.inf}, SHAPE), ({18: -1}, SHAPE),
         ({22: None}, WORKSPACE), ({23: need - 1}, WORKSPACE),
         ({0: P(0x10008)}, ALIGN), ({6: P(0x10008)}, ALIGN), ({7: H4}, ALIGN), ({11: ODD}, ALIGN), ({19: ODD}, ALIGN),
-        ({21: P(0x10002)}, ALIGN), ({22: P(0x10008)}, ALIGN),
+        ({21: P(0x10002)}, ALIGN), ({22: P(0x10010)}, ALIGN),
     ])
 
 
