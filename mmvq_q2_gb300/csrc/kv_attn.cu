@@ -699,13 +699,29 @@ __global__ void __launch_bounds__(kThreads, 1)
                 it.span(a, s, first, last);
                 const int v_lo = first_key(a, it.q.base + it.i0), v_hi = it.q.base + it.i1;
                 const uint32_t qd = uniform(desc_lo(q_smem + (it.two ? s * kTile : 0), kDescLoQK));
-                // both streams pass every tile of a block of two row tiles; of a
-                // block of one, this stream passes every other tile, alone
+                // Both streams work on every tile of a block of two row tiles; of
+                // a block of one, this stream works on every other tile.  It
+                // waits for the stages of the tiles between all the same, and
+                // frees them: a warp that left out a use of a stage could take
+                // the parity of an earlier one for its own.
                 const int hop = it.two ? 1 : 2;
                 int k = it.two ? it.k0 : it.k0 + s;
                 Ring ks = at;  // K tile k's place
-                if (!it.two && s == 1)
+                auto pass = [&](Ring r) {  // the K and V stages from r on
+                    for (int x = 0; x < 2; ++x) {
+                        if (!warp_wait(sh.full[r.s], r.phase))
+                            return false;
+                        if (lane == 0)
+                            mbar_arrive(smem_u32(&sh.empty[r.s]));
+                        r.next(a.nst);
+                    }
+                    return true;
+                };
+                if (!it.two && s == 1) {
+                    if (!(ok = pass(ks)))
+                        break;
                     ks.skip(2, a.nst);
+                }
                 // Two row tiles: a stream takes a turn for its O += P V and the
                 // first MMAs of its next S.  Without turns the streams' products
                 // interleave and end together, both softmaxes then run at once
@@ -737,8 +753,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         atomicExch(&sh.turn, 0);
                     mine = false;
                 };
-                const bool alone = !it.two;  // then the stage is released for the other stream too
-                auto score = [&]() {         // S of tile k
+                auto score = [&]() {  // S of tile k
                     if (!warp_wait(sh.full[ks.s], ks.phase))
                         return false;
                     fence_after();
@@ -758,8 +773,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                             umma_commit(s_bar);
                         }
                         umma_commit(bar);
-                        if (alone)
-                            umma_commit(bar);
                     }
                     __syncwarp();
                     return true;
@@ -817,12 +830,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 umma_commit(o_bar);  // O is complete
                         }
                         umma_commit(bar);
-                        if (alone)
-                            umma_commit(bar);
                     }
                     __syncwarp();
                     begun |= act;
-                    ks.skip(2 * hop, a.nst);
+                    ks.skip(2, a.nst);
+                    if (!it.two) {
+                        if (k + 1 < it.k1 && !(ok = pass(ks)))
+                            break;
+                        ks.skip(2, a.nst);
+                    }
                     k += hop;
                     if (k < it.k1)
                         ok = score();
