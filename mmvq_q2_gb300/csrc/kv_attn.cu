@@ -19,8 +19,9 @@
 // in a fixed order.
 //
 // One CTA, twelve warps:
-//   warp 0       copies Q, K and V tiles (64 values of D by 128 rows, 128-byte
+//   warp 0       copies Q and K tiles (64 values of D by 128 rows, 128-byte
 //                swizzle) into shared memory, a TMA box per page;
+//   warp 3       works out the items and copies the V tiles;
 //   warps 1, 2   issue the MMAs of streams 0 and 1: S into tensor memory, and
 //                O += P V with P read from tensor memory (in S's place) and V
 //                as it lies;
@@ -69,6 +70,7 @@ constexpr int kMaxCtas = 160;
 constexpr int kRows = 128;                  // rows of a tile, keys of a tile
 constexpr int kHalfBytes = kRows * 128;     // 128 rows of 64 values
 constexpr int kMaxStages = 12;
+constexpr int kItems = 4;                   // items worked out ahead
 constexpr float kGrow = 8.0f;               // log2 of how far P may pass 1 before its reference moves
 constexpr int kTurnMmas = 2;                // MMAs of S within a turn
 constexpr float kRange = 64.0f;             // and of how far within one tile
@@ -131,29 +133,11 @@ __device__ __forceinline__ int tiles_of(const AttnArgs& a, const Request& q, int
 // One item, or the part of it that lies in this CTA's run of units.
 struct Item {
     int r, h, j;
-    Request q;
-    int i0, i1;      // tokens of the request
-    int k0, k1;      // this CTA's key tiles [k0, k1)
-    int lo, hi;      // the item's key tiles
-    bool two;        // two row tiles (else one, its key tiles dealt to both streams)
-
-    // The key tiles of the run that stream s works on: of a block of two row
-    // tiles those that its own tile sees, else every other one.
-    __device__ __forceinline__ void span(const AttnArgs& a, int s, int& first, int& last) const
-    {
-        first = k0;
-        last = k1 - 1;
-        if (two) {
-            int l, x;
-            key_tiles(a, q, s ? i0 + a.tq : i0, s ? i1 : i0 + a.tq, l, x);
-            first = max(first, l);
-            last = min(last, x);
-        }
-    }
-    __device__ __forceinline__ int kind() const
-    {
-        return kPiece | (k0 == lo ? kFirst : 0) | (k1 == hi + 1 ? kLast : 0);
-    }
+    int t0, n, p0;   // first token (of all), tokens, position of the first
+    int k0, k1;      // this CTA's key tiles [k0, k1); none: the run is over
+    int first[2], last[2];  // the tiles of the run that a stream works on
+    int kind;
+    int two;         // two row tiles (else one, its key tiles dealt to both streams)
 };
 
 // Where a CTA's run starts: item (r, h, j), key tile lo + off, and its units.
@@ -162,6 +146,7 @@ struct Start {
     int64_t units;
 };
 
+// The items of a run, one after the other.
 struct Walk {
     int r, h, j, off, blocks;
     int64_t left;
@@ -172,36 +157,46 @@ struct Walk {
         q = load_request(a, r);
         blocks = blocks_of(a, q);
     }
-    // The next item of the run; false when it is done.
-    __device__ __forceinline__ bool next(const AttnArgs& a, Item& it)
+    __device__ __forceinline__ void next(const AttnArgs& a, Item& it)
     {
+        it.k0 = it.k1 = 0;
         if (left <= 0)
-            return false;
+            return;
         it.r = r;
         it.h = h;
         it.j = j;
-        it.q = q;
-        it.i0 = j * 2 * a.tq;
-        it.i1 = min(q.n, it.i0 + 2 * a.tq);
-        key_tiles(a, q, it.i0, it.i1, it.lo, it.hi);
-        it.k0 = it.lo + off;
-        it.k1 = (int)min((int64_t)it.hi + 1, it.k0 + left);
-        it.two = it.i1 - it.i0 > a.tq;
-        left -= it.k1 - it.k0;
-        off = 0;
-        if (left > 0) {
-            if (++j >= blocks) {
-                j = 0;
-                if (++h >= a.Hkv) {
-                    h = 0;
-                    do
-                        q = load_request(a, ++r);
-                    while (q.n == 0);
-                    blocks = blocks_of(a, q);
-                }
+        const int i0 = j * 2 * a.tq, i1 = min(q.n, i0 + 2 * a.tq);
+        it.t0 = q.t0 + i0;
+        it.n = i1 - i0;
+        it.p0 = q.base + i0;
+        it.two = it.n > a.tq;
+        int lo, hi;
+        key_tiles(a, q, i0, i1, lo, hi);
+        it.k0 = lo + off;
+        it.k1 = (int)min((int64_t)hi + 1, it.k0 + left);
+        it.kind = kPiece | (it.k0 == lo ? kFirst : 0) | (it.k1 == hi + 1 ? kLast : 0);
+        for (int s = 0; s < 2; ++s) {
+            it.first[s] = it.k0;
+            it.last[s] = it.k1 - 1;
+            if (it.two) {  // a row tile may see fewer keys than its block
+                int l, x;
+                key_tiles(a, q, s ? i0 + a.tq : i0, s ? i1 : i0 + a.tq, l, x);
+                it.first[s] = max(it.k0, l);
+                it.last[s] = min(it.k1 - 1, x);
             }
         }
-        return true;
+        left -= it.k1 - it.k0;
+        off = 0;
+        if (left > 0 && ++j >= blocks) {
+            j = 0;
+            if (++h >= a.Hkv) {
+                h = 0;
+                do
+                    q = load_request(a, ++r);
+                while (q.n == 0);
+                blocks = blocks_of(a, q);
+            }
+        }
     }
 };
 
@@ -479,13 +474,14 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
 struct Shared {
     uint64_t q_full, q_empty, mma_done, s_full[2], p_ready[2], o_done[2], traded, read;
     uint64_t full[kMaxStages], empty[kMaxStages];
+    uint64_t item_full[kItems], item_empty[kItems];
+    Item items[kItems];
     int64_t warp_sums[kThreads / 32];
     Start start;
     float2 ml[2][kRows];  // one-tile items: each stream's maximum (times c) and sum
     uint32_t tmem;
     int abort_flag, turn;
-    int loads;            // stages filled, for the clean-up
-    int q_loads;
+    int loads[2], q_loads;  // K, V and Q tiles asked for, for the clean-up
 };
 
 __device__ __forceinline__ void store_32b(void* dst, const uint32_t (&w)[8])
@@ -568,7 +564,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(smem_u32(&sh.empty[s]), 2);
         }
         sh.abort_flag = sh.turn = 0;
-        sh.loads = sh.q_loads = 0;
+        for (int s = 0; s < kItems; ++s) {
+            mbar_init(smem_u32(&sh.item_full[s]), 1);
+            mbar_init(smem_u32(&sh.item_empty[s]), 12);  // every working warp
+        }
+        sh.loads[0] = sh.loads[1] = sh.q_loads = 0;
         fence_mbar_init();
     }
     pdl_wait();
@@ -609,74 +609,113 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     auto warp_wait = [&](uint64_t& bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(bar, parity)); };
 
-    Walk walk(a, sh.start);
-    Item it{};
+    // The items, from warp 3 to every warp (itself too): next_item() gives the
+    // next one, done_item() hands its place back.
+    Ring item_at;
+    auto next_item = [&](const Item*& it) {
+        it = &sh.items[item_at.s];
+        return warp_wait(sh.item_full[item_at.s], item_at.phase) && it->k0 < it->k1;
+    };
+    auto done_item = [&]() {
+        __syncwarp();
+        if (lane == 0)
+            mbar_arrive(smem_u32(&sh.item_empty[item_at.s]));
+        item_at.next(kItems);
+    };
+    const Item* it;
+    bool ok = true;
     // 384 threads started with 168 registers each: 4 warps give up 80, 8 take 40 more
     if (warp < 4) {
         set_regs_down<88>();
-        if (warp == 0) {
+        if (warp == 0 || warp == 3) {
             // ---- copies ----
+            // Warp 0 takes K (and Q), warp 3 V: with pages of 16 a tile is 16
+            // boxes, and one warp issued them too slowly (64 decodes of 4100
+            // tokens: 220 us, 196 us with pages of 32).
+            const bool is_v = warp == 3;
+            const CUtensorMap* map = is_v ? &tv : &tk;
             const int box_rows = min(1 << a.shift, kRows), boxes = kRows / box_rows;
-            Ring at;
-            int loads = 0, items = 0;
-            // the page that holds this lane's box of key tile k, or one past the cache where no row needs it
-            auto page_of = [&](int k) -> int {
-                const int key = k * kRows + lane * box_rows;
-                if (lane >= boxes || key > it.q.base + it.i1 - 1 || key + box_rows <= first_key(a, it.q.base + it.i0))
-                    return (int)a.n_pages;
-                const int col = key >> a.shift;
-                const int page = col < a.max_pages ? a.table[it.r * a.ld_table + col] : -1;
-                if (page >= 0 && page < a.n_pages)
-                    return page;
-                atomicOr(&g_attn_error, kErrBadPage);
-                return (int)a.n_pages;
-            };
-            auto load = [&](const CUtensorMap* map, int k, int page) {
-                const int s = at.s;
-                if (loads >= a.nst && !warp_wait(sh.empty[s], at.phase ^ 1u))
+            Ring at, item_in;  // the stage of the next tile; the place of the next item to work out
+            if (is_v)
+                at.next(a.nst);
+            int loads = 0, items = 0, put = 0;
+            Walk walk(a, sh.start);
+            auto put_item = [&]() {  // warp 3
+                if (put >= kItems && !warp_wait(sh.item_empty[item_in.s], item_in.phase ^ 1u))
                     return false;
-                ++loads;
+                ++put;
+                Item x;
+                walk.next(a, x);
                 if (lane == 0) {
-                    mbar_arrive_expect_tx(smem_u32(&sh.full[s]), kTile);
-                    sh.loads = loads;
+                    sh.items[item_in.s] = x;
+                    mbar_arrive(smem_u32(&sh.item_full[item_in.s]));
                 }
                 __syncwarp();
-                if (lane < boxes) {
-                    const uint32_t dst = ring + (uint32_t)s * kTile + (uint32_t)(lane * box_rows * 128);
-                    const int row = (k * kRows + lane * box_rows) & ((1 << a.shift) - 1);
-    #pragma unroll
-                    for (int b = 0; b < DB; ++b)
-                        tma_load_4d(dst + b * kHalfBytes, map, b * 64, row, it.h, page, smem_u32(&sh.full[s]));
-                }
-                at.next(a.nst);
+                item_in.next(kItems);
                 return true;
             };
-            bool ok = true;
-            while (ok && walk.next(a, it)) {
-                if (items > 0 && !warp_wait(sh.q_empty, (uint32_t)(items - 1)))
-                    break;
-                if (lane == 0) {
-                    const int tiles = it.two ? 2 : 1;
-                    mbar_arrive_expect_tx(smem_u32(&sh.q_full), (uint32_t)(tiles * DB * a.g * a.tq * 128));
-                    sh.q_loads = items + 1;
-                    for (int s = 0; s < tiles; ++s)
-    #pragma unroll
-                        for (int b = 0; b < DB; ++b)
-                            tma_load_3d(q_smem + s * kTile + b * kHalfBytes, &tq, b * 64, it.h * a.g,
-                                        it.q.t0 + it.i0 + s * a.tq, smem_u32(&sh.q_full));
+            if (is_v)
+                ok = put_item() && put_item();
+            while (ok && next_item(it)) {
+                if (is_v) {
+                    if (!(ok = put_item()))
+                        break;
+                } else {
+                    if (items > 0 && !(ok = warp_wait(sh.q_empty, (uint32_t)(items - 1))))
+                        break;
+                    if (lane == 0) {
+                        const int tiles = it->two ? 2 : 1;
+                        mbar_arrive_expect_tx(smem_u32(&sh.q_full), (uint32_t)(tiles * DB * a.g * a.tq * 128));
+                        sh.q_loads = items + 1;
+                        for (int s = 0; s < tiles; ++s)
+#pragma unroll
+                            for (int b = 0; b < DB; ++b)
+                                tma_load_3d(q_smem + s * kTile + b * kHalfBytes, &tq, b * 64, it->h * a.g,
+                                            it->t0 + s * a.tq, smem_u32(&sh.q_full));
+                    }
+                    __syncwarp();
+                    ++items;
                 }
-                __syncwarp();
-                ++items;
-                // K and V of each key tile, with the pages of the next tile on their way
-                int here = page_of(it.k0);
-                for (int k = it.k0; ok && k < it.k1; ++k) {
+                const int key_lo = first_key(a, it->p0), key_hi = it->p0 + it->n - 1, h = it->h, k1 = it->k1;
+                const int32_t* table = a.table + it->r * a.ld_table;
+                // the page that holds this lane's box of key tile k, or one past the cache where no row needs it
+                auto page_of = [&](int k) -> int {
+                    const int key = k * kRows + lane * box_rows;
+                    if (lane >= boxes || key > key_hi || key + box_rows <= key_lo)
+                        return (int)a.n_pages;
+                    const int col = key >> a.shift;
+                    const int page = col < a.max_pages ? table[col] : -1;
+                    if (page >= 0 && page < a.n_pages)
+                        return page;
+                    atomicOr(&g_attn_error, kErrBadPage);
+                    return (int)a.n_pages;
+                };
+                int here = page_of(it->k0);
+                for (int k = it->k0; k < k1; ++k) {
                     const int page = here;
-                    if (k + 1 < it.k1)
-                        here = page_of(k + 1);
-                    ok = load(&tk, k, page) && load(&tv, k, page);
+                    if (k + 1 < k1)
+                        here = page_of(k + 1);  // on its way while this tile's stage is awaited
+                    const int s = at.s;
+                    if (2 * loads + is_v >= a.nst && !(ok = warp_wait(sh.empty[s], at.phase ^ 1u)))
+                        break;
+                    ++loads;
+                    if (lane == 0) {
+                        mbar_arrive_expect_tx(smem_u32(&sh.full[s]), kTile);
+                        sh.loads[is_v] = loads;
+                    }
+                    __syncwarp();
+                    if (lane < boxes) {
+                        const uint32_t dst = ring + (uint32_t)s * kTile + (uint32_t)(lane * box_rows * 128);
+                        const int row = (k * kRows + lane * box_rows) & ((1 << a.shift) - 1);
+#pragma unroll
+                        for (int b = 0; b < DB; ++b)
+                            tma_load_4d(dst + b * kHalfBytes, map, b * 64, row, h, page, smem_u32(&sh.full[s]));
+                    }
+                    at.skip(2, a.nst);
                 }
+                done_item();
             }
-        } else if (warp < 3) {
+        } else {
             // ---- MMAs ----
             // Warp 1 issues for stream 0, warp 2 for stream 1: the issue from
             // one warp (an MMA takes it 30 to 50 cycles, a wait or commit
@@ -690,22 +729,22 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t s_bar = uniform(smem_u32(&sh.s_full[s])), o_bar = uniform(smem_u32(&sh.o_done[s]));
             Ring at;  // the place of the item's first K tile; its V tile lies behind it, and so on
             uint32_t q_phase = 0, p_phase = 0;
-            bool ok = true;
-            while (ok && walk.next(a, it)) {
+            while (ok && next_item(it)) {
                 if (!(ok = warp_wait(sh.q_full, q_phase)))
                     break;
                 q_phase ^= 1u;
-                int first, last;
-                it.span(a, s, first, last);
-                const int v_lo = first_key(a, it.q.base + it.i0), v_hi = it.q.base + it.i1;
-                const uint32_t qd = uniform(desc_lo(q_smem + (it.two ? s * kTile : 0), kDescLoQK));
+                const int first = it->first[s], last = it->last[s], k0 = it->k0, k1 = it->k1;
+                const int v_lo = first_key(a, it->p0), v_hi = it->p0 + it->n;
+                const bool two = it->two;
+                done_item();
+                const uint32_t qd = uniform(desc_lo(q_smem + (two ? s * kTile : 0), kDescLoQK));
                 // Both streams work on every tile of a block of two row tiles; of
                 // a block of one, this stream works on every other tile.  It
                 // waits for the stages of the tiles between all the same, and
                 // frees them: a warp that left out a use of a stage could take
                 // the parity of an earlier one for its own.
-                const int hop = it.two ? 1 : 2;
-                int k = it.two ? it.k0 : it.k0 + s;
+                const int hop = two ? 1 : 2;
+                int k = two ? k0 : k0 + s;
                 Ring ks = at;  // K tile k's place
                 auto pass = [&](Ring r) {  // the K and V stages from r on
                     for (int x = 0; x < 2; ++x) {
@@ -717,7 +756,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     return true;
                 };
-                if (!it.two && s == 1) {
+                if (!two && s == 1) {
                     if (!(ok = pass(ks)))
                         break;
                     ks.skip(2, a.nst);
@@ -778,12 +817,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                     return true;
                 };
                 bool begun = false;  // O holds a product of this item
-                if (k < it.k1)
+                if (k < k1)
                     ok = score();
-                while (ok && k < it.k1) {
+                while (ok && k < k1) {
                     Ring vs = ks;
                     vs.next(a.nst);
-                    if (k + hop >= it.k1 && elect_one())
+                    if (k + hop >= k1 && elect_one())
                         umma_commit(smem_u32(&sh.q_empty));  // this was the last S of the item
                     __syncwarp();
                     if (!(ok = warp_wait(sh.full[vs.s], vs.phase)))
@@ -809,12 +848,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (!(ok = warp_wait(sh.p_ready[s], p_phase)))
                             break;
                         p_phase ^= 1u;
-                        if (it.two) {
+                        if (two) {
                             // nothing is waited for during a turn: the next K tile
                             // may need a stage that the other stream has yet to free
                             Ring ns = vs;
                             ns.next(a.nst);
-                            if (!(ok = (k + 1 >= it.k1 || warp_wait(sh.full[ns.s], ns.phase)) && take_turn()))
+                            if (!(ok = (k + 1 >= k1 || warp_wait(sh.full[ns.s], ns.phase)) && take_turn()))
                                 break;
                         }
                         fence_after();
@@ -834,21 +873,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                     __syncwarp();
                     begun |= act;
                     ks.skip(2, a.nst);
-                    if (!it.two) {
-                        if (k + 1 < it.k1 && !(ok = pass(ks)))
+                    if (!two) {
+                        if (k + 1 < k1 && !(ok = pass(ks)))
                             break;
                         ks.skip(2, a.nst);
                     }
                     k += hop;
-                    if (k < it.k1)
+                    if (k < k1)
                         ok = score();
-                    if (!(k < it.k1 && k >= first && k <= last))
+                    if (!(k < k1 && k >= first && k <= last))
                         end_turn();  // no S to end it
                     mine = false;
                 }
-                if (it.k0 + (it.two ? 0 : s) >= it.k1 && lane == 0)
+                if (k0 + (two ? 0 : s) >= k1 && lane == 0)
                     mbar_arrive(smem_u32(&sh.q_empty));  // no tile of this item was this stream's
-                const int used = 2 * (it.k1 - it.k0), rounds = used / a.nst;
+                const int used = 2 * (k1 - k0), rounds = used / a.nst;
                 at.phase ^= (uint32_t)rounds & 1u;
                 at.skip(used - rounds * a.nst, a.nst);
             }
@@ -864,23 +903,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ---- softmax ----
         const int s = (warp - 4) >> 2, quarter = warp & 3, row = quarter * 32 + lane;
         const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16), t_s = lanes + s * 256, t_o = t_s + 128;
+        const int ti = row / a.g, head = row - ti * a.g;
         uint32_t phase = 0, done = 0, trade = 0;
-        bool ok = true, more = walk.next(a, it);
-        while (ok && more) {
-            const int ti = row / a.g, head = row - ti * a.g;
-            const int i = it.i0 + ti + (it.two && s ? a.tq : 0);  // token of the request
-            const bool live = row < a.g * a.tq && i < it.i1;
+        while (ok && next_item(it)) {
+            const bool two = it->two;
+            const int i = ti + (two && s ? a.tq : 0);  // token of the block
+            const bool live = row < a.g * a.tq && i < it->n;
             const bool warp_live = __any_sync(0xffffffffu, live);
-            const int p = it.q.base + i;
+            const int p = it->p0 + i;
             const int k_max = live ? p : INT_MAX, k_min = live ? first_key(a, p) : 0;
             float m = -INFINITY, l = 0.f;  // m: what P is relative to
             float m_next = -INFINITY;
             bool pending = false;          // m_next takes over with the next tile
             int count = 0;
-            int k_first, k_last;
-            it.span(a, s, k_first, k_last);
-            const int stride = it.two ? 1 : 2;
-            for (int k = it.two ? k_first : k_first + s; k <= k_last; k += stride) {
+            const int k_last = it->last[s], stride = two ? 1 : 2;
+            for (int k = it->first[s] + (two ? 0 : s); k <= k_last; k += stride) {
                 if (!(ok = warp_wait(sh.s_full[s], phase)))
                     break;
                 fence_after();
@@ -1002,19 +1039,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!ok)
                 break;
             // ---- the item's result ----
-            // (what the next item is gets worked out while the last product runs)
-            const bool two = it.two;
-            const int kind = it.kind();
+            const int kind = it->kind;
             const bool whole = (kind & kFirst) && (kind & kLast);
             const int slot = 2 * blockIdx.x + ((kind & kFirst) ? 1 : 0);
             if (!whole && warp == 4 && lane == 0)
-                a.heads[slot] = make_int4(kind, it.r, it.h, it.j);
-            const int64_t out_row = (int64_t)(it.q.t0 + i);
-            const int out_head = it.h * a.g + head;
+                a.heads[slot] = make_int4(kind, it->r, it->h, it->j);
+            const int64_t out_row = (int64_t)(it->t0 + i);
+            const int out_head = it->h * a.g + head;
+            done_item();
             uint16_t* dst = a.out + out_row * a.ld_o + (int64_t)out_head * a.D;
             float* part = a.part_o + ((int64_t)slot * a.row_cap + (two ? s * kRows : 0) + row) * a.D;
             const float mc = m == -INFINITY ? -INFINITY : m * a.c;
-            more = walk.next(a, it);
             if (count > 0) {
                 if (!(ok = warp_wait(sh.o_done[s], done)))
                     break;
@@ -1091,8 +1126,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     if (*abort_flag && threadIdx.x == 0) {
         // let the copies that were issued land before the CTA exits
-        for (int i = max(0, sh.loads - a.nst); i < sh.loads; ++i)
-            mbar_wait_bounded(smem_u32(&sh.full[i % a.nst]), (uint32_t)(i / a.nst) & 1u, nullptr);
+        for (int v = 0; v < 2; ++v)
+            for (int i = max(0, sh.loads[v] - a.nst); i < sh.loads[v]; ++i)
+                mbar_wait_bounded(smem_u32(&sh.full[(2 * i + v) % a.nst]), (uint32_t)((2 * i + v) / a.nst) & 1u, nullptr);
         if (sh.q_loads > 0)
             mbar_wait_bounded(smem_u32(&sh.q_full), (uint32_t)(sh.q_loads - 1) & 1u, nullptr);
     }
