@@ -124,7 +124,7 @@ def _stream(stream=None):
 
 
 def _call(name, *args):
-    st = getattr(lib(), name)(*args)
+    st = getattr(_lib or lib(), name)(*args)
     if st != Q2K_OK:
         raise Q2KError(name, st)
 
@@ -394,51 +394,73 @@ def dense_gemm_bf16(x, W, out=None, stream=None):
 Q2K_F32 = 0
 Q2K_BF16 = 1
 _TYPES = {torch.float32: Q2K_F32, torch.bfloat16: Q2K_BF16}
+_F32, _BF16, _I32, _I64, _U8 = torch.float32, torch.bfloat16, torch.int32, torch.int64, torch.uint8
+
+# The calls below run once or more per layer and step, where a few
+# microseconds of host time count: addresses go to ctypes as plain integers,
+# the current stream is asked for as its handle, and a tensor's checks are one
+# short function.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_cur_device = getattr(torch._C, "_cuda_getDevice", None)
 
 
-def _type(t, what):
+def _stream_handle(stream):
+    if stream is not None:
+        return stream.cuda_stream
+    if _raw_stream is None or _cur_device is None:
+        return torch.cuda.current_stream().cuda_stream
+    return _raw_stream(_cur_device())
+
+
+def _at(t, dtype, name):
+    """Address of a CUDA tensor of the given type."""
+    if not t.is_cuda:
+        raise ValueError(f"tensors must be on a CUDA device ({name} is not)")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
+    return t.data_ptr()
+
+
+def _dense_at(t, dtype, name):
+    """The same for a tensor that has to be contiguous, or None."""
+    if t is None:
+        return None
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return _at(t, dtype, name)
+
+
+def _type(t, name):
     try:
         return _TYPES[t.dtype]
     except KeyError:
-        raise TypeError(f"{what} must be fp32 or bf16, not {t.dtype}") from None
-
-
-def _typed(dtype, **ts):
-    for name, t in ts.items():
-        if t is not None and t.dtype != dtype:
-            raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
-
-
-def _dense(**ts):
-    for name, t in ts.items():
-        if t is not None and not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
-
-
-def _addr(t):
-    return None if t is None else t.data_ptr()
+        raise TypeError(f"{name} must be fp32 or bf16, not {t.dtype}") from None
 
 
 def _heads(t, name):
     """``[T, H, D]`` whose heads of a token lie back to back -> the stride between tokens."""
-    if t.dim() != 3 or t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != t.shape[2]):
+    T, H, D = t.shape
+    s0, s1, s2 = t.stride()
+    if s2 != 1 or (H > 1 and s1 != D):
         raise ValueError(f"{name} must be [T, H, D] with the heads of a token back to back")
-    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1] * t.shape[2])
+    return s0 if T > 1 or s0 > H * D else H * D
+
+
+def _row(t, dim):
+    """Stride between the rows of ``t`` (a single row has none of its own)."""
+    s = t.stride(0)
+    return s if t.shape[0] > 1 or s > dim else dim
 
 
 def _cache(k_cache, v_cache):
     """``[n_pages, Hkv, page_size, D]`` twice, pages dense, the pages themselves at any equal stride."""
-    n_pages, Hkv, page, D = k_cache.shape
-    if v_cache.shape != k_cache.shape or k_cache.stride() != v_cache.stride():
+    shape, stride = k_cache.shape, k_cache.stride()
+    n_pages, Hkv, page, D = shape
+    if v_cache.shape != shape or v_cache.stride() != stride:
         raise ValueError("k_cache and v_cache must have one shape and one set of strides")
-    if k_cache.stride()[1:] != (page * D, D, 1):
+    if stride[1:] != (page * D, D, 1):
         raise ValueError("a page of the cache must be contiguous [Hkv, page_size, D]")
-    return n_pages, Hkv, page, D, k_cache.stride(0) if n_pages > 1 else max(k_cache.stride(0), Hkv * page * D)
-
-
-def _table(t):
-    """Columns of a block table and the stride between its rows."""
-    return t.shape[1], t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+    return n_pages, Hkv, page, D, max(stride[0], Hkv * page * D) if n_pages == 1 else stride[0]
 
 
 PagePlan = collections.namedtuple("PagePlan", "cu_q seq_lens positions token_req slot_map free_head")
@@ -451,31 +473,28 @@ def kv_page_plan(ctx_lens, new_lens, page_size, free_pages, block_table, max_tok
     and returns ``PagePlan(cu_q [n_req+1], seq_lens [n_req], positions,
     token_req, slot_map [max_tokens], free_head [1])``.  ``out``: a
     ``PagePlan`` to write into."""
-    _need_cuda(ctx_lens, new_lens, free_pages, block_table, free_head, err_flag)
-    _typed(torch.int32, ctx_lens=ctx_lens, new_lens=new_lens, free_pages=free_pages, block_table=block_table,
-           free_head=free_head, err_flag=err_flag)
-    _dense(ctx_lens=ctx_lens, new_lens=new_lens, free_pages=free_pages)
     n = ctx_lens.numel()
-    if new_lens.numel() != n or block_table.dim() != 2 or block_table.shape[0] != n or block_table.stride(1) != 1:
+    shape = block_table.shape
+    if new_lens.numel() != n or len(shape) != 2 or shape[0] != n or block_table.stride(1) != 1:
         raise ValueError("one ctx_len, new_len and row of block_table per request")
     if out is None:
-        # one allocation; the arrays start on 16-byte boundaries
-        n4, t4 = (n + 4) & ~3, (max_tokens + 3) & ~3
-        buf = torch.empty(2 * n4 + 3 * t4 + 1, dtype=torch.int32, device=ctx_lens.device)
-        sizes = (n + 1, n, max_tokens, max_tokens, max_tokens, 1)
-        starts = (0, n4, 2 * n4, 2 * n4 + t4, 2 * n4 + 2 * t4, 2 * n4 + 3 * t4)
-        out = PagePlan(*(buf[a:a + c] for a, c in zip(starts, sizes)))
+        if not ctx_lens.is_cuda:
+            raise ValueError("tensors must be on a CUDA device (ctx_lens is not)")
+        # one allocation for the six arrays
+        buf = torch.empty(2 * n + 3 * max_tokens + 2, dtype=_I32, device=ctx_lens.device)
+        out = PagePlan(*buf.split_with_sizes((n + 1, n, max_tokens, max_tokens, max_tokens, 1)))
+        at = buf.data_ptr()
+        cu, pos = at, at + 8 * n + 4
+        outs = (cu, at + 4 * n + 4, pos, pos + 4 * max_tokens, pos + 8 * max_tokens)
+        head = pos + 12 * max_tokens
     else:
-        _need_cuda(*out)
-        _typed(torch.int32, **out._asdict())
-        _dense(**out._asdict())
         if tuple(t.numel() for t in out) != (n + 1, n, max_tokens, max_tokens, max_tokens, 1):
             raise ValueError("out does not fit n_req and max_tokens")
-    cols, ld = _table(block_table)
-    _call("kv_page_plan", _addr(ctx_lens), _addr(new_lens), n, page_size, _addr(free_pages), free_pages.numel(),
-          _addr(free_head), _addr(block_table), cols, ld, _addr(out.cu_q), _addr(out.seq_lens), _addr(out.positions),
-          _addr(out.token_req), _addr(out.slot_map), max_tokens, _addr(out.free_head), _addr(err_flag),
-          _stream(stream))
+        *outs, head = (_dense_at(t, _I32, name) for t, name in zip(out, PagePlan._fields))
+    _call("kv_page_plan", _dense_at(ctx_lens, _I32, "ctx_lens"), _dense_at(new_lens, _I32, "new_lens"), n, page_size,
+          _dense_at(free_pages, _I32, "free_pages"), free_pages.numel(), _dense_at(free_head, _I32, "free_head"),
+          _at(block_table, _I32, "block_table"), shape[1], _row(block_table, shape[1]), *outs, max_tokens, head,
+          _dense_at(err_flag, _I32, "err_flag"), _stream_handle(stream))
     return out
 
 
@@ -485,39 +504,45 @@ def kv_rope_store(q, k, v, positions, inv_freq, slot_map, k_cache, v_cache, sect
     stride allowed) by ``positions [T]`` or ``[n_axes, T]`` and store k and
     ``v`` into the pages at ``slot_map``; returns bf16 ``q_out`` (None when q
     is None).  ``sections``: rotary pairs of each axis."""
-    _need_cuda(q, k, v, positions, inv_freq, slot_map, k_cache, v_cache, q_out, err_flag)
-    x_type = _type(k, "k")
-    _typed(k.dtype, q=q, v=v)
-    _typed(torch.bfloat16, k_cache=k_cache, v_cache=v_cache, q_out=q_out)
-    _typed(torch.int32, positions=positions, slot_map=slot_map, err_flag=err_flag)
-    _typed(torch.float32, inv_freq=inv_freq)
-    _dense(positions=positions, inv_freq=inv_freq, slot_map=slot_map)
+    x_type, dtype = _type(k, "k"), k.dtype
     T, Hkv, D = k.shape
     n_pages, Hc, page, Dc, page_stride = _cache(k_cache, v_cache)
+    pairs = inv_freq.numel()
     n_axes = 1 if positions.dim() == 1 else positions.shape[0]
-    if v.shape != k.shape or (Hc, Dc) != (Hkv, D) or slot_map.numel() != T or positions.numel() != n_axes * T or \
-            (q is not None and (q.shape[0], q.shape[2]) != (T, D)):
-        raise ValueError("q, k, v, positions, slot_map and the cache do not fit one another")
+    if v.shape != k.shape or Hc != Hkv or Dc != D or slot_map.numel() != T or positions.numel() != n_axes * T:
+        raise ValueError("k, v, positions, slot_map and the cache do not fit one another")
     if sections is None:
-        sections = (inv_freq.numel(),)
+        sections = (pairs,)
     if len(sections) != n_axes or n_axes > 3:
         raise ValueError("one section per axis, three at most")
-    Hq = 0
+    kp, vp = _at(k, dtype, "k"), _at(v, dtype, "v")
+    qp = qo = None
+    Hq = ld_q = ld_qo = 0
     if q is None:
         if q_out is not None:
             raise ValueError("q_out without q")
     else:
-        Hq = q.shape[1]
+        Tq, Hq, Dq = q.shape
+        if Tq != T or Dq != D:
+            raise ValueError("q and k do not fit one another")
+        qp, ld_q = _at(q, dtype, "q"), _heads(q, "q")
         if q_out is None:
-            q_out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=k.device)
+            q_out = torch.empty((T, Hq, D), dtype=_BF16, device=k.device)
+            ld_qo = Hq * D
         elif q_out.shape != q.shape:
             raise ValueError("q_out must have q's shape")
-    _call("kv_rope_store", _addr(q), 0 if q is None else _heads(q, "q"), _addr(k), _heads(k, "k"), _addr(v),
-          _heads(v, "v"), x_type, T, Hq, Hkv, D, _addr(positions), n_axes, (ctypes.c_int32 * 3)(*sections),
-          _addr(inv_freq), 2 * inv_freq.numel(), 1 if interleaved else 0, _addr(slot_map), _addr(q_out),
-          0 if q is None else _heads(q_out, "q_out"), _addr(k_cache), _addr(v_cache), n_pages, page, page_stride,
-          _addr(err_flag), _stream(stream))
+        else:
+            ld_qo = _heads(q_out, "q_out")
+        qo = _at(q_out, _BF16, "q_out")
+    _call("kv_rope_store", qp, ld_q, kp, _heads(k, "k"), vp, _heads(v, "v"), x_type, T, Hq, Hkv, D,
+          _dense_at(positions, _I32, "positions"), n_axes, _I32x3(*sections), _dense_at(inv_freq, _F32, "inv_freq"),
+          2 * pairs, 1 if interleaved else 0, _dense_at(slot_map, _I32, "slot_map"), qo, ld_qo,
+          _at(k_cache, _BF16, "k_cache"), _at(v_cache, _BF16, "v_cache"), n_pages, page, page_stride,
+          _dense_at(err_flag, _I32, "err_flag"), _stream_handle(stream))
     return q_out
+
+
+_I32x3 = ctypes.c_int32 * 3
 
 
 def kv_attention_workspace_bytes(T, Hq, Hkv, D) -> int:
@@ -531,35 +556,41 @@ def kv_attention_bf16(q, k_cache, v_cache, block_table, cu_q, seq_lens, scale=No
     ``seq_lens [n_req]`` tokens of each request, the new ones last ->
     (out bf16 ``[T, Hq, D]``, lse fp32 ``[T, Hq]`` or None).  ``scale``
     defaults to ``D ** -0.5``; ``window`` 0 sees all earlier keys."""
-    _need_cuda(q, k_cache, v_cache, block_table, cu_q, seq_lens, out, lse, workspace)
-    _typed(torch.bfloat16, q=q, k_cache=k_cache, v_cache=v_cache, out=out)
-    _typed(torch.int32, block_table=block_table, cu_q=cu_q, seq_lens=seq_lens)
-    _typed(torch.float32, lse=lse)
-    _dense(cu_q=cu_q, seq_lens=seq_lens, lse=lse)
+    qp = _at(q, _BF16, "q")
     T, Hq, D = q.shape
     n_pages, Hkv, page, Dc, page_stride = _cache(k_cache, v_cache)
     n = seq_lens.numel()
-    if Dc != D or cu_q.numel() != n + 1 or block_table.dim() != 2 or block_table.shape[0] != n or \
-            (n and block_table.stride(1) != 1):
+    rows, cols = block_table.shape
+    if Dc != D or cu_q.numel() != n + 1 or rows != n or (n and block_table.stride(1) != 1):
         raise ValueError("q, the cache, block_table, cu_q and seq_lens do not fit one another")
+    device = q.device
     if out is None:
-        out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=q.device)
+        out = torch.empty((T, Hq, D), dtype=_BF16, device=device)
+        ld_o = Hq * D
     elif out.shape != q.shape:
         raise ValueError("out must have q's shape")
+    else:
+        ld_o = _heads(out, "out")
     if lse is None:
         if want_lse:
-            lse = torch.empty((T, Hq), dtype=torch.float32, device=q.device)
+            lse = torch.empty((T, Hq), dtype=_F32, device=device)
     elif lse.shape != (T, Hq):
         raise ValueError("lse must be [T, Hq]")
     if workspace is None:
-        workspace = torch.empty(max(lib().kv_attention_workspace_bytes(T, Hq, Hkv, D), 16), dtype=torch.uint8,
-                                device=q.device)
-    cols, ld_table = _table(block_table)
-    _call("kv_attention_bf16", _addr(q), _heads(q, "q"), T, Hq, Hkv, D, _addr(k_cache), _addr(v_cache), n_pages, page,
-          page_stride, _addr(block_table), cols, ld_table, _addr(cu_q), _addr(seq_lens), n,
-          D ** -0.5 if scale is None else scale, window, _addr(out), _heads(out, "out"), _addr(lse),
-          _addr(workspace), workspace.numel(), _stream(stream))
+        workspace = torch.empty(lib().kv_attention_workspace_bytes(T, Hq, Hkv, D), dtype=_U8, device=device)
+    _call("kv_attention_bf16", qp, _heads(q, "q"), T, Hq, Hkv, D, _at(k_cache, _BF16, "k_cache"),
+          _at(v_cache, _BF16, "v_cache"), n_pages, page, page_stride, _at(block_table, _I32, "block_table"), cols,
+          _row(block_table, cols), _dense_at(cu_q, _I32, "cu_q"), _dense_at(seq_lens, _I32, "seq_lens"), n,
+          D ** -0.5 if scale is None else scale, window, _at(out, _BF16, "out"), ld_o, _dense_at(lse, _F32, "lse"),
+          _dense_at(workspace, _U8, "workspace"), workspace.numel(), _stream_handle(stream))
     return out, lse
+
+
+def _rows_at(t, dtype, T, dim, name):
+    """Address and row stride of ``[T, dim]`` with dense rows."""
+    if t.shape != (T, dim) or t.stride(1) != 1:
+        raise ValueError(f"{name} must be [T, dim] with dense rows")
+    return _at(t, dtype, name), _row(t, dim)
 
 
 def norm_gate_residual(residual, pre_w, eps, y=None, post_w=None, gate=None, alpha=1.0, residual_out=None, out=None,
@@ -570,45 +601,37 @@ def norm_gate_residual(residual, pre_w, eps, y=None, post_w=None, gate=None, alp
     and ``y`` ``[T, dim]`` fp32 or bf16 (row stride allowed), ``gate``
     ``[dim]`` or ``[T, dim]`` of y's type, weights fp32 ``[dim]``; without y,
     h is the residual.  ``residual_out`` may be ``residual``."""
-    _need_cuda(residual, pre_w, y, post_w, gate, residual_out, out, out_q8)
     T, dim = residual.shape
-    s_type = _type(residual, "residual")
-    y_type = Q2K_F32 if y is None else _type(y, "y")
-    _typed(residual.dtype, residual_out=residual_out)
-    _typed(torch.float32, pre_w=pre_w, post_w=post_w)
-    _typed(torch.bfloat16, out=out)
-    _dense(pre_w=pre_w, post_w=post_w, out_q8=out_q8)
-    if y is not None:
-        _typed(y.dtype, gate=gate)
+    s_type, s_dtype = _type(residual, "residual"), residual.dtype
+    res, ld_res = _rows_at(residual, s_dtype, T, dim, "residual")
+    device = residual.device
     if residual_out is None:
-        residual_out = torch.empty((T, dim), dtype=residual.dtype, device=residual.device)
+        residual_out = torch.empty((T, dim), dtype=s_dtype, device=device)
     if out is None:
-        out = torch.empty((T, dim), dtype=torch.bfloat16, device=residual.device)
-    for name, t in (("residual", residual), ("y", y), ("residual_out", residual_out), ("out", out)):
-        if t is not None and (t.shape != (T, dim) or t.stride(1) != 1):
-            raise ValueError(f"{name} must be [T, dim] with dense rows")
+        out = torch.empty((T, dim), dtype=_BF16, device=device)
+    ro, ld_ro = _rows_at(residual_out, s_dtype, T, dim, "residual_out")
+    n, ld_n = _rows_at(out, _BF16, T, dim, "out")
     if pre_w.numel() != dim or (post_w is not None and post_w.numel() != dim):
         raise ValueError("a weight must have dim values")
-    ld_gate = 0
+    y_type, yp, ld_y, gp, ld_gate = Q2K_F32, None, 0, None, 0
+    if y is not None:
+        y_type = _type(y, "y")
+        yp, ld_y = _rows_at(y, y.dtype, T, dim, "y")
     if gate is not None:
-        if gate.shape[-1] != dim or gate.stride(-1) != 1 or (gate.dim() == 2 and gate.shape[0] not in (1, T)):
+        if gate.shape[-1] != dim or gate.stride(-1) != 1 or gate.numel() not in (dim, T * dim):
             raise ValueError("gate must be [dim] or [T, dim] with dense rows")
-        if gate.dim() == 2 and gate.shape[0] == T and T > 1:
+        gp = _at(gate, residual.dtype if y is None else y.dtype, "gate")
+        if gate.numel() != dim:
             ld_gate = gate.stride(0)
     if out_q8 is None:
         if want_q8:
-            out_q8 = torch.empty((T, q8_1_row_bytes(dim)), dtype=torch.uint8, device=residual.device)
+            out_q8 = torch.empty((T, q8_1_row_bytes(dim)), dtype=_U8, device=device)
     elif out_q8.numel() != T * q8_1_row_bytes(dim):
         raise ValueError("out_q8 must hold T q8_1 rows")
-    _call("norm_gate_residual", _addr(y), y_type, _row(y, dim), _addr(post_w), _addr(gate), ld_gate, _addr(residual),
-          s_type, _row(residual, dim), alpha, _addr(pre_w), eps, T, dim, _addr(residual_out),
-          _row(residual_out, dim), _addr(out), _row(out, dim), _addr(out_q8), _stream(stream))
+    _call("norm_gate_residual", yp, y_type, ld_y, _dense_at(post_w, _F32, "post_w"), gp, ld_gate, res, s_type, ld_res,
+          alpha, _dense_at(pre_w, _F32, "pre_w"), eps, T, dim, ro, ld_ro, n, ld_n, _dense_at(out_q8, _U8, "out_q8"),
+          _stream_handle(stream))
     return (residual_out, out) if out_q8 is None else (residual_out, out, out_q8)
-
-
-def _row(t, dim):
-    """Stride between the rows of ``t`` (a single row has none of its own)."""
-    return 0 if t is None else t.stride(0) if t.shape[0] > 1 else max(t.stride(0), dim)
 
 
 ROUTE_SCORES = {"softmax": 0, "sigmoid": 1}
@@ -620,29 +643,26 @@ def moe_route_topk(logits, topk, bias=None, score="softmax", n_group=1, topk_gro
     (ids int32 ``[m, topk]``, weights fp32 ``[m, topk]``), and with
     ``expert_ptrs`` (int64 ``[3, E]``: gate, up and down addresses) the
     pointer tables int64 ``[m, 3 * topk]`` that ``q2k_moe_m1`` takes."""
-    _need_cuda(logits, bias, expert_ptrs, ids, weights, ptrs)
-    if score not in ROUTE_SCORES:
+    kind = ROUTE_SCORES.get(score)
+    if kind is None:
         raise ValueError(f"score must be one of {sorted(ROUTE_SCORES)}")
-    l_type = _type(logits, "logits")
-    _typed(torch.float32, bias=bias, weights=weights)
-    _typed(torch.int32, ids=ids)
-    _typed(torch.int64, expert_ptrs=expert_ptrs, ptrs=ptrs)
-    _dense(bias=bias, ids=ids, weights=weights, expert_ptrs=expert_ptrs, ptrs=ptrs)
     m, E = logits.shape
-    if logits.stride(1) != 1 or (bias is not None and bias.numel() != E) or \
-            (expert_ptrs is not None and expert_ptrs.numel() != 3 * E):
-        raise ValueError("logits must be [m, E] with dense rows, bias [E], expert_ptrs [3, E]")
+    x, ld = _rows_at(logits, logits.dtype, m, E, "logits")
+    l_type = _type(logits, "logits")
+    if (bias is not None and bias.numel() != E) or (expert_ptrs is not None and expert_ptrs.numel() != 3 * E):
+        raise ValueError("bias must be [E], expert_ptrs [3, E]")
+    device = logits.device
     if ids is None:
-        ids = torch.empty((m, topk), dtype=torch.int32, device=logits.device)
+        ids = torch.empty((m, topk), dtype=_I32, device=device)
     if weights is None:
-        weights = torch.empty((m, topk), dtype=torch.float32, device=logits.device)
+        weights = torch.empty((m, topk), dtype=_F32, device=device)
     if ptrs is None and expert_ptrs is not None:
-        ptrs = torch.empty((m, 3 * topk), dtype=torch.int64, device=logits.device)
+        ptrs = torch.empty((m, 3 * topk), dtype=_I64, device=device)
     if ids.numel() != m * topk or weights.numel() != m * topk or (ptrs is not None and ptrs.numel() != 3 * m * topk):
         raise ValueError("ids, weights and ptrs must hold topk (3 * topk) entries per token")
-    _call("moe_route_topk", _addr(logits), l_type, m, E, _row(logits, E), _addr(bias), ROUTE_SCORES[score], n_group,
-          topk_group, topk, 1 if renorm else 0, scale, _addr(ids), _addr(weights), _addr(expert_ptrs), _addr(ptrs),
-          _stream(stream))
+    _call("moe_route_topk", x, l_type, m, E, ld, _dense_at(bias, _F32, "bias"), kind, n_group, topk_group, topk,
+          1 if renorm else 0, scale, _dense_at(ids, _I32, "ids"), _dense_at(weights, _F32, "weights"),
+          _dense_at(expert_ptrs, _I64, "expert_ptrs"), _dense_at(ptrs, _I64, "ptrs"), _stream_handle(stream))
     return (ids, weights) if ptrs is None else (ids, weights, ptrs)
 
 
