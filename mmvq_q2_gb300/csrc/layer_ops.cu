@@ -104,74 +104,133 @@ __device__ __forceinline__ void encode_row(const uint16_t* n_row, int dim, uint8
     }
 }
 
-// 8 values a thread; rows and pointers on 16-byte boundaries.
+// 8 values of a row as they lie in memory, one load (32 bytes of fp32 in one
+// where they are aligned so; a row's start need only be on 16 bytes).
+template <bool BF16>
+struct Raw8 {
+    uint4 w[BF16 ? 1 : 2];
+    __device__ __forceinline__ void load(const void* p, int64_t i)
+    {
+        const char* at = static_cast<const char*>(p) + i * (BF16 ? 2 : 4);
+#pragma unroll
+        for (int k = 0; k < (BF16 ? 1 : 2); ++k)
+            w[k] = reinterpret_cast<const uint4*>(at)[k];
+    }
+    __device__ __forceinline__ float at(int j) const
+    {
+        const uint32_t* u = reinterpret_cast<const uint32_t*>(w);
+        if (BF16)
+            return __uint_as_float(j & 1 ? u[j >> 1] & 0xffff0000u : u[j >> 1] << 16);
+        return __uint_as_float(u[j]);
+    }
+};
+
+// NR runs of 8 values a thread, rows and pointers on 16-byte boundaries.  A
+// block takes rows blockIdx.x, + gridDim.x, ...: where it has more than one,
+// the weights wait in shared memory (read again for every row they were 32 of
+// 72 KB of a row's traffic from L2), and the next row is on its way while
+// this one is summed.  Two runs a thread where there are rows enough: half
+// the warps meet at a barrier, and more blocks share an SM to work meanwhile
+// (8192 rows of 4096, bf16: 62.6 us with one run, DRAM floor 49.4).
 constexpr int kNormVecDim = 8 * 1024;
 
-__global__ void __launch_bounds__(1024) norm_vec_kernel(const NormArgs a)
+template <int NR, bool YB, bool SB>
+__global__ void __launch_bounds__(NR == 1 ? 1024 : 256, NR == 1 ? 1 : 3) norm_vec_kernel(const NormArgs a)
 {
-    extern __shared__ __align__(16) uint16_t n_row[];  // with out_q8: the bf16 row
-    __shared__ float part[2][32];
+    extern __shared__ __align__(16) uint8_t norm_smem[];
+    __shared__ float part[2][2][32];
     pdl_launch_dependents();
     pdl_wait();
-    const int64_t t = blockIdx.x;
-    const int i = (int)threadIdx.x * 8;
-    const bool live = i < a.dim;
-    float h[8], u[8], g[8], w[8];
-    if (live) {
-        load8(a.residual, t * a.ld_res + i, a.stream_bf16, h);
-        if (a.y)
-            load8(a.y, t * a.ld_y + i, a.y_bf16, u);
-        if (a.gate)
-            load8(a.gate, t * a.ld_gate + i, a.y_bf16, g);
-        if (a.post_w)
-            load8(a.post_w, i, 0, w);
-    }
-    if (a.post_w) {
-        float s = 0.f;
-        if (live) {
+    const bool many = gridDim.x < a.T;
+    float* const w_smem = reinterpret_cast<float*>(norm_smem);
+    uint16_t* const n_row = reinterpret_cast<uint16_t*>(norm_smem + (many ? (size_t)a.dim * 8 : 0));  // with out_q8
+    const float* pre_w = many ? w_smem : a.pre_w;
+    const float* post_w = many ? w_smem + a.dim : a.post_w;
+    const bool has_y = a.y != nullptr, has_gate = a.gate != nullptr, has_post = a.post_w != nullptr;
+    Raw8<SB> res[NR];
+    Raw8<YB> y[NR], gate[NR];
+    auto at = [&](int r) { return (r * (int)blockDim.x + (int)threadIdx.x) * 8; };
+    auto fetch = [&](int64_t t) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-                s = fmaf(u[j], u[j], s);
+        for (int r = 0; r < NR; ++r)
+            if (at(r) < a.dim && t < a.T) {
+                res[r].load(a.residual, t * a.ld_res + at(r));
+                if (has_y)
+                    y[r].load(a.y, t * a.ld_y + at(r));
+                if (has_gate)
+                    gate[r].load(a.gate, t * a.ld_gate + at(r));
+            }
+    };
+    int64_t t = blockIdx.x;
+    fetch(t);
+    if (many) {
+        for (int i = (int)threadIdx.x * 4; i < a.dim; i += (int)blockDim.x * 4) {
+            *reinterpret_cast<float4*>(w_smem + i) = *reinterpret_cast<const float4*>(a.pre_w + i);
+            if (has_post)
+                *reinterpret_cast<float4*>(w_smem + a.dim + i) = *reinterpret_cast<const float4*>(a.post_w + i);
         }
-        const float inv = 1.0f / sqrtf(block_sum(s, part[0]) / (float)a.dim + a.eps);
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-            u[j] = u[j] * inv * w[j];
-    }
-    if (a.gate) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-            u[j] *= g[j];
-    }
-    float s = 0.f;
-    if (live) {
-        if (a.y) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                h[j] = fmaf(a.alpha, u[j], h[j]);
-        }
-        load8(a.pre_w, i, 0, w);
-        if (a.residual_out)
-            store8(a.residual_out, t * a.ld_ro + i, a.stream_bf16, h);
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-            s = fmaf(h[j], h[j], s);
-    }
-    if (!a.out && !a.out_q8)
-        return;
-    const float inv = 1.0f / sqrtf(block_sum(s, part[1]) / (float)a.dim + a.eps);
-    if (live) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-            h[j] = h[j] * inv * w[j];
-        if (a.out)
-            store8(a.out, t * a.ld_out + i, 1, h);
-        if (a.out_q8)
-            store8(n_row, i, 1, h);
-    }
-    if (a.out_q8) {
         __syncthreads();
-        encode_row(n_row, a.dim, static_cast<uint8_t*>(a.out_q8) + t * (a.dim / kQ8Values) * kQ8Bytes);
+    }
+    for (int odd = 0; t < a.T; t += gridDim.x, odd ^= 1) {
+        float h[NR][8], u[NR][8];
+        float s = 0.f;
+#pragma unroll
+        for (int r = 0; r < NR; ++r) {
+            const bool live = at(r) < a.dim;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                h[r][j] = live ? res[r].at(j) : 0.f;
+                u[r][j] = live && has_y ? y[r].at(j) : 0.f;
+                s = fmaf(u[r][j], u[r][j], s);
+            }
+        }
+        if (has_post) {
+            const float inv = 1.0f / sqrtf(block_sum(s, part[odd][0]) / (float)a.dim + a.eps);
+#pragma unroll
+            for (int r = 0; r < NR; ++r)
+                if (at(r) < a.dim) {
+                    float w[8];
+                    load8(post_w, at(r), 0, w);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        u[r][j] = u[r][j] * inv * w[j];
+                }
+        }
+        s = 0.f;
+#pragma unroll
+        for (int r = 0; r < NR; ++r)
+            if (at(r) < a.dim) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    if (has_y)
+                        h[r][j] = fmaf(a.alpha, has_gate ? u[r][j] * gate[r].at(j) : u[r][j], h[r][j]);
+                    s = fmaf(h[r][j], h[r][j], s);
+                }
+                if (a.residual_out)
+                    store8(a.residual_out, t * a.ld_ro + at(r), SB, h[r]);
+            }
+        fetch(t + gridDim.x);
+        if (!a.out && !a.out_q8)
+            continue;
+        const float inv = 1.0f / sqrtf(block_sum(s, part[odd][1]) / (float)a.dim + a.eps);
+#pragma unroll
+        for (int r = 0; r < NR; ++r)
+            if (at(r) < a.dim) {
+                float w[8];
+                load8(pre_w, at(r), 0, w);
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    h[r][j] = h[r][j] * inv * w[j];
+                if (a.out)
+                    store8(a.out, t * a.ld_out + at(r), 1, h[r]);
+                if (a.out_q8)
+                    store8(n_row, at(r), 1, h[r]);
+            }
+        if (a.out_q8) {
+            __syncthreads();
+            encode_row(n_row, a.dim, static_cast<uint8_t*>(a.out_q8) + t * (a.dim / kQ8Values) * kQ8Bytes);
+            __syncthreads();
+        }
     }
 }
 
@@ -410,6 +469,48 @@ __global__ void __launch_bounds__(128) moe_route_kernel(const RouteArgs a)
 
 bool on16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
+template <int NR, bool YB, bool SB>
+cudaError_t launch_norm_runs(const NormArgs& a, const DeviceInfo& di, cudaStream_t s)
+{
+    auto* kernel = norm_vec_kernel<NR, YB, SB>;
+    const int threads = (a.dim / 8 + NR * 32 - 1) / (NR * 32) * 32;
+    const size_t row = a.out_q8 ? (size_t)a.dim * 2 : 0, weights = (size_t)a.dim * 8;
+    // weights and the bf16 row: at most 80 KB
+    static std::atomic<unsigned long long> devs{0};
+    static std::atomic<int> fits[33];  // blocks an SM by warps a block, once asked
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess)
+        return e;
+    const unsigned long long bit = dev < 64 ? 1ull << dev : 0ull;
+    if (!(devs.load(std::memory_order_acquire) & bit)) {
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kNormVecDim * 10);
+        if (e != cudaSuccess)
+            return e;
+        devs.fetch_or(bit, std::memory_order_acq_rel);
+    }
+    int blocks = fits[threads / 32].load(std::memory_order_relaxed);
+    if (blocks == 0) {
+        // (the same on every device: the library runs on one kind)
+        e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&blocks, kernel, threads, (size_t)threads * NR * 80);
+        if (e != cudaSuccess)
+            return e;
+        blocks = std::max(1, blocks);
+        fits[threads / 32].store(blocks, std::memory_order_relaxed);
+    }
+    const unsigned grid = (unsigned)std::min<int64_t>(a.T, (int64_t)di.sm_count * blocks);
+    return launch_pdl(kernel, dim3(grid), dim3(threads), row + (grid < a.T ? weights : 0), s, a);
+}
+
+template <bool YB, bool SB>
+cudaError_t launch_norm_vec(const NormArgs& a, const DeviceInfo& di, cudaStream_t s)
+{
+    // a row an SM or less: latency, so as many threads as the row has runs
+    if (a.dim >= 512 && a.T > di.sm_count)
+        return launch_norm_runs<2, YB, SB>(a, di, s);
+    return launch_norm_runs<1, YB, SB>(a, di, s);
+}
+
 }  // namespace
 
 cudaError_t launch_norm_gate_residual(const NormProblem& p, cudaStream_t s)
@@ -447,8 +548,13 @@ cudaError_t launch_norm_gate_residual(const NormProblem& p, cudaStream_t s)
         return launch_pdl(norm_any_kernel, dim3((unsigned)a.T), dim3(256),
                           (size_t)(64 + a.dim) * sizeof(float) + (a.out_q8 ? (size_t)a.dim * 2 : 0), s, a);
     }
-    const int threads = (a.dim / 8 + 31) / 32 * 32;
-    return launch_pdl(norm_vec_kernel, dim3((unsigned)a.T), dim3(threads), a.out_q8 ? (size_t)a.dim * 2 : 0, s, a);
+    DeviceInfo di;
+    cudaError_t e = device_info(&di);
+    if (e != cudaSuccess)
+        return e;
+    if (a.y_bf16)
+        return a.stream_bf16 ? launch_norm_vec<true, true>(a, di, s) : launch_norm_vec<true, false>(a, di, s);
+    return a.stream_bf16 ? launch_norm_vec<false, true>(a, di, s) : launch_norm_vec<false, false>(a, di, s);
 }
 
 cudaError_t launch_moe_route(const RouteProblem& p, cudaStream_t s)
