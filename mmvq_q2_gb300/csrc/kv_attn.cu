@@ -75,6 +75,15 @@ constexpr float kGrow = 8.0f;               // log2 of how far P may pass 1 befo
 constexpr int kTurnMmas = 2;                // MMAs of S within a turn
 constexpr float kRange = 64.0f;             // and of how far within one tile
 
+// A split item whose last piece CTA x wrote (its first slot): what the join
+// needs to know, in one read.
+struct alignas(16) Head {
+    int first;      // CTA of the item's first piece (its second slot); -1: nothing to join
+    int t0, n, h;   // first token, tokens, kv head
+    int64_t total;  // units of all requests
+    int64_t pad;
+};
+
 struct AttnArgs {
     uint16_t* out;
     float* lse;
@@ -86,13 +95,13 @@ struct AttnArgs {
     int row_cap;       // rows of a piece in the workspace
     float c;           // scale * log2(e)
     int out_align;     // of the rows of out: 32, 16 or 2 bytes
-    int4* heads;       // [2 * gridDim.x] pieces: {kind, r, h, j}
+    Head* heads;       // [gridDim.x] what each CTA's first item ended, if it did
     float* part_o;     // [2 * gridDim.x][row_cap][D]
     float2* part_ml;   // [2 * gridDim.x][row_cap] maximum (times c) and sum
 };
 
-// Kinds of pieces: first and last key tile of the item, or not.
-constexpr int kNone = 0, kPiece = 1, kFirst = 2, kLast = 4;
+// What of its item a run holds: the first key tile, the last.
+constexpr int kFirst = 1, kLast = 2;
 
 // ---- the work ------------------------------------------------------------------
 
@@ -135,6 +144,7 @@ struct Item {
     int r, h, j;
     int t0, n, p0;   // first token (of all), tokens, position of the first
     int k0, k1;      // this CTA's key tiles [k0, k1); none: the run is over
+    int lo;          // the item's first key tile
     int first[2], last[2];  // the tiles of the run that a stream works on
     int kind;
     int two;         // two row tiles (else one, its key tiles dealt to both streams)
@@ -172,9 +182,10 @@ struct Walk {
         it.two = it.n > a.tq;
         int lo, hi;
         key_tiles(a, q, i0, i1, lo, hi);
+        it.lo = lo;
         it.k0 = lo + off;
         it.k1 = (int)min((int64_t)hi + 1, it.k0 + left);
-        it.kind = kPiece | (it.k0 == lo ? kFirst : 0) | (it.k1 == hi + 1 ? kLast : 0);
+        it.kind = (it.k0 == lo ? kFirst : 0) | (it.k1 == hi + 1 ? kLast : 0);
         for (int s = 0; s < 2; ++s) {
             it.first[s] = it.k0;
             it.last[s] = it.k1 - 1;
@@ -204,10 +215,11 @@ struct Walk {
 // memory), with warp_sums as scratch.
 __device__ __forceinline__ void sum_units(const AttnArgs& a, int64_t* sums, int64_t* warp_sums)
 {
+    constexpr int kWarps = kThreads / 32;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int64_t base = 0;
+    // requests side by side go to different warps: a long one keeps a whole warp
     for (int r0 = 0; r0 < a.n_req; r0 += kThreads) {
-        const int r = r0 + (int)threadIdx.x;
+        const int r = r0 + lane * kWarps + warp;
         Request q{0, 0, 0};
         if (r < a.n_req)
             q = load_request(a, r);
@@ -216,7 +228,6 @@ __device__ __forceinline__ void sum_units(const AttnArgs& a, int64_t* sums, int6
         if (nb <= 2)
             for (int j = 0; j < nb; ++j)
                 units += tiles_of(a, q, j);
-        // many blocks: the warp shares them
         for (uint32_t big = __ballot_sync(0xffffffffu, nb > 2); big; big &= big - 1) {
             const int src = __ffs(big) - 1;
             const Request b{__shfl_sync(0xffffffffu, q.t0, src), __shfl_sync(0xffffffffu, q.n, src),
@@ -231,7 +242,16 @@ __device__ __forceinline__ void sum_units(const AttnArgs& a, int64_t* sums, int6
             if (lane == src)
                 units = mine;
         }
-        units *= a.Hkv;
+        if (r < a.n_req)
+            sums[r + 1] = units * a.Hkv;
+    }
+    if (threadIdx.x == 0)
+        sums[0] = 0;
+    __syncthreads();
+    int64_t base = 0;
+    for (int r0 = 0; r0 < a.n_req; r0 += kThreads) {
+        const int r = r0 + (int)threadIdx.x;
+        int64_t units = r < a.n_req ? sums[r + 1] : 0;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const int64_t v = __shfl_up_sync(0xffffffffu, units, o);
@@ -242,7 +262,7 @@ __device__ __forceinline__ void sum_units(const AttnArgs& a, int64_t* sums, int6
             warp_sums[warp] = units;
         __syncthreads();
         int64_t before = base;
-        for (int w = 0; w < kThreads / 32; ++w) {
+        for (int w = 0; w < kWarps; ++w) {
             if (w < warp)
                 before += warp_sums[w];
             base += warp_sums[w];
@@ -251,9 +271,13 @@ __device__ __forceinline__ void sum_units(const AttnArgs& a, int64_t* sums, int6
             sums[r + 1] = before + units;
         __syncthreads();
     }
-    if (threadIdx.x == 0)
-        sums[0] = 0;
-    __syncthreads();
+}
+
+// CTA c of n takes the units [run_start(c), run_start(c + 1)).
+// (A 64-bit division is a long piece of code, and few calls have 2^23 units.)
+__device__ __forceinline__ int64_t run_start(int64_t total, int c, int n)
+{
+    return total < 1 << 23 ? (int64_t)((uint32_t)total * (uint32_t)c / (uint32_t)n) : total * c / n;
 }
 
 // One warp: the item and key tile of unit `at`.
@@ -478,6 +502,7 @@ struct Shared {
     Item items[kItems];
     int64_t warp_sums[kThreads / 32];
     Start start;
+    int64_t total;
     float2 ml[2][kRows];  // one-tile items: each stream's maximum (times c) and sum
     uint32_t tmem;
     int abort_flag, turn;
@@ -576,9 +601,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     int64_t* sums = reinterpret_cast<int64_t*>(smem + 2 * kTile);
     sum_units(a, sums, sh.warp_sums);
     const int64_t total = sums[a.n_req];
-    const int64_t from = total * blockIdx.x / gridDim.x, to = total * (blockIdx.x + 1) / gridDim.x;
-    if (threadIdx.x < 2)
-        a.heads[2 * blockIdx.x + threadIdx.x] = make_int4(kNone, 0, 0, 0);
+    const int64_t from = run_start(total, blockIdx.x, gridDim.x), to = run_start(total, blockIdx.x + 1, gridDim.x);
+    if (threadIdx.x == 0) {
+        a.heads[blockIdx.x].first = -1;
+        sh.total = total;
+    }
     if (from == to)
         return;
     if (warp == 0) {
@@ -1042,8 +1069,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int kind = it->kind;
             const bool whole = (kind & kFirst) && (kind & kLast);
             const int slot = 2 * blockIdx.x + ((kind & kFirst) ? 1 : 0);
-            if (!whole && warp == 4 && lane == 0)
-                a.heads[slot] = make_int4(kind, it->r, it->h, it->j);
+            if (!(kind & kFirst) && (kind & kLast) && warp == 4 && lane == 0) {
+                // the CTA whose run holds the item's first unit
+                const int64_t tot = sh.total;
+                const int64_t unit = run_start(tot, blockIdx.x, gridDim.x) - (it->k0 - it->lo);
+                int c = (int)((float)unit / (float)tot * (float)gridDim.x);
+                while (run_start(tot, c + 1, gridDim.x) <= unit)
+                    ++c;
+                while (run_start(tot, c, gridDim.x) > unit)
+                    --c;
+                a.heads[blockIdx.x] = Head{c, it->t0, it->n, it->h, tot, 0};
+            }
             const int64_t out_row = (int64_t)(it->t0 + i);
             const int out_head = it->h * a.g + head;
             done_item();
@@ -1140,69 +1176,82 @@ __global__ void __launch_bounds__(kThreads, 1)
 // Joins the pieces of split items: block x takes the item whose last piece
 // CTA x of the first launch wrote, a warp a row, a lane a piece for the
 // weights and then four columns of every piece, in the order of their keys.
-// What bounds it is latency: few dependent loads, and those of the pieces
-// four at a time.
-constexpr int kJoinWarps = 8;
+// What bounds it is latency, so what it has to know comes in one read, and a
+// row's first pieces are on their way together with their maxima.
+constexpr int kJoinWarps = 8, kJoinAhead = 4;
 
-__global__ void __launch_bounds__(kJoinWarps * 32) kv_attn_join_kernel(const AttnArgs a)
+__global__ void __launch_bounds__(kJoinWarps * 32, 5) kv_attn_join_kernel(const AttnArgs a)
 {
     pdl_launch_dependents();
     pdl_wait();
     const int last = (int)blockIdx.x, lane = threadIdx.x & 31;
-    const int4 head = a.heads[2 * last];
-    if (!(head.x & kLast))
+    const Head head = a.heads[last];
+    const int first = head.first;
+    if (first < 0)
         return;
-    // the first piece is some CTA's second slot; CTAs without units may lie between
-    int first = 0;
-    for (int c0 = last - 1; c0 >= 0; c0 -= 32) {
-        const int c = c0 - lane;
-        const uint32_t hit = __ballot_sync(0xffffffffu, c >= 0 && (a.heads[2 * max(c, 0) + 1].x & kFirst));
-        if (hit) {
-            first = c0 - (__ffs(hit) - 1);
-            break;
-        }
-    }
-    const Request q = load_request(a, head.y);
-    const int i0 = head.w * 2 * a.tq, i1 = min(q.n, i0 + 2 * a.tq);
-    const int rows = i1 - i0 > a.tq ? 2 * kRows : kRows;
+    const int rows = head.n > a.tq ? 2 * kRows : kRows;
+    const uint32_t n_cta = gridDim.x, total = (uint32_t)head.total;  // total matters below n_cta alone
+    const bool column = lane * 4 < a.D, all = head.total >= n_cta;
     for (int row = (int)blockIdx.y * kJoinWarps + (threadIdx.x >> 5); row < rows; row += kJoinWarps * (int)gridDim.y) {
-        const int s = row >> 7, in = row & 127, ti = in / a.g;
-        const int i = i0 + s * a.tq + ti;
-        if (in >= a.g * a.tq || i >= i1)
+        const int in = row & 127, ti = in / a.g;
+        const int i = (row >> 7) * a.tq + ti;
+        if (in >= a.g * a.tq || i >= head.n)
             continue;
-        auto piece = [&](int c) {
-            const int slot = 2 * c + (c == first);
-            return c <= last && a.heads[slot].x ? a.part_ml[(int64_t)slot * a.row_cap + row] : make_float2(-INFINITY, 0.f);
+        const float* const part = a.part_o + (int64_t)row * a.D + lane * 4;
+        const int64_t step = (int64_t)2 * a.row_cap;  // rows from one CTA's slot to the next one's
+        // a bit a piece of the 32 from CTA c0 on: a CTA without units has none
+        // (there are no such CTAs where units are enough for all)
+        auto pieces = [&](int c0) {
+            const int c = c0 + lane;
+            return __ballot_sync(0xffffffffu, c <= last && (all || total * c / n_cta < total * (c + 1) / n_cta));
         };
-        float top = -INFINITY;
-        for (int c0 = first; c0 <= last; c0 += 32)
-            top = fmaxf(top, piece(c0 + lane).x);
+        auto slot = [&](int c) { return c * step + (c == first ? a.row_cap : 0); };
+        float top = -INFINITY, sum = 0.f, o4[4] = {0.f, 0.f, 0.f, 0.f};
+        float2 ml = make_float2(-INFINITY, 0.f);
+        float4 v[kJoinAhead];
+        uint32_t have = pieces(first);
+        auto load_from = [&](int c) {
+#pragma unroll
+            for (int j = 0; j < kJoinAhead; ++j) {
+                v[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (column && (have >> ((c + j - first) & 31) & 1u) && c + j <= last)
+                    v[j] = *reinterpret_cast<const float4*>(part + slot(c + j) * a.D);
+            }
+        };
+        load_from(first);
+        if (have >> lane & 1u)
+            ml = a.part_ml[slot(first + lane) + row];
+        top = ml.x;
+        for (int c0 = first + 32; c0 <= last; c0 += 32)
+            if (pieces(c0) >> lane & 1u)
+                top = fmaxf(top, a.part_ml[slot(c0 + lane) + row].x);
 #pragma unroll
         for (int o = 16; o >= 1; o >>= 1)
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-        float sum = 0.f, o4[4] = {0.f, 0.f, 0.f, 0.f};
         for (int c0 = first; c0 <= last; c0 += 32) {
-            const float2 ml = piece(c0 + lane);
+            if (c0 != first) {
+                have = pieces(c0);
+                load_from(c0);
+                ml = have >> lane & 1u ? a.part_ml[slot(c0 + lane) + row] : make_float2(-INFINITY, 0.f);
+            }
             const float f = ml.y > 0.f ? exp2_approx(ml.x - top) : 0.f;
             sum = fmaf(ml.y, f, sum);
-            for (int i = 0; i < min(32, last - c0 + 1); i += 4) {
-                float w[4];
-                float4 v[4];
+            const int n = min(32, last - c0 + 1);
+            for (int p = 0; p < n; p += kJoinAhead) {
+                float4 w[kJoinAhead];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    w[j] = __shfl_sync(0xffffffffu, f, i + j);
-                    const int c = c0 + i + j;
-                    v[j] = make_float4(0.f, 0.f, 0.f, 0.f);
-                    if (w[j] > 0.f && lane * 4 < a.D)
-                        v[j] = *reinterpret_cast<const float4*>(
-                            a.part_o + ((int64_t)(2 * c + (c == first)) * a.row_cap + row) * a.D + lane * 4);
-                }
+                for (int j = 0; j < kJoinAhead; ++j)
+                    w[j] = v[j];
+                if (p + kJoinAhead < n)
+                    load_from(c0 + p + kJoinAhead);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    o4[0] = fmaf(v[j].x, w[j], o4[0]);
-                    o4[1] = fmaf(v[j].y, w[j], o4[1]);
-                    o4[2] = fmaf(v[j].z, w[j], o4[2]);
-                    o4[3] = fmaf(v[j].w, w[j], o4[3]);
+                for (int j = 0; j < kJoinAhead; ++j) {
+                    const float g = __shfl_sync(0xffffffffu, f, p + j);
+                    // a piece without a key for this row holds zeros
+                    o4[0] = fmaf(w[j].x, g, o4[0]);
+                    o4[1] = fmaf(w[j].y, g, o4[1]);
+                    o4[2] = fmaf(w[j].z, g, o4[2]);
+                    o4[3] = fmaf(w[j].w, g, o4[3]);
                 }
             }
         }
@@ -1210,9 +1259,9 @@ __global__ void __launch_bounds__(kJoinWarps * 32) kv_attn_join_kernel(const Att
         for (int o = 16; o >= 1; o >>= 1)
             sum += __shfl_xor_sync(0xffffffffu, sum, o);
         const float inv = sum > 0.f ? 1.0f / sum : 0.f;
-        const int64_t t = q.t0 + i;
-        const int h = head.z * a.g + (in - ti * a.g);
-        if (lane * 4 < a.D) {
+        const int64_t t = head.t0 + i;
+        const int h = head.h * a.g + (in - ti * a.g);
+        if (column) {
             uint16_t* dst = a.out + t * a.ld_o + (int64_t)h * a.D + lane * 4;
             const uint32_t lo = pack_bf16(o4[0] * inv, o4[1] * inv), hi = pack_bf16(o4[2] * inv, o4[3] * inv);
             if (a.out_align >= 16)
@@ -1265,7 +1314,7 @@ Layout layout_of(int64_t T, int64_t Hq, int64_t Hkv, int64_t D)
     const int64_t g = Hq / Hkv, tq = kRows / g;
     Layout w{};
     w.row_cap = T <= tq ? std::max<int64_t>(1, T * g) : 2 * kRows;
-    w.ml = (size_t)2 * kMaxCtas * sizeof(int4);
+    w.ml = (size_t)kMaxCtas * sizeof(Head);
     w.o = w.ml + ((size_t)2 * kMaxCtas * w.row_cap * sizeof(float2) + 31) / 32 * 32;
     w.bytes = w.o + (size_t)2 * kMaxCtas * w.row_cap * D * sizeof(float);
     return w;
@@ -1286,7 +1335,7 @@ cudaError_t launch_tc(AttnArgs& a, const CUtensorMap& tq, const CUtensorMap& tk,
     const size_t smem = (2 + (size_t)a.nst) * tile + sizeof(Shared);
     if ((e = launch_pdl(kv_attn_kernel<DB>, dim3(grid), dim3(kThreads), smem, s, a, tq, tk, tv)) != cudaSuccess)
         return e;
-    const int y = std::min(16, (a.row_cap + kJoinWarps - 1) / kJoinWarps);
+    const int y = std::min(8, (a.row_cap + kJoinWarps - 1) / kJoinWarps);
     return launch_pdl(kv_attn_join_kernel, dim3(grid, y), dim3(kJoinWarps * 32), 0, s, a);
 }
 
@@ -1326,7 +1375,7 @@ cudaError_t launch_kv_attention(const AttnProblem& p, cudaStream_t s)
     const Layout w = layout_of(p.T, p.Hq, p.Hkv, p.D);
     uint8_t* ws = static_cast<uint8_t*>(p.workspace);
     a.row_cap = (int)w.row_cap;
-    a.heads = reinterpret_cast<int4*>(ws);
+    a.heads = reinterpret_cast<Head*>(ws);
     a.part_ml = reinterpret_cast<float2*>(ws + w.ml);
     a.part_o = reinterpret_cast<float*>(ws + w.o);
 
