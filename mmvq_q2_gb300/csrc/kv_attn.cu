@@ -80,8 +80,6 @@ constexpr float kRange = 64.0f;             // and of how far within one tile
 struct alignas(16) Head {
     int first;      // CTA of the item's first piece (its second slot); -1: nothing to join
     int t0, n, h;   // first token, tokens, kv head
-    int64_t total;  // units of all requests
-    int64_t pad;
 };
 
 struct AttnArgs {
@@ -273,7 +271,8 @@ __device__ __forceinline__ void sum_units(const AttnArgs& a, int64_t* sums, int6
     }
 }
 
-// CTA c of n takes the units [run_start(c), run_start(c + 1)).
+// CTA c of n takes the units [run_start(c), run_start(c + 1)), one at least: n
+// is the grid, or the units where they are fewer.
 // (A 64-bit division is a long piece of code, and few calls have 2^23 units.)
 __device__ __forceinline__ int64_t run_start(int64_t total, int c, int n)
 {
@@ -601,13 +600,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     int64_t* sums = reinterpret_cast<int64_t*>(smem + 2 * kTile);
     sum_units(a, sums, sh.warp_sums);
     const int64_t total = sums[a.n_req];
-    const int64_t from = run_start(total, blockIdx.x, gridDim.x), to = run_start(total, blockIdx.x + 1, gridDim.x);
+    const int runs = (int)min(total, (int64_t)gridDim.x);
     if (threadIdx.x == 0) {
         a.heads[blockIdx.x].first = -1;
         sh.total = total;
     }
-    if (from == to)
+    if ((int)blockIdx.x >= runs)
         return;
+    const int64_t from = run_start(total, blockIdx.x, runs), to = run_start(total, blockIdx.x + 1, runs);
     if (warp == 0) {
         Start s;
         find_start(a, sums, from, s);
@@ -1072,13 +1072,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!(kind & kFirst) && (kind & kLast) && warp == 4 && lane == 0) {
                 // the CTA whose run holds the item's first unit
                 const int64_t tot = sh.total;
-                const int64_t unit = run_start(tot, blockIdx.x, gridDim.x) - (it->k0 - it->lo);
-                int c = (int)((float)unit / (float)tot * (float)gridDim.x);
-                while (run_start(tot, c + 1, gridDim.x) <= unit)
+                const int runs = (int)min(tot, (int64_t)gridDim.x);
+                const int64_t unit = run_start(tot, blockIdx.x, runs) - (it->k0 - it->lo);
+                int c = (int)((float)unit / (float)tot * (float)runs);
+                while (run_start(tot, c + 1, runs) <= unit)
                     ++c;
-                while (run_start(tot, c, gridDim.x) > unit)
+                while (run_start(tot, c, runs) > unit)
                     --c;
-                a.heads[blockIdx.x] = Head{c, it->t0, it->n, it->h, tot, 0};
+                a.heads[blockIdx.x] = Head{c, it->t0, it->n, it->h};
             }
             const int64_t out_row = (int64_t)(it->t0 + i);
             const int out_head = it->h * a.g + head;
@@ -1174,96 +1175,94 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // Joins the pieces of split items: block x takes the item whose last piece
-// CTA x of the first launch wrote, a warp a row, a lane a piece for the
-// weights and then four columns of every piece, in the order of their keys.
-// What bounds it is latency, so what it has to know comes in one read, and a
-// row's first pieces are on their way together with their maxima.
-constexpr int kJoinWarps = 8, kJoinAhead = 4;
+// CTA x of the first launch wrote, in the order of the keys.  What bounds it
+// is latency: what it has to know comes in one read, and AHEAD pieces of a
+// row are on their way together with their maxima.  LANES lanes share a row
+// (each takes C columns): few where there are many rows, which then mostly
+// have two pieces, so that all rows of all items run at once; a warp where
+// there are few, which have many.
+constexpr int kJoinWarps = 8, kJoinY = 8;
 
-__global__ void __launch_bounds__(kJoinWarps * 32, 5) kv_attn_join_kernel(const AttnArgs a)
+template <int LANES, int AHEAD>
+__device__ __forceinline__ void join_rows(const AttnArgs& a, const Head& head, int first, int last)
 {
-    pdl_launch_dependents();
-    pdl_wait();
-    const int last = (int)blockIdx.x, lane = threadIdx.x & 31;
-    const Head head = a.heads[last];
-    const int first = head.first;
-    if (first < 0)
-        return;
+    constexpr int C = kRows / LANES, kPer = 32 / LANES;  // columns of a lane, rows of a warp
+    const int lane = threadIdx.x & 31, in_row = lane % LANES, col = in_row * C;
     const int rows = head.n > a.tq ? 2 * kRows : kRows;
-    const uint32_t n_cta = gridDim.x, total = (uint32_t)head.total;  // total matters below n_cta alone
-    const bool column = lane * 4 < a.D, all = head.total >= n_cta;
-    for (int row = (int)blockIdx.y * kJoinWarps + (threadIdx.x >> 5); row < rows; row += kJoinWarps * (int)gridDim.y) {
+    const int64_t step = (int64_t)2 * a.row_cap;  // rows from one CTA's slot to the next one's
+    for (int r0 = ((int)blockIdx.y * kJoinWarps + (threadIdx.x >> 5)) * kPer; r0 < rows;
+         r0 += kJoinWarps * (int)gridDim.y * kPer) {
+        const int row = r0 + lane / LANES;
         const int in = row & 127, ti = in / a.g;
         const int i = (row >> 7) * a.tq + ti;
-        if (in >= a.g * a.tq || i >= head.n)
+        const bool live = in < a.g * a.tq && i < head.n;
+        if (!__any_sync(0xffffffffu, live))
             continue;
-        const float* const part = a.part_o + (int64_t)row * a.D + lane * 4;
-        const int64_t step = (int64_t)2 * a.row_cap;  // rows from one CTA's slot to the next one's
-        // a bit a piece of the 32 from CTA c0 on: a CTA without units has none
-        // (there are no such CTAs where units are enough for all)
-        auto pieces = [&](int c0) {
-            const int c = c0 + lane;
-            return __ballot_sync(0xffffffffu, c <= last && (all || total * c / n_cta < total * (c + 1) / n_cta));
+        auto slot = [&](int c) { return c * step + (c == first ? a.row_cap : 0) + row; };
+        auto has = [&](int c) { return live && c <= last; };
+        // the maximum of all pieces, LANES at a time
+        float top = -INFINITY;
+        struct Pieces {
+            float4 v[AHEAD][C / 4];
+            float2 ml[AHEAD];
         };
-        auto slot = [&](int c) { return c * step + (c == first ? a.row_cap : 0); };
-        float top = -INFINITY, sum = 0.f, o4[4] = {0.f, 0.f, 0.f, 0.f};
-        float2 ml = make_float2(-INFINITY, 0.f);
-        float4 v[kJoinAhead];
-        uint32_t have = pieces(first);
-        auto load_from = [&](int c) {
+        Pieces now, next;
+        auto fetch = [&](Pieces& p, int c) {
 #pragma unroll
-            for (int j = 0; j < kJoinAhead; ++j) {
-                v[j] = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (column && (have >> ((c + j - first) & 31) & 1u) && c + j <= last)
-                    v[j] = *reinterpret_cast<const float4*>(part + slot(c + j) * a.D);
+            for (int j = 0; j < AHEAD; ++j) {
+                const bool there = has(c + j);
+                p.ml[j] = there ? a.part_ml[slot(c + j)] : make_float2(-INFINITY, 0.f);
+#pragma unroll
+                for (int x = 0; x < C / 4; ++x)
+                    p.v[j][x] = there && col + 4 * x < a.D
+                                    ? *reinterpret_cast<const float4*>(a.part_o + slot(c + j) * a.D + col + 4 * x)
+                                    : make_float4(0.f, 0.f, 0.f, 0.f);
             }
         };
-        load_from(first);
-        if (have >> lane & 1u)
-            ml = a.part_ml[slot(first + lane) + row];
-        top = ml.x;
-        for (int c0 = first + 32; c0 <= last; c0 += 32)
-            if (pieces(c0) >> lane & 1u)
-                top = fmaxf(top, a.part_ml[slot(c0 + lane) + row].x);
+        fetch(now, first);
+        for (int c = first; c <= last; c += LANES)
+            if (has(c + in_row))
+                top = fmaxf(top, a.part_ml[slot(c + in_row)].x);
 #pragma unroll
-        for (int o = 16; o >= 1; o >>= 1)
+        for (int o = LANES / 2; o >= 1; o >>= 1)
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-        for (int c0 = first; c0 <= last; c0 += 32) {
-            if (c0 != first) {
-                have = pieces(c0);
-                load_from(c0);
-                ml = have >> lane & 1u ? a.part_ml[slot(c0 + lane) + row] : make_float2(-INFINITY, 0.f);
-            }
-            const float f = ml.y > 0.f ? exp2_approx(ml.x - top) : 0.f;
-            sum = fmaf(ml.y, f, sum);
-            const int n = min(32, last - c0 + 1);
-            for (int p = 0; p < n; p += kJoinAhead) {
-                float4 w[kJoinAhead];
+        float sum = 0.f;
+        float4 o[C / 4];
 #pragma unroll
-                for (int j = 0; j < kJoinAhead; ++j)
-                    w[j] = v[j];
-                if (p + kJoinAhead < n)
-                    load_from(c0 + p + kJoinAhead);
+        for (int x = 0; x < C / 4; ++x)
+            o[x] = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int c = first; c <= last; c += AHEAD) {
+            if (LANES == 32)  // many pieces: the next ones meanwhile
+                fetch(next, c + AHEAD);
+            else if (c != first)
+                fetch(now, c);
 #pragma unroll
-                for (int j = 0; j < kJoinAhead; ++j) {
-                    const float g = __shfl_sync(0xffffffffu, f, p + j);
-                    // a piece without a key for this row holds zeros
-                    o4[0] = fmaf(w[j].x, g, o4[0]);
-                    o4[1] = fmaf(w[j].y, g, o4[1]);
-                    o4[2] = fmaf(w[j].z, g, o4[2]);
-                    o4[3] = fmaf(w[j].w, g, o4[3]);
+            for (int j = 0; j < AHEAD; ++j) {
+                // a piece without a key for this row holds zeros
+                const float f = now.ml[j].y > 0.f ? exp2_approx(now.ml[j].x - top) : 0.f;
+                sum = fmaf(now.ml[j].y, f, sum);
+#pragma unroll
+                for (int x = 0; x < C / 4; ++x) {
+                    o[x].x = fmaf(now.v[j][x].x, f, o[x].x);
+                    o[x].y = fmaf(now.v[j][x].y, f, o[x].y);
+                    o[x].z = fmaf(now.v[j][x].z, f, o[x].z);
+                    o[x].w = fmaf(now.v[j][x].w, f, o[x].w);
                 }
             }
+            if (LANES == 32)
+                now = next;
         }
-#pragma unroll
-        for (int o = 16; o >= 1; o >>= 1)
-            sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        if (!live)
+            continue;
         const float inv = sum > 0.f ? 1.0f / sum : 0.f;
         const int64_t t = head.t0 + i;
         const int h = head.h * a.g + (in - ti * a.g);
-        if (column) {
-            uint16_t* dst = a.out + t * a.ld_o + (int64_t)h * a.D + lane * 4;
-            const uint32_t lo = pack_bf16(o4[0] * inv, o4[1] * inv), hi = pack_bf16(o4[2] * inv, o4[3] * inv);
+#pragma unroll
+        for (int x = 0; x < C / 4; ++x) {
+            if (col + 4 * x >= a.D)
+                break;
+            uint16_t* dst = a.out + t * a.ld_o + (int64_t)h * a.D + col + 4 * x;
+            const uint32_t lo = pack_bf16(o[x].x * inv, o[x].y * inv), hi = pack_bf16(o[x].z * inv, o[x].w * inv);
             if (a.out_align >= 16)
                 *reinterpret_cast<uint2*>(dst) = make_uint2(lo, hi);
             else {
@@ -1273,9 +1272,23 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 5) kv_attn_join_kernel(const 
                 dst[3] = (uint16_t)(hi >> 16);
             }
         }
-        if (a.lse && lane == 0)
+        if (a.lse && in_row == 0)
             a.lse[t * a.Hq + h] = lse_of(top, sum);
     }
+}
+
+__global__ void __launch_bounds__(kJoinWarps * 32, 4) kv_attn_join_kernel(const AttnArgs a)
+{
+    pdl_launch_dependents();
+    pdl_wait();
+    const int last = (int)blockIdx.x;
+    const Head head = a.heads[last];
+    if (head.first < 0)
+        return;
+    if (head.n * a.g > 64)
+        join_rows<8, 2>(a, head, head.first, last);
+    else
+        join_rows<32, 4>(a, head, head.first, last);
 }
 
 PFN_cuTensorMapEncodeTiled_v12000 encoder()
@@ -1335,7 +1348,7 @@ cudaError_t launch_tc(AttnArgs& a, const CUtensorMap& tq, const CUtensorMap& tk,
     const size_t smem = (2 + (size_t)a.nst) * tile + sizeof(Shared);
     if ((e = launch_pdl(kv_attn_kernel<DB>, dim3(grid), dim3(kThreads), smem, s, a, tq, tk, tv)) != cudaSuccess)
         return e;
-    const int y = std::min(8, (a.row_cap + kJoinWarps - 1) / kJoinWarps);
+    const int y = a.row_cap <= 64 ? (a.row_cap + kJoinWarps - 1) / kJoinWarps : kJoinY;
     return launch_pdl(kv_attn_join_kernel, dim3(grid, y), dim3(kJoinWarps * 32), 0, s, a);
 }
 
