@@ -692,3 +692,41 @@ def test_route_strided_logits_and_pointer_tables(lib):
     assert torch.equal(ptrs, want)
     ids, w = lib.moe_route_topk(wide[:0, :E], k)
     assert ids.shape == (0, k)
+
+
+# ---- together --------------------------------------------------------------------
+
+def test_one_layer_prompt_decode_and_replay():
+    """The example's layer at small sizes: prompts of uneven length, decode, and a captured decode step whose
+    lengths, pages and positions move on the device alone."""
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "decode_layer.py")
+    spec = importlib.util.spec_from_file_location("decode_layer", path)
+    example = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(example)
+    layer = example.Layer(dim=1024, hq=8, hkv=2, d=128, experts=16, groups=4, topk=4, inter=512, requests=3,
+                          max_len=128)
+    history = [[torch.empty((0, 2, 128), dtype=torch.bfloat16, device=DEV)] * 2 for _ in range(3)]
+    # the library's bars: q8_1 activations 1e-2, bf16 matmuls 2e-3 of the result; the experts quantise twice
+    bars = {"projections": 1e-2, "attention": 5e-3, "out projection": 1e-2, "norms": 4e-3, "route": 0.0,
+            "route weights": 1e-6, "experts": 2e-2, "stream": 1e-6}
+
+    def held(s):
+        far = example.check(layer, s, history)
+        assert all(far[name] <= bars[name] for name in bars), far
+
+    g = gen(31)
+    held(layer.step(normal(g, 24, 1024), i32([17, 0, 7])))   # more than 8 tokens: the matmul's projections
+    held(layer.step(normal(g, 5, 1024), i32([1, 3, 1])))
+    stream, one = normal(g, 3, 1024), i32([1, 1, 1])
+    held(layer.step(stream, one))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        s = layer.step(stream, one)
+    for _ in range(10):  # across page boundaries
+        stream.copy_(normal(g, 3, 1024))
+        graph.replay()
+        torch.cuda.synchronize()
+        held(s)
+    assert layer.ctx.tolist() == [17 + 1 + 11, 3 + 11, 8 + 11]
