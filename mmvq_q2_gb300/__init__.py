@@ -13,7 +13,10 @@ from __future__ import annotations
 
 import collections
 import ctypes
+import importlib.machinery
+import importlib.util
 import os
+import sysconfig
 import threading
 
 import torch
@@ -393,15 +396,34 @@ def dense_gemm_bf16(x, W, out=None, stream=None):
 
 Q2K_F32 = 0
 Q2K_BF16 = 1
-_TYPES = {torch.float32: Q2K_F32, torch.bfloat16: Q2K_BF16}
 _F32, _BF16, _I32, _I64, _U8 = torch.float32, torch.bfloat16, torch.int32, torch.int64, torch.uint8
 
 # The calls below run once or more per layer and step, where a few
-# microseconds of host time count: addresses go to ctypes as plain integers,
-# the current stream is asked for as its handle, and a tensor's checks are one
-# short function.
+# microseconds of host time count.  Their arguments are read, checked and
+# passed on by a small extension module (csrc/q2k_python.c); here outputs are
+# allocated and a status becomes an exception.
+_CALLS = ("kv_page_plan", "kv_rope_store", "kv_attention_bf16", "norm_gate_residual", "moe_route_topk")
+_native = None
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 _cur_device = getattr(torch._C, "_cuda_getDevice", None)
+
+
+def _calls():
+    """The extension module, set up with the library's functions; raises when it has not been built."""
+    global _native
+    L = lib()
+    with _lock:
+        if _native is None:
+            path = os.path.join(os.path.dirname(LIB_PATH), "_q2kcall" + (sysconfig.get_config_var("EXT_SUFFIX") or ".so"))
+            if not os.path.exists(path):
+                raise RuntimeError(f"{path} is missing: build it with `python -m mmvq_q2_gb300.build`")
+            loader = importlib.machinery.ExtensionFileLoader("_q2kcall", path)
+            m = importlib.util.module_from_spec(importlib.util.spec_from_loader("_q2kcall", loader))
+            loader.exec_module(m)
+            m.setup((_F32, _BF16, _I32, _I64, _U8),
+                    tuple(ctypes.cast(getattr(L, name), ctypes.c_void_p).value for name in _CALLS))
+            _native = m
+        return _native
 
 
 def _stream_handle(stream):
@@ -412,55 +434,10 @@ def _stream_handle(stream):
     return _raw_stream(_cur_device())
 
 
-def _at(t, dtype, name):
-    """Address of a CUDA tensor of the given type."""
+def _cuda_device(t, name):
     if not t.is_cuda:
         raise ValueError(f"tensors must be on a CUDA device ({name} is not)")
-    if t.dtype is not dtype:
-        raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
-    return t.data_ptr()
-
-
-def _dense_at(t, dtype, name):
-    """The same for a tensor that has to be contiguous, or None."""
-    if t is None:
-        return None
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return _at(t, dtype, name)
-
-
-def _type(t, name):
-    try:
-        return _TYPES[t.dtype]
-    except KeyError:
-        raise TypeError(f"{name} must be fp32 or bf16, not {t.dtype}") from None
-
-
-def _heads(t, name):
-    """``[T, H, D]`` whose heads of a token lie back to back -> the stride between tokens."""
-    T, H, D = t.shape
-    s0, s1, s2 = t.stride()
-    if s2 != 1 or (H > 1 and s1 != D):
-        raise ValueError(f"{name} must be [T, H, D] with the heads of a token back to back")
-    return s0 if T > 1 or s0 > H * D else H * D
-
-
-def _row(t, dim):
-    """Stride between the rows of ``t`` (a single row has none of its own)."""
-    s = t.stride(0)
-    return s if t.shape[0] > 1 or s > dim else dim
-
-
-def _cache(k_cache, v_cache):
-    """``[n_pages, Hkv, page_size, D]`` twice, pages dense, the pages themselves at any equal stride."""
-    shape, stride = k_cache.shape, k_cache.stride()
-    n_pages, Hkv, page, D = shape
-    if v_cache.shape != shape or v_cache.stride() != stride:
-        raise ValueError("k_cache and v_cache must have one shape and one set of strides")
-    if stride[1:] != (page * D, D, 1):
-        raise ValueError("a page of the cache must be contiguous [Hkv, page_size, D]")
-    return n_pages, Hkv, page, D, max(stride[0], Hkv * page * D) if n_pages == 1 else stride[0]
+    return t.device
 
 
 PagePlan = collections.namedtuple("PagePlan", "cu_q seq_lens positions token_req slot_map free_head")
@@ -473,28 +450,16 @@ def kv_page_plan(ctx_lens, new_lens, page_size, free_pages, block_table, max_tok
     and returns ``PagePlan(cu_q [n_req+1], seq_lens [n_req], positions,
     token_req, slot_map [max_tokens], free_head [1])``.  ``out``: a
     ``PagePlan`` to write into."""
-    n = ctx_lens.numel()
-    shape = block_table.shape
-    if new_lens.numel() != n or len(shape) != 2 or shape[0] != n or block_table.stride(1) != 1:
-        raise ValueError("one ctx_len, new_len and row of block_table per request")
+    to = out
+    if out is None:  # one allocation for the six arrays
+        n = ctx_lens.numel()
+        to = torch.empty(2 * n + 3 * max_tokens + 2, dtype=_I32, device=_cuda_device(ctx_lens, "ctx_lens"))
+    st = (_native or _calls()).kv_page_plan(ctx_lens, new_lens, page_size, free_pages, free_head, block_table, max_tokens,
+                                            to, err_flag, _stream_handle(stream))
+    if st:
+        raise Q2KError("kv_page_plan", st)
     if out is None:
-        if not ctx_lens.is_cuda:
-            raise ValueError("tensors must be on a CUDA device (ctx_lens is not)")
-        # one allocation for the six arrays
-        buf = torch.empty(2 * n + 3 * max_tokens + 2, dtype=_I32, device=ctx_lens.device)
-        out = PagePlan(*buf.split_with_sizes((n + 1, n, max_tokens, max_tokens, max_tokens, 1)))
-        at = buf.data_ptr()
-        cu, pos = at, at + 8 * n + 4
-        outs = (cu, at + 4 * n + 4, pos, pos + 4 * max_tokens, pos + 8 * max_tokens)
-        head = pos + 12 * max_tokens
-    else:
-        if tuple(t.numel() for t in out) != (n + 1, n, max_tokens, max_tokens, max_tokens, 1):
-            raise ValueError("out does not fit n_req and max_tokens")
-        *outs, head = (_dense_at(t, _I32, name) for t, name in zip(out, PagePlan._fields))
-    _call("kv_page_plan", _dense_at(ctx_lens, _I32, "ctx_lens"), _dense_at(new_lens, _I32, "new_lens"), n, page_size,
-          _dense_at(free_pages, _I32, "free_pages"), free_pages.numel(), _dense_at(free_head, _I32, "free_head"),
-          _at(block_table, _I32, "block_table"), shape[1], _row(block_table, shape[1]), *outs, max_tokens, head,
-          _dense_at(err_flag, _I32, "err_flag"), _stream_handle(stream))
+        out = PagePlan._make(to.split_with_sizes((n + 1, n, max_tokens, max_tokens, max_tokens, 1)))
     return out
 
 
@@ -504,45 +469,17 @@ def kv_rope_store(q, k, v, positions, inv_freq, slot_map, k_cache, v_cache, sect
     stride allowed) by ``positions [T]`` or ``[n_axes, T]`` and store k and
     ``v`` into the pages at ``slot_map``; returns bf16 ``q_out`` (None when q
     is None).  ``sections``: rotary pairs of each axis."""
-    x_type, dtype = _type(k, "k"), k.dtype
-    T, Hkv, D = k.shape
-    n_pages, Hc, page, Dc, page_stride = _cache(k_cache, v_cache)
-    pairs = inv_freq.numel()
-    n_axes = 1 if positions.dim() == 1 else positions.shape[0]
-    if v.shape != k.shape or Hc != Hkv or Dc != D or slot_map.numel() != T or positions.numel() != n_axes * T:
-        raise ValueError("k, v, positions, slot_map and the cache do not fit one another")
-    if sections is None:
-        sections = (pairs,)
-    if len(sections) != n_axes or n_axes > 3:
-        raise ValueError("one section per axis, three at most")
-    kp, vp = _at(k, dtype, "k"), _at(v, dtype, "v")
-    qp = qo = None
-    Hq = ld_q = ld_qo = 0
     if q is None:
         if q_out is not None:
             raise ValueError("q_out without q")
-    else:
-        Tq, Hq, Dq = q.shape
-        if Tq != T or Dq != D:
-            raise ValueError("q and k do not fit one another")
-        qp, ld_q = _at(q, dtype, "q"), _heads(q, "q")
-        if q_out is None:
-            q_out = torch.empty((T, Hq, D), dtype=_BF16, device=k.device)
-            ld_qo = Hq * D
-        elif q_out.shape != q.shape:
-            raise ValueError("q_out must have q's shape")
-        else:
-            ld_qo = _heads(q_out, "q_out")
-        qo = _at(q_out, _BF16, "q_out")
-    _call("kv_rope_store", qp, ld_q, kp, _heads(k, "k"), vp, _heads(v, "v"), x_type, T, Hq, Hkv, D,
-          _dense_at(positions, _I32, "positions"), n_axes, _I32x3(*sections), _dense_at(inv_freq, _F32, "inv_freq"),
-          2 * pairs, 1 if interleaved else 0, _dense_at(slot_map, _I32, "slot_map"), qo, ld_qo,
-          _at(k_cache, _BF16, "k_cache"), _at(v_cache, _BF16, "v_cache"), n_pages, page, page_stride,
-          _dense_at(err_flag, _I32, "err_flag"), _stream_handle(stream))
+    elif q_out is None:
+        q_out = torch.empty(q.shape, dtype=_BF16, device=_cuda_device(q, "q"))
+    st = (_native or _calls()).kv_rope_store(q, k, v, positions, inv_freq, slot_map, k_cache, v_cache,
+                                             (inv_freq.numel(),) if sections is None else tuple(sections), interleaved,
+                                             q_out, err_flag, _stream_handle(stream))
+    if st:
+        raise Q2KError("kv_rope_store", st)
     return q_out
-
-
-_I32x3 = ctypes.c_int32 * 3
 
 
 def kv_attention_workspace_bytes(T, Hq, Hkv, D) -> int:
@@ -556,41 +493,20 @@ def kv_attention_bf16(q, k_cache, v_cache, block_table, cu_q, seq_lens, scale=No
     ``seq_lens [n_req]`` tokens of each request, the new ones last ->
     (out bf16 ``[T, Hq, D]``, lse fp32 ``[T, Hq]`` or None).  ``scale``
     defaults to ``D ** -0.5``; ``window`` 0 sees all earlier keys."""
-    qp = _at(q, _BF16, "q")
-    T, Hq, D = q.shape
-    n_pages, Hkv, page, Dc, page_stride = _cache(k_cache, v_cache)
-    n = seq_lens.numel()
-    rows, cols = block_table.shape
-    if Dc != D or cu_q.numel() != n + 1 or rows != n or (n and block_table.stride(1) != 1):
-        raise ValueError("q, the cache, block_table, cu_q and seq_lens do not fit one another")
-    device = q.device
+    shape, device = q.shape, _cuda_device(q, "q")
     if out is None:
-        out = torch.empty((T, Hq, D), dtype=_BF16, device=device)
-        ld_o = Hq * D
-    elif out.shape != q.shape:
-        raise ValueError("out must have q's shape")
-    else:
-        ld_o = _heads(out, "out")
-    if lse is None:
-        if want_lse:
-            lse = torch.empty((T, Hq), dtype=_F32, device=device)
-    elif lse.shape != (T, Hq):
-        raise ValueError("lse must be [T, Hq]")
+        out = torch.empty(shape, dtype=_BF16, device=device)
+    if lse is None and want_lse:
+        lse = torch.empty(shape[:2], dtype=_F32, device=device)
     if workspace is None:
-        workspace = torch.empty(lib().kv_attention_workspace_bytes(T, Hq, Hkv, D), dtype=_U8, device=device)
-    _call("kv_attention_bf16", qp, _heads(q, "q"), T, Hq, Hkv, D, _at(k_cache, _BF16, "k_cache"),
-          _at(v_cache, _BF16, "v_cache"), n_pages, page, page_stride, _at(block_table, _I32, "block_table"), cols,
-          _row(block_table, cols), _dense_at(cu_q, _I32, "cu_q"), _dense_at(seq_lens, _I32, "seq_lens"), n,
-          D ** -0.5 if scale is None else scale, window, _at(out, _BF16, "out"), ld_o, _dense_at(lse, _F32, "lse"),
-          _dense_at(workspace, _U8, "workspace"), workspace.numel(), _stream_handle(stream))
+        T, Hq, D = shape
+        workspace = torch.empty((_lib or lib()).kv_attention_workspace_bytes(T, Hq, k_cache.shape[1], D), dtype=_U8,
+                                device=device)
+    st = (_native or _calls()).kv_attention_bf16(q, k_cache, v_cache, block_table, cu_q, seq_lens, scale, window, out, lse,
+                                                 workspace, _stream_handle(stream))
+    if st:
+        raise Q2KError("kv_attention_bf16", st)
     return out, lse
-
-
-def _rows_at(t, dtype, T, dim, name):
-    """Address and row stride of ``[T, dim]`` with dense rows."""
-    if t.shape != (T, dim) or t.stride(1) != 1:
-        raise ValueError(f"{name} must be [T, dim] with dense rows")
-    return _at(t, dtype, name), _row(t, dim)
 
 
 def norm_gate_residual(residual, pre_w, eps, y=None, post_w=None, gate=None, alpha=1.0, residual_out=None, out=None,
@@ -601,36 +517,17 @@ def norm_gate_residual(residual, pre_w, eps, y=None, post_w=None, gate=None, alp
     and ``y`` ``[T, dim]`` fp32 or bf16 (row stride allowed), ``gate``
     ``[dim]`` or ``[T, dim]`` of y's type, weights fp32 ``[dim]``; without y,
     h is the residual.  ``residual_out`` may be ``residual``."""
-    T, dim = residual.shape
-    s_type, s_dtype = _type(residual, "residual"), residual.dtype
-    res, ld_res = _rows_at(residual, s_dtype, T, dim, "residual")
-    device = residual.device
+    shape, device = residual.shape, _cuda_device(residual, "residual")
     if residual_out is None:
-        residual_out = torch.empty((T, dim), dtype=s_dtype, device=device)
+        residual_out = torch.empty(shape, dtype=residual.dtype, device=device)
     if out is None:
-        out = torch.empty((T, dim), dtype=_BF16, device=device)
-    ro, ld_ro = _rows_at(residual_out, s_dtype, T, dim, "residual_out")
-    n, ld_n = _rows_at(out, _BF16, T, dim, "out")
-    if pre_w.numel() != dim or (post_w is not None and post_w.numel() != dim):
-        raise ValueError("a weight must have dim values")
-    y_type, yp, ld_y, gp, ld_gate = Q2K_F32, None, 0, None, 0
-    if y is not None:
-        y_type = _type(y, "y")
-        yp, ld_y = _rows_at(y, y.dtype, T, dim, "y")
-    if gate is not None:
-        if gate.shape[-1] != dim or gate.stride(-1) != 1 or gate.numel() not in (dim, T * dim):
-            raise ValueError("gate must be [dim] or [T, dim] with dense rows")
-        gp = _at(gate, residual.dtype if y is None else y.dtype, "gate")
-        if gate.numel() != dim:
-            ld_gate = gate.stride(0)
-    if out_q8 is None:
-        if want_q8:
-            out_q8 = torch.empty((T, q8_1_row_bytes(dim)), dtype=_U8, device=device)
-    elif out_q8.numel() != T * q8_1_row_bytes(dim):
-        raise ValueError("out_q8 must hold T q8_1 rows")
-    _call("norm_gate_residual", yp, y_type, ld_y, _dense_at(post_w, _F32, "post_w"), gp, ld_gate, res, s_type, ld_res,
-          alpha, _dense_at(pre_w, _F32, "pre_w"), eps, T, dim, ro, ld_ro, n, ld_n, _dense_at(out_q8, _U8, "out_q8"),
-          _stream_handle(stream))
+        out = torch.empty(shape, dtype=_BF16, device=device)
+    if out_q8 is None and want_q8:
+        out_q8 = torch.empty((shape[0], q8_1_row_bytes(shape[1])), dtype=_U8, device=device)
+    st = (_native or _calls()).norm_gate_residual(residual, pre_w, eps, y, post_w, gate, alpha, residual_out, out, out_q8,
+                                                  _stream_handle(stream))
+    if st:
+        raise Q2KError("norm_gate_residual", st)
     return (residual_out, out) if out_q8 is None else (residual_out, out, out_q8)
 
 
@@ -646,23 +543,17 @@ def moe_route_topk(logits, topk, bias=None, score="softmax", n_group=1, topk_gro
     kind = ROUTE_SCORES.get(score)
     if kind is None:
         raise ValueError(f"score must be one of {sorted(ROUTE_SCORES)}")
-    m, E = logits.shape
-    x, ld = _rows_at(logits, logits.dtype, m, E, "logits")
-    l_type = _type(logits, "logits")
-    if (bias is not None and bias.numel() != E) or (expert_ptrs is not None and expert_ptrs.numel() != 3 * E):
-        raise ValueError("bias must be [E], expert_ptrs [3, E]")
-    device = logits.device
+    device, m = _cuda_device(logits, "logits"), logits.shape[0]
     if ids is None:
         ids = torch.empty((m, topk), dtype=_I32, device=device)
     if weights is None:
         weights = torch.empty((m, topk), dtype=_F32, device=device)
     if ptrs is None and expert_ptrs is not None:
         ptrs = torch.empty((m, 3 * topk), dtype=_I64, device=device)
-    if ids.numel() != m * topk or weights.numel() != m * topk or (ptrs is not None and ptrs.numel() != 3 * m * topk):
-        raise ValueError("ids, weights and ptrs must hold topk (3 * topk) entries per token")
-    _call("moe_route_topk", x, l_type, m, E, ld, _dense_at(bias, _F32, "bias"), kind, n_group, topk_group, topk,
-          1 if renorm else 0, scale, _dense_at(ids, _I32, "ids"), _dense_at(weights, _F32, "weights"),
-          _dense_at(expert_ptrs, _I64, "expert_ptrs"), _dense_at(ptrs, _I64, "ptrs"), _stream_handle(stream))
+    st = (_native or _calls()).moe_route_topk(logits, topk, bias, kind, n_group, topk_group, renorm, scale, ids, weights,
+                                              expert_ptrs, ptrs, _stream_handle(stream))
+    if st:
+        raise Q2KError("moe_route_topk", st)
     return (ids, weights) if ptrs is None else (ids, weights, ptrs)
 
 

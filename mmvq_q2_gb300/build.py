@@ -1,8 +1,9 @@
-"""Build libq2k.so in-tree with nvcc for sm_103a (no cmake, no torch).
+"""Build libq2k.so in-tree with nvcc for sm_103a (no cmake, no torch), and
+the binding's native half with the host's C compiler and Python's headers.
 
 Usage: ``python -m mmvq_q2_gb300.build`` or ``build()`` from Python.  The
 translation units compile in parallel; the shared library lands in
-``mmvq_q2_gb300/_lib/libq2k.so``.
+``mmvq_q2_gb300/_lib/libq2k.so``, the extension module beside it.
 """
 from __future__ import annotations
 
@@ -11,6 +12,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
@@ -18,6 +20,8 @@ OUT = os.path.join(HERE, "_lib")
 LIB = os.path.join(OUT, "libq2k.so")
 SOURCES = ["q2k_api.cu", "q2k_mv.cu", "q2k_m1.cu", "q2k_mmq.cu", "q2k_mt.cu", "q2k_small.cu", "q2k_gemm.cu", "q2k_umma.cu", "q3k_mv.cu", "q3k_mt.cu",
            "kv_page.cu", "kv_attn.cu", "layer_ops.cu"]
+CALLS_SOURCE = "q2k_python.c"
+CALLS = os.path.join(OUT, "_q2kcall" + (sysconfig.get_config_var("EXT_SUFFIX") or ".so"))
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -34,9 +38,9 @@ def _flags(extra=()):
 
 
 def _up_to_date() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(CALLS):
         return False
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(CALLS))
     deps = [os.path.join(CSRC, f) for f in os.listdir(CSRC)]
     deps.append(os.path.join(os.path.dirname(HERE), "include", "q2k.h"))
     return all(os.path.getmtime(d) <= t for d in deps)
@@ -56,8 +60,22 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
             raise RuntimeError(f"nvcc failed on {src}:\n{r.stdout}\n{r.stderr}")
         return obj, r.stderr
 
-    with cf.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    def compile_calls():
+        tmp = CALLS + f".{os.getpid()}.tmp"
+        host = os.environ.get("CC") or shutil.which("gcc") or shutil.which("cc")
+        if host is None:
+            raise RuntimeError("no host C compiler found")
+        cmd = [host, "-O2", "-std=c11", "-Wall", "-shared", "-fPIC", "-I", sysconfig.get_paths()["include"],
+               os.path.join(CSRC, CALLS_SOURCE), "-o", tmp, "-lm"]
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"{host} failed on {CALLS_SOURCE}:\n{r.stdout}\n{r.stderr}")
+        os.replace(tmp, CALLS)
+
+    with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        calls = ex.submit(compile_calls)
         results = list(ex.map(compile_one, SOURCES))
+        calls.result()
     if verbose:
         for obj, err in results:
             if err.strip():
