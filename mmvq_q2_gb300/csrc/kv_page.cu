@@ -191,7 +191,7 @@ __device__ __forceinline__ void rope_angles(const RopeArgs& a, int64_t t0, float
 {
     const int tid = (int)(threadIdx.y * blockDim.x + threadIdx.x), nt = (int)(blockDim.x * blockDim.y);
     for (int i = tid; i < a.tokens * a.half; i += nt) {
-        const int t = i / a.half, p = i - t * a.half;
+        const int t = a.tokens == 1 ? 0 : i / a.half, p = i - t * a.half;
         if (t0 + t >= a.T)
             break;
         const int axis = p < a.sec0 ? 0 : p < a.sec1 ? 1 : 2;
@@ -270,7 +270,7 @@ __device__ __forceinline__ void store8(uint16_t* p, const float (&v)[8])
 // 16 values a thread: threadIdx.x is the part of the head (D / 16 of them),
 // threadIdx.y the head of one of the block's tokens.
 template <typename T>
-__global__ void __launch_bounds__(1024) kv_rope_vec_kernel(const RopeArgs a)
+__global__ void __launch_bounds__(512, 2) kv_rope_vec_kernel(const RopeArgs a)
 {
     extern __shared__ float2 cs[];  // [tokens][half] cosine, sine
     pdl_launch_dependents();
@@ -281,7 +281,7 @@ __global__ void __launch_bounds__(1024) kv_rope_vec_kernel(const RopeArgs a)
     const int rot_parts = a.half / 8;
     bool ready = false;
     for (int y = (int)threadIdx.y; y < a.tokens * heads || !ready; y += (int)blockDim.y) {
-        const int tl = y / heads, row = y - tl * heads;
+        const int tl = a.tokens == 1 ? 0 : y / heads, row = y - tl * heads;
         const int64_t t = t0 + tl;
         const bool live = y < a.tokens * heads && t < a.T;
         const T* src = nullptr;
@@ -438,7 +438,7 @@ cudaError_t launch_kv_rope_store(const RopeStore& p, cudaStream_t s)
         const int parts = a.D / 16;
         // whole tokens to about 256 threads; a token of more heads takes up to 1024 and then loops
         a.tokens = (int)std::max<int64_t>(1, std::min<int64_t>(256 / (parts * heads), p.T));
-        const int rows = std::min(a.tokens * heads, 1024 / parts);
+        const int rows = std::min(a.tokens * heads, 512 / parts);
         const size_t smem = (size_t)a.tokens * a.half * sizeof(float2);
         const unsigned grid = (unsigned)((p.T + a.tokens - 1) / a.tokens);
         return launch_pdl(p.x_bf16 ? kv_rope_vec_kernel<uint16_t> : kv_rope_vec_kernel<float>, dim3(grid),
