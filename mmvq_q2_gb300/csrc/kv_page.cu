@@ -267,6 +267,29 @@ __device__ __forceinline__ void store8(uint16_t* p, const float (&v)[8])
     *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+// The 8 pairs of a rotated part: (u, w) value by value, or side by side.
+__device__ __forceinline__ void turn16(const RopeArgs& a, const float2* p, float (&u)[8], float (&w)[8])
+{
+    if (!a.interleaved) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float x = u[i], y = w[i];
+            u[i] = x * p[i].x - y * p[i].y;
+            w[i] = y * p[i].x + x * p[i].y;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float x = u[2 * i], y = u[2 * i + 1];
+            u[2 * i] = x * p[i].x - y * p[i].y;
+            u[2 * i + 1] = y * p[i].x + x * p[i].y;
+            const float z = w[2 * i], z2 = w[2 * i + 1];
+            w[2 * i] = z * p[4 + i].x - z2 * p[4 + i].y;
+            w[2 * i + 1] = z2 * p[4 + i].x + z * p[4 + i].y;
+        }
+    }
+}
+
 // 16 values a thread: threadIdx.x is the part of the head (D / 16 of them),
 // threadIdx.y the head of one of the block's tokens.
 template <typename T>
@@ -305,29 +328,59 @@ __global__ void __launch_bounds__(512, 2) kv_rope_vec_kernel(const RopeArgs a)
         }
         if (!live || !dst)
             continue;
-        if (turn) {
-            const float2* p = cs + tl * a.half + part * 8;
-            if (!a.interleaved) {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float x = u[i], y2 = w[i];
-                    u[i] = x * p[i].x - y2 * p[i].y;
-                    w[i] = y2 * p[i].x + x * p[i].y;
-                }
-            } else {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float x = u[2 * i], y2 = u[2 * i + 1];
-                    u[2 * i] = x * p[i].x - y2 * p[i].y;
-                    u[2 * i + 1] = y2 * p[i].x + x * p[i].y;
-                    const float z = w[2 * i], z2 = w[2 * i + 1];
-                    w[2 * i] = z * p[4 + i].x - z2 * p[4 + i].y;
-                    w[2 * i + 1] = z2 * p[4 + i].x + z * p[4 + i].y;
-                }
-            }
-        }
+        if (turn)
+            turn16(a, cs + tl * a.half + part * 8, u, w);
         store8(dst + o1, u);
         store8(dst + o2, w);
+    }
+}
+
+// The same for many tokens where a token fills a block: a thread keeps its
+// part of its head through kRopeGroup tokens, whose angles are worked out at
+// once (one token a block, the block waited for its sines longer than for
+// its values), with the next token's values on their way.
+constexpr int kRopeGroup = 4;
+
+template <typename T>
+__global__ void __launch_bounds__(512, 2) kv_rope_group_kernel(const RopeArgs a)
+{
+    extern __shared__ float2 cs[];  // [kRopeGroup][half] cosine, sine
+    pdl_launch_dependents();
+    pdl_wait();
+    const int64_t t0 = (int64_t)blockIdx.x * kRopeGroup;
+    const int n = (int)min((int64_t)kRopeGroup, a.T - t0);
+    const int part = (int)threadIdx.x, row = (int)threadIdx.y;
+    const bool turn = row < a.Hq + a.Hkv && part < a.half / 8;
+    const int o1 = turn && !a.interleaved ? part * 8 : part * 16;
+    const int o2 = turn && !a.interleaved ? a.half + part * 8 : part * 16 + 8;
+    float u[8], w[8], u2[8], w2[8];
+    uint16_t *dst = nullptr, *dst2 = nullptr;
+    auto fetch = [&](int tl, float (&x)[8], float (&y)[8], uint16_t*& to) {
+        const T* src;
+        rope_row<T>(a, t0 + tl, row, src, to);
+        if (to) {
+            load8(src + o1, x);
+            load8(src + o2, y);
+        }
+    };
+    fetch(0, u, w, dst);
+    rope_angles(a, t0, cs);
+    __syncthreads();
+    for (int tl = 0; tl < n; ++tl) {
+        if (tl + 1 < n)
+            fetch(tl + 1, u2, w2, dst2);
+        if (dst) {
+            if (turn)
+                turn16(a, cs + tl * a.half + part * 8, u, w);
+            store8(dst + o1, u);
+            store8(dst + o2, w);
+        }
+        dst = dst2;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            u[i] = u2[i];
+            w[i] = w2[i];
+        }
     }
 }
 
@@ -436,6 +489,17 @@ cudaError_t launch_kv_rope_store(const RopeStore& p, cudaStream_t s)
                      (!a.Hq || (on16(a.q) && on16(a.q_out) && a.ld_q % in8 == 0 && a.ld_qo % 8 == 0));
     if (vec) {
         const int parts = a.D / 16;
+        DeviceInfo di;
+        cudaError_t e = device_info(&di);
+        if (e != cudaSuccess)
+            return e;
+        // groups where they are enough for two waves of two blocks an SM
+        if (parts * heads > 128 && parts * heads <= 512 && p.T >= (int64_t)4 * kRopeGroup * di.sm_count) {
+            a.tokens = kRopeGroup;
+            return launch_pdl(p.x_bf16 ? kv_rope_group_kernel<uint16_t> : kv_rope_group_kernel<float>,
+                              dim3((unsigned)((p.T + kRopeGroup - 1) / kRopeGroup)), dim3(parts, heads),
+                              (size_t)kRopeGroup * a.half * sizeof(float2), s, a);
+        }
         // whole tokens to about 256 threads; a token of more heads takes up to 1024 and then loops
         a.tokens = (int)std::max<int64_t>(1, std::min<int64_t>(256 / (parts * heads), p.T));
         const int rows = std::min(a.tokens * heads, 512 / parts);

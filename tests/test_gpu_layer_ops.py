@@ -169,6 +169,10 @@ ROPES = [
     (4, 2, 2, 16, 0, (0,), False, torch.float32, 16),
     (3, 2, 1, 512, 512, (256,), False, torch.float32, 1024),
     (3, 1, 1, 1, 0, (0,), False, torch.float32, 16),
+    # many tokens, a token to a block
+    (2501, 12, 4, 128, 128, (16, 24, 24), False, torch.float32, 64),
+    (2434, 12, 4, 128, 64, (32,), True, torch.bfloat16, 16),
+    (9999, 4, 2, 96, 96, (48,), False, torch.bfloat16, 16),
 ]
 
 
