@@ -788,12 +788,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                         break;
                     ks.skip(2, a.nst);
                 }
-                // Two row tiles: a stream takes a turn for its O += P V and the
-                // first MMAs of its next S.  Without turns the streams' products
-                // interleave and end together, both softmaxes then run at once
-                // and the tensor cores wait; with the whole of S in the turn
-                // they wait for its hand-over (8192 new tokens over 4096:
-                // 972 us without, 930 us with all of S, 883 us with two MMAs).
+                // Two row tiles, D above 64: a stream takes a turn for its O += P V
+                // and the first MMAs of its next S.  Without turns the streams'
+                // products interleave and end together, both softmaxes then run
+                // at once and the tensor cores wait; with the whole of S in the
+                // turn they wait for its hand-over (8192 new tokens over 4096:
+                // 906 us without, 836 us with none to three MMAs of S, more with
+                // all).  At D <= 64 the products are half as long and the
+                // softmaxes bind: 697 us without turns, 728 us with them.
                 bool mine = false;
                 auto take_turn = [&]() {
                     bool got = true;
@@ -875,7 +877,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (!(ok = warp_wait(sh.p_ready[s], p_phase)))
                             break;
                         p_phase ^= 1u;
-                        if (two) {
+                        if (two && DB == 2) {
                             // nothing is waited for during a turn: the next K tile
                             // may need a stage that the other stream has yet to free
                             Ring ns = vs;
