@@ -550,7 +550,9 @@ int q2k_last_cuda_error(void);
  * device's library error word into *host_out (0 = none; bit 0 = a bounded
  * wait in a kernel gave up and that kernel returned early, outputs
  * incomplete; bit 1 = a Q3_K table entry off a 4-byte boundary was
- * skipped) and clears it when clear != 0. */
+ * skipped, or an attention call met a block table entry that names no page;
+ * bit 2 = a kernel's shared memory was not placed as it needs, and it did
+ * nothing) and clears it when clear != 0. */
 int q2k_device_error(int32_t* host_out, int clear);
 
 #ifdef __cplusplus

@@ -52,10 +52,12 @@ __device__ __forceinline__ void load8(const void* p, int64_t i, int bf16, float 
     }
 }
 
+// (One instruction for two; a conversion alone goes through a slower unit.)
 __device__ __forceinline__ uint32_t bf16_pair(float lo, float hi)
 {
-    return (uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(lo)) |
-           ((uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(hi)) << 16);
+    uint32_t d;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+    return d;
 }
 
 __device__ __forceinline__ void store8(void* p, int64_t i, int bf16, const float (&v)[8])
@@ -130,9 +132,10 @@ struct Raw8 {
 // block takes rows blockIdx.x, + gridDim.x, ...: where it has more than one,
 // the weights wait in shared memory (read again for every row they were 32 of
 // 72 KB of a row's traffic from L2), and the next row is on its way while
-// this one is summed.  Two runs a thread where there are rows enough: half
-// the warps meet at a barrier, and more blocks share an SM to work meanwhile
-// (8192 rows of 4096, bf16: 62.6 us with one run, DRAM floor 49.4).
+// this one is summed.  Where two runs a thread pay (launch_norm_vec), half the
+// warps meet at a barrier, and more blocks share an SM to work meanwhile.
+// 8192 rows of 4096, all bf16, a gate per token: 60 us, 5.6 TB/s; all fp32:
+// 92 us, 6.5 TB/s.
 constexpr int kNormVecDim = 8 * 1024;
 
 template <int NR, bool YB, bool SB>
@@ -581,9 +584,13 @@ cudaError_t launch_norm_runs(const NormArgs& a, const DeviceInfo& di, cudaStream
 template <bool YB, bool SB>
 cudaError_t launch_norm_vec(const NormArgs& a, const DeviceInfo& di, cudaStream_t s)
 {
-    // a row an SM or less: latency, so as many threads as the row has runs
-    if (a.dim >= 512 && a.T > di.sm_count)
-        return launch_norm_runs<2, YB, SB>(a, di, s);
+    // Two runs a thread: 60 us against 68 (8192 rows of 4096, all bf16) and 43
+    // against 57 (of 2880).  With fp32 rows a run is twice the bytes and two
+    // of them spill (108 us against 92), and few rows want many threads each
+    // (300 rows of 4096: 5.0 us against 4.0).
+    if constexpr (YB && SB)
+        if (a.dim >= 2048 && a.dim <= 4096 && a.T > 4 * di.sm_count)
+            return launch_norm_runs<2, YB, SB>(a, di, s);
     return launch_norm_runs<1, YB, SB>(a, di, s);
 }
 

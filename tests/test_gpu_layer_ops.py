@@ -521,6 +521,13 @@ NORMS = [
     (300, 1024, "bf16", "bf16", True, "row", 0.1),
     (2, 4096, None, "bf16", False, "none", 1.0),
     (2, 77, None, "f32", False, "none", 1.0),
+    # more rows than blocks
+    (700, 2880, "bf16", "bf16", True, "token", 0.3),
+    (1300, 4096, "bf16", "bf16", True, "row", 1.0),
+    (900, 4096, None, "bf16", False, "none", 1.0),
+    (1500, 2048, "f32", "f32", False, "token", 1.0),
+    (5000, 160, "f32", "bf16", True, "row", 1.0),
+    (400, 8192, "bf16", "f32", True, "row", 1.0),
 ]
 TYPES = {"f32": torch.float32, "bf16": torch.bfloat16}
 
