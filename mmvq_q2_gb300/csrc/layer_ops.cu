@@ -316,6 +316,8 @@ struct RouteArgs {
     int64_t* ptrs_out;
     int64_t m, ld;
     int E, sigmoid, n_group, topk_group, topk, renorm;
+    int share;          // log2 of the lanes that a group gets
+    uint32_t per_size;  // 2^20 / (experts of a group), rounded up: e * per_size >> 20 is e / size for e and size to 1024
     float scale;
 };
 
@@ -425,7 +427,7 @@ __global__ void __launch_bounds__(128) moe_route_kernel(const RouteArgs a)
 #pragma unroll
         for (int j = 0; j < NE; ++j) {
             s[j] = expf(s[j] - top);
-            const float h = __fadd_rn(__fadd_rn(s[j], 3072.f), -3072.f);
+            const float h = __fadd_rn(__fadd_rn(s[j], 0x1.8p11f), -0x1.8p11f);
             hi = __fadd_rn(hi, h);
             lo = __fadd_rn(lo, __fadd_rn(s[j], -h));
         }
@@ -489,43 +491,46 @@ __global__ void __launch_bounds__(128) moe_route_kernel(const RouteArgs a)
         key[j] = e < a.E ? order_key(a.bias ? __fadd_rn(s[j], a.bias[e]) : s[j]) : 0u;
     }
     if (a.n_group > 1) {
-        const int size = a.E / a.n_group;
-        uint32_t gkey = 0;  // lane g: group g's score
-        for (int g = 0; g < a.n_group; ++g) {
-            uint32_t k1 = 0, k2 = 0;
+        // A group's best two, by 2^share lanes of its own from shared memory.
+        // (By the whole warp, group after group: 16384 tokens of 256 experts in
+        // 8 groups 27.4 us against 20.1, of 160 in 8 32.1 against 20.1, one
+        // token 6.1 against 4.6.)
+        __shared__ uint32_t sh_key[4][NE * 33];
+        uint32_t* k = sh_key[threadIdx.x >> 5];
 #pragma unroll
-            for (int j = 0; j < NE; ++j) {
-                const int e = j * 32 + lane - g * size;
-                if (e >= 0 && e < size) {
-                    const uint32_t k = key[j];
-                    k2 = max(k2, min(k1, k));
-                    k1 = max(k1, k);
+        for (int j = 0; j < NE; ++j)
+            k[j * 33 + lane] = key[j];
+        __syncwarp();
+        const int size = a.E / a.n_group, g = lane >> a.share;
+        uint32_t gkey = 0;  // group g's score
+        {
+            uint32_t k1 = 0, k2 = 0;
+            if (g < a.n_group)
+                for (int e = g * size + lane - (g << a.share); e < (g + 1) * size; e += 1 << a.share) {
+                    const uint32_t x = k[e + (e >> 5)];
+                    k2 = max(k2, min(k1, x));
+                    k1 = max(k1, x);
                 }
+            for (int o = 1; o < 1 << a.share; o <<= 1) {
+                const uint32_t b1 = __shfl_xor_sync(0xffffffffu, k1, o), b2 = __shfl_xor_sync(0xffffffffu, k2, o);
+                k2 = max(min(k1, b1), max(k2, b2));
+                k1 = max(k1, b1);
             }
-            const uint32_t b1 = __reduce_max_sync(0xffffffffu, k1);
-            float score = key_value(b1);
-            if (size > 1) {
-                // the first lane that holds the largest gives its next one
-                const uint32_t has = __ballot_sync(0xffffffffu, k1 == b1);
-                if (lane == __ffs(has) - 1)
-                    k1 = k2;
-                score += key_value(__reduce_max_sync(0xffffffffu, k1));
-            }
-            if (lane == g)
-                gkey = order_key(score);
+            if (g < a.n_group)
+                gkey = order_key(size > 1 ? key_value(k1) + key_value(k2) : key_value(k1));
         }
         uint32_t kept = 0;
         for (int i = 0; i < a.topk_group; ++i) {
             const uint32_t best = __reduce_max_sync(0xffffffffu, gkey);
-            const int g = __ffs(__ballot_sync(0xffffffffu, gkey == best)) - 1;
-            kept |= 1u << g;
-            if (lane == g)
+            const int first = (__ffs(__ballot_sync(0xffffffffu, gkey == best)) - 1) >> a.share;
+            kept |= 1u << first;
+            if (g == first)
                 gkey = 0;
         }
 #pragma unroll
         for (int j = 0; j < NE; ++j) {
-            const int e = j * 32 + lane;
-            if (e < a.E && !(kept >> (e / size) & 1u))
+            const uint32_t e = (uint32_t)(j * 32 + lane);
+            if (e < (uint32_t)a.E && !(kept >> (e * a.per_size >> 20) & 1u))  // e / size
                 key[j] = 0;
         }
     }
@@ -658,6 +663,10 @@ cudaError_t launch_moe_route(const RouteProblem& p, cudaStream_t s)
     a.topk = p.topk;
     a.renorm = p.renorm;
     a.scale = p.scale;
+    for (int lanes = 32; lanes >= 2 * a.n_group; lanes /= 2)
+        ++a.share;
+    const uint32_t size = (uint32_t)(a.E / a.n_group);
+    a.per_size = ((1u << 20) + size - 1) / size;
     const int ne = (a.E + 31) / 32;
     auto pick = [&](auto bf16) {
         constexpr bool B = decltype(bf16)::value;
