@@ -480,7 +480,8 @@ size_t kv_attention_workspace_bytes(int64_t T, int64_t Hq, int64_t Hkv, int64_t 
  * Hkv)) new tokens of a request.
  * D a multiple of 16, 16..128; Hq / Hkv 1..128; caches 16-byte aligned.
  * workspace: kv_attention_workspace_bytes(T, Hq, Hkv, D) bytes, 32-byte
- * aligned.  Results repeat bit for bit.  Two launches. */
+ * aligned.  Results repeat bit for bit.  Two launches.
+ * Q2K_ERR_UNSUPPORTED when the CUDA driver offers no tensor-map encoder. */
 int kv_attention_bf16(const uint16_t* q, int64_t ld_q, int64_t T, int64_t Hq, int64_t Hkv, int64_t D,
                       const uint16_t* k_cache, const uint16_t* v_cache, int64_t n_pages, int64_t page_size,
                       int64_t page_stride, const int32_t* block_table, int64_t max_pages, int64_t ld_table,

@@ -402,7 +402,8 @@ _F32, _BF16, _I32, _I64, _U8 = torch.float32, torch.bfloat16, torch.int32, torch
 # microseconds of host time count.  Their arguments are read, checked and
 # passed on by a small extension module (csrc/q2k_python.c); here outputs are
 # allocated and a status becomes an exception.
-_CALLS = ("kv_page_plan", "kv_rope_store", "kv_attention_bf16", "norm_gate_residual", "moe_route_topk")
+_CALLS = ("kv_page_plan", "kv_rope_store", "kv_attention_bf16", "norm_gate_residual", "moe_route_topk",
+          "kv_attention_workspace_bytes")
 _native = None
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 _cur_device = getattr(torch._C, "_cuda_getDevice", None)
@@ -440,6 +441,15 @@ def _cuda_device(t, name):
     return t.device
 
 
+def _empty(shape, dtype, device, stream):
+    # A tensor belongs to the stream it is allocated on: a workspace given back
+    # at the call's end is then not handed out while the call still runs.
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 PagePlan = collections.namedtuple("PagePlan", "cu_q seq_lens positions token_req slot_map free_head")
 
 
@@ -453,7 +463,7 @@ def kv_page_plan(ctx_lens, new_lens, page_size, free_pages, block_table, max_tok
     to = out
     if out is None:  # one allocation for the six arrays
         n = ctx_lens.numel()
-        to = torch.empty(2 * n + 3 * max_tokens + 2, dtype=_I32, device=_cuda_device(ctx_lens, "ctx_lens"))
+        to = _empty(2 * n + 3 * max_tokens + 2, _I32, _cuda_device(ctx_lens, "ctx_lens"), stream)
     st = (_native or _calls()).kv_page_plan(ctx_lens, new_lens, page_size, free_pages, free_head, block_table, max_tokens,
                                             to, err_flag, _stream_handle(stream))
     if st:
@@ -473,7 +483,7 @@ def kv_rope_store(q, k, v, positions, inv_freq, slot_map, k_cache, v_cache, sect
         if q_out is not None:
             raise ValueError("q_out without q")
     elif q_out is None:
-        q_out = torch.empty(q.shape, dtype=_BF16, device=_cuda_device(q, "q"))
+        q_out = _empty(q.shape, _BF16, _cuda_device(q, "q"), stream)
     st = (_native or _calls()).kv_rope_store(q, k, v, positions, inv_freq, slot_map, k_cache, v_cache,
                                              (inv_freq.numel(),) if sections is None else tuple(sections), interleaved,
                                              q_out, err_flag, _stream_handle(stream))
@@ -495,13 +505,13 @@ def kv_attention_bf16(q, k_cache, v_cache, block_table, cu_q, seq_lens, scale=No
     defaults to ``D ** -0.5``; ``window`` 0 sees all earlier keys."""
     shape, device = q.shape, _cuda_device(q, "q")
     if out is None:
-        out = torch.empty(shape, dtype=_BF16, device=device)
+        out = _empty(shape, _BF16, device, stream)
     if lse is None and want_lse:
-        lse = torch.empty(shape[:2], dtype=_F32, device=device)
+        lse = _empty(shape[:2], _F32, device, stream)
     if workspace is None:
         T, Hq, D = shape
-        workspace = torch.empty((_lib or lib()).kv_attention_workspace_bytes(T, Hq, k_cache.shape[1], D), dtype=_U8,
-                                device=device)
+        need = (_native or _calls()).kv_attention_workspace_bytes(T, Hq, k_cache.shape[1], D)
+        workspace = _empty(need, _U8, device, stream)
     st = (_native or _calls()).kv_attention_bf16(q, k_cache, v_cache, block_table, cu_q, seq_lens, scale, window, out, lse,
                                                  workspace, _stream_handle(stream))
     if st:
@@ -519,11 +529,11 @@ def norm_gate_residual(residual, pre_w, eps, y=None, post_w=None, gate=None, alp
     h is the residual.  ``residual_out`` may be ``residual``."""
     shape, device = residual.shape, _cuda_device(residual, "residual")
     if residual_out is None:
-        residual_out = torch.empty(shape, dtype=residual.dtype, device=device)
+        residual_out = _empty(shape, residual.dtype, device, stream)
     if out is None:
-        out = torch.empty(shape, dtype=_BF16, device=device)
+        out = _empty(shape, _BF16, device, stream)
     if out_q8 is None and want_q8:
-        out_q8 = torch.empty((shape[0], q8_1_row_bytes(shape[1])), dtype=_U8, device=device)
+        out_q8 = _empty((shape[0], q8_1_row_bytes(shape[1])), _U8, device, stream)
     st = (_native or _calls()).norm_gate_residual(residual, pre_w, eps, y, post_w, gate, alpha, residual_out, out, out_q8,
                                                   _stream_handle(stream))
     if st:
@@ -545,11 +555,11 @@ def moe_route_topk(logits, topk, bias=None, score="softmax", n_group=1, topk_gro
         raise ValueError(f"score must be one of {sorted(ROUTE_SCORES)}")
     device, m = _cuda_device(logits, "logits"), logits.shape[0]
     if ids is None:
-        ids = torch.empty((m, topk), dtype=_I32, device=device)
+        ids = _empty((m, topk), _I32, device, stream)
     if weights is None:
-        weights = torch.empty((m, topk), dtype=_F32, device=device)
+        weights = _empty((m, topk), _F32, device, stream)
     if ptrs is None and expert_ptrs is not None:
-        ptrs = torch.empty((m, 3 * topk), dtype=_I64, device=device)
+        ptrs = _empty((m, 3 * topk), _I64, device, stream)
     st = (_native or _calls()).moe_route_topk(logits, topk, bias, kind, n_group, topk_group, renorm, scale, ids, weights,
                                               expert_ptrs, ptrs, _stream_handle(stream))
     if st:

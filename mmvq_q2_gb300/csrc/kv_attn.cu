@@ -744,12 +744,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         } else {
             // ---- MMAs ----
-            // Warp 1 issues for stream 0, warp 2 for stream 1: the issue from
-            // one warp (an MMA takes it 30 to 50 cycles, a wait or commit
-            // about as much) came to 2650 cycles per key tile of two row
-            // tiles, more than the 2048 that the tensor cores need.  The
-            // whole warp runs the loop and one elected lane issues, so that
-            // descriptors stay in warp-uniform registers.
+            // Warp 1 issues for stream 0, warp 2 for stream 1: one warp keeps
+            // few MMAs in flight (87 cycles or more for one of 128 x 128 x 16,
+            // 70 to 80 from two warps; 64 would be the tensor cores' rate).
+            // The whole warp runs the loop and one elected lane issues, so
+            // that descriptors stay in warp-uniform registers.
             const int s = warp - 1;
             const uint32_t idesc_s = instr_desc(kRows), idesc_o = instr_desc(a.D) | kTransposeB;
             const uint32_t t_s = uniform(tmem + s * 256), t_o = t_s + 128;
@@ -1355,6 +1354,8 @@ cudaError_t launch_tc(AttnArgs& a, const CUtensorMap& tq, const CUtensorMap& tk,
 }
 
 }  // namespace
+
+bool attn_supported() { return encoder() != nullptr; }
 
 size_t kv_attention_workspace(int64_t T, int64_t Hq, int64_t Hkv, int64_t D) { return layout_of(T, Hq, Hkv, D).bytes; }
 

@@ -803,6 +803,8 @@ int kv_attention_bf16(const uint16_t* q, int64_t ld_q, int64_t T, int64_t Hq, in
         return st;
     if (T == 0 || n_req == 0)
         return Q2K_OK;
+    if (!attn_supported())
+        return Q2K_ERR_UNSUPPORTED;  // no tensor-map encoder in this driver
     AttnProblem p{};
     p.q = q;
     p.ld_q = ld_q;

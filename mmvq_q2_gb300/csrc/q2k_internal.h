@@ -202,6 +202,7 @@ struct AttnProblem {
     float* lse;
     void* workspace;
 };
+bool attn_supported();  // the driver has a tensor-map encoder
 size_t kv_attention_workspace(int64_t T, int64_t Hq, int64_t Hkv, int64_t D);
 cudaError_t launch_kv_attention(const AttnProblem& p, cudaStream_t s);
 

@@ -28,6 +28,7 @@ static int (*f_rope)(const void*, int64_t, const void*, int64_t, const void*, in
 static int (*f_attn)(const uint16_t*, int64_t, int64_t, int64_t, int64_t, int64_t, const uint16_t*, const uint16_t*,
                      int64_t, int64_t, int64_t, const int32_t*, int64_t, int64_t, const int32_t*, const int32_t*,
                      int64_t, float, int64_t, uint16_t*, int64_t, float*, void*, size_t, q2k_stream_t);
+static size_t (*f_attn_bytes)(int64_t, int64_t, int64_t, int64_t);
 static int (*f_norm)(const void*, int, int64_t, const float*, const void*, int64_t, const void*, int, int64_t, float,
                      const float*, float, int64_t, int64_t, void*, int64_t, uint16_t*, int64_t, void*, q2k_stream_t);
 static int (*f_route)(const void*, int, int64_t, int64_t, int64_t, const float*, int, int64_t, int64_t, int64_t, int,
@@ -339,6 +340,18 @@ static PyObject* py_attn(PyObject* self, PyObject* const* a, Py_ssize_t n)
                          stream));
 }
 
+/* T, Hq, Hkv, D */
+static PyObject* py_attn_bytes(PyObject* self, PyObject* const* a, Py_ssize_t n)
+{
+    (void)self;
+    if (want_args(n, 4))
+        return NULL;
+    const int64_t T = as_int(a[0]), Hq = as_int(a[1]), Hkv = as_int(a[2]), D = as_int(a[3]);
+    if (PyErr_Occurred())
+        return NULL;
+    return PyLong_FromSize_t(f_attn_bytes(T, Hq, Hkv, D));
+}
+
 /* residual, pre_w, eps, y, post_w, gate, alpha, residual_out, out, out_q8, stream */
 static PyObject* py_norm(PyObject* self, PyObject* const* a, Py_ssize_t n)
 {
@@ -430,20 +443,20 @@ static PyObject* py_route(PyObject* self, PyObject* const* a, Py_ssize_t n)
                           stream));
 }
 
-/* setup((fp32, bf16, int32, int64, uint8), (addresses of the five functions)) */
+/* setup((fp32, bf16, int32, int64, uint8), (addresses of the six functions)) */
 static PyObject* py_setup(PyObject* self, PyObject* const* a, Py_ssize_t n)
 {
     (void)self;
     if (want_args(n, 2))
         return NULL;
-    void* f[5];
+    void* f[6];
     if (!PyArg_ParseTuple(a[0], "OOOOO", &t_f32, &t_bf16, &t_i32, &t_i64, &t_u8))
         return NULL;
-    for (int i = 0; i < 5; ++i) {
-        if (!PyTuple_Check(a[1]) || PyTuple_GET_SIZE(a[1]) != 5 ||
+    for (int i = 0; i < 6; ++i) {
+        if (!PyTuple_Check(a[1]) || PyTuple_GET_SIZE(a[1]) != 6 ||
             !(f[i] = PyLong_AsVoidPtr(PyTuple_GET_ITEM(a[1], i)))) {
             if (!PyErr_Occurred())
-                fail("five function addresses");
+                fail("six function addresses");
             return NULL;
         }
     }
@@ -457,6 +470,7 @@ static PyObject* py_setup(PyObject* self, PyObject* const* a, Py_ssize_t n)
     *(void**)&f_attn = f[2];
     *(void**)&f_norm = f[3];
     *(void**)&f_route = f[4];
+    *(void**)&f_attn_bytes = f[5];
     Py_RETURN_NONE;
 }
 
@@ -465,6 +479,7 @@ static PyMethodDef methods[] = {
     {"kv_page_plan", (PyCFunction)(void (*)(void))py_plan, METH_FASTCALL, NULL},
     {"kv_rope_store", (PyCFunction)(void (*)(void))py_rope, METH_FASTCALL, NULL},
     {"kv_attention_bf16", (PyCFunction)(void (*)(void))py_attn, METH_FASTCALL, NULL},
+    {"kv_attention_workspace_bytes", (PyCFunction)(void (*)(void))py_attn_bytes, METH_FASTCALL, NULL},
     {"norm_gate_residual", (PyCFunction)(void (*)(void))py_norm, METH_FASTCALL, NULL},
     {"moe_route_topk", (PyCFunction)(void (*)(void))py_route, METH_FASTCALL, NULL},
     {NULL, NULL, 0, NULL}};

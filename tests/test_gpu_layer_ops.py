@@ -488,6 +488,33 @@ def test_attention_on_another_stream_and_in_a_graph(lib):
     within(out, want[0], HALF_ULP * want[0].abs() + (HALF_ULP + 2.0 ** -12) * want[2], "replayed")
 
 
+def test_what_a_call_allocates_belongs_to_the_stream_it_runs_on(lib, monkeypatch):
+    """A workspace that goes back at the call's end must not serve another stream while the kernels run."""
+    side, streams, empty = torch.cuda.Stream(), [], torch.empty
+    g = gen(21)
+    c = Cache(g, [40], 2, 64, 16)
+    q, x, k = normal(g, 1, 4, 64, dtype=torch.bfloat16), normal(g, 2, 256), normal(g, 1, 2, 64)
+    args = i32([0, 1]), i32([40])
+    free, table, head = i32(list(range(8))), torch.full((1, 8), -1, dtype=torch.int32, device=DEV), i32([0])
+    logits, one, freq = normal(g, 2, 16), torch.ones(256, device=DEV), torch.ones(32, device=DEV)
+    pos, slot, ctx, new = i32([3]), i32([-1]), i32([3]), i32([1])
+    torch.cuda.synchronize()
+
+    def noted(*a, **kw):
+        streams.append(torch.cuda.current_stream())
+        return empty(*a, **kw)
+
+    monkeypatch.setattr(torch, "empty", noted)
+    lib.kv_page_plan(ctx, new, 16, free, table, 1, free_head=head, stream=side)
+    lib.kv_rope_store(q, k.to(torch.bfloat16), k.to(torch.bfloat16), pos, freq, slot, c.k, c.v, stream=side)
+    lib.kv_attention_bf16(q, c.k, c.v, c.table, *args, want_lse=True, stream=side)
+    lib.norm_gate_residual(x, one, 1e-6, want_q8=True, stream=side)
+    lib.moe_route_topk(logits, 2, stream=side)
+    monkeypatch.undo()
+    side.synchronize()
+    assert len(streams) == 10 and all(s == side for s in streams), streams
+
+
 # ---- norm_gate_residual ----------------------------------------------------------
 
 def norm_64(residual, y, post_w, gate, alpha, pre_w, eps):
