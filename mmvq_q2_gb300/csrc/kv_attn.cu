@@ -137,6 +137,18 @@ __device__ __forceinline__ int tiles_of(const AttnArgs& a, const Request& q, int
     return hi - lo + 1;
 }
 
+// An item counts as its key tiles and some more, its first units, for its
+// start and end: without them the CTAs with many short items (the first
+// blocks of a prompt) end last, and a cut near an item's first tile makes two
+// items of one.  Two units: 64 decodes of 4100 tokens 189.8 us without, 179.4
+// with one, 173.2 with two, 174.8 with five; 1346 tokens of 64 heads 54.1,
+// 48.0, 46.7, 50.8; 8192 tokens over 4096 802, 792, 788, 794.  None where
+// there are less than two tiles a CTA: then what counts is the most tiles of
+// one (1500 tokens of 8 heads, window 323: 17.4 us without, 19.5 with two).
+constexpr int kItemCost = 2;
+
+__device__ __forceinline__ int cost_of_item(int64_t tiles) { return tiles >= 2 * (int64_t)gridDim.x ? kItemCost : 0; }
+
 // One item, or the part of it that lies in this CTA's run of units.
 struct Item {
     int r, h, j;
@@ -148,21 +160,22 @@ struct Item {
     int two;         // two row tiles (else one, its key tiles dealt to both streams)
 };
 
-// Where a CTA's run starts: item (r, h, j), key tile lo + off, and its units.
+// Where a CTA's run starts: item (r, h, j), its unit off, and the run's units.
 struct Start {
     int r, h, j, off;
+    int cost;  // units of an item before its first tile
     int64_t units;
     Request q;
 };
 
 // The items of a run, one after the other.
 struct Walk {
-    int r, h, j, off, blocks;
+    int r, h, j, off, cost, blocks;
     int64_t left;
     Request q;
 
     __device__ __forceinline__ Walk(const AttnArgs& a, const Start& s)
-        : r(s.r), h(s.h), j(s.j), off(s.off), blocks(blocks_of(a, s.q)), left(s.units), q(s.q)
+        : r(s.r), h(s.h), j(s.j), off(s.off), cost(s.cost), blocks(blocks_of(a, s.q)), left(s.units), q(s.q)
     {
     }
     __device__ __forceinline__ void next(const AttnArgs& a, Item& it)
@@ -181,8 +194,9 @@ struct Walk {
         int lo, hi;
         key_tiles(a, q, i0, i1, lo, hi);
         it.lo = lo;
-        it.k0 = lo + off;
-        it.k1 = (int)min((int64_t)hi + 1, it.k0 + left);
+        const int end = (int)min((int64_t)(hi - lo + 1 + cost), off + left);
+        it.k0 = lo + max(0, off - cost);
+        it.k1 = lo + max(0, end - cost);  // k0 where the run ends before the first tile
         it.kind = (it.k0 == lo ? kFirst : 0) | (it.k1 == hi + 1 ? kLast : 0);
         for (int s = 0; s < 2; ++s) {
             it.first[s] = it.k0;
@@ -194,7 +208,7 @@ struct Walk {
                 it.last[s] = min(it.k1 - 1, x);
             }
         }
-        left -= it.k1 - it.k0;
+        left -= end - off;
         off = 0;
         if (left > 0 && ++j >= blocks) {
             j = 0;
@@ -209,14 +223,14 @@ struct Walk {
     }
 };
 
-// One warp, a request a lane (n = 0 where there is none): its units on one kv head.
-__device__ __forceinline__ int64_t units_of(const AttnArgs& a, const Request& q)
+// One warp, a request a lane (n = 0 where there is none): its key tiles on one kv head.
+__device__ __forceinline__ int64_t tiles_of(const AttnArgs& a, const Request& q)
 {
     const int lane = threadIdx.x & 31, nb = blocks_of(a, q);
-    int64_t units = 0;
+    int64_t tiles = 0;
     if (nb <= 8)
         for (int j = 0; j < nb; ++j)
-            units += tiles_of(a, q, j);
+            tiles += tiles_of(a, q, j);
     for (uint32_t big = __ballot_sync(0xffffffffu, nb > 8); big; big &= big - 1) {
         const int src = __ffs(big) - 1;
         const Request b{__shfl_sync(0xffffffffu, q.t0, src), __shfl_sync(0xffffffffu, q.n, src),
@@ -229,9 +243,9 @@ __device__ __forceinline__ int64_t units_of(const AttnArgs& a, const Request& q)
         for (int o = 16; o >= 1; o >>= 1)
             mine += __shfl_xor_sync(0xffffffffu, mine, o);
         if (lane == src)
-            units = mine;
+            tiles = mine;
     }
-    return units;
+    return tiles;
 }
 
 // The sum over the lanes up to this one.
@@ -247,25 +261,38 @@ __device__ __forceinline__ int64_t sum_to_lane(int64_t v)
 }
 
 // All threads: the units before each request into sums[0..n_req] (shared
-// memory), with warp_sums as scratch.
-__device__ __forceinline__ void sum_units(const AttnArgs& a, int64_t* sums, int64_t* warp_sums)
+// memory), with warp_sums as scratch; returns cost_of_item.
+__device__ __forceinline__ int sum_units(const AttnArgs& a, int64_t* sums, int64_t* warp_sums)
 {
     constexpr int kWarps = kThreads / 32;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     // requests side by side go to different warps: a long one keeps a whole warp
+    int64_t all = 0;
     for (int r0 = 0; r0 < a.n_req; r0 += kThreads) {
         const int r = r0 + lane * kWarps + warp;
-        const int64_t units = units_of(a, r < a.n_req ? load_request(a, r) : Request{0, 0, 0});
+        const int64_t tiles = tiles_of(a, r < a.n_req ? load_request(a, r) : Request{0, 0, 0}) * a.Hkv;
         if (r < a.n_req)
-            sums[r + 1] = units * a.Hkv;
+            sums[r + 1] = tiles;
+        all += tiles;
     }
+    all = sum_to_lane(all);
+    if (lane == 31)
+        warp_sums[warp] = all;
     if (threadIdx.x == 0)
         sums[0] = 0;
+    __syncthreads();
+    all = 0;
+    for (int w = 0; w < kWarps; ++w)
+        all += warp_sums[w];
+    const int cost = cost_of_item(all);
     __syncthreads();
     int64_t base = 0;
     for (int r0 = 0; r0 < a.n_req; r0 += kThreads) {
         const int r = r0 + (int)threadIdx.x;
-        const int64_t units = sum_to_lane(r < a.n_req ? sums[r + 1] : 0);
+        int64_t units = 0;
+        if (r < a.n_req)
+            units = sums[r + 1] + (int64_t)cost * a.Hkv * blocks_of(a, load_request(a, r));
+        units = sum_to_lane(units);
         if (lane == 31)
             warp_sums[warp] = units;
         __syncthreads();
@@ -279,6 +306,7 @@ __device__ __forceinline__ void sum_units(const AttnArgs& a, int64_t* sums, int6
             sums[r + 1] = before + units;
         __syncthreads();
     }
+    return cost;
 }
 
 // CTA c of n takes the units [run_start(c), run_start(c + 1)), one at least: n
@@ -303,8 +331,8 @@ __device__ __forceinline__ int find_request(const AttnArgs& a, const int64_t* su
     return lo;
 }
 
-// One warp: the item and key tile of unit rem of request r, which has
-// per_head of them on each kv head.
+// One warp: the item and the unit in it of unit rem of request r, which has
+// per_head of them on each kv head; s.cost is set.
 __device__ __forceinline__ void find_start(const AttnArgs& a, int r, const Request& q, int64_t per_head, int64_t rem,
                                            Start& s)
 {
@@ -317,7 +345,7 @@ __device__ __forceinline__ void find_start(const AttnArgs& a, int r, const Reque
     s.j = 0;
     s.off = 0;
     for (int j0 = 0; j0 < nb; j0 += 32) {
-        const int n = j0 + lane < nb ? tiles_of(a, q, j0 + lane) : 0;
+        const int n = j0 + lane < nb ? tiles_of(a, q, j0 + lane) + s.cost : 0;
         int sum = n;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -630,14 +658,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool few = a.n_req <= 32;
     Request req{0, 0, 0};
     int64_t upto = 0, per_head = 0, total;
+    int cost;
     if (few) {  // every warp for itself, a request a lane: no barrier
         if (lane < a.n_req)
             req = load_request(a, lane);
-        per_head = units_of(a, req);
+        per_head = tiles_of(a, req);
         upto = sum_to_lane(per_head * a.Hkv);
+        cost = cost_of_item(__shfl_sync(0xffffffffu, upto, 31));
+        if (cost) {
+            per_head += (int64_t)cost * blocks_of(a, req);
+            upto = sum_to_lane(per_head * a.Hkv);
+        }
         total = __shfl_sync(0xffffffffu, upto, 31);
     } else {
-        sum_units(a, sums, sh.warp_sums);
+        cost = sum_units(a, sums, sh.warp_sums);
         total = sums[a.n_req];
     }
     const int runs = (int)min(total, (int64_t)gridDim.x);
@@ -650,6 +684,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int64_t from = run_start(total, blockIdx.x, runs), to = run_start(total, blockIdx.x + 1, runs);
     if (warp == 0) {
         Start s;
+        s.cost = cost;
         if (few) {
             const int r = __ffs(__ballot_sync(0xffffffffu, upto > from)) - 1;
             const int64_t rem = from - (upto - per_head * a.Hkv);
@@ -1148,7 +1183,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool whole = (kind & kFirst) && (kind & kLast);
             const int slot = 2 * blockIdx.x + ((kind & kFirst) ? 1 : 0);
             if (!(kind & kFirst) && (kind & kLast) && warp == 4 && lane == 0) {
-                // the CTA whose run holds the item's first unit
+                // the CTA whose run holds the item's first tile
                 const int64_t tot = sh.total;
                 const int runs = (int)min(tot, (int64_t)gridDim.x);
                 const int64_t unit = run_start(tot, blockIdx.x, runs) - (it->k0 - it->lo);
