@@ -1334,36 +1334,44 @@ __device__ __forceinline__ void join_columns(const AttnArgs& a, const Head& head
     const JoinRow r(a, head, row);
     if (!r.live)
         return;
-    auto fetch = [&](int c, float(&v)[16], float2& ml) {
-        const int64_t at = piece_row(a, c, first);
-        ml = a.part_ml[at + row];
-        const float* src = a.part_o + at * a.D + ((x >> 3) * a.row_cap + row) * 8;
-        load_32b(src, v);
-        load_32b(src + a.row_cap * 8, v + 8);
+    struct Piece {
+        float v[16];
+        float2 ml;
     };
-    float now[16], o[16];
-    float2 ml;
-    fetch(first, now, ml);
-    float top = ml.x, sum = 0.f;
-    for (int c = first + 1; c <= last; ++c)
-        top = fmaxf(top, a.part_ml[piece_row(a, c, first) + row].x);
+    auto fetch = [&](int c, Piece& p) {
+        if (c > last)
+            return;
+        const int64_t at = piece_row(a, c, first);
+        p.ml = a.part_ml[at + row];
+        const float* src = a.part_o + at * a.D + ((x >> 3) * a.row_cap + row) * 8;
+        load_32b(src, p.v);
+        load_32b(src + a.row_cap * 8, p.v + 8);
+    };
+    constexpr int kAhead = 2;
+    Piece p[kAhead] = {};
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i)
+        fetch(first + i, p[i]);
+    float top = -INFINITY, sum = 0.f, o[16];
 #pragma unroll
     for (int y = 0; y < 16; ++y)
         o[y] = 0.f;
-    for (int c = first; c <= last; ++c) {
-        float next[16] = {};
-        float2 ml_next = ml;
-        if (c < last)
-            fetch(c + 1, next, ml_next);
-        // a piece without a key for this row holds zeros
-        const float f = ml.y > 0.f ? exp2_approx(ml.x - top) : 0.f;
-        sum = fmaf(ml.y, f, sum);
+#pragma unroll 4
+    for (int c = first; c <= last; ++c)
+        top = fmaxf(top, a.part_ml[piece_row(a, c, first) + row].x);
+    for (int c0 = first; c0 <= last; c0 += kAhead) {
 #pragma unroll
-        for (int y = 0; y < 16; ++y) {
-            o[y] = fmaf(now[y], f, o[y]);
-            now[y] = next[y];
+        for (int i = 0; i < kAhead; ++i) {
+            if (c0 + i > last)
+                break;
+            // a piece without a key for this row holds zeros
+            const float f = p[i].ml.y > 0.f ? exp2_approx(p[i].ml.x - top) : 0.f;
+            sum = fmaf(p[i].ml.y, f, sum);
+#pragma unroll
+            for (int y = 0; y < 16; ++y)
+                o[y] = fmaf(p[i].v[y], f, o[y]);
+            fetch(c0 + i + kAhead, p[i]);
         }
-        ml = ml_next;
     }
     const int64_t t = head.t0 + r.i;
     const int h = head.h * a.g + r.in;
