@@ -364,6 +364,30 @@ def test_attention(lib, case):
     assert torch.equal(out, again) and torch.equal(lse, lse2)
 
 
+@pytest.mark.parametrize("n_req, new, ctx, heads, window", [
+    (32, [1], [0, 700, 90], (8, 2), 0),          # as many as one warp takes
+    (33, [1], [0, 700, 90], (8, 2), 0),
+    (33, [1, 0, 40], [900, 3, 0], (2, 1), 0),
+    (64, [0, 1, 150, 1], [5, 1300, 0, 260], (4, 1), 0),
+    (385, [1, 2], [0, 127, 300], (4, 2), 0),     # more than a block has threads
+    (385, [0, 33, 1, 5], [0, 127, 130], (4, 2), 50),
+    (1000, [1, 0, 0, 3], [20, 1, 0], (1, 1), 0),
+])
+def test_attention_of_many_requests(lib, n_req, new, ctx, heads, window):
+    """Every way the work is counted and divided: few and many requests, with few and many key tiles."""
+    g = gen(31)
+    news = [new[i % len(new)] for i in range(n_req)]
+    seq = [news[i] + ctx[i % len(ctx)] for i in range(n_req)]
+    cu = [0]
+    for n in news:
+        cu.append(cu[-1] + n)
+    c = Cache(g, seq, heads[1], 64, 16)
+    q = normal(g, cu[-1], heads[0], 64, dtype=torch.bfloat16)
+    out, lse = lib.kv_attention_bf16(q, c.k, c.v, c.table, i32(cu), i32(seq), window=window, want_lse=True)
+    check_attention(out, lse, attention_64(q, c.keys, c.values, cu, seq, 64 ** -0.5, window))
+    assert lib.q2k_device_error(clear=True) == 0
+
+
 def test_attention_without_cached_rows(lib):
     """Requests whose cache is shorter than their new tokens: the first rows see nothing."""
     g = gen(1)
