@@ -875,11 +875,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // Two row tiles, D above 64: a stream takes a turn for its O += P V
                 // and the first MMAs of its next S.  Without turns the streams'
                 // products interleave and end together, both softmaxes then run
-                // at once and the tensor cores wait; with the whole of S in the
-                // turn they wait for its hand-over (8192 new tokens over 4096:
-                // 906 us without, 836 us with none to three MMAs of S, more with
-                // all).  At D <= 64 the products are half as long and the
-                // softmaxes bind: 697 us without turns, 728 us with them.
+                // at once and the tensor cores wait (8192 new tokens over 4096:
+                // 876 us without, 787 with; none to six MMAs of S in the turn
+                // give 782 to 790).  At D <= 64 the products are half as long and
+                // the softmaxes bind: 12 chunks in a window take 45.4 us without
+                // turns, 47.6 with them.
                 bool mine = false;
                 auto take_turn = [&]() {
                     bool got = true;

@@ -299,7 +299,7 @@ __global__ void __launch_bounds__(256) norm_any_kernel(const NormArgs a)
 // The choice works on whole numbers that order like the floats, so that a
 // maximum over the warp is one redux instruction and a tie falls to the
 // lowest index exactly.  What bounds it is the number of instructions (256
-// experts: 1 KB to read, about 500 instructions of a warp).  So a lane keeps
+// experts: 1 KB to read, 840 instructions of a warp).  So a lane keeps
 // its two best at hand and looks its scores through again only when both are
 // gone; and a softmax without bias or groups is chosen by its exponentials,
 // since dividing all by one sum keeps their order: the scores are worked out
