@@ -10,13 +10,13 @@
 // tile of 128 rows, from one new token (g rows) to long prompts.
 //
 // Work.  An item is a request's block of two row tiles on one kv head, its
-// unit a tile of 128 keys.  Every CTA (one per SM) sums the units of all
-// requests from the lengths on the device and takes an equal run of them,
-// wherever it starts and ends: a long decode is split over the whole GPU,
-// a batch of ragged ones and causal prompts balance, and the host needs to
-// know no length.  An item that one CTA finishes is written at once; the
-// pieces of a split one go to the workspace, and a second launch joins them
-// in a fixed order.
+// units its tiles of 128 keys and, in calls of some size, two for its start
+// and end.  Every CTA (one per SM) sums the units of all requests from the
+// lengths on the device and takes an equal run of them, wherever it starts
+// and ends: a long decode is split over the whole GPU, a batch of ragged ones
+// and causal prompts balance, and the host needs to know no length.  An item
+// that one CTA finishes is written at once; the pieces of a split one go to
+// the workspace, and a second launch joins them in a fixed order.
 //
 // One CTA, twelve warps:
 //   warp 0       copies Q and K tiles (64 values of D by 128 rows, 128-byte
@@ -51,6 +51,7 @@
 #include <cudaTypedefs.h>
 
 #include <algorithm>
+#include <climits>
 #include <cmath>
 #include <mutex>
 

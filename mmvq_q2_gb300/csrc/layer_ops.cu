@@ -17,7 +17,7 @@ namespace {
 //
 // h = residual + alpha * gate * norm(y), n = norm(h): two sums over a row,
 // the second of values that need the first.  Bound by memory: a row stays in
-// registers (8 values a run, up to four runs a thread) from its one read to
+// registers (8 values a run, one or two runs a thread) from its one read to
 // its one write.
 
 struct NormArgs {
