@@ -150,6 +150,14 @@ constexpr int kItemCost = 2;
 
 __device__ __forceinline__ int cost_of_item(int64_t tiles) { return tiles >= 2 * (int64_t)gridDim.x ? kItemCost : 0; }
 
+// Items of one row tile, no more of them than CTAs (and at most 32 requests),
+// are not split where none has more than four key tiles above a CTA's share:
+// such an item takes less time than its join, and counts as one unit.  One
+// token over 200, 300, 450 (32 heads of 128): 14.6, 14.4, 14.6 us split, 10.6,
+// 12.6, 13.7 whole (600: 15.0, 15.7); 16 tokens over 200, 500 each: 17.4, 21.7
+// split, 14.0, 19.2 whole.
+constexpr int kWholeTiles = 4;
+
 // One item, or the part of it that lies in this CTA's run of units.
 struct Item {
     int r, h, j;
@@ -164,19 +172,20 @@ struct Item {
 // Where a CTA's run starts: item (r, h, j), its unit off, and the run's units.
 struct Start {
     int r, h, j, off;
-    int cost;  // units of an item before its first tile
+    int cost;   // units of an item before its first tile
+    int whole;  // an item is one unit
     int64_t units;
     Request q;
 };
 
 // The items of a run, one after the other.
 struct Walk {
-    int r, h, j, off, cost, blocks;
+    int r, h, j, off, cost, whole, blocks;
     int64_t left;
     Request q;
 
     __device__ __forceinline__ Walk(const AttnArgs& a, const Start& s)
-        : r(s.r), h(s.h), j(s.j), off(s.off), cost(s.cost), blocks(blocks_of(a, s.q)), left(s.units), q(s.q)
+        : r(s.r), h(s.h), j(s.j), off(s.off), cost(s.cost), whole(s.whole), blocks(blocks_of(a, s.q)), left(s.units), q(s.q)
     {
     }
     __device__ __forceinline__ void next(const AttnArgs& a, Item& it)
@@ -195,9 +204,9 @@ struct Walk {
         int lo, hi;
         key_tiles(a, q, i0, i1, lo, hi);
         it.lo = lo;
-        const int end = (int)min((int64_t)(hi - lo + 1 + cost), off + left);
+        const int end = (int)min((int64_t)(whole ? 1 : hi - lo + 1 + cost), off + left);
         it.k0 = lo + max(0, off - cost);
-        it.k1 = lo + max(0, end - cost);  // k0 where the run ends before the first tile
+        it.k1 = whole ? hi + 1 : lo + max(0, end - cost);  // k0 where the run ends before the first tile
         it.kind = (it.k0 == lo ? kFirst : 0) | (it.k1 == hi + 1 ? kLast : 0);
         for (int s = 0; s < 2; ++s) {
             it.first[s] = it.k0;
@@ -333,7 +342,7 @@ __device__ __forceinline__ int find_request(const AttnArgs& a, const int64_t* su
 }
 
 // One warp: the item and the unit in it of unit rem of request r, which has
-// per_head of them on each kv head; s.cost is set.
+// per_head of them on each kv head; s.cost and s.whole are set.
 __device__ __forceinline__ void find_start(const AttnArgs& a, int r, const Request& q, int64_t per_head, int64_t rem,
                                            Start& s)
 {
@@ -346,7 +355,7 @@ __device__ __forceinline__ void find_start(const AttnArgs& a, int r, const Reque
     s.j = 0;
     s.off = 0;
     for (int j0 = 0; j0 < nb; j0 += 32) {
-        const int n = j0 + lane < nb ? tiles_of(a, q, j0 + lane) + s.cost : 0;
+        const int n = j0 + lane < nb ? s.whole ? 1 : tiles_of(a, q, j0 + lane) + s.cost : 0;
         int sum = n;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -660,13 +669,21 @@ __global__ void __launch_bounds__(kThreads, 1)
     Request req{0, 0, 0};
     int64_t upto = 0, per_head = 0, total;
     int cost;
+    bool whole = false;
     if (few) {  // every warp for itself, a request a lane: no barrier
         if (lane < a.n_req)
             req = load_request(a, lane);
         per_head = tiles_of(a, req);
         upto = sum_to_lane(per_head * a.Hkv);
-        cost = cost_of_item(__shfl_sync(0xffffffffu, upto, 31));
-        if (cost) {
+        const int64_t tiles = __shfl_sync(0xffffffffu, upto, 31);
+        const uint32_t with = __ballot_sync(0xffffffffu, req.n > 0);
+        whole = __all_sync(0xffffffffu, req.n <= a.tq && (per_head - kWholeTiles) * gridDim.x <= tiles) &&
+                __popc(with) * a.Hkv <= (int)gridDim.x;
+        cost = whole ? 0 : cost_of_item(tiles);
+        if (whole) {
+            per_head = with >> lane & 1u;
+            upto = __popc(with & ((2u << lane) - 1u)) * a.Hkv;
+        } else if (cost) {
             per_head += (int64_t)cost * blocks_of(a, req);
             upto = sum_to_lane(per_head * a.Hkv);
         }
@@ -686,6 +703,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 0) {
         Start s;
         s.cost = cost;
+        s.whole = whole;
         if (few) {
             const int r = __ffs(__ballot_sync(0xffffffffu, upto > from)) - 1;
             const int64_t rem = from - (upto - per_head * a.Hkv);

@@ -388,6 +388,31 @@ def test_attention_of_many_requests(lib, n_req, new, ctx, heads, window):
     assert lib.q2k_device_error(clear=True) == 0
 
 
+@pytest.mark.parametrize("ctx, new, heads, d, window", [
+    ([511], [1], (4, 1), 128, 0),                     # four key tiles
+    ([512], [1], (4, 1), 128, 0),                     # five
+    ([300, 0, 0, 129, 7], [1, 0, 1, 3, 2], (8, 2), 64, 0),
+    ([300, 450], [2, 2], (128, 2), 96, 0),            # a token fills half a row tile
+    ([400, 90], [16, 5], (16, 2), 128, 100),          # a window that leaves out whole tiles
+    ([40 * i for i in range(16)], [1] * 16, (16, 8), 128, 0),
+    ([60 * i for i in range(16)], [1] * 16, (32, 8), 64, 0),  # as long as a CTA's share and four tiles
+    ([500] * 19, [1] * 19, (8, 8), 64, 0),            # 152 items
+    ([500] * 20, [1] * 20, (8, 8), 64, 0),            # more
+])
+def test_attention_of_few_key_tiles(lib, ctx, new, heads, d, window):
+    """Items that are not split, next to such as are."""
+    g = gen(32)
+    seq = [c + n for c, n in zip(ctx, new)]
+    cu = [0]
+    for n in new:
+        cu.append(cu[-1] + n)
+    c = Cache(g, seq, heads[1], d, 16)
+    q = normal(g, cu[-1], heads[0], d, dtype=torch.bfloat16)
+    out, lse = lib.kv_attention_bf16(q, c.k, c.v, c.table, i32(cu), i32(seq), window=window, want_lse=True)
+    check_attention(out, lse, attention_64(q, c.keys, c.values, cu, seq, d ** -0.5, window))
+    assert lib.q2k_device_error(clear=True) == 0
+
+
 def test_attention_without_cached_rows(lib):
     """Requests whose cache is shorter than their new tokens: the first rows see nothing."""
     g = gen(1)
