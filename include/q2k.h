@@ -470,7 +470,11 @@ size_t kv_attention_workspace_bytes(int64_t T, int64_t Hq, int64_t Hkv, int64_t 
  *   out          bf16, token t's head h at t * ld_o + h * D
  *   lse          fp32 [T, Hq], nullable: ln of the sum of e^score
  * Query head h reads kv head h / (Hq / Hkv).  A row that sees no key (p < 0)
- * gives zeros and lse -inf.  Keys outside a row's range may hold anything in
+ * gives zeros and lse -inf.  A row with a NaN or +inf among its scores gives
+ * NaN in out and lse, one whose scores are all -inf NaN in out and lse -inf
+ * (0 / 0); a score of -inf beside others counts nothing.  (Scores are taken
+ * times log2(e) in fp32: those past 2^127 are +inf here.)
+ * Keys outside a row's range may hold anything in
  * K; V rows that no row of a request's tile can see may too (they are never
  * multiplied), so an uninitialised page is safe.  Table entries outside
  * [0, n_pages), and positions past max_pages pages, read as zeros and set

@@ -51,6 +51,7 @@
 #include <cudaTypedefs.h>
 
 #include <algorithm>
+#include <cfloat>
 #include <climits>
 #include <cmath>
 #include <mutex>
@@ -611,9 +612,21 @@ __device__ __forceinline__ void store_out16(uint16_t* dst, const float* v, float
     }
 }
 
+// A row's maximum (times c) and sum, over all keys or some.  No key: the
+// maximum is -inf and the sum 0, exactly; keys of score -inf alone leave a sum
+// of 0 under a finite maximum (max_c); a sum of NaN (a score of NaN or +inf)
+// is passed on.  So a sum is asked for being 0, never for being above it.
+__device__ __forceinline__ float max_c(float m, float c, bool has_key) { return has_key ? fmaxf(m * c, -FLT_MAX) : -INFINITY; }
+
+// What a part counts in a whole of the given maximum.
+__device__ __forceinline__ float part_weight(float2 ml, float top) { return ml.y == 0.f ? 0.f : exp2_approx(ml.x - top); }
+
+// 1 / l; zero for a row without a key.
+__device__ __forceinline__ float inverse(float top, float l) { return top == -INFINITY && l == 0.f ? 0.f : 1.0f / l; }
+
 __device__ __forceinline__ float lse_of(float mc, float l)
 {
-    return l > 0.f ? (mc + log2f(l)) * 0.6931471805599453f : -INFINITY;
+    return l == 0.f ? -INFINITY : (mc + log2f(l)) * 0.6931471805599453f;
 }
 
 template <int DB>  // halves of 64 values of D
@@ -1218,7 +1231,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             done_item();
             uint16_t* dst = a.out + out_row * a.ld_o + (int64_t)out_head * a.D;
             float* part = a.part_o + (int64_t)slot * a.row_cap * a.D + ((two ? s * kRows : 0) + row) * 8;
-            const float mc = m == -INFINITY ? -INFINITY : m * a.c;
+            const float mc = max_c(m, a.c, live && p >= 0);
             if (count > 0) {
                 if (!(ok = warp_wait(sh.o_done[s], done)))
                     break;
@@ -1236,15 +1249,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                     break;
                 const float2 e0 = sh.ml[0][row], e1 = sh.ml[1][row];
                 top = fmaxf(e0.x, e1.x);
-                f0 = e0.y > 0.f ? exp2_approx(e0.x - top) : 0.f;
-                f1 = e1.y > 0.f ? exp2_approx(e1.x - top) : 0.f;
+                f0 = part_weight(e0, top);
+                f1 = part_weight(e1, top);
                 sum = e0.y * f0 + e1.y * f1;
-            } else if (!(l > 0.f)) {
+            } else if (l == 0.f) {
                 f0 = 0.f;  // a row without a key is zero, whatever O holds
             }
             fence_after();
             if (warp_live) {
-                const float inv = whole ? (sum > 0.f ? 1.0f / sum : 0.f) : 1.f;
+                const float inv = whole ? inverse(top, sum) : 1.f;
                 for (int x = two ? 0 : s * 32; x < a.D; x += two ? 32 : 64) {
                     float o[32];
                     tmem_ld32<0>((two ? t_o : lanes + 128) + x, o);
@@ -1254,12 +1267,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                         tmem_wait_ld();
 #pragma unroll
                         for (int y = 0; y < 32; ++y)
-                            o[y] = (f0 > 0.f ? o[y] * f0 : 0.f) + (f1 > 0.f ? o1[y] * f1 : 0.f);
+                            o[y] = (f0 == 0.f ? 0.f : o[y] * f0) + (f1 == 0.f ? 0.f : o1[y] * f1);
                     } else {
                         tmem_wait_ld();
 #pragma unroll
                         for (int y = 0; y < 32; ++y)
-                            o[y] = f0 > 0.f ? o[y] : 0.f;
+                            o[y] = f0 == 0.f ? 0.f : o[y];
                     }
                     if (live) {
 #pragma unroll
@@ -1384,7 +1397,7 @@ __device__ __forceinline__ void join_columns(const AttnArgs& a, const Head& head
             if (c0 + i > last)
                 break;
             // a piece without a key for this row holds zeros
-            const float f = p[i].ml.y > 0.f ? exp2_approx(p[i].ml.x - top) : 0.f;
+            const float f = part_weight(p[i].ml, top);
             sum = fmaf(p[i].ml.y, f, sum);
 #pragma unroll
             for (int y = 0; y < 16; ++y)
@@ -1394,7 +1407,7 @@ __device__ __forceinline__ void join_columns(const AttnArgs& a, const Head& head
     }
     const int64_t t = head.t0 + r.i;
     const int h = head.h * a.g + r.in;
-    store_out16(a.out + t * a.ld_o + (int64_t)h * a.D + x, o, sum > 0.f ? 1.0f / sum : 0.f, a.out_align);
+    store_out16(a.out + t * a.ld_o + (int64_t)h * a.D + x, o, inverse(top, sum), a.out_align);
     if (a.lse && x == 0)
         a.lse[t * a.Hq + h] = lse_of(top, sum);
 }
@@ -1438,7 +1451,7 @@ __device__ __forceinline__ void join_rows(const AttnArgs& a, const Head& head, i
             fetch(next, c + kAhead);
 #pragma unroll
             for (int j = 0; j < kAhead; ++j) {
-                const float f = now.ml[j].y > 0.f ? exp2_approx(now.ml[j].x - top) : 0.f;
+                const float f = part_weight(now.ml[j], top);
                 sum = fmaf(now.ml[j].y, f, sum);
                 o.x = fmaf(now.v[j].x, f, o.x);
                 o.y = fmaf(now.v[j].y, f, o.y);
@@ -1447,7 +1460,7 @@ __device__ __forceinline__ void join_rows(const AttnArgs& a, const Head& head, i
             }
             now = next;
         }
-        const float inv = sum > 0.f ? 1.0f / sum : 0.f;
+        const float inv = inverse(top, sum);
         const int64_t t = head.t0 + r.i;
         const int h = head.h * a.g + r.in;
         if (col < a.D) {
