@@ -408,7 +408,7 @@ enum q2k_type {
  *                first ceil(ctx/page_size) entries in use; the entries of
  *                pages that the new tokens open are written, the others left
  *   cu_q         int32 [n_req + 1]: sums of new_lens, 0 first
- *   seq_lens     int32 [n_req]: ctx_lens + new_lens
+ *   seq_lens     int32 [n_req]: ctx_lens + new_lens (of what is kept: bit 8)
  *   positions, token_req, slot_map   int32 [max_tokens]: position, request
  *                and slot of each new token, request by request; entries
  *                past the last token are -1 (a captured step of fixed size
@@ -419,7 +419,11 @@ enum q2k_type {
  *                (those pages and their slots are -1), 2 = a request
  *                outgrew its table row (its later slots are -1), 4 = a
  *                negative length or head (read as 0), 8 = more than
- *                max_tokens tokens (cu_q and the token arrays are cut)
+ *                max_tokens tokens: the plan is that of the first
+ *                max_tokens of them, request by request, in every output
+ *                (a request keeps cu_q[r + 1] - cu_q[r] of its new tokens,
+ *                seq_lens counts those, pages are opened for those), so
+ *                that the rest can go in the next step
  * 1 <= n_req <= 16384, 0 <= max_tokens <= 2^30, page_size a power of two
  * 16..1024.  One launch. */
 int kv_page_plan(const int32_t* ctx_lens, const int32_t* new_lens, int64_t n_req, int64_t page_size,

@@ -458,8 +458,9 @@ def kv_page_plan(ctx_lens, new_lens, page_size, free_pages, block_table, max_tok
     """A step's cache bookkeeping from the requests' lengths (all int32):
     opens pages for the new tokens in ``block_table [n_req, ld]`` (in place)
     and returns ``PagePlan(cu_q [n_req+1], seq_lens [n_req], positions,
-    token_req, slot_map [max_tokens], free_head [1])``.  ``out``: a
-    ``PagePlan`` to write into."""
+    token_req, slot_map [max_tokens], free_head [1])``.  Of more than
+    ``max_tokens`` new tokens the first are planned (bit 8 of ``err_flag``).
+    ``out``: a ``PagePlan`` to write into."""
     to = out
     if out is None:  # one allocation for the six arrays
         n = ctx_lens.numel()

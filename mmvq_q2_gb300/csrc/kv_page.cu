@@ -57,58 +57,71 @@ __global__ void __launch_bounds__(kPlanThreads) kv_page_plan_kernel(const PlanAr
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     pdl_launch_dependents();
     pdl_wait();
+    if (threadIdx.x == 0)
+        cu[0] = need[0] = 0;
     int err = 0;
-    int64_t base_new = 0, base_need = 0;
-    for (int r0 = 0; r0 < a.n; r0 += kPlanThreads) {
-        const int r = r0 + (int)threadIdx.x;
-        int64_t nw = 0, nd = 0;
-        if (r < a.n) {
-            int c = a.ctx[r], w = a.add[r];
-            if (c < 0 || w < 0)
-                err |= 4;
-            c = max(c, 0);
-            w = max(w, 0);
-            const int64_t seq = (int64_t)c + w;
-            if (blockIdx.x == 0)
-                a.seq_lens[r] = (int32_t)min(seq, (int64_t)INT_MAX);
-            if (w > 0 && seq > (a.max_pages << a.shift))
-                err |= 2;
-            nw = w;
-            // pages past the table's row cannot be recorded and are not taken
-            nd = min(pages_of(seq, a.shift), a.max_pages) - min(pages_of(c, a.shift), a.max_pages);
-        }
-        int64_t sn = nw, sd = nd;  // inclusive sums over the block
+    int64_t base_new, base_need;
+    // Where there are more new tokens than max_tokens, once more for those
+    // that are kept: lengths, pages and positions then fit one another, and
+    // the rest can be the next step.
+    bool cut = false;
+    for (;;) {
+        base_new = base_need = 0;
+        for (int r0 = 0; r0 < a.n; r0 += kPlanThreads) {
+            const int r = r0 + (int)threadIdx.x;
+            int64_t nw = 0, nd = 0;
+            if (r < a.n) {
+                int c = a.ctx[r], w = a.add[r];
+                if (c < 0 || w < 0)
+                    err |= 4;
+                c = max(c, 0);
+                w = cut ? cu[r + 1] - cu[r] : max(w, 0);
+                const int64_t seq = (int64_t)c + w;
+                if (blockIdx.x == 0)
+                    a.seq_lens[r] = (int32_t)min(seq, (int64_t)INT_MAX);
+                if (w > 0 && seq > (a.max_pages << a.shift))
+                    err |= 2;
+                nw = w;
+                // pages past the table's row cannot be recorded and are not taken
+                nd = min(pages_of(seq, a.shift), a.max_pages) - min(pages_of(c, a.shift), a.max_pages);
+            }
+            int64_t sn = nw, sd = nd;  // inclusive sums over the block
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int64_t u = __shfl_up_sync(0xffffffffu, sn, o), v = __shfl_up_sync(0xffffffffu, sd, o);
-            if (lane >= o) {
-                sn += u;
-                sd += v;
+            for (int o = 1; o < 32; o <<= 1) {
+                const int64_t u = __shfl_up_sync(0xffffffffu, sn, o), v = __shfl_up_sync(0xffffffffu, sd, o);
+                if (lane >= o) {
+                    sn += u;
+                    sd += v;
+                }
             }
-        }
-        if (lane == 31) {
-            warp_new[warp] = sn;
-            warp_need[warp] = sd;
-        }
-        __syncthreads();
-        int64_t tn = 0, td = 0;
-        for (int w = 0; w < kPlanThreads / 32; ++w) {
-            if (w == warp) {
-                sn += base_new + tn;
-                sd += base_need + td;
+            if (lane == 31) {
+                warp_new[warp] = sn;
+                warp_need[warp] = sd;
             }
-            tn += warp_new[w];
-            td += warp_need[w];
+            __syncthreads();
+            int64_t tn = 0, td = 0;
+            for (int w = 0; w < kPlanThreads / 32; ++w) {
+                if (w == warp) {
+                    sn += base_new + tn;
+                    sd += base_need + td;
+                }
+                tn += warp_new[w];
+                td += warp_need[w];
+            }
+            if (r < a.n) {
+                cu[r + 1] = (int32_t)min(sn, (int64_t)a.max_tokens);
+                need[r + 1] = (int32_t)min(sd, (int64_t)INT_MAX);
+                if (blockIdx.x == 0)
+                    a.cu_q[r + 1] = cu[r + 1];
+            }
+            base_new += tn;
+            base_need += td;
+            __syncthreads();
         }
-        if (r < a.n) {
-            cu[r + 1] = (int32_t)min(sn, (int64_t)a.max_tokens);
-            need[r + 1] = (int32_t)min(sd, (int64_t)INT_MAX);
-            if (blockIdx.x == 0)
-                a.cu_q[r + 1] = cu[r + 1];
-        }
-        base_new += tn;
-        base_need += td;
-        __syncthreads();
+        if (base_new <= a.max_tokens)
+            break;
+        cut = true;
+        err &= ~2;  // asked again of what is kept
     }
     int head = a.free_head ? *a.free_head : 0;
     if (head < 0) {
@@ -116,8 +129,7 @@ __global__ void __launch_bounds__(kPlanThreads) kv_page_plan_kernel(const PlanAr
         err |= 4;
     }
     if (threadIdx.x == 0) {
-        cu[0] = need[0] = 0;
-        if (base_new > a.max_tokens)
+        if (cut)
             err |= 8;
         if (head + base_need > a.n_free && base_need > 0)
             err |= 1;
