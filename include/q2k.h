@@ -413,8 +413,7 @@ enum q2k_type {
  *                and slot of each new token, request by request; entries
  *                past the last token are -1 (a captured step of fixed size
  *                can be padded)
- *   free_head_out  int32 [1]: free_head + pages taken (may not be
- *                free_head itself: a repeated call then gives the same)
+ *   free_head_out  int32 [1]: free_head + pages taken
  *   err_flag     int32, nullable; bits OR'ed in: 1 = the pool ran out
  *                (those pages and their slots are -1), 2 = a request
  *                outgrew its table row (its later slots are -1), 4 = a
@@ -424,6 +423,9 @@ enum q2k_type {
  *                (a request keeps cu_q[r + 1] - cu_q[r] of its new tokens,
  *                seq_lens counts those, pages are opened for those), so
  *                that the rest can go in the next step
+ * No output may lie over ctx_lens, new_lens, free_pages or free_head, which
+ * are read throughout (Q2K_ERR_BAD_SHAPE): a step's lengths and head are
+ * taken over by a copy after the call, and a repeated call gives the same.
  * 1 <= n_req <= 16384, 0 <= max_tokens <= 2^30, page_size a power of two
  * 16..1024.  One launch. */
 int kv_page_plan(const int32_t* ctx_lens, const int32_t* new_lens, int64_t n_req, int64_t page_size,

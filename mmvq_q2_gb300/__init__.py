@@ -460,7 +460,8 @@ def kv_page_plan(ctx_lens, new_lens, page_size, free_pages, block_table, max_tok
     and returns ``PagePlan(cu_q [n_req+1], seq_lens [n_req], positions,
     token_req, slot_map [max_tokens], free_head [1])``.  Of more than
     ``max_tokens`` new tokens the first are planned (bit 8 of ``err_flag``).
-    ``out``: a ``PagePlan`` to write into."""
+    ``out``: a ``PagePlan`` to write into; none of it may be an input (the
+    lengths are read throughout: advance them by a copy afterwards)."""
     to = out
     if out is None:  # one allocation for the six arrays
         n = ctx_lens.numel()

@@ -86,6 +86,13 @@ constexpr int64_t kMaxSlots = (int64_t)1 << 31;
 
 bool type_ok(int t) { return t == Q2K_F32 || t == Q2K_BF16; }
 
+// int32 arrays of na and nb entries share an address.
+bool overlap(const int32_t* a, int64_t na, const int32_t* b, int64_t nb)
+{
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return a && b && na > 0 && nb > 0 && x < y + (uintptr_t)nb * 4 && y < x + (uintptr_t)na * 4;
+}
+
 bool page_size_ok(int64_t p) { return p >= 16 && p <= 1024 && (p & (p - 1)) == 0; }
 
 bool cache_ok(int64_t n_pages, int64_t page_size, int64_t page_stride, int64_t Hkv, int64_t D)
@@ -687,6 +694,17 @@ int kv_page_plan(const int32_t* ctx_lens, const int32_t* new_lens, int64_t n_req
         !aligned(block_table, 4) || !aligned(cu_q, 4) || !aligned(seq_lens, 4) || !aligned(positions, 4) ||
         !aligned(token_req, 4) || !aligned(slot_map, 4) || !aligned(free_head_out, 4) || !aligned(err_flag, 4))
         return Q2K_ERR_MISALIGNED;
+    // every block reads the inputs, at any time: none may be written meanwhile
+    const struct {
+        const int32_t* p;
+        int64_t n;
+    } in[] = {{ctx_lens, n_req}, {new_lens, n_req}, {free_pages, n_free}, {free_head, 1}},
+      out[] = {{cu_q, n_req + 1},     {seq_lens, n_req},      {positions, max_tokens}, {token_req, max_tokens},
+               {slot_map, max_tokens}, {free_head_out, 1}, {err_flag, 1}};
+    for (const auto& i : in)
+        for (const auto& o : out)
+            if (overlap(i.p, i.n, o.p, o.n))
+                return Q2K_ERR_BAD_SHAPE;
     int st = check_device();
     if (st != Q2K_OK)
         return st;

@@ -122,3 +122,23 @@ def test_a_request_that_outgrows_a_strided_table(lib):  # noqa: F811
     p = lib.kv_page_plan(i32(ctx), i32(new), page, i32(free), wide[:, :ld], 63, err_flag=err)
     assert wide[:, :ld].tolist() == want[0] and (wide[:, ld:] == -9).all()
     assert p.slot_map.tolist() == want[5] and p.free_head.item() == want[6] and err.item() == want[7] == 2
+
+
+def test_plan_arrays_side_by_side_and_over_one_another(lib):  # noqa: F811
+    """Inputs and outputs in one buffer, back to back, are fine; the lengths updated in place are refused."""
+    ctx, new, page, free = [3, 16, 40], [5, 0, 9], 16, list(range(50, 70))
+    want = plan_by_hand(ctx, new, page, free, 2, [[7, -7, -7, -7], [8, -7, -7, -7], [1, 2, 3, -7]], 15)
+    sizes = (3, 3, 20, 1, 4, 3, 15, 15, 15, 1)  # ctx, new, free, head, cu_q .. free_head
+    buf = torch.full((sum(sizes),), -77, dtype=torch.int32, device=DEV)
+    a, b, pool, head, *out = buf.split_with_sizes(sizes)
+    for x, v in ((a, ctx), (b, new), (pool, free), (head, [2])):
+        x.copy_(i32(v))
+    table = i32([[7, -7, -7, -7], [8, -7, -7, -7], [1, 2, 3, -7]])
+    out = lib.PagePlan._make(out)
+    p = lib.kv_page_plan(a, b, page, pool, table, 15, free_head=head, out=out)
+    got = (table.tolist(), p.cu_q.tolist(), p.seq_lens.tolist(), p.positions.tolist(), p.token_req.tolist(),
+           p.slot_map.tolist(), p.free_head.item())
+    assert got == want[:-1] and a.tolist() == ctx and b.tolist() == new
+    for wrong in (out._replace(seq_lens=a), out._replace(seq_lens=b), out._replace(free_head=head)):
+        with pytest.raises(lib.Q2KError):
+            lib.kv_page_plan(a, b, page, pool, table, 15, free_head=head, out=wrong)
