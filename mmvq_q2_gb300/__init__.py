@@ -399,9 +399,10 @@ Q2K_BF16 = 1
 _F32, _BF16, _I32, _I64, _U8 = torch.float32, torch.bfloat16, torch.int32, torch.int64, torch.uint8
 
 # The calls below run once or more per layer and step, where a few
-# microseconds of host time count.  Their arguments are read, checked and
-# passed on by a small extension module (csrc/q2k_python.c); here outputs are
-# allocated and a status becomes an exception.
+# microseconds of host time count.  Their arguments are read, checked (that
+# they fit one another, and lie on the current device) and passed on by a small
+# extension module (csrc/q2k_python.c); here outputs are allocated and a status
+# becomes an exception.
 _CALLS = ("kv_page_plan", "kv_rope_store", "kv_attention_bf16", "norm_gate_residual", "moe_route_topk",
           "kv_attention_workspace_bytes")
 _native = None
@@ -422,7 +423,8 @@ def _calls():
             m = importlib.util.module_from_spec(importlib.util.spec_from_loader("_q2kcall", loader))
             loader.exec_module(m)
             m.setup((_F32, _BF16, _I32, _I64, _U8),
-                    tuple(ctypes.cast(getattr(L, name), ctypes.c_void_p).value for name in _CALLS))
+                    tuple(ctypes.cast(getattr(L, name), ctypes.c_void_p).value for name in _CALLS),
+                    _cur_device or torch.cuda.current_device)
             _native = m
         return _native
 

@@ -16,8 +16,9 @@
 
 #include "../../include/q2k.h"
 
-static PyObject *n_is_cuda, *n_dtype, *n_data_ptr, *n_shape, *n_stride;
+static PyObject *n_get_device, *n_dtype, *n_data_ptr, *n_shape, *n_stride;
 static PyObject *t_f32, *t_bf16, *t_i32, *t_i64, *t_u8;
+static PyObject* current_device;  /* a callable */
 
 static int (*f_plan)(const int32_t*, const int32_t*, int64_t, int64_t, const int32_t*, int64_t, const int32_t*, int32_t*,
                      int64_t, int64_t, int32_t*, int32_t*, int32_t*, int32_t*, int32_t*, int64_t, int32_t*, int32_t*,
@@ -66,7 +67,38 @@ static int read_ints(PyObject* seq, int64_t* to, const char* name)
     return n;
 }
 
-/* A CUDA tensor of the given type (any, where type is NULL); None gives p = NULL when it may. */
+/* The device that the kernels of the call at hand run on, asked once a call. */
+static _Thread_local long launch_device;
+
+static void begin_call(void) { launch_device = -1; }
+
+static int on_launch_device(long device, const char* name)
+{
+    if (device < 0) {
+        PyErr_Format(PyExc_ValueError, "tensors must be on a CUDA device (%s is not)", name);
+        return -1;
+    }
+    if (launch_device < 0) {
+        PyObject* v = PyObject_CallNoArgs(current_device);
+        if (!v)
+            return -1;
+        launch_device = PyLong_AsLong(v);
+        Py_DECREF(v);
+        if (launch_device < 0) {
+            if (!PyErr_Occurred())
+                PyErr_SetString(PyExc_RuntimeError, "no current CUDA device");
+            return -1;
+        }
+    }
+    if (device != launch_device) {
+        PyErr_Format(PyExc_ValueError, "tensors must be on the current CUDA device, %ld (%s is on %ld)", launch_device, name,
+                     device);
+        return -1;
+    }
+    return 0;
+}
+
+/* A tensor of the current CUDA device and the given type (any, where type is NULL); None gives p = NULL when it may. */
 static int read_tensor(PyObject* t, PyObject* type, const char* name, int may_be_none, Tensor* x)
 {
     x->p = NULL;
@@ -79,15 +111,13 @@ static int read_tensor(PyObject* t, PyObject* type, const char* name, int may_be
         PyErr_Format(PyExc_ValueError, "%s is required", name);
         return -1;
     }
-    PyObject* v = PyObject_GetAttr(t, n_is_cuda);
+    PyObject* v = PyObject_CallMethodNoArgs(t, n_get_device);  /* -1 on the host */
     if (!v)
         return -1;
-    const int cuda = v == Py_True;
+    const long device = PyLong_AsLong(v);
     Py_DECREF(v);
-    if (!cuda) {
-        PyErr_Format(PyExc_ValueError, "tensors must be on a CUDA device (%s is not)", name);
+    if ((device == -1 && PyErr_Occurred()) || on_launch_device(device, name))
         return -1;
-    }
     if (!(v = PyObject_GetAttr(t, n_dtype)))
         return -1;
     x->dtype = v;
@@ -205,6 +235,7 @@ static PyObject* status(int st) { return PyLong_FromLong(st); }
 static PyObject* py_plan(PyObject* self, PyObject* const* a, Py_ssize_t n)
 {
     (void)self;
+    begin_call();
     Tensor ctx, add, pool, head, table, err, o[6];
     static const char* const names[6] = {"cu_q", "seq_lens", "positions", "token_req", "slot_map", "free_head"};
     if (want_args(n, 10) || read_dense(a[0], t_i32, "ctx_lens", 0, &ctx) ||
@@ -261,6 +292,7 @@ static PyObject* py_plan(PyObject* self, PyObject* const* a, Py_ssize_t n)
 static PyObject* py_rope(PyObject* self, PyObject* const* a, Py_ssize_t n)
 {
     (void)self;
+    begin_call();
     Tensor q, k, v, pos, freq, slots, kc, vc, out, err;
     if (want_args(n, 13) || read_tensor(a[1], NULL, "k", 0, &k))
         return NULL;
@@ -306,6 +338,7 @@ static PyObject* py_rope(PyObject* self, PyObject* const* a, Py_ssize_t n)
 static PyObject* py_attn(PyObject* self, PyObject* const* a, Py_ssize_t n)
 {
     (void)self;
+    begin_call();
     Tensor q, kc, vc, table, cu, seq, out, lse, ws;
     int64_t ld_q, ld_o, ld_t = 0, page_stride;
     if (want_args(n, 12) || read_tensor(a[0], t_bf16, "q", 0, &q) || read_tensor(a[1], t_bf16, "k_cache", 0, &kc) ||
@@ -356,6 +389,7 @@ static PyObject* py_attn_bytes(PyObject* self, PyObject* const* a, Py_ssize_t n)
 static PyObject* py_norm(PyObject* self, PyObject* const* a, Py_ssize_t n)
 {
     (void)self;
+    begin_call();
     Tensor res, pre, y, post, gate, ro, out, q8;
     if (want_args(n, 11) || read_tensor(a[0], NULL, "residual", 0, &res))
         return NULL;
@@ -409,6 +443,7 @@ static PyObject* py_norm(PyObject* self, PyObject* const* a, Py_ssize_t n)
 static PyObject* py_route(PyObject* self, PyObject* const* a, Py_ssize_t n)
 {
     (void)self;
+    begin_call();
     Tensor x, bias, ids, w, table, ptrs;
     int64_t ld;
     if (want_args(n, 13) || read_tensor(a[0], NULL, "logits", 0, &x))
@@ -443,11 +478,11 @@ static PyObject* py_route(PyObject* self, PyObject* const* a, Py_ssize_t n)
                           stream));
 }
 
-/* setup((fp32, bf16, int32, int64, uint8), (addresses of the six functions)) */
+/* setup((fp32, bf16, int32, int64, uint8), (addresses of the six functions), callable: the current device's index) */
 static PyObject* py_setup(PyObject* self, PyObject* const* a, Py_ssize_t n)
 {
     (void)self;
-    if (want_args(n, 2))
+    if (want_args(n, 3))
         return NULL;
     void* f[6];
     if (!PyArg_ParseTuple(a[0], "OOOOO", &t_f32, &t_bf16, &t_i32, &t_i64, &t_u8))
@@ -460,6 +495,7 @@ static PyObject* py_setup(PyObject* self, PyObject* const* a, Py_ssize_t n)
             return NULL;
         }
     }
+    Py_XSETREF(current_device, Py_NewRef(a[2]));
     Py_INCREF(t_f32);
     Py_INCREF(t_bf16);
     Py_INCREF(t_i32);
@@ -488,12 +524,12 @@ static struct PyModuleDef module = {PyModuleDef_HEAD_INIT, "_q2kcall", NULL, -1,
 
 PyMODINIT_FUNC PyInit__q2kcall(void)
 {
-    n_is_cuda = PyUnicode_InternFromString("is_cuda");
+    n_get_device = PyUnicode_InternFromString("get_device");
     n_dtype = PyUnicode_InternFromString("dtype");
     n_data_ptr = PyUnicode_InternFromString("data_ptr");
     n_shape = PyUnicode_InternFromString("shape");
     n_stride = PyUnicode_InternFromString("stride");
-    if (!n_is_cuda || !n_dtype || !n_data_ptr || !n_shape || !n_stride)
+    if (!n_get_device || !n_dtype || !n_data_ptr || !n_shape || !n_stride)
         return NULL;
     return PyModule_Create(&module);
 }
