@@ -418,7 +418,8 @@ def _calls():
         if _native is None:
             path = os.path.join(os.path.dirname(LIB_PATH), "_q2kcall" + (sysconfig.get_config_var("EXT_SUFFIX") or ".so"))
             if not os.path.exists(path):
-                raise RuntimeError(f"{path} is missing: build it with `python -m mmvq_q2_gb300.build`")
+                raise RuntimeError(f"{path} is missing: build it with `python -m mmvq_q2_gb300.build` "
+                                   "(it needs a host C compiler and Python.h)")
             loader = importlib.machinery.ExtensionFileLoader("_q2kcall", path)
             m = importlib.util.module_from_spec(importlib.util.spec_from_loader("_q2kcall", loader))
             loader.exec_module(m)

@@ -3,12 +3,15 @@ the binding's native half with the host's C compiler and Python's headers.
 
 Usage: ``python -m mmvq_q2_gb300.build`` or ``build()`` from Python.  The
 translation units compile in parallel; the shared library lands in
-``mmvq_q2_gb300/_lib/libq2k.so``, the extension module beside it.
+``mmvq_q2_gb300/_lib/libq2k.so``, the extension module beside it.  Where there
+is no Python.h or no host C compiler the library is built all the same, and
+the Python calls that need the extension module say so.
 """
 from __future__ import annotations
 
 import concurrent.futures as cf
 import os
+import shlex
 import shutil
 import subprocess
 import sys
@@ -37,10 +40,25 @@ def _flags(extra=()):
                    "-Xptxas", "-warn-spills"] + list(extra)
 
 
+def host_cc():
+    """The host's C compiler as a list of words ($CC may have arguments), None without one."""
+    cc = shlex.split(os.environ.get("CC", "")) or [shutil.which("gcc") or shutil.which("cc")]
+    return cc if cc[0] else None
+
+
+def _no_calls() -> str:
+    """Why the extension module cannot be built here; empty where it can."""
+    include = sysconfig.get_paths()["include"]
+    if not os.path.exists(os.path.join(include, "Python.h")):
+        return f"no Python.h in {include}"
+    return "" if host_cc() else "no host C compiler"
+
+
 def _up_to_date() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(CALLS):
+    built = [LIB] + ([] if _no_calls() and not os.path.exists(CALLS) else [CALLS])
+    if not all(os.path.exists(f) for f in built):
         return False
-    t = min(os.path.getmtime(LIB), os.path.getmtime(CALLS))
+    t = min(os.path.getmtime(f) for f in built)
     deps = [os.path.join(CSRC, f) for f in os.listdir(CSRC)]
     deps.append(os.path.join(os.path.dirname(HERE), "include", "q2k.h"))
     return all(os.path.getmtime(d) <= t for d in deps)
@@ -61,21 +79,25 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
         return obj, r.stderr
 
     def compile_calls():
+        why = _no_calls()
+        if why:
+            if os.path.exists(CALLS):  # of older sources
+                os.remove(CALLS)
+            print(f"{os.path.basename(CALLS)} is not built ({why}): the decode-layer calls of the Python binding need it",
+                  file=sys.stderr)
+            return
         tmp = CALLS + f".{os.getpid()}.tmp"
-        host = os.environ.get("CC") or shutil.which("gcc") or shutil.which("cc")
-        if host is None:
-            raise RuntimeError("no host C compiler found")
-        cmd = [host, "-O2", "-std=c11", "-Wall", "-shared", "-fPIC", "-I", sysconfig.get_paths()["include"],
+        host = host_cc()
+        cmd = [*host, "-O2", "-std=c11", "-Wall", "-shared", "-fPIC", "-I", sysconfig.get_paths()["include"],
                os.path.join(CSRC, CALLS_SOURCE), "-o", tmp, "-lm"]
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
-            raise RuntimeError(f"{host} failed on {CALLS_SOURCE}:\n{r.stdout}\n{r.stderr}")
+            raise RuntimeError(f"{host[0]} failed on {CALLS_SOURCE}:\n{r.stdout}\n{r.stderr}")
         os.replace(tmp, CALLS)
 
     with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
         calls = ex.submit(compile_calls)
         results = list(ex.map(compile_one, SOURCES))
-        calls.result()
     if verbose:
         for obj, err in results:
             if err.strip():
@@ -86,6 +108,7 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+    calls.result()  # the library does not depend on it
     return LIB
 
 
