@@ -643,8 +643,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     volatile int* abort_flag = &sh.abort_flag;
 
     if (smem_u32(smem) & 1023u) {  // the swizzle repeats every 1024 bytes
-        if (threadIdx.x == 0)
+        pdl_wait();
+        if (threadIdx.x == 0) {
+            a.heads[blockIdx.x].first = -1;  // nothing to join
             atomicOr(&g_attn_error, kErrSetup);
+        }
         return;
     }
     if (threadIdx.x == 32) {
