@@ -505,7 +505,9 @@ int kv_attention_bf16(const uint16_t* q, int64_t ld_q, int64_t T, int64_t Hq, in
  *   h = residual + alpha * u                -> residual_out
  *   n = h / rms(h) * pre_w                  -> out (bf16), out_q8 (q8_1)
  * rms(z) = sqrt(mean(z^2) + eps); fp32 throughout, each result rounded once
- * (n comes from the unrounded h).
+ * (n comes from the unrounded h).  The squares of a row have to add up within
+ * fp32's range (values up to about 1e17): past it rms is infinite, and the
+ * row's u or n is 0.
  *   y, gate       y_type, rows ld_y / ld_gate apart; ld_gate 0: one row for
  *                 every token.  y NULL needs post_w and gate NULL.
  *   residual      stream_type, rows ld_res apart; residual_out likewise,
