@@ -58,3 +58,22 @@ def test_route_decides_by_small_gaps(lib, case):  # noqa: F811
     got_ids, got_w = lib.moe_route_topk(x, topk, n_group=groups, topk_group=topk_group, renorm=renorm)
     assert torch.equal(got_ids.cpu(), ids)
     within(got_w.cpu(), w, 2.0 ** -20 * w.abs(), "weights")
+
+
+@pytest.mark.parametrize("T, dim", [(3, 4096), (700, 2880), (3, 1001), (900, 64)])  # few and many rows, value by value
+def test_norm_without_some_of_its_outputs(lib, T, dim):  # noqa: F811
+    """The C call takes NULL for outputs that are not wanted; the others have the bits that they have beside them."""
+    g = gen(T + dim)
+    res, y, post, pre = normal(g, T, dim), normal(g, T, dim), normal(g, dim), normal(g, dim)
+    q8 = dim % 32 == 0
+    want = lib.norm_gate_residual(res, pre, 1e-6, y=y, post_w=post, alpha=0.5, want_q8=q8)
+    stream = torch.cuda.current_stream().cuda_stream
+    for keep in ((0,), (1,), (2,), (0, 1), (1, 2), (0, 2)):
+        if 2 in keep and not q8:
+            continue
+        got = [torch.full_like(w, 1) if i in keep else None for i, w in enumerate(want)] + [None] * (not q8)
+        h, n, e = (None if t is None else t.data_ptr() for t in got)
+        assert lib.lib().norm_gate_residual(y.data_ptr(), 0, dim, post.data_ptr(), None, 0, res.data_ptr(), 0, dim, 0.5,
+                                            pre.data_ptr(), 1e-6, T, dim, h, dim, n, dim, e, stream) == 0
+        for i in keep:
+            assert torch.equal(got[i], want[i]), (keep, i)
