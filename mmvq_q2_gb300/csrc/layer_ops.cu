@@ -107,8 +107,8 @@ __device__ __forceinline__ void encode_row(const uint16_t* n_row, int dim, uint8
     }
 }
 
-// 8 values of a row as they lie in memory, one load (32 bytes of fp32 in one
-// where they are aligned so; a row's start need only be on 16 bytes).
+// 8 values of a row as they lie in memory: a load of 16 bytes, of fp32 two (a
+// row's start need only be on 16 bytes).
 template <bool BF16>
 struct Raw8 {
     uint4 w[BF16 ? 1 : 2];
