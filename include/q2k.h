@@ -552,6 +552,88 @@ int moe_route_topk(const void* logits, int type, int64_t m, int64_t E, int64_t l
                    int64_t n_group, int64_t topk_group, int64_t topk, int renorm, float scale, int32_t* ids,
                    float* weights, const int64_t* expert_ptrs, int64_t* ptrs_out, q2k_stream_t stream);
 
+/* ---- 8-bit floating-point weights ----------------------------------------
+ *
+ * Beside the k-quants: matrices and activations in e4m3 (one byte a value, a
+ * sign, 4 exponent bits of bias 7, 3 mantissa bits, no infinities, 0x7f and
+ * 0xff NaN, largest value 448) with fp32 scales over blocks of 128 along K:
+ * a matrix [N, K] has a scale for each 128 x 128 values, [ceil(N / 128),
+ * ceil(K / 128)]; activation rows [m, K] have one for each 128 values,
+ * [m, ceil(K / 128)].  The last block of a row or column may be short.  A
+ * value stands for code * scale. */
+
+/* Encode rows or a matrix.
+ *   x       x_type [rows, K], rows ldx apart
+ *   block_rows  1: a scale for each 128 values of a row (activations);
+ *               128: one for each 128 x 128 values (weights)
+ *   q       [rows, K] codes, rows ldq apart
+ *   scales  fp32 [ceil(rows / block_rows), ceil(K / 128)], rows ld_scales
+ *           apart
+ * With c = max(largest |x| of the block, 448 * 2^-120): scale = c / 448 and
+ * q = the e4m3 value nearest to x * (448 * (1 / c)), ties to even; each of
+ * these operations in fp32 and rounded.  (Values below 2^-111 share the scale
+ * of that size.)  A block with a NaN or an infinity gets scale NaN and codes
+ * NaN.
+ * 0 <= rows, 1 <= K <= 2^20.  One launch. */
+int fp8_quantize(const void* x, int x_type, int64_t rows, int64_t K, int64_t ldx, int64_t block_rows, uint8_t* q,
+                 int64_t ldq, float* scales, int64_t ld_scales, q2k_stream_t stream);
+
+/* SwiGLU and the encoding of its rows (the twin of swiglu_q8_1_rows).
+ *   gate_up  type [rows, 2 N], rows ld apart: N gate values, then N up values
+ *   q, ldq, scales, ld_scales   as for fp8_quantize of [rows, N], block_rows 1
+ * h = g / (1 + e^-g) * u in fp32 (expf), not rounded before it is encoded.
+ * 0 <= rows, 1 <= N <= 2^19.  One launch. */
+int swiglu_fp8_rows(const void* gate_up, int type, int64_t rows, int64_t N, int64_t ld, uint8_t* q, int64_t ldq,
+                    float* scales, int64_t ld_scales, q2k_stream_t stream);
+
+/* y = x W^T over e4m3 operands.
+ *   x         [m, K] codes, rows ldx apart, 16-byte aligned, ldx % 16 == 0
+ *   x_scales  fp32 [m, ceil(K / 128)], rows ld_xs apart
+ *   W         [N, K] codes, contiguous, 16-byte aligned
+ *   w_scales  fp32 [ceil(N / 128), ceil(K / 128)], contiguous
+ *   y         y_type [m, N], rows ldy apart
+ * y[t, n] = sum over blocks b of x_scales[t, b] * w_scales[n / 128, b] *
+ * (sum over k in b of x[t, k] w[n, k]): the inner sums on the tensor cores
+ * with fp32 accumulation, scaled and added in fp32, rounded once to bf16
+ * where y is bf16.  A call repeats bit for bit.
+ * 0 <= m, 1 <= N, m and N below 2^30, K % 16 == 0, 16 <= K <= 2^20.  One launch.
+ * Q2K_ERR_UNSUPPORTED when the CUDA driver offers no tensor-map encoder. */
+int fp8_gemm(const uint8_t* x, int64_t m, int64_t K, int64_t ldx, const float* x_scales, int64_t ld_xs,
+             const uint8_t* W, int64_t N, const float* w_scales, void* y, int y_type, int64_t ldy,
+             q2k_stream_t stream);
+
+/* Workspace bytes fp8_moe needs (0 for a bad shape). */
+size_t fp8_moe_workspace_bytes(int64_t m, int64_t topk, int64_t dim, int64_t inter);
+
+/* The routed experts of a few tokens as one call: gate and up, SwiGLU, down,
+ * the route-weighted sum, every expert that a token chose read once for all
+ * its tokens (up to the 16 that one pass takes).
+ *   x         bf16 [m, dim], rows ldx apart
+ *   ids       int32 [m, topk]: experts; one outside [0, E) counts nothing
+ *             (a step of fixed size can be padded with -1), one that a token
+ *             names twice counts twice
+ *   route_w   fp32 [m, topk]
+ *   gate_up   [E, 2, inter, dim] codes: gate rows, then up rows, 16-byte
+ *             aligned;  gate_up_scales  fp32 [E, 2, ceil(inter / 128),
+ *             ceil(dim / 128)]
+ *   down      [E, dim, inter] codes, 16-byte aligned;  down_scales  fp32
+ *             [E, ceil(dim / 128), ceil(inter / 128)]
+ *   y         y_type [m, dim], rows ldy apart:  y[t] = sum over j of
+ *             route_w[t, j] * (down_e h),  h = g / (1 + e^-g) * u,
+ *             g = gate_e x_t,  u = up_e x_t,  e = ids[t, j]
+ * Products accumulate in fp32 as in fp8_gemm; x enters as it is (bf16), h
+ * is rounded to bf16 (as the buffers of the other expert calls are); the sum
+ * over j is fp32 in j's order; rounded once to bf16 where y is bf16.  A call
+ * repeats bit for bit.  A token with a NaN or an infinity gives NaN.
+ *   workspace  at least fp8_moe_workspace_bytes(m, topk, dim, inter) bytes,
+ *              256-byte aligned; calls that overlap need one each
+ * 0 <= m <= 128, 1 <= topk <= 32, m * topk <= 1024, 1 <= E <= 1024, dim and
+ * inter multiples of 16, 16..16384.  Two launches. */
+int fp8_moe(const uint16_t* x, int64_t m, int64_t dim, int64_t ldx, const int32_t* ids, const float* route_w,
+            int64_t topk, int64_t E, const uint8_t* gate_up, const float* gate_up_scales, const uint8_t* down,
+            const float* down_scales, int64_t inter, void* y, int y_type, int64_t ldy, void* workspace,
+            size_t workspace_bytes, q2k_stream_t stream);
+
 /* Human-readable name of a status code (static string). */
 const char* q2k_status_string(int status);
 

@@ -36,6 +36,7 @@ EXPORTS = (
     "q2k_last_cuda_error", "q2k_device_error",
     "kv_page_plan", "kv_rope_store", "kv_attention_workspace_bytes", "kv_attention_bf16", "norm_gate_residual",
     "moe_route_topk",
+    "fp8_quantize", "swiglu_fp8_rows", "fp8_gemm", "fp8_moe_workspace_bytes", "fp8_moe",
 )
 
 Q2K_OK = 0
@@ -105,6 +106,11 @@ def lib() -> ctypes.CDLL:
             "norm_gate_residual": (I32, [P, I32, I64, P, P, I64, P, I32, I64, ctypes.c_float, P, ctypes.c_float, I64, I64,
                                          P, I64, P, I64, P, P]),
             "moe_route_topk": (I32, [P, I32, I64, I64, I64, P, I32, I64, I64, I64, I32, ctypes.c_float, P, P, P, P, P]),
+            "fp8_quantize": (I32, [P, I32, I64, I64, I64, I64, P, I64, P, I64, P]),
+            "swiglu_fp8_rows": (I32, [P, I32, I64, I64, I64, P, I64, P, I64, P]),
+            "fp8_gemm": (I32, [P, I64, I64, I64, P, I64, P, I64, P, P, I32, I64, P]),
+            "fp8_moe_workspace_bytes": (SZ, [I64, I64, I64, I64]),
+            "fp8_moe": (I32, [P, I64, I64, I64, P, P, I64, I64, P, P, P, P, I64, P, I32, I64, P, SZ, P]),
             "q2k_status_string": (ctypes.c_char_p, [I32]),
             "q2k_last_cuda_error": (I32, []),
             "q2k_device_error": (I32, [ctypes.POINTER(ctypes.c_int32), I32]),
@@ -405,6 +411,8 @@ _F32, _BF16, _I32, _I64, _U8 = torch.float32, torch.bfloat16, torch.int32, torch
 # becomes an exception.
 _CALLS = ("kv_page_plan", "kv_rope_store", "kv_attention_bf16", "norm_gate_residual", "moe_route_topk",
           "kv_attention_workspace_bytes")
+_FP8_CALLS = ("fp8_quantize", "swiglu_fp8_rows", "fp8_gemm", "fp8_moe", "fp8_moe_workspace_bytes")
+_E4M3 = torch.float8_e4m3fn
 _native = None
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 _cur_device = getattr(torch._C, "_cuda_getDevice", None)
@@ -426,6 +434,7 @@ def _calls():
             m.setup((_F32, _BF16, _I32, _I64, _U8),
                     tuple(ctypes.cast(getattr(L, name), ctypes.c_void_p).value for name in _CALLS),
                     _cur_device or torch.cuda.current_device)
+            m.setup_fp8(_E4M3, tuple(ctypes.cast(getattr(L, name), ctypes.c_void_p).value for name in _FP8_CALLS))
             _native = m
         return _native
 
@@ -570,6 +579,76 @@ def moe_route_topk(logits, topk, bias=None, score="softmax", n_group=1, topk_gro
     if st:
         raise Q2KError("moe_route_topk", st)
     return (ids, weights) if ptrs is None else (ids, weights, ptrs)
+
+
+def fp8_quantize(x, block_rows=1, values=None, scales=None, stream=None):
+    """``x [rows, K]`` (fp32 or bf16, row stride allowed) -> (e4m3 values
+    ``[rows, K]``, fp32 scales ``[rows, ceil(K/128)]``), a scale for each 128
+    values of a row; with ``block_rows=128`` one for each 128 x 128 values,
+    ``[ceil(rows/128), ceil(K/128)]`` (weights)."""
+    if block_rows not in (1, 128):
+        raise ValueError("block_rows must be 1 or 128")
+    device, (n, K) = _cuda_device(x, "x"), x.shape
+    if values is None:
+        values = _empty((n, K), _E4M3, device, stream)
+    if scales is None:
+        scales = _empty((n if block_rows == 1 else -(-n // 128), -(-K // 128)), _F32, device, stream)
+    st = (_native or _calls()).fp8_quantize(x, block_rows, values, scales, _stream_handle(stream))
+    if st:
+        raise Q2KError("fp8_quantize", st)
+    return values, scales
+
+
+def swiglu_fp8_rows(gate_up, values=None, scales=None, stream=None):
+    """``silu(gate) * up`` of ``gate_up [rows, 2 N]`` (fp32 or bf16: gate
+    values, then up values; row stride allowed) -> (e4m3 values ``[rows, N]``,
+    fp32 scales ``[rows, ceil(N/128)]``)."""
+    device, (n, K) = _cuda_device(gate_up, "gate_up"), gate_up.shape
+    if values is None:
+        values = _empty((n, K // 2), _E4M3, device, stream)
+    if scales is None:
+        scales = _empty((n, (K // 2 + 127) // 128), _F32, device, stream)
+    st = (_native or _calls()).swiglu_fp8_rows(gate_up, 1, values, scales, _stream_handle(stream))
+    if st:
+        raise Q2KError("swiglu_fp8_rows", st)
+    return values, scales
+
+
+def fp8_gemm(x, x_scales, w, w_scales, out=None, out_dtype=_F32, stream=None):
+    """e4m3 ``x [m, K]`` (row stride allowed) times e4m3 ``w [N, K]``^T with
+    their scales ``[m, ceil(K/128)]`` and ``[ceil(N/128), ceil(K/128)]`` ->
+    ``[m, N]``, fp32 or bf16."""
+    device, m = _cuda_device(x, "x"), x.shape[0]
+    if out is None:
+        out = _empty((m, w.shape[0]), out_dtype, device, stream)
+    st = (_native or _calls()).fp8_gemm(x, x_scales, w, w_scales, out, _stream_handle(stream))
+    if st:
+        raise Q2KError("fp8_gemm", st)
+    return out
+
+
+def fp8_moe_workspace_bytes(m, topk, dim, inter) -> int:
+    return lib().fp8_moe_workspace_bytes(m, topk, dim, inter)
+
+
+def fp8_moe(x, ids, route_w, gate_up, gate_up_scales, down, down_scales, out=None, out_dtype=_F32, workspace=None,
+            stream=None):
+    """The routed experts of a few tokens: bf16 ``x [m, dim]`` (row stride
+    allowed), ``ids`` int32 and ``route_w`` fp32 ``[m, topk]`` (as
+    ``moe_route_topk`` gives them; ids outside ``[0, E)`` count nothing), e4m3
+    ``gate_up [E, 2, inter, dim]`` and ``down [E, dim, inter]`` with their
+    scales -> ``[m, dim]``, fp32 or bf16."""
+    shape, device = x.shape, _cuda_device(x, "x")
+    if out is None:
+        out = _empty(shape, out_dtype, device, stream)
+    if workspace is None:
+        need = (_native or _calls()).fp8_moe_workspace_bytes(shape[0], ids.shape[-1], shape[1], down.shape[-1])
+        workspace = _empty(need, _U8, device, stream)
+    st = (_native or _calls()).fp8_moe(x, ids, route_w, gate_up, gate_up_scales, down, down_scales, out, workspace,
+                                       _stream_handle(stream))
+    if st:
+        raise Q2KError("fp8_moe", st)
+    return out
 
 
 def q2k_device_error(clear=True) -> int:

@@ -22,7 +22,7 @@ CSRC = os.path.join(HERE, "csrc")
 OUT = os.path.join(HERE, "_lib")
 LIB = os.path.join(OUT, "libq2k.so")
 SOURCES = ["q2k_api.cu", "q2k_mv.cu", "q2k_m1.cu", "q2k_mmq.cu", "q2k_mt.cu", "q2k_small.cu", "q2k_gemm.cu", "q2k_umma.cu", "q3k_mv.cu", "q3k_mt.cu",
-           "kv_page.cu", "kv_attn.cu", "layer_ops.cu"]
+           "kv_page.cu", "kv_attn.cu", "layer_ops.cu", "fp8_ops.cu", "fp8_gemm.cu", "fp8_stream.cu"]
 CALLS_SOURCE = "q2k_python.c"
 CALLS = os.path.join(OUT, "_q2kcall" + (sysconfig.get_config_var("EXT_SUFFIX") or ".so"))
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

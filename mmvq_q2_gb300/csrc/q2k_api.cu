@@ -101,6 +101,14 @@ bool cache_ok(int64_t n_pages, int64_t page_size, int64_t page_stride, int64_t H
            page_stride >= Hkv * page_size * D && page_stride % 8 == 0 && page_stride < ((int64_t)1 << 36);
 }
 
+int64_t fp8_blocks(int64_t K) { return (K + 127) / 128; }
+
+bool fp8_moe_shape_ok(int64_t m, int64_t topk, int64_t dim, int64_t inter)
+{
+    return m >= 0 && m <= 128 && topk >= 1 && topk <= 32 && m * topk <= 1024 && dim >= 16 && dim <= 16384 &&
+           dim % 16 == 0 && inter >= 16 && inter <= 16384 && inter % 16 == 0;
+}
+
 bool attn_heads_ok(int64_t Hq, int64_t Hkv, int64_t D)
 {
     return Hkv >= 1 && Hkv <= 4096 && Hq >= Hkv && Hq % Hkv == 0 && Hq / Hkv <= 128 && D >= 16 && D <= 128 && D % 16 == 0;
@@ -931,6 +939,145 @@ int moe_route_topk(const void* logits, int type, int64_t m, int64_t E, int64_t l
     p.expert_ptrs = expert_ptrs;
     p.ptrs_out = ptrs_out;
     return finish(launch_moe_route(p, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int fp8_quantize(const void* x, int x_type, int64_t rows, int64_t K, int64_t ldx, int64_t block_rows, uint8_t* q,
+                 int64_t ldq, float* scales, int64_t ld_scales, q2k_stream_t stream)
+{
+    if (rows != 0 && (!x || !q || !scales))
+        return Q2K_ERR_NULL_ARG;
+    if (!type_ok(x_type) || rows < 0 || rows > (1 << 30) || K < 1 || K > kMaxK || (block_rows != 1 && block_rows != 128) ||
+        ldx < K || ldq < K || ld_scales < fp8_blocks(K))
+        return Q2K_ERR_BAD_SHAPE;
+    if (!aligned(x, x_type == Q2K_BF16 ? 2 : 4) || !aligned(scales, 4))
+        return Q2K_ERR_MISALIGNED;
+    int st = check_device();
+    if (st != Q2K_OK)
+        return st;
+    if (rows == 0)
+        return Q2K_OK;
+    Fp8Encode p{};
+    p.x = x;
+    p.x_bf16 = x_type == Q2K_BF16;
+    p.block_rows = (int)block_rows;
+    p.rows = rows;
+    p.K = K;
+    p.ldx = ldx;
+    p.q = q;
+    p.ldq = ldq;
+    p.scales = scales;
+    p.ld_scales = ld_scales;
+    return finish(launch_fp8_encode(p, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int swiglu_fp8_rows(const void* gate_up, int type, int64_t rows, int64_t N, int64_t ld, uint8_t* q, int64_t ldq,
+                    float* scales, int64_t ld_scales, q2k_stream_t stream)
+{
+    if (rows != 0 && (!gate_up || !q || !scales))
+        return Q2K_ERR_NULL_ARG;
+    if (!type_ok(type) || rows < 0 || rows > (1 << 30) || N < 1 || N > kMaxK / 2 || ld < 2 * N || ldq < N ||
+        ld_scales < fp8_blocks(N))
+        return Q2K_ERR_BAD_SHAPE;
+    if (!aligned(gate_up, type == Q2K_BF16 ? 2 : 4) || !aligned(scales, 4))
+        return Q2K_ERR_MISALIGNED;
+    int st = check_device();
+    if (st != Q2K_OK)
+        return st;
+    if (rows == 0)
+        return Q2K_OK;
+    Fp8Encode p{};
+    p.x = gate_up;
+    p.x_bf16 = type == Q2K_BF16;
+    p.swiglu = 1;
+    p.block_rows = 1;
+    p.rows = rows;
+    p.K = N;
+    p.ldx = ld;
+    p.q = q;
+    p.ldq = ldq;
+    p.scales = scales;
+    p.ld_scales = ld_scales;
+    return finish(launch_fp8_encode(p, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int fp8_gemm(const uint8_t* x, int64_t m, int64_t K, int64_t ldx, const float* x_scales, int64_t ld_xs,
+             const uint8_t* W, int64_t N, const float* w_scales, void* y, int y_type, int64_t ldy, q2k_stream_t stream)
+{
+    if (!W || !w_scales || (m != 0 && (!x || !x_scales || !y)))
+        return Q2K_ERR_NULL_ARG;
+    if (!type_ok(y_type) || m < 0 || m >= (1 << 30) || N < 1 || N >= (1 << 30) || K < 16 || K > kMaxK || K % 16 ||
+        ldx < K || ldx % 16 || ldx >= ((int64_t)1 << 36) || ld_xs < fp8_blocks(K) || ldy < N)
+        return Q2K_ERR_BAD_SHAPE;
+    if (!aligned(x, 16) || !aligned(W, 16) || !aligned(x_scales, 4) || !aligned(w_scales, 4) ||
+        !aligned(y, y_type == Q2K_BF16 ? 2 : 4))
+        return Q2K_ERR_MISALIGNED;
+    int st = check_device();
+    if (st != Q2K_OK)
+        return st;
+    if (m == 0)
+        return Q2K_OK;
+    Fp8Gemm p{};
+    p.x = x;
+    p.m = m;
+    p.K = K;
+    p.ldx = ldx;
+    p.x_scales = x_scales;
+    p.ld_xs = ld_xs;
+    p.W = W;
+    p.N = N;
+    p.w_scales = w_scales;
+    p.y = y;
+    p.y_bf16 = y_type == Q2K_BF16;
+    p.ldy = ldy;
+    return finish(launch_fp8_gemm(p, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+size_t fp8_moe_workspace_bytes(int64_t m, int64_t topk, int64_t dim, int64_t inter)
+{
+    if (!fp8_moe_shape_ok(m, topk, dim, inter))
+        return 0;
+    return fp8_moe_workspace(m, topk, dim, inter);
+}
+
+int fp8_moe(const uint16_t* x, int64_t m, int64_t dim, int64_t ldx, const int32_t* ids, const float* route_w,
+            int64_t topk, int64_t E, const uint8_t* gate_up, const float* gate_up_scales, const uint8_t* down,
+            const float* down_scales, int64_t inter, void* y, int y_type, int64_t ldy, void* workspace,
+            size_t workspace_bytes, q2k_stream_t stream)
+{
+    if (!gate_up || !gate_up_scales || !down || !down_scales || (m != 0 && (!x || !ids || !route_w || !y)))
+        return Q2K_ERR_NULL_ARG;
+    if (!fp8_moe_shape_ok(m, topk, dim, inter) || !type_ok(y_type) || E < 1 || E > 1024 || ldx < dim || ldy < dim)
+        return Q2K_ERR_BAD_SHAPE;
+    if (m != 0 && (!workspace || workspace_bytes < fp8_moe_workspace(m, topk, dim, inter)))
+        return Q2K_ERR_WORKSPACE;
+    if (!aligned(x, 2) || !aligned(ids, 4) || !aligned(route_w, 4) || !aligned(gate_up, 16) || !aligned(down, 16) ||
+        !aligned(gate_up_scales, 4) || !aligned(down_scales, 4) || !aligned(y, y_type == Q2K_BF16 ? 2 : 4) ||
+        !aligned(workspace, 256))
+        return Q2K_ERR_MISALIGNED;
+    int st = check_device();
+    if (st != Q2K_OK)
+        return st;
+    if (m == 0)
+        return Q2K_OK;
+    Fp8Moe p{};
+    p.x = x;
+    p.m = m;
+    p.dim = dim;
+    p.ldx = ldx;
+    p.ids = ids;
+    p.route_w = route_w;
+    p.topk = (int)topk;
+    p.E = (int)E;
+    p.gate_up = gate_up;
+    p.gate_up_scales = gate_up_scales;
+    p.down = down;
+    p.down_scales = down_scales;
+    p.inter = inter;
+    p.y = y;
+    p.y_bf16 = y_type == Q2K_BF16;
+    p.ldy = ldy;
+    p.workspace = workspace;
+    return finish(launch_fp8_moe(p, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -245,6 +245,56 @@ struct RouteProblem {
 };
 cudaError_t launch_moe_route(const RouteProblem& p, cudaStream_t s);
 
+// Encoders of e4m3 rows and blocks (fp8_ops.cu; q2k.h, fp8_quantize and
+// swiglu_fp8_rows).
+struct Fp8Encode {
+    const void* x;
+    int x_bf16;
+    int swiglu;      // x is [rows, 2 K]: gate, then up
+    int block_rows;  // 1 or 128
+    int64_t rows, K, ldx;
+    uint8_t* q;
+    int64_t ldq;
+    float* scales;
+    int64_t ld_scales;
+};
+cudaError_t launch_fp8_encode(const Fp8Encode& p, cudaStream_t s);
+
+// The product of e4m3 operands (fp8_gemm.cu, and fp8_stream.cu for few tokens).
+struct Fp8Gemm {
+    const uint8_t* x;
+    int64_t m, K, ldx;
+    const float* x_scales;
+    int64_t ld_xs;
+    const uint8_t* W;
+    int64_t N;
+    const float* w_scales;
+    void* y;
+    int y_bf16;
+    int64_t ldy;
+};
+cudaError_t launch_fp8_gemm(const Fp8Gemm& p, cudaStream_t s);
+
+// The routed experts of a few tokens (fp8_stream.cu; q2k.h, fp8_moe).
+struct Fp8Moe {
+    const uint16_t* x;
+    int64_t m, dim, ldx;
+    const int32_t* ids;
+    const float* route_w;
+    int topk, E;
+    const uint8_t* gate_up;
+    const float* gate_up_scales;
+    const uint8_t* down;
+    const float* down_scales;
+    int64_t inter;
+    void* y;
+    int y_bf16;
+    int64_t ldy;
+    void* workspace;
+};
+size_t fp8_moe_workspace(int64_t m, int64_t topk, int64_t dim, int64_t inter);
+cudaError_t launch_fp8_moe(const Fp8Moe& p, cudaStream_t s);
+
 // Read (and optionally clear) this translation unit's device error word.
 cudaError_t mv_error_word(int32_t* out, bool clear);
 cudaError_t m1_error_word(int32_t* out, bool clear);

@@ -1,6 +1,6 @@
 /* The binding's native half for the calls that run per layer and step
  * (kv_page_plan, kv_rope_store, kv_attention_bf16, norm_gate_residual,
- * moe_route_topk): it reads address, type, shape and strides off the tensors,
+ * moe_route_topk, fp8_quantize, swiglu_fp8_rows, fp8_gemm, fp8_moe): it reads address, type, shape and strides off the tensors,
  * checks that they fit one another, and calls the C ABI.  Done in Python and
  * through ctypes the same took 5 to 9 us a call on the host, more than the
  * kernels of a decoded token take on the device.
@@ -34,6 +34,16 @@ static int (*f_norm)(const void*, int, int64_t, const float*, const void*, int64
                      const float*, float, int64_t, int64_t, void*, int64_t, uint16_t*, int64_t, void*, q2k_stream_t);
 static int (*f_route)(const void*, int, int64_t, int64_t, int64_t, const float*, int, int64_t, int64_t, int64_t, int,
                       float, int32_t*, float*, const int64_t*, int64_t*, q2k_stream_t);
+static PyObject* t_e4m3;
+static int (*f_quantize)(const void*, int, int64_t, int64_t, int64_t, int64_t, uint8_t*, int64_t, float*, int64_t,
+                         q2k_stream_t);
+static int (*f_swiglu)(const void*, int, int64_t, int64_t, int64_t, uint8_t*, int64_t, float*, int64_t, q2k_stream_t);
+static int (*f_gemm)(const uint8_t*, int64_t, int64_t, int64_t, const float*, int64_t, const uint8_t*, int64_t,
+                     const float*, void*, int, int64_t, q2k_stream_t);
+static size_t (*f_moe_bytes)(int64_t, int64_t, int64_t, int64_t);
+static int (*f_moe)(const uint16_t*, int64_t, int64_t, int64_t, const int32_t*, const float*, int64_t, int64_t,
+                    const uint8_t*, const float*, const uint8_t*, const float*, int64_t, void*, int, int64_t, void*,
+                    size_t, q2k_stream_t);
 
 /* ---- tensors ---------------------------------------------------------------- */
 
@@ -478,6 +488,162 @@ static PyObject* py_route(PyObject* self, PyObject* const* a, Py_ssize_t n)
                           stream));
 }
 
+static int64_t blocks(int64_t n) { return (n + 127) / 128; }
+
+/* x, block_rows, values, scales, stream; with swiglu, x holds gate and up and block_rows is 1 */
+static PyObject* encode(PyObject* const* a, Py_ssize_t n, int swiglu)
+{
+    begin_call();
+    Tensor x, q, scales;
+    int64_t ldx, ldq, lds;
+    const char* const name = swiglu ? "gate_up" : "x";
+    if (want_args(n, 5) || read_tensor(a[0], NULL, name, 0, &x))
+        return NULL;
+    const int type = type_of(&x, name);
+    if (type < 0)
+        return NULL;
+    const int64_t block_rows = as_int(a[1]);
+    if (PyErr_Occurred())
+        return NULL;
+    if (x.dims != 2 || (swiglu && x.size[1] % 2)) {
+        fail(swiglu ? "gate_up must be [rows, 2 N] with dense rows" : "x must be [rows, K] with dense rows");
+        return NULL;
+    }
+    const int64_t T = x.size[0], K = swiglu ? x.size[1] / 2 : x.size[1];
+    const int64_t s_rows = block_rows == 128 ? blocks(T) : T;
+    if (rows(&x, T, x.size[1], name, &ldx) || read_tensor(a[2], t_e4m3, "values", 0, &q) ||
+        rows(&q, T, K, "values", &ldq) || read_tensor(a[3], t_f32, "scales", 0, &scales) ||
+        rows(&scales, s_rows, blocks(K), "scales", &lds))
+        return NULL;
+    const q2k_stream_t stream = as_stream(a[4]);
+    if (PyErr_Occurred())
+        return NULL;
+    return status(swiglu ? f_swiglu(x.p, type, T, K, ldx, q.p, ldq, scales.p, lds, stream)
+                         : f_quantize(x.p, type, T, K, ldx, block_rows, q.p, ldq, scales.p, lds, stream));
+}
+
+static PyObject* py_quantize(PyObject* self, PyObject* const* a, Py_ssize_t n)
+{
+    (void)self;
+    return encode(a, n, 0);
+}
+
+static PyObject* py_swiglu(PyObject* self, PyObject* const* a, Py_ssize_t n)
+{
+    (void)self;
+    return encode(a, n, 1);
+}
+
+/* x, x_scales, w, w_scales, out, stream */
+static PyObject* py_gemm(PyObject* self, PyObject* const* a, Py_ssize_t n)
+{
+    (void)self;
+    begin_call();
+    Tensor x, xs, w, ws, out;
+    int64_t ldx, ld_xs, ldy;
+    if (want_args(n, 6) || read_tensor(a[0], t_e4m3, "x", 0, &x) || read_tensor(a[1], t_f32, "x_scales", 0, &xs) ||
+        read_dense(a[2], t_e4m3, "w", 0, &w) || read_dense(a[3], t_f32, "w_scales", 0, &ws) ||
+        read_tensor(a[4], NULL, "out", 0, &out))
+        return NULL;
+    const int type = type_of(&out, "out");
+    if (type < 0)
+        return NULL;
+    if (x.dims != 2 || w.dims != 2 || w.size[1] != x.size[1]) {
+        fail("x must be [m, K] and w [N, K]");
+        return NULL;
+    }
+    const int64_t m = x.size[0], K = x.size[1], N = w.size[0];
+    if (rows(&x, m, K, "x", &ldx) || rows(&xs, m, blocks(K), "x_scales", &ld_xs) || rows(&out, m, N, "out", &ldy))
+        return NULL;
+    if (ws.dims != 2 || ws.size[0] != blocks(N) || ws.size[1] != blocks(K)) {
+        fail("w_scales must be [ceil(N / 128), ceil(K / 128)]");
+        return NULL;
+    }
+    const q2k_stream_t stream = as_stream(a[5]);
+    if (PyErr_Occurred())
+        return NULL;
+    return status(f_gemm(x.p, m, K, ldx, xs.p, ld_xs, w.p, N, ws.p, out.p, type, ldy, stream));
+}
+
+/* x, ids, route_w, gate_up, gate_up_scales, down, down_scales, out, workspace, stream */
+static PyObject* py_moe(PyObject* self, PyObject* const* a, Py_ssize_t n)
+{
+    (void)self;
+    begin_call();
+    Tensor x, ids, w, gu, gs, down, ds, out, ws;
+    int64_t ldx, ldy;
+    if (want_args(n, 10) || read_tensor(a[0], t_bf16, "x", 0, &x) || read_dense(a[1], t_i32, "ids", 0, &ids) ||
+        read_dense(a[2], t_f32, "route_w", 0, &w) || read_dense(a[3], t_e4m3, "gate_up", 0, &gu) ||
+        read_dense(a[4], t_f32, "gate_up_scales", 0, &gs) || read_dense(a[5], t_e4m3, "down", 0, &down) ||
+        read_dense(a[6], t_f32, "down_scales", 0, &ds) || read_tensor(a[7], NULL, "out", 0, &out) ||
+        read_dense(a[8], t_u8, "workspace", 0, &ws))
+        return NULL;
+    const int type = type_of(&out, "out");
+    if (type < 0)
+        return NULL;
+    if (x.dims != 2 || ids.dims != 2 || w.dims != 2 || ids.size[0] != x.size[0] || w.size[0] != x.size[0] ||
+        w.size[1] != ids.size[1]) {
+        fail("x must be [m, dim], ids and route_w [m, topk]");
+        return NULL;
+    }
+    const int64_t m = x.size[0], dim = x.size[1], topk = ids.size[1];
+    if (down.dims != 3 || down.size[1] != dim || gu.dims != 4 || gu.size[0] != down.size[0] || gu.size[1] != 2 ||
+        gu.size[2] != down.size[2] || gu.size[3] != dim) {
+        fail("gate_up must be [E, 2, inter, dim] and down [E, dim, inter]");
+        return NULL;
+    }
+    const int64_t E = down.size[0], inter = down.size[2];
+    if (gs.dims != 4 || gs.size[0] != E || gs.size[1] != 2 || gs.size[2] != blocks(inter) || gs.size[3] != blocks(dim) ||
+        ds.dims != 3 || ds.size[0] != E || ds.size[1] != blocks(dim) || ds.size[2] != blocks(inter)) {
+        fail("gate_up_scales must be [E, 2, ceil(inter / 128), ceil(dim / 128)] and down_scales "
+             "[E, ceil(dim / 128), ceil(inter / 128)]");
+        return NULL;
+    }
+    if (rows(&x, m, dim, "x", &ldx) || rows(&out, m, dim, "out", &ldy))
+        return NULL;
+    const q2k_stream_t stream = as_stream(a[9]);
+    if (PyErr_Occurred())
+        return NULL;
+    return status(f_moe(x.p, m, dim, ldx, ids.p, w.p, topk, E, gu.p, gs.p, down.p, ds.p, inter, out.p, type, ldy, ws.p,
+                        (size_t)ws.count, stream));
+}
+
+/* m, topk, dim, inter */
+static PyObject* py_moe_bytes(PyObject* self, PyObject* const* a, Py_ssize_t n)
+{
+    (void)self;
+    if (want_args(n, 4))
+        return NULL;
+    const int64_t m = as_int(a[0]), topk = as_int(a[1]), dim = as_int(a[2]), inter = as_int(a[3]);
+    if (PyErr_Occurred())
+        return NULL;
+    return PyLong_FromSize_t(f_moe_bytes(m, topk, dim, inter));
+}
+
+/* setup_fp8(e4m3, addresses of the five functions) */
+static PyObject* py_setup_fp8(PyObject* self, PyObject* const* a, Py_ssize_t n)
+{
+    (void)self;
+    if (want_args(n, 2))
+        return NULL;
+    void* f[5];
+    for (int i = 0; i < 5; ++i) {
+        if (!PyTuple_Check(a[1]) || PyTuple_GET_SIZE(a[1]) != 5 ||
+            !(f[i] = PyLong_AsVoidPtr(PyTuple_GET_ITEM(a[1], i)))) {
+            if (!PyErr_Occurred())
+                fail("five function addresses");
+            return NULL;
+        }
+    }
+    t_e4m3 = Py_NewRef(a[0]);
+    *(void**)&f_quantize = f[0];
+    *(void**)&f_swiglu = f[1];
+    *(void**)&f_gemm = f[2];
+    *(void**)&f_moe = f[3];
+    *(void**)&f_moe_bytes = f[4];
+    Py_RETURN_NONE;
+}
+
 /* setup((fp32, bf16, int32, int64, uint8), (addresses of the six functions), callable: the current device's index) */
 static PyObject* py_setup(PyObject* self, PyObject* const* a, Py_ssize_t n)
 {
@@ -518,6 +684,12 @@ static PyMethodDef methods[] = {
     {"kv_attention_workspace_bytes", (PyCFunction)(void (*)(void))py_attn_bytes, METH_FASTCALL, NULL},
     {"norm_gate_residual", (PyCFunction)(void (*)(void))py_norm, METH_FASTCALL, NULL},
     {"moe_route_topk", (PyCFunction)(void (*)(void))py_route, METH_FASTCALL, NULL},
+    {"setup_fp8", (PyCFunction)(void (*)(void))py_setup_fp8, METH_FASTCALL, NULL},
+    {"fp8_quantize", (PyCFunction)(void (*)(void))py_quantize, METH_FASTCALL, NULL},
+    {"swiglu_fp8_rows", (PyCFunction)(void (*)(void))py_swiglu, METH_FASTCALL, NULL},
+    {"fp8_gemm", (PyCFunction)(void (*)(void))py_gemm, METH_FASTCALL, NULL},
+    {"fp8_moe", (PyCFunction)(void (*)(void))py_moe, METH_FASTCALL, NULL},
+    {"fp8_moe_workspace_bytes", (PyCFunction)(void (*)(void))py_moe_bytes, METH_FASTCALL, NULL},
     {NULL, NULL, 0, NULL}};
 
 static struct PyModuleDef module = {PyModuleDef_HEAD_INIT, "_q2kcall", NULL, -1, methods, NULL, NULL, NULL, NULL};
