@@ -628,7 +628,8 @@ size_t fp8_moe_workspace_bytes(int64_t m, int64_t topk, int64_t dim, int64_t int
  *   workspace  at least fp8_moe_workspace_bytes(m, topk, dim, inter) bytes,
  *              256-byte aligned; calls that overlap need one each
  * 0 <= m <= 128, 1 <= topk <= 32, m * topk <= 1024, 1 <= E <= 1024, dim and
- * inter multiples of 16, 16..16384.  Two launches. */
+ * inter multiples of 16, 16..16384.  Two launches.
+ * Q2K_ERR_UNSUPPORTED when the CUDA driver offers no tensor-map encoder. */
 int fp8_moe(const uint16_t* x, int64_t m, int64_t dim, int64_t ldx, const int32_t* ids, const float* route_w,
             int64_t topk, int64_t E, const uint8_t* gate_up, const float* gate_up_scales, const uint8_t* down,
             const float* down_scales, int64_t inter, void* y, int y_type, int64_t ldy, void* workspace,

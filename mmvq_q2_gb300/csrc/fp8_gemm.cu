@@ -42,6 +42,8 @@ __global__ void __launch_bounds__(256) fp8_gemm_kernel(const Fp8Gemm a)
 
 cudaError_t launch_fp8_gemm(const Fp8Gemm& p, cudaStream_t s)
 {
+    if (fp8_stream_supported(p))
+        return launch_fp8_gemm_stream(p, s);
     return launch_pdl(fp8_gemm_kernel, dim3((unsigned)((p.N + 31) / 32), (unsigned)((p.m + 7) / 8)), dim3(256), 0, s, p);
 }
 

@@ -159,7 +159,7 @@ int q2k_device_error(int32_t* host_out, int clear)
 {
     if (!host_out)
         return Q2K_ERR_NULL_ARG;
-    int32_t a = 0, b = 0, c = 0, d = 0, q = 0, o = 0, mq = 0, q3t = 0, at = 0;
+    int32_t a = 0, b = 0, c = 0, d = 0, q = 0, o = 0, mq = 0, q3t = 0, at = 0, fs = 0;
     cudaError_t e = mv_error_word(&a, clear != 0);
     if (e == cudaSuccess)
         e = m1_error_word(&o, clear != 0);
@@ -177,9 +177,11 @@ int q2k_device_error(int32_t* host_out, int clear)
         e = q3mt_error_word(&q3t, clear != 0);
     if (e == cudaSuccess)
         e = attn_error_word(&at, clear != 0);
+    if (e == cudaSuccess)
+        e = fp8_stream_error_word(&fs, clear != 0);
     if (e != cudaSuccess)
         return fail_cuda(e);
-    *host_out = a | b | c | d | q | o | mq | q3t | at;
+    *host_out = a | b | c | d | q | o | mq | q3t | at | fs;
     return Q2K_OK;
 }
 
@@ -1016,6 +1018,8 @@ int fp8_gemm(const uint8_t* x, int64_t m, int64_t K, int64_t ldx, const float* x
         return st;
     if (m == 0)
         return Q2K_OK;
+    if (!fp8_encoder_there())
+        return Q2K_ERR_UNSUPPORTED;  // no tensor-map encoder in this driver
     Fp8Gemm p{};
     p.x = x;
     p.m = m;
@@ -1059,6 +1063,8 @@ int fp8_moe(const uint16_t* x, int64_t m, int64_t dim, int64_t ldx, const int32_
         return st;
     if (m == 0)
         return Q2K_OK;
+    if (!fp8_encoder_there())
+        return Q2K_ERR_UNSUPPORTED;  // no tensor-map encoder in this driver
     Fp8Moe p{};
     p.x = x;
     p.m = m;

@@ -274,6 +274,9 @@ struct Fp8Gemm {
     int64_t ldy;
 };
 cudaError_t launch_fp8_gemm(const Fp8Gemm& p, cudaStream_t s);
+bool fp8_encoder_there();  // the driver has a tensor-map encoder
+bool fp8_stream_supported(const Fp8Gemm& p);
+cudaError_t launch_fp8_gemm_stream(const Fp8Gemm& p, cudaStream_t s);
 
 // The routed experts of a few tokens (fp8_stream.cu; q2k.h, fp8_moe).
 struct Fp8Moe {
@@ -305,5 +308,6 @@ cudaError_t umma_error_word(int32_t* out, bool clear);
 cudaError_t q3_error_word(int32_t* out, bool clear);
 cudaError_t q3mt_error_word(int32_t* out, bool clear);
 cudaError_t attn_error_word(int32_t* out, bool clear);
+cudaError_t fp8_stream_error_word(int32_t* out, bool clear);
 
 }  // namespace q2k
