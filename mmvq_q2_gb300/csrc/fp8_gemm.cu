@@ -1,41 +1,443 @@
-// The product of 8-bit floating-point operands (include/q2k.h, fp8_gemm).
+// The product of 8-bit floating-point operands for many rows (include/q2k.h,
+// fp8_gemm; up to 32 rows go to fp8_stream.cu) on the 5th-generation tensor
+// cores: tcgen05.mma kind::f8f6f4 on e4m3, fp32 accumulators in tensor memory.
+//
+// The scales change every 128 values along K, so an accumulator holds one such
+// block alone: four MMAs of K = 32 fill one of two accumulators while the
+// other is read back, multiplied by its rows' and its block's scale and added
+// to fp32 sums in registers.  A tile is 128 rows of x (a tensor memory lane
+// each, so a thread has one row and its scale is one number) by BN rows of W
+// (half of BN to a group of four warps; within one block of 128, so W's scale
+// is one number too):
+//   warp 0       copies tiles of 128 values of K (128-byte swizzled) into a
+//                ring of shared-memory stages;
+//   warp 1       issues the MMAs;
+//   warps 4..11  read back, scale, add; at the end store y.
+// CTAs walk the tiles, 16 tiles of x at a time, so that what runs together
+// shares operands in L2.  Where there are fewer tiles than SMs, the CTAs of a
+// cluster share a tile along K and add their sums through shared memory, in
+// the order of K (no atomics: a call repeats bit for bit).
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
 #include <algorithm>
+#include <mutex>
 
 #include "q2k_common.cuh"
 #include "q2k_internal.h"
+#include "q2k_umma.cuh"
 
 namespace q2k {
 
+__device__ int g_fp8_gemm_error = 0;
+
 namespace {
 
-__device__ __forceinline__ float e4m3_f(uint32_t code)
+constexpr int kThreads = 384;
+constexpr int kTM = 128;             // rows of x in a tile
+constexpr int kTK = 128;             // values of K in a stage: one swizzle row, one block of the scales
+constexpr int kXTile = kTM * kTK;
+constexpr int kMaxStages = 12;
+constexpr int kGroup = 16;           // tiles of x that are walked together
+
+struct GemmArgs {
+    const float *x_scales, *w_scales;
+    void* y;
+    int64_t ld_xs, ldy;
+    int m, N, blocks;  // blocks of 128 along K
+    int tiles_m, tiles_n, stages;
+    int y_bf16, align;  // bytes that the start of every 32 values of y is aligned to: 32, 16 or less
+};
+
+struct GemmShared {
+    uint64_t full[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2];
+    uint32_t tmem;
+    int abort_flag, issued;
+};
+
+// D fp32, A and B e4m3, both K-major, M = 128.
+constexpr uint32_t instr_desc_e4m3(int n) { return (1u << 4) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(kTM >> 4) << 24); }
+
+__device__ __forceinline__ void umma_e4m3(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc, bool acc)
 {
-    uint32_t h;
-    asm("{\n\t.reg .b16 t;\n\tcvt.u16.u32 t, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, t;\n\t}" : "=r"(h) : "r"(code));
-    return half_lo_f(h);
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)acc)
+        : "memory");
 }
 
-// A thread a value of y.
-__global__ void __launch_bounds__(256) fp8_gemm_kernel(const Fp8Gemm a)
+// 32 fp32 columns of this warp's 32 lanes; complete after settle().
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&v)[32])
 {
-    pdl_launch_dependents();
-    pdl_wait();
-    const int64_t n = (int64_t)blockIdx.x * 32 + (threadIdx.x & 31);
-    const int64_t t = (int64_t)blockIdx.y * 8 + (threadIdx.x >> 5);
-    if (n >= a.N || t >= a.m)
-        return;
-    const int64_t blocks = (a.K + 127) / 128;
-    float y = 0.f;
-    for (int64_t b = 0; b < blocks; ++b) {
-        float s = 0.f;
-        for (int64_t k = b * 128; k < min(a.K, b * 128 + 128); ++k)
-            s = fmaf(e4m3_f(a.x[t * a.ldx + k]), e4m3_f(a.W[n * a.K + k]), s);
-        y = fmaf(s, a.x_scales[t * a.ld_xs + b] * a.w_scales[n / 128 * blocks + b], y);
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
+        "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]),
+          "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]), "=f"(v[16]),
+          "=f"(v[17]), "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]), "=f"(v[24]),
+          "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
+        : "r"(taddr));
+}
+
+// Waits for this warp's loads; what uses the values comes after.
+__device__ __forceinline__ void settle(float (&v)[32])
+{
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < 32; i += 8)
+        asm volatile(""
+                     : "+f"(v[i]), "+f"(v[i + 1]), "+f"(v[i + 2]), "+f"(v[i + 3]), "+f"(v[i + 4]), "+f"(v[i + 5]),
+                       "+f"(v[i + 6]), "+f"(v[i + 7]));
+}
+
+// acc += v * f, two values an instruction.
+__device__ __forceinline__ void fma_pairs(float* acc, const float (&v)[32], float f)
+{
+#pragma unroll
+    for (int i = 0; i < 32; i += 2)
+        asm("{\n\t.reg .b64 a, b, c;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %4};\n\tmov.b64 c, {%0, %1};\n\t"
+            "fma.rn.f32x2 c, a, b, c;\n\tmov.b64 {%0, %1}, c;\n\t}"
+            : "+f"(acc[i]), "+f"(acc[i + 1])
+            : "f"(v[i]), "f"(v[i + 1]), "f"(f));
+}
+
+__device__ __forceinline__ void store32(void* dst, const uint32_t (&w)[8])
+{
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(dst), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+                 "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+}
+
+// The 32 bytes at dst where they are aligned to `align`, a sector in one store if that is 32.
+__device__ __forceinline__ void store32(void* dst, const uint32_t (&w)[8], int align)
+{
+    if (align >= 32) {
+        store32(dst, w);
+    } else {
+        reinterpret_cast<uint4*>(dst)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+        reinterpret_cast<uint4*>(dst)[1] = make_uint4(w[4], w[5], w[6], w[7]);
     }
-    if (a.y_bf16)
-        static_cast<uint16_t*>(a.y)[t * a.ldy + n] = __bfloat16_as_ushort(__float2bfloat16_rn(y));
-    else
-        static_cast<float*>(a.y)[t * a.ldy + n] = y;
+}
+
+// n values of a row of y from column `col` on, 8 at a time (n a multiple of 8).
+template <int n>
+__device__ __forceinline__ void store_row(const GemmArgs& a, int64_t row, int col, const float* v)
+{
+    if (a.y_bf16) {
+        uint16_t* y = static_cast<uint16_t*>(a.y) + row * a.ldy + col;
+        if (n % 16 == 0 && a.align >= 16 && col + n <= a.N) {
+#pragma unroll
+            for (int i = 0; i < n; i += 16) {
+                uint32_t w[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[j]) : "f"(v[i + 2 * j + 1]), "f"(v[i + 2 * j]));
+                store32(y + i, w, a.align);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < n; ++i)
+                if (col + i < a.N)
+                    y[i] = __bfloat16_as_ushort(__float2bfloat16_rn(v[i]));
+        }
+    } else {
+        float* y = static_cast<float*>(a.y) + row * a.ldy + col;
+        if (a.align >= 16 && col + n <= a.N) {
+#pragma unroll
+            for (int i = 0; i < n; i += 8) {
+                uint32_t w[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    w[j] = __float_as_uint(v[i + j]);
+                store32(y + i, w, a.align);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < n; ++i)
+                if (col + i < a.N)
+                    y[i] = v[i];
+        }
+    }
+}
+
+__device__ __forceinline__ void cluster_sync()
+{
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ void store_peer(uint32_t addr, uint32_t rank, float v)
+{
+    asm volatile("{\n\t.reg .b32 p;\n\tmapa.shared::cluster.u32 p, %0, %1;\n\tst.shared::cluster.f32 [p], %2;\n\t}" ::"r"(addr),
+                 "r"(rank), "f"(v)
+                 : "memory");
+}
+
+// S CTAs of a cluster share a tile along K.
+template <int BN, int S>
+__global__ void __launch_bounds__(kThreads, 1)
+    fp8_gemm_kernel(const GemmArgs a, const __grid_constant__ CUtensorMap tx, const __grid_constant__ CUtensorMap tw)
+{
+    constexpr int WGC = BN / 2;  // columns of a group of four warps
+    constexpr uint32_t kStage = (uint32_t)(kXTile + BN * kTK);
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    pdl_launch_dependents();
+    // the 128-byte swizzle repeats every 1024 bytes: stages start on 1024
+    uint8_t* const ring = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    float* const red = reinterpret_cast<float*>(ring + (size_t)a.stages * kStage);  // S > 1: [S][BN / S][128]
+    GemmShared& sh = *reinterpret_cast<GemmShared*>(red + (S > 1 ? BN * 128 : 0));
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = S > 1 ? (int)blockIdx.x % S : 0;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < a.stages; ++s) {
+            mbar_init(smem_u32(&sh.full[s]), 1);
+            mbar_init(smem_u32(&sh.empty[s]), 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(smem_u32(&sh.acc_full[b]), 1);
+            mbar_init(smem_u32(&sh.acc_empty[b]), 8);
+        }
+        sh.abort_flag = 0;
+        sh.issued = 0;
+        fence_mbar_init();
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&sh.tmem)),
+                     "r"(2 * BN)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    pdl_wait();
+    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+    __syncthreads();
+    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+    if (S > 1)
+        cluster_sync();  // every CTA of the cluster has started
+    const uint32_t tmem = sh.tmem;
+    volatile int* const abort_flag = &sh.abort_flag;
+    auto give_up = [&]() {
+        atomicOr(&g_fp8_gemm_error, Q2K_ERR_BIT_WAIT_TIMEOUT);
+        *abort_flag = 1;
+    };
+    const int tiles = a.tiles_m * a.tiles_n;
+    const int tile0 = (int)blockIdx.x / S, step = (int)gridDim.x / S;
+    const int k_first = rank * a.blocks / S, k_end = (rank + 1) * a.blocks / S;
+    auto place = [&](int t, int& m0, int& n0) {
+        const int per = kGroup * a.tiles_n, group = t / per, in = t - group * per;
+        const int high = min(kGroup, a.tiles_m - group * kGroup);
+        m0 = (group * kGroup + in % high) * kTM;
+        n0 = in / high * BN;
+    };
+
+    if (warp < 4) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+        if (warp == 0) {
+            if (lane == 0) {  // copies
+                const uint64_t pol = l2_policy_evict_last();
+                int slot = 0, use = 0;
+                bool ok = true;
+                for (int t = tile0; t < tiles && ok; t += step) {
+                    int m0, n0;
+                    place(t, m0, n0);
+                    for (int k = k_first; k < k_end; ++k) {
+                        if (use > 0 && !mbar_wait_bounded(smem_u32(&sh.empty[slot]), (uint32_t)(use - 1) & 1u, abort_flag)) {
+                            give_up();
+                            ok = false;
+                            break;
+                        }
+                        const uint32_t bar = smem_u32(&sh.full[slot]), dst = smem_u32(ring + (size_t)slot * kStage);
+                        mbar_arrive_expect_tx(bar, kStage);
+                        tma_load_2d(dst, &tx, k * kTK, m0, bar, pol);
+                        tma_load_2d(dst + kXTile, &tw, k * kTK, n0, bar, pol);
+                        sh.issued = sh.issued + 1;
+                        if (++slot == a.stages) {
+                            slot = 0;
+                            ++use;
+                        }
+                    }
+                }
+            }
+            __syncwarp();
+        } else if (warp == 1) {  // MMAs
+            constexpr uint32_t idesc = instr_desc_e4m3(BN);
+            int slot = 0, use = 0, n = 0;
+            bool ok = true;
+            for (int t = tile0; t < tiles && ok; t += step)
+                for (int k = k_first; k < k_end; ++k, ++n) {
+                    const int buf = n & 1;
+                    if (!mbar_wait_bounded(smem_u32(&sh.full[slot]), (uint32_t)use & 1u, abort_flag) ||
+                        (n >= 2 && !mbar_wait_bounded(smem_u32(&sh.acc_empty[buf]), (uint32_t)((n >> 1) - 1) & 1u, abort_flag)))
+                        ok = false;
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) {
+                        if (lane == 0)
+                            give_up();
+                        break;
+                    }
+                    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+                    const uint32_t sa = smem_u32(ring + (size_t)slot * kStage);
+                    if (elect_one()) {
+#pragma unroll
+                        for (int i = 0; i < kTK / 32; ++i)  // K = 32 an MMA: 32 bytes along the swizzled row
+                            umma_e4m3(tmem + buf * BN, smem_desc_sw128(sa + 32 * i), smem_desc_sw128(sa + kXTile + 32 * i),
+                                      idesc, i > 0);
+                        umma_commit(smem_u32(&sh.empty[slot]));
+                        umma_commit(smem_u32(&sh.acc_full[buf]));
+                    }
+                    __syncwarp();
+                    if (++slot == a.stages) {
+                        slot = 0;
+                        ++use;
+                    }
+                }
+        }
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+        const int q = warp & 3, wg = (warp - 4) >> 2;
+        const uint32_t t_addr = tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(wg * WGC);
+        int n = 0;
+        for (int t = tile0; t < tiles; t += step) {
+            int m0, n0;
+            place(t, m0, n0);
+            const int row = m0 + 32 * q + lane, col = n0 + wg * WGC;
+            const float* xs = a.x_scales + (int64_t)min(row, a.m - 1) * a.ld_xs;
+            const float* ws = a.w_scales + (int64_t)(min(col, a.N - 1) / 128) * a.blocks;
+            float acc[WGC];
+#pragma unroll
+            for (int i = 0; i < WGC; ++i)
+                acc[i] = 0.f;
+            float f = k_first < k_end ? xs[k_first] * ws[k_first] : 0.f;
+            for (int k = k_first; k < k_end; ++k, ++n) {
+                const int buf = n & 1;
+                const float f_next = k + 1 < k_end ? xs[k + 1] * ws[k + 1] : 0.f;
+                const bool ok = __all_sync(
+                    0xffffffffu, mbar_wait_bounded(smem_u32(&sh.acc_full[buf]), (uint32_t)(n >> 1) & 1u, abort_flag));
+                if (!ok) {
+                    if (lane == 0)
+                        give_up();
+                    break;
+                }
+                asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+                float v[2][32];
+                tmem_ld32(t_addr + buf * BN, v[0]);
+#pragma unroll
+                for (int c = 0; c < WGC; c += 32) {
+                    settle(v[(c / 32) & 1]);
+                    if (c + 32 < WGC) {
+                        tmem_ld32(t_addr + buf * BN + c + 32, v[(c / 32 + 1) & 1]);
+                    } else {
+                        asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+                        if (lane == 0)
+                            mbar_arrive(smem_u32(&sh.acc_empty[buf]));
+                    }
+                    fma_pairs(acc + c, v[(c / 32) & 1], f);
+                }
+                f = f_next;
+            }
+            if constexpr (S == 1) {
+                if (row < a.m && !*abort_flag)
+                    store_row<WGC>(a, row, col, acc);
+            } else {
+                // slice r of the columns is added up and stored by CTA r
+                constexpr int SC = WGC / S;
+                const uint32_t at = smem_u32(red) + (uint32_t)(((rank * 2 + wg) * SC * 128 + 32 * q + lane) * 4);
+#pragma unroll
+                for (int i = 0; i < WGC; ++i)
+                    store_peer(at + (uint32_t)(i % SC) * 512u, (uint32_t)(i / SC), acc[i]);
+            }
+        }
+    }
+    if constexpr (S > 1) {
+        cluster_sync();
+        if (warp >= 4) {
+            constexpr int SC = WGC / S;
+            const int q = warp & 3, wg = (warp - 4) >> 2;
+            int m0, n0;
+            place(tile0, m0, n0);
+            const int row = m0 + 32 * q + lane;
+            float sum[SC];
+#pragma unroll
+            for (int i = 0; i < SC; ++i) {
+                sum[i] = red[(wg * SC + i) * 128 + 32 * q + lane];
+#pragma unroll
+                for (int r = 1; r < S; ++r)
+                    sum[i] += red[((r * 2 + wg) * SC + i) * 128 + 32 * q + lane];
+            }
+            if (row < a.m && !*abort_flag)
+                store_row<SC>(a, row, n0 + wg * WGC + rank * SC, sum);
+        }
+    }
+    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+    __syncthreads();
+    if (sh.abort_flag && threadIdx.x == 0)  // let the copies that were issued land before the CTA exits
+        for (int i = max(0, sh.issued - a.stages); i < sh.issued; ++i)
+            mbar_wait_bounded(smem_u32(&sh.full[i % a.stages]), (uint32_t)(i / a.stages) & 1u, nullptr);
+    __syncthreads();
+    if (warp == 1)
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(2 * BN) : "memory");
+}
+
+PFN_cuTensorMapEncodeTiled_v12000 gemm_encoder()
+{
+    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+    static std::once_flag once;
+    std::call_once(once, [] {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult q{};
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+    });
+    return fn;
+}
+
+// Codes [rows, K], rows ld apart; a box is 128 values by box_rows, 128-byte swizzled, zeros past the edges.
+bool encode_codes(CUtensorMap* map, const void* base, int64_t rows, int64_t K, int64_t ld, int box_rows)
+{
+    PFN_cuTensorMapEncodeTiled_v12000 enc = gemm_encoder();
+    const cuuint64_t dims[2] = {(cuuint64_t)K, (cuuint64_t)rows};
+    const cuuint64_t strides[1] = {(cuuint64_t)ld};
+    const cuuint32_t box[2] = {(cuuint32_t)kTK, (cuuint32_t)box_rows};
+    const cuuint32_t ones[2] = {1, 1};
+    return enc && enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, ones,
+                      CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int BN, int S>
+cudaError_t launch_tiles(GemmArgs a, const Fp8Gemm& p, const DeviceInfo& di, cudaStream_t s)
+{
+    constexpr size_t kStage = kXTile + BN * kTK;
+    auto* kernel = fp8_gemm_kernel<BN, S>;
+    static std::atomic<unsigned long long> devs{0};
+    cudaError_t e = allow_max_smem(kernel, devs);
+    if (e != cudaSuccess)
+        return e;
+    a.tiles_m = (a.m + kTM - 1) / kTM;
+    a.tiles_n = (a.N + BN - 1) / BN;
+    const size_t extra = 1024 + sizeof(GemmShared) + (S > 1 ? (size_t)BN * 512 : 0);
+    a.stages = (int)std::min<size_t>(kMaxStages, ((size_t)di.smem_optin - extra) / kStage);
+    CUtensorMap tx{}, tw{};
+    if (!encode_codes(&tx, p.x, p.m, p.K, p.ldx, kTM) || !encode_codes(&tw, p.W, p.N, p.K, p.K, BN))
+        return cudaErrorInvalidValue;
+    const int64_t tiles = (int64_t)a.tiles_m * a.tiles_n;
+    if (tiles * S > 0x7fffffff)
+        return cudaErrorInvalidConfiguration;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)(S > 1 ? tiles * S : std::min<int64_t>(tiles, di.sm_count)));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = extra + (size_t)a.stages * kStage;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = S;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = S > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kernel, a, tx, tw);
 }
 
 }  // namespace
@@ -44,7 +446,56 @@ cudaError_t launch_fp8_gemm(const Fp8Gemm& p, cudaStream_t s)
 {
     if (fp8_stream_supported(p))
         return launch_fp8_gemm_stream(p, s);
-    return launch_pdl(fp8_gemm_kernel, dim3((unsigned)((p.N + 31) / 32), (unsigned)((p.m + 7) / 8)), dim3(256), 0, s, p);
+    DeviceInfo di;
+    cudaError_t e = device_info(&di);
+    if (e != cudaSuccess)
+        return e;
+    GemmArgs a{};
+    a.x_scales = p.x_scales;
+    a.w_scales = p.w_scales;
+    a.y = p.y;
+    a.ld_xs = p.ld_xs;
+    a.ldy = p.ldy;
+    a.m = (int)p.m;
+    a.N = (int)p.N;
+    a.blocks = (int)((p.K + kTK - 1) / kTK);
+    a.y_bf16 = p.y_bf16;
+    const uintptr_t bits = reinterpret_cast<uintptr_t>(p.y) | (uintptr_t)(p.ldy * (p.y_bf16 ? 2 : 4));
+    a.align = bits % 32 == 0 ? 32 : bits % 16 == 0 ? 16 : 1;
+    // What each choice of tile and split would take, in cycles: blocks of K one after another, each bound by the MMA, the
+    // read-back or its operands' way from L2.
+    auto cost = [&](int bn, int split) {
+        const int64_t tiles = (int64_t)((a.m + kTM - 1) / kTM) * ((a.N + bn - 1) / bn) * split;
+        const int64_t waves = (tiles + di.sm_count - 1) / di.sm_count;
+        const int64_t block = std::max<int64_t>(2 * bn + 60, (std::min(a.m, kTM) + bn) * (int64_t)kTK / 48);
+        return waves * ((a.blocks + split - 1) / split * block + 1500 + 6 * bn) + (split > 1 ? 1500 : 0);
+    };
+    int best = 0;
+    const int options[5][2] = {{256, 1}, {128, 1}, {128, 2}, {64, 1}, {64, 4}};
+    for (int i = 1; i < 5; ++i)
+        if (options[i][1] <= a.blocks && cost(options[i][0], options[i][1]) < cost(options[best][0], options[best][1]))
+            best = i;
+    switch (best) {
+    case 0: return launch_tiles<256, 1>(a, p, di, s);
+    case 1: return launch_tiles<128, 1>(a, p, di, s);
+    case 2: return launch_tiles<128, 2>(a, p, di, s);
+    case 3: return launch_tiles<64, 1>(a, p, di, s);
+    default: return launch_tiles<64, 4>(a, p, di, s);
+    }
+}
+
+cudaError_t fp8_gemm_error_word(int32_t* out, bool clear)
+{
+    int v = 0;
+    cudaError_t e = cudaMemcpyFromSymbol(&v, g_fp8_gemm_error, sizeof(int));
+    if (e != cudaSuccess)
+        return e;
+    *out = v;
+    if (clear) {
+        int z = 0;
+        e = cudaMemcpyToSymbol(g_fp8_gemm_error, &z, sizeof(int));
+    }
+    return e;
 }
 
 }  // namespace q2k

@@ -159,7 +159,7 @@ int q2k_device_error(int32_t* host_out, int clear)
 {
     if (!host_out)
         return Q2K_ERR_NULL_ARG;
-    int32_t a = 0, b = 0, c = 0, d = 0, q = 0, o = 0, mq = 0, q3t = 0, at = 0, fs = 0;
+    int32_t a = 0, b = 0, c = 0, d = 0, q = 0, o = 0, mq = 0, q3t = 0, at = 0, fs = 0, fg = 0;
     cudaError_t e = mv_error_word(&a, clear != 0);
     if (e == cudaSuccess)
         e = m1_error_word(&o, clear != 0);
@@ -179,9 +179,11 @@ int q2k_device_error(int32_t* host_out, int clear)
         e = attn_error_word(&at, clear != 0);
     if (e == cudaSuccess)
         e = fp8_stream_error_word(&fs, clear != 0);
+    if (e == cudaSuccess)
+        e = fp8_gemm_error_word(&fg, clear != 0);
     if (e != cudaSuccess)
         return fail_cuda(e);
-    *host_out = a | b | c | d | q | o | mq | q3t | at | fs;
+    *host_out = a | b | c | d | q | o | mq | q3t | at | fs | fg;
     return Q2K_OK;
 }
 

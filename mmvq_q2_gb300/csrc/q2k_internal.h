@@ -309,5 +309,6 @@ cudaError_t q3_error_word(int32_t* out, bool clear);
 cudaError_t q3mt_error_word(int32_t* out, bool clear);
 cudaError_t attn_error_word(int32_t* out, bool clear);
 cudaError_t fp8_stream_error_word(int32_t* out, bool clear);
+cudaError_t fp8_gemm_error_word(int32_t* out, bool clear);
 
 }  // namespace q2k
