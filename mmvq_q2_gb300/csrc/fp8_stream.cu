@@ -3,18 +3,22 @@
 //
 // Bound by memory: each weight is read once and used for a handful of tokens.
 // A persistent CTA an SM walks items of 32 weight rows.  One warp copies the
-// rows, 512 values at a time, into a ring of shared-memory stages with bulk
-// copies; eight warps, each with a 128-value block of 16 rows of every stage,
-// feed them to the tensor cores as they are (mma.sync m16n8k32 on e4m3,
-// weights as the 16 rows, tokens as the 8 columns), scale each block's sums
-// in fp32 and add them up; the four warps of a row tile are joined through
-// shared memory at the item's end.  (The 5th-generation tensor cores would
-// want 128 weight rows or tokens a tile; at these sizes the MMAs take a few
-// percent of the time either way.)
+// rows, 512 values at a time, into a ring of shared-memory stages, a tensor
+// copy each (with a bulk copy a row, 73 cycles each, their issue was the
+// bound: 2.0 TB/s).  Two groups of four warps take turns at the stages; a
+// warp feeds its 128 values of all 32 rows to the tensor cores as they are
+// (mma.sync m16n8k32 on e4m3, weights as the 16 rows, tokens as the 8
+// columns), scales each block's sums in fp32 and adds them up.  The eight
+// warps are joined through shared memory at the item's end.  (The
+// 5th-generation tensor cores would want 128 weight rows or tokens a tile; at
+// these sizes the MMAs take a few percent of the time either way.)
 //
 // A thread needs 4 values of a row for each MMA.  Since the order along K is
 // free as long as both operands share it, it takes 16 neighbouring bytes of
 // its row and feeds them to two MMAs: one 16-byte load a row and 64 values.
+// The copies swizzle lines of 128 bytes, so that the loads of two rows meet no
+// bank twice; rows that are no multiple of 128 bytes cannot be cut into such
+// lines and lie as they are (loads then take twice the cycles).
 //
 // bf16 tokens (fp8_moe) enter as two columns of e4m3 each: with a power of
 // two that brings a block's largest below 256, the upper 4 bits of a value
@@ -38,7 +42,7 @@ __device__ int g_fp8_stream_error = 0;
 
 namespace {
 
-constexpr int kWarps = 8;                      // that compute; one more copies
+constexpr int kWarps = 8;                      // that compute, in two groups; one more copies
 constexpr int kThreads = (kWarps + 1) * 32;
 constexpr int kRows = 32;                      // weight rows of an item
 constexpr int kChunk = 512;                    // values of a row in a stage
@@ -54,7 +58,9 @@ struct StreamArgs {
     int rows;           // weight rows: N; inter (UP); dim (DOWN)
     int row_blocks;     // of w_scales
     int tiles;          // items of one matrix
-    int stages, stage_bytes;
+    int stages, stage_bytes;  // stages: an even number, so that a stage is always the same group's
+    int swizzled;             // lines of 128 bytes
+    int k_step, block_step;   // coordinates of a chunk: (0, 4 blocks) swizzled, (128 words, 0) otherwise
     int m;
     // GEMM
     const uint8_t* x;
@@ -201,23 +207,14 @@ __device__ __forceinline__ void split_block(const float (&v)[4], uint8_t* upper,
         *scale = inv;
 }
 
-// A box of 512 bytes by rows [by gate/up by expert], and of 512 bytes by rows.
-__device__ __forceinline__ void copy_weights(uint32_t dst, const CUtensorMap* map, int k, int row, int expert, uint32_t bar,
-                                             uint64_t policy)
+// A box of 512 bytes by rows, by gate and up, by expert.
+__device__ __forceinline__ void copy_box(uint32_t dst, const CUtensorMap* map, int k, int block, int row, int expert, uint32_t bar,
+                                         uint64_t policy)
 {
     asm volatile(
-        "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
-        " [%0], [%1, {%2, %3, %4, %5}], [%6], %7;" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(k), "r"(row), "r"(0), "r"(expert), "r"(bar), "l"(policy)
-        : "memory");
-}
-
-__device__ __forceinline__ void copy_tokens(uint32_t dst, const CUtensorMap* map, int k, uint32_t bar, uint64_t policy)
-{
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
-        " [%0], [%1, {%2, %3}], [%4], %5;" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(k), "r"(0), "r"(bar), "l"(policy)
+        "cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
+        " [%0], [%1, {%2, %3, %4, %5, %6}], [%7], %8;" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(k), "r"(block), "r"(row), "r"(0), "r"(expert), "r"(bar), "l"(policy)
         : "memory");
 }
 
@@ -225,8 +222,9 @@ template <int MODE, int NT>
 struct Shared {
     static constexpr int kTok = MODE == GEMM ? 8 * NT : 4 * NT;  // tokens of a pass
     uint64_t full[16], empty[16];
+    static constexpr int kBufs = MODE == GEMM && NT == 4 ? 1 : 2;
     int abort_flag, issued, last[2];
-    float red[2][2][4][kTok * 20];  // [buffer][row tile][warp]: 16 rows of a token, 20 apart
+    float red[kBufs][2][kWarps][kTok * 20];  // [buffer][row tile][warp]: 16 rows of a token, 20 apart
     Lists lists[MODE == GEMM ? 0 : 1];
 };
 
@@ -236,11 +234,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 {
     using Sh = Shared<MODE, NT>;
     constexpr int TOK = Sh::kTok;
-    extern __shared__ __align__(128) uint8_t smem[];
-    Sh& sh = *reinterpret_cast<Sh*>(smem);
+    extern __shared__ __align__(1024) uint8_t smem[];
+    // the 128-byte swizzle repeats every 1024 bytes: stages start on 1024
+    uint8_t* const ring = smem + ((1024u - (smem_u32(smem) & 1023u)) & 1023u);
+    Sh& sh = *reinterpret_cast<Sh*>(ring + (size_t)a.stages * a.stage_bytes);
     constexpr int kFixed = ((int)sizeof(Sh) + 127) / 128 * 128;
-    uint8_t* const ring = smem + kFixed;
-    float* const xs = reinterpret_cast<float*>(ring + (size_t)a.stages * a.stage_bytes);  // [blocks][TOK]
+    float* const xs = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(&sh) + kFixed);  // [blocks][TOK]
     uint8_t* const cols = reinterpret_cast<uint8_t*>(xs) + (a.blocks * TOK * 4 + 127) / 128 * 128;
     const int col_pitch = a.blocks * 128 + 64;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -248,7 +247,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (threadIdx.x == 0) {
         for (int s = 0; s < a.stages; ++s) {
             mbar_init(smem_u32(&sh.full[s]), 1);
-            mbar_init(smem_u32(&sh.empty[s]), kWarps);
+            mbar_init(smem_u32(&sh.empty[s]), kWarps / 2);
         }
         sh.abort_flag = 0;
         sh.issued = 0;
@@ -299,9 +298,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const uint32_t bar = smem_u32(&sh.full[slot]);
                     const uint32_t dst = smem_u32(ring + (size_t)slot * a.stage_bytes);
                     mbar_arrive_expect_tx(bar, (uint32_t)a.stage_bytes);
-                    copy_weights(dst, &tw, c * (kChunk / 4), row, expert, bar, wpol);
+                    copy_box(dst, &tw, c * a.k_step, c * a.block_step, row, expert, bar, wpol);
                     if (MODE == GEMM)
-                        copy_tokens(dst + kWStage, &tx, c * (kChunk / 4), bar, xpol);
+                        copy_box(dst + kWStage, &tx, c * a.k_step, c * a.block_step, 0, 0, bar, xpol);
                     sh.issued = sh.issued + 1;
                     if (++slot == a.stages) {
                         slot = 0;
@@ -317,10 +316,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (MODE == UP && blockIdx.x == 0)
             for (int i = threadIdx.x; i < a.done_count; i += kWarps * 32)
                 a.done[i] = 0;
-        const int kb = warp & 3, mt = warp >> 2, g = lane >> 2, c4 = lane & 3;
-        int slot = 0, use = 0, cur_v = -1, n_tok = a.m, buf = 0;
+        const int kb = warp & 3, group = warp >> 2, g = lane >> 2, c4 = lane & 3;
+        int slot = group, use = 0, turn = 0, cur_v = -1, n_tok = a.m, buf = 0;
+        // where this thread's 16 bytes of a row's two halves lie
+        int at[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+            at[h] = kb * 128 + 16 * (a.swizzled ? (4 * h + c4) ^ (kb | (g & 1) << 2) : 4 * h + c4);
         // scale of this warp's block of chunk `lane`, fetched an item ahead
-        auto scale_of = [&](int it, int chunk) {
+        auto scale_of = [&](int it, int chunk, int part) {
             const int b = chunk * 4 + kb;
             if (it >= end || b >= a.blocks)
                 return 0.f;
@@ -329,17 +333,20 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (MODE == GEMM)
                 row_block = tile * kRows / 128;
             else if (MODE == UP)
-                row_block = ((int64_t)sh.lists[0].v_expert[v] * 2 + mt) * a.row_blocks + tile * 16 / 128;
+                row_block = ((int64_t)sh.lists[0].v_expert[v] * 2 + part) * a.row_blocks + tile * 16 / 128;
             else
                 row_block = (int64_t)sh.lists[0].v_expert[v] * a.row_blocks + tile * kRows / 128;
             return a.w_scales[row_block * a.blocks + b];
         };
-        float next_ws = scale_of(first, lane);
+        // (gate and up have scales of their own; otherwise both row tiles share one)
+        float next_ws[2] = {scale_of(first, lane, 0), MODE == UP ? scale_of(first, lane, 1) : 0.f};
         const int col_step = MODE == GEMM ? kChunk : col_pitch;
         for (int it = first; it < end; ++it) {
             const int v = it / a.tiles, tile = it - v * a.tiles;
-            float ws_lane = next_ws;
-            next_ws = scale_of(it + 1, lane);
+            float ws_lane[2] = {next_ws[0], next_ws[1]};
+            next_ws[0] = scale_of(it + 1, lane, 0);
+            if (MODE == UP)
+                next_ws[1] = scale_of(it + 1, lane, 1);
             if constexpr (MODE != GEMM) {
                 if (v != cur_v) {
                     cur_v = v;
@@ -387,86 +394,105 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
             const int n_nt = MODE == GEMM ? NT : (n_tok + 3) / 4;
-            float acc[NT][4];
+            float acc[2][NT][4];
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
-                acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.f;
-            for (int c = 0; c < n_chunks; ++c) {
+            for (int i = 0; i < 2 * NT; ++i)
+                acc[i / NT][i % NT][0] = acc[i / NT][i % NT][1] = acc[i / NT][i % NT][2] = acc[i / NT][i % NT][3] = 0.f;
+            for (int c = 0; c < n_chunks; ++c, turn ^= 1) {
                 if (MODE == GEMM && c > 0 && (c & 31) == 0)
-                    ws_lane = scale_of(it, c + lane);
+                    ws_lane[0] = scale_of(it, c + lane, 0);
+                if (turn != group)
+                    continue;
                 const bool ok = __all_sync(0xffffffffu, mbar_wait_bounded(smem_u32(&sh.full[slot]), (uint32_t)use & 1u, abort_flag));
                 if (!ok) {
                     if (lane == 0)
                         give_up();
                 } else if (c * 4 + kb < a.blocks) {
                     const uint8_t* st = ring + (size_t)slot * a.stage_bytes;
-                    const uint8_t* pa = st + (mt * 16 + g) * kChunk + kb * 128 + c4 * 16;
-                    const uint8_t* pb = (MODE == GEMM ? st + kWStage : cols + c * kChunk) + g * col_step + kb * 128 + c4 * 16;
-                    uint4 w[2][2];
+                    uint4 w[2][2][2];  // [row tile][rows g and g + 8][half]
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        w[h][0] = *reinterpret_cast<const uint4*>(pa + 64 * h);
-                        w[h][1] = *reinterpret_cast<const uint4*>(pa + 8 * kChunk + 64 * h);
-                    }
-                    const float ws = __shfl_sync(0xffffffffu, ws_lane, c & 31);
+                    for (int i = 0; i < 8; ++i)
+                        w[i >> 2][(i >> 1) & 1][i & 1] =
+                            *reinterpret_cast<const uint4*>(st + (g + (i >> 1) * 8) * kChunk + at[i & 1]);
+                    const float ws0 = __shfl_sync(0xffffffffu, ws_lane[0], c & 31);
+                    const float ws1 = MODE == UP ? __shfl_sync(0xffffffffu, ws_lane[1], c & 31) : ws0;
                     const float* px = xs + (c * 4 + kb) * TOK;
+                    const uint8_t* pb = (MODE == GEMM ? st + kWStage : cols + c * kChunk + kb * 128 + c4 * 16) + g * col_step;
 #pragma unroll
                     for (int n = 0; n < NT; ++n) {
                         if (MODE != GEMM && n >= n_nt)
                             break;
-                        float d[4] = {0.f, 0.f, 0.f, 0.f};
+                        float d[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
-                            const uint4 x = *reinterpret_cast<const uint4*>(pb + n * 8 * col_step + 64 * h);
-                            mma_e4m3(d, w[h][0].x, w[h][1].x, w[h][0].y, w[h][1].y, x.x, x.y);
-                            mma_e4m3(d, w[h][0].z, w[h][1].z, w[h][0].w, w[h][1].w, x.z, x.w);
+                            const uint4 x = *reinterpret_cast<const uint4*>(pb + n * 8 * col_step + (MODE == GEMM ? at[h] : 64 * h));
+#pragma unroll
+                            for (int t = 0; t < 2; ++t)
+                                mma_e4m3(d[t], w[t][0][h].x, w[t][1][h].x, w[t][0][h].y, w[t][1][h].y, x.x, x.y);
+#pragma unroll
+                            for (int t = 0; t < 2; ++t)
+                                mma_e4m3(d[t], w[t][0][h].z, w[t][1][h].z, w[t][0][h].w, w[t][1][h].w, x.z, x.w);
                         }
                         if (MODE == GEMM) {
                             const float2 s = *reinterpret_cast<const float2*>(px + n * 8 + 2 * c4);
-                            const float s0 = ws * s.x, s1 = ws * s.y;
-                            acc[n][0] = fmaf(d[0], s0, acc[n][0]);
-                            acc[n][1] = fmaf(d[1], s1, acc[n][1]);
-                            acc[n][2] = fmaf(d[2], s0, acc[n][2]);
-                            acc[n][3] = fmaf(d[3], s1, acc[n][3]);
+                            const float s0 = ws0 * s.x, s1 = ws0 * s.y;
+#pragma unroll
+                            for (int t = 0; t < 2; ++t) {
+                                acc[t][n][0] = fmaf(d[t][0], s0, acc[t][n][0]);
+                                acc[t][n][1] = fmaf(d[t][1], s1, acc[t][n][1]);
+                                acc[t][n][2] = fmaf(d[t][2], s0, acc[t][n][2]);
+                                acc[t][n][3] = fmaf(d[t][3], s1, acc[t][n][3]);
+                            }
                         } else {  // columns 2t and 2t + 1 are token t's upper and lower part
-                            const float s = ws * px[n * 4 + c4];
-                            acc[n][0] = fmaf(fmaf(d[1], 0.0625f, d[0]), s, acc[n][0]);
-                            acc[n][2] = fmaf(fmaf(d[3], 0.0625f, d[2]), s, acc[n][2]);
+                            const float sx = px[n * 4 + c4];
+#pragma unroll
+                            for (int t = 0; t < 2; ++t) {
+                                const float s = (t ? ws1 : ws0) * sx;
+                                acc[t][n][0] = fmaf(fmaf(d[t][1], 0.0625f, d[t][0]), s, acc[t][n][0]);
+                                acc[t][n][2] = fmaf(fmaf(d[t][3], 0.0625f, d[t][2]), s, acc[t][n][2]);
+                            }
                         }
                     }
                 }
                 __syncwarp();
                 if (lane == 0)
                     mbar_arrive(smem_u32(&sh.empty[slot]));
-                if (++slot == a.stages) {
-                    slot = 0;
+                if ((slot += 2) >= a.stages) {
+                    slot = group;
                     ++use;
                 }
             }
-            float* red = sh.red[buf][mt][kb];
+            if (Sh::kBufs == 1)
+                consumers_sync();  // the item before has been read
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                if (MODE == GEMM) {
+            for (int t = 0; t < 2; ++t) {
+                float* red = sh.red[buf][t][warp];
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        red[(n * 8 + 2 * c4 + (j & 1)) * 20 + g + (j >> 1) * 8] = acc[n][j];
-                } else {
-                    red[(n * 4 + c4) * 20 + g] = acc[n][0];
-                    red[(n * 4 + c4) * 20 + g + 8] = acc[n][2];
+                for (int n = 0; n < NT; ++n) {
+                    if (MODE == GEMM) {
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            red[(n * 8 + 2 * c4 + (j & 1)) * 20 + g + (j >> 1) * 8] = acc[t][n][j];
+                    } else if (n < n_nt) {
+                        red[(n * 4 + c4) * 20 + g] = acc[t][n][0];
+                        red[(n * 4 + c4) * 20 + g + 8] = acc[t][n][2];
+                    }
                 }
             }
             consumers_sync();
-            auto sum4 = [&](int tile16, int t, int r) {
-                const int i = t * 20 + r;
-                return (sh.red[buf][tile16][0][i] + sh.red[buf][tile16][1][i]) +
-                       (sh.red[buf][tile16][2][i] + sh.red[buf][tile16][3][i]);
+            auto total_of = [&](int tile16, int t, int r) {
+                float v = 0.f;
+#pragma unroll
+                for (int w = 0; w < kWarps; ++w)
+                    v += sh.red[buf][tile16][w][t * 20 + r];
+                return v;
             };
             const int tid = threadIdx.x;
             if constexpr (MODE == GEMM) {
                 for (int o = tid; o < a.m * kRows; o += kWarps * 32) {
                     const int t = o >> 5, r = o & 31, n = tile * kRows + r;
                     if (n < a.rows) {
-                        const float yv = sum4(r >> 4, t, r & 15);
+                        const float yv = total_of(r >> 4, t, r & 15);
                         if (a.y_bf16)
                             static_cast<uint16_t*>(a.y)[t * a.ldy + n] = __bfloat16_as_ushort(__float2bfloat16_rn(yv));
                         else
@@ -478,7 +504,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int o = tid; o < n_tok * 16; o += kWarps * 32) {
                     const int t = o >> 4, r = o & 15, row = tile * 16 + r;
                     if (row < a.rows) {
-                        const float gate = sum4(0, t, r), up = sum4(1, t, r);
+                        const float gate = total_of(0, t, r), up = total_of(1, t, r);
                         const float hv = __fdiv_rn(gate, 1.0f + expf(-gate)) * up;
                         a.h[(int64_t)l.list[l.v_first[v] + t] * a.rows + row] = __bfloat16_as_ushort(__float2bfloat16_rn(hv));
                     }
@@ -488,7 +514,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int o = tid; o < n_tok * kRows; o += kWarps * 32) {
                     const int t = o >> 5, r = o & 31, row = tile * kRows + r;
                     if (row < a.rows)
-                        a.part[(int64_t)l.list[l.v_first[v] + t] * a.rows + row] = sum4(r >> 4, t, r & 15);
+                        a.part[(int64_t)l.list[l.v_first[v] + t] * a.rows + row] = total_of(r >> 4, t, r & 15);
                 }
                 // The pass that finishes a tile last adds up its tokens' choices, in their order.
                 __threadfence();
@@ -515,7 +541,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
             }
-            buf ^= 1;
+            buf ^= Sh::kBufs - 1;
         }
         if (MODE == DOWN && passes == 0)  // no token has an expert
             for (int64_t o = (int64_t)blockIdx.x * kWarps * 32 + threadIdx.x; o < (int64_t)a.m * a.rows;
@@ -547,15 +573,20 @@ PFN_cuTensorMapEncodeTiled_v12000 stream_encoder()
     return fn;
 }
 
-// Rows of K codes as words (a box is 512 bytes wide; words past K, and rows past
-// the last, read as zeros).
-bool encode_words(CUtensorMap* map, const void* base, int rank, const cuuint64_t (&dims)[4], const cuuint64_t (&strides)[3],
-                  const cuuint32_t (&box)[4])
+// [experts, parts, rows, K] codes, rows ld bytes apart.  A box is 512 bytes of K, zeros past the edges: as lines of 128
+// bytes where K is cut into such, as words otherwise.
+bool encode_rows(CUtensorMap* map, const void* base, bool lines, int64_t K, int64_t rows, int64_t ld, int64_t parts,
+                 int64_t experts, int box_rows)
 {
-    const cuuint32_t ones[4] = {1, 1, 1, 1};
     PFN_cuTensorMapEncodeTiled_v12000 enc = stream_encoder();
-    return enc && enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT32, (cuuint32_t)rank, const_cast<void*>(base), dims, strides, box, ones,
-                      CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+    const cuuint64_t k = (cuuint64_t)K, l = (cuuint64_t)ld, r = (cuuint64_t)rows, p = (cuuint64_t)parts;
+    const cuuint64_t dims[5] = {lines ? 128 : k / 4, lines ? k / 128 : 1, r, p, (cuuint64_t)experts};
+    const cuuint64_t strides[4] = {lines ? 128 : l, l, l * r, l * r * p};
+    const cuuint32_t box[5] = {128, lines ? 4u : 1u, (cuuint32_t)box_rows, (cuuint32_t)parts, 1};
+    const cuuint32_t ones[5] = {1, 1, 1, 1, 1};
+    return enc && enc(map, lines ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_UINT32, 5, const_cast<void*>(base),
+                      dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                      lines ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                       CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -572,18 +603,19 @@ cudaError_t launch_stream(StreamArgs a, int items, cudaStream_t s)
         return e;
     a.blocks = (a.K + 127) / 128;
     a.stage_bytes = kWStage + (MODE == GEMM ? 8 * NT * kChunk : 0);
-    const cuuint64_t K = (cuuint64_t)a.K, rows = (cuuint64_t)a.rows, parts = MODE == UP ? 2 : 1;
+    a.swizzled = a.K % 128 == 0;
+    a.k_step = a.swizzled ? 0 : kChunk / 4;
+    a.block_step = a.swizzled ? 4 : 0;
+    const int parts = MODE == UP ? 2 : 1;
     CUtensorMap tw{}, tx{};
-    if (!encode_words(&tw, a.W, 4, {K / 4, rows, parts, (cuuint64_t)std::max(a.E, 1)}, {K, K * rows, K * rows * parts},
-                      {kChunk / 4, (cuuint32_t)(kRows / parts), (cuuint32_t)parts, 1}) ||
-        (MODE == GEMM && !encode_words(&tx, a.x, 2, {K / 4, (cuuint64_t)a.m, 1, 1}, {(cuuint64_t)a.ldx, 0, 0},
-                                       {kChunk / 4, 8 * NT, 1, 1})))
+    if (!encode_rows(&tw, a.W, a.swizzled, a.K, a.rows, a.K, parts, std::max(a.E, 1), kRows / parts) ||
+        (MODE == GEMM && !encode_rows(&tx, a.x, a.swizzled, a.K, a.m, a.ldx, 1, 1, 8 * NT)))
         return cudaErrorInvalidValue;
-    const size_t fixed = (sizeof(Sh) + 127) / 128 * 128 + (size_t)(a.blocks * Sh::kTok * 4 + 127) / 128 * 128 +
+    const size_t fixed = 1024 + (sizeof(Sh) + 127) / 128 * 128 + (size_t)(a.blocks * Sh::kTok * 4 + 127) / 128 * 128 +
                          (MODE == GEMM ? 0 : (size_t)(8 * NT) * (a.blocks * 128 + 64));
     if (fixed + 2 * (size_t)a.stage_bytes > (size_t)di.smem_optin)
         return cudaErrorInvalidConfiguration;
-    a.stages = (int)std::min<size_t>(16, ((size_t)di.smem_optin - fixed) / a.stage_bytes);
+    a.stages = (int)std::min<size_t>(16, ((size_t)di.smem_optin - fixed) / a.stage_bytes) & ~1;
     return launch_pdl(fp8_stream_kernel<MODE, NT>, dim3((unsigned)std::min(items, di.sm_count)), dim3(kThreads),
                       fixed + (size_t)a.stages * a.stage_bytes, s, a, tw, tx);
 }
