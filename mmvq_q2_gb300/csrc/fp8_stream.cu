@@ -8,8 +8,10 @@
 // bound: 2.0 TB/s).  Two groups of four warps take turns at the stages; a
 // warp feeds its 128 values of all 32 rows to the tensor cores as they are
 // (mma.sync m16n8k32 on e4m3, weights as the 16 rows, tokens as the 8
-// columns), scales each block's sums in fp32 and adds them up.  The eight
-// warps are joined through shared memory at the item's end.  (The
+// columns), scales each block's sums in fp32 and adds them up.  Three more
+// warps join the eight through shared memory and store, while those go on
+// with the next item (with the eight doing it themselves, fp8_moe's second
+// launch, with its counters, took twice the time).  (The
 // 5th-generation tensor cores would want 128 weight rows or tokens a tile; at
 // these sizes the MMAs take a few percent of the time either way.)
 //
@@ -43,7 +45,8 @@ __device__ int g_fp8_stream_error = 0;
 namespace {
 
 constexpr int kWarps = 8;                      // that compute, in two groups; one more copies
-constexpr int kThreads = (kWarps + 1) * 32;
+constexpr int kEndWarps = 3;                   // that join and store
+constexpr int kThreads = (kWarps + 1 + kEndWarps) * 32;
 constexpr int kRows = 32;                      // weight rows of an item
 constexpr int kChunk = 512;                    // values of a row in a stage
 constexpr int kWStage = kRows * kChunk;
@@ -104,8 +107,14 @@ __device__ __forceinline__ float2 from_e4m3x2(uint32_t v)
     return make_float2(half_lo_f(h), half_hi_f(h));
 }
 
-// The eight computing warps.
-__device__ __forceinline__ void consumers_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+// The computing warps among themselves, and those that end items.
+__device__ __forceinline__ void consumers_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kWarps * 32) : "memory"); }
+__device__ __forceinline__ void enders_sync() { asm volatile("bar.sync 6, %0;" ::"n"(kEndWarps * 32) : "memory"); }
+// Between the two: buffer `buf` is full, or free again; one side arrives, the other waits.
+constexpr int kBothSides = (kWarps + kEndWarps) * 32;
+__device__ __forceinline__ void pair_arrive(int id) { asm volatile("bar.arrive %0, %1;" ::"r"(id), "n"(kBothSides) : "memory"); }
+__device__ __forceinline__ void pair_sync(int id) { asm volatile("bar.sync %0, %1;" ::"r"(id), "n"(kBothSides) : "memory"); }
+constexpr int kBarFull = 2, kBarFree = 4;
 
 // The experts that have a token, as passes of up to CAP (token, choice) pairs.
 struct Lists {
@@ -223,7 +232,7 @@ struct Shared {
     static constexpr int kTok = MODE == GEMM ? 8 * NT : 4 * NT;  // tokens of a pass
     uint64_t full[16], empty[16];
     static constexpr int kBufs = MODE == GEMM && NT == 4 ? 1 : 2;
-    int abort_flag, issued, last[2];
+    int abort_flag, issued, last;
     float red[kBufs][2][kWarps][kTok * 20];  // [buffer][row tile][warp]: 16 rows of a token, 20 apart
     Lists lists[MODE == GEMM ? 0 : 1];
 };
@@ -310,12 +319,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
         __syncwarp();
-    } else {
+    } else if (warp < kWarps) {
         if (MODE == DOWN)
             pdl_wait();
-        if (MODE == UP && blockIdx.x == 0)
-            for (int i = threadIdx.x; i < a.done_count; i += kWarps * 32)
-                a.done[i] = 0;
         const int kb = warp & 3, group = warp >> 2, g = lane >> 2, c4 = lane & 3;
         int slot = group, use = 0, turn = 0, cur_v = -1, n_tok = a.m, buf = 0;
         // where this thread's 16 bytes of a row's two halves lie
@@ -342,7 +348,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         float next_ws[2] = {scale_of(first, lane, 0), MODE == UP ? scale_of(first, lane, 1) : 0.f};
         const int col_step = MODE == GEMM ? kChunk : col_pitch;
         for (int it = first; it < end; ++it) {
-            const int v = it / a.tiles, tile = it - v * a.tiles;
+            const int v = it / a.tiles;
             float ws_lane[2] = {next_ws[0], next_ws[1]};
             next_ws[0] = scale_of(it + 1, lane, 0);
             if (MODE == UP)
@@ -462,8 +468,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     ++use;
                 }
             }
-            if (Sh::kBufs == 1)
-                consumers_sync();  // the item before has been read
+            if (it - first >= Sh::kBufs)
+                pair_sync(kBarFree + buf);
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
                 float* red = sh.red[buf][t][warp];
@@ -479,7 +485,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
             }
-            consumers_sync();
+            pair_arrive(kBarFull + buf);
+            buf ^= Sh::kBufs - 1;
+        }
+    } else {
+        if (MODE == DOWN)
+            pdl_wait();
+        const int tid = (int)threadIdx.x - (kWarps + 1) * 32;
+        if (MODE == UP && blockIdx.x == 0)
+            for (int i = tid; i < a.done_count; i += kEndWarps * 32)
+                a.done[i] = 0;
+        int buf = 0;
+        for (int it = first; it < end; ++it) {
+            const int v = it / a.tiles, tile = it - v * a.tiles;
+            const int n_tok = MODE == GEMM ? a.m : sh.lists[0].v_count[v];
+            pair_sync(kBarFull + buf);
             auto total_of = [&](int tile16, int t, int r) {
                 float v = 0.f;
 #pragma unroll
@@ -487,9 +507,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     v += sh.red[buf][tile16][w][t * 20 + r];
                 return v;
             };
-            const int tid = threadIdx.x;
             if constexpr (MODE == GEMM) {
-                for (int o = tid; o < a.m * kRows; o += kWarps * 32) {
+                for (int o = tid; o < a.m * kRows; o += kEndWarps * 32) {
                     const int t = o >> 5, r = o & 31, n = tile * kRows + r;
                     if (n < a.rows) {
                         const float yv = total_of(r >> 4, t, r & 15);
@@ -501,7 +520,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             } else if constexpr (MODE == UP) {
                 const Lists& l = sh.lists[0];
-                for (int o = tid; o < n_tok * 16; o += kWarps * 32) {
+                for (int o = tid; o < n_tok * 16; o += kEndWarps * 32) {
                     const int t = o >> 4, r = o & 15, row = tile * 16 + r;
                     if (row < a.rows) {
                         const float gate = total_of(0, t, r), up = total_of(1, t, r);
@@ -511,20 +530,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             } else {
                 const Lists& l = sh.lists[0];
-                for (int o = tid; o < n_tok * kRows; o += kWarps * 32) {
+                for (int o = tid; o < n_tok * kRows; o += kEndWarps * 32) {
                     const int t = o >> 5, r = o & 31, row = tile * kRows + r;
                     if (row < a.rows)
                         a.part[(int64_t)l.list[l.v_first[v] + t] * a.rows + row] = total_of(r >> 4, t, r & 15);
                 }
                 // The pass that finishes a tile last adds up its tokens' choices, in their order.
                 __threadfence();
-                consumers_sync();
+                enders_sync();
                 if (tid == 0)
-                    sh.last[buf] = atomicAdd(&a.done[tile], 1) == passes - 1;
-                consumers_sync();
-                if (sh.last[buf]) {
+                    sh.last = atomicAdd(&a.done[tile], 1) == passes - 1;
+                enders_sync();
+                if (sh.last) {
                     __threadfence();
-                    for (int o = tid; o < a.m * kRows; o += kWarps * 32) {
+                    for (int o = tid; o < a.m * kRows; o += kEndWarps * 32) {
                         const int t = o >> 5, row = tile * kRows + (o & 31);
                         if (row >= a.rows)
                             continue;
@@ -541,11 +560,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
             }
+            if (it + Sh::kBufs < end)
+                pair_arrive(kBarFree + buf);
             buf ^= Sh::kBufs - 1;
         }
         if (MODE == DOWN && passes == 0)  // no token has an expert
-            for (int64_t o = (int64_t)blockIdx.x * kWarps * 32 + threadIdx.x; o < (int64_t)a.m * a.rows;
-                 o += (int64_t)gridDim.x * kWarps * 32) {
+            for (int64_t o = (int64_t)blockIdx.x * kEndWarps * 32 + tid; o < (int64_t)a.m * a.rows;
+                 o += (int64_t)gridDim.x * kEndWarps * 32) {
                 const int64_t at = o / a.rows * a.ldy + o % a.rows;
                 if (a.y_bf16)
                     static_cast<uint16_t*>(a.y)[at] = 0;
