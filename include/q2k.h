@@ -623,7 +623,7 @@ size_t fp8_moe_workspace_bytes(int64_t m, int64_t topk, int64_t dim, int64_t int
  *             g = gate_e x_t,  u = up_e x_t,  e = ids[t, j]
  * Products accumulate in fp32 as in fp8_gemm; x enters as it is (bf16), h
  * is rounded to bf16 (as the buffers of the other expert calls are); the sum
- * over j is fp32 in j's order; rounded once to bf16 where y is bf16.  A call
+ * over j is fp32, by rising expert; rounded once to bf16 where y is bf16.  A call
  * repeats bit for bit.  A token with a NaN or an infinity gives NaN.
  *   workspace  at least fp8_moe_workspace_bytes(m, topk, dim, inter) bytes,
  *              256-byte aligned; calls that overlap need one each

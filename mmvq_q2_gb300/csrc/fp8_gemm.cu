@@ -23,9 +23,8 @@
 #include <algorithm>
 #include <mutex>
 
-#include "q2k_common.cuh"
+#include "fp8_common.cuh"
 #include "q2k_internal.h"
-#include "q2k_umma.cuh"
 
 namespace q2k {
 
@@ -55,18 +54,6 @@ struct GemmShared {
     int abort_flag, issued;
 };
 
-// D fp32, A and B e4m3, both K-major, M = 128.
-constexpr uint32_t instr_desc_e4m3(int n) { return (1u << 4) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(kTM >> 4) << 24); }
-
-__device__ __forceinline__ void umma_e4m3(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc, bool acc)
-{
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)acc)
-        : "memory");
-}
-
 // 32 fp32 columns of this warp's 32 lanes; complete after settle().
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&v)[32])
 {
@@ -78,17 +65,6 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&v)[32])
           "=f"(v[17]), "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]), "=f"(v[24]),
           "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
         : "r"(taddr));
-}
-
-// Waits for this warp's loads; what uses the values comes after.
-__device__ __forceinline__ void settle(float (&v)[32])
-{
-    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-#pragma unroll
-    for (int i = 0; i < 32; i += 8)
-        asm volatile(""
-                     : "+f"(v[i]), "+f"(v[i + 1]), "+f"(v[i + 2]), "+f"(v[i + 3]), "+f"(v[i + 4]), "+f"(v[i + 5]),
-                       "+f"(v[i + 6]), "+f"(v[i + 7]));
 }
 
 // acc += v * f, two values an instruction.
@@ -159,11 +135,6 @@ __device__ __forceinline__ void store_row(const GemmArgs& a, int64_t row, int co
                     y[i] = v[i];
         }
     }
-}
-
-__device__ __forceinline__ void cluster_sync()
-{
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
 __device__ __forceinline__ void store_peer(uint32_t addr, uint32_t rank, float v)
@@ -241,7 +212,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     int m0, n0;
                     place(t, m0, n0);
                     for (int k = k_first; k < k_end; ++k) {
-                        if (use > 0 && !mbar_wait_bounded(smem_u32(&sh.empty[slot]), (uint32_t)(use - 1) & 1u, abort_flag)) {
+                        if (use > 0 && !mbar_wait_near(smem_u32(&sh.empty[slot]), (uint32_t)(use - 1) & 1u, abort_flag)) {
                             give_up();
                             ok = false;
                             break;
@@ -266,8 +237,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int t = tile0; t < tiles && ok; t += step)
                 for (int k = k_first; k < k_end; ++k, ++n) {
                     const int buf = n & 1;
-                    if (!mbar_wait_bounded(smem_u32(&sh.full[slot]), (uint32_t)use & 1u, abort_flag) ||
-                        (n >= 2 && !mbar_wait_bounded(smem_u32(&sh.acc_empty[buf]), (uint32_t)((n >> 1) - 1) & 1u, abort_flag)))
+                    if (!mbar_wait_near(smem_u32(&sh.full[slot]), (uint32_t)use & 1u, abort_flag) ||
+                        (n >= 2 && !mbar_wait_near(smem_u32(&sh.acc_empty[buf]), (uint32_t)((n >> 1) - 1) & 1u, abort_flag)))
                         ok = false;
                     ok = __all_sync(0xffffffffu, ok);
                     if (!ok) {
@@ -312,7 +283,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int buf = n & 1;
                 const float f_next = k + 1 < k_end ? xs[k + 1] * ws[k + 1] : 0.f;
                 const bool ok = __all_sync(
-                    0xffffffffu, mbar_wait_bounded(smem_u32(&sh.acc_full[buf]), (uint32_t)(n >> 1) & 1u, abort_flag));
+                    0xffffffffu, mbar_wait_near(smem_u32(&sh.acc_full[buf]), (uint32_t)(n >> 1) & 1u, abort_flag));
                 if (!ok) {
                     if (lane == 0)
                         give_up();
@@ -370,9 +341,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
     __syncthreads();
+    const volatile int never = 0;
     if (sh.abort_flag && threadIdx.x == 0)  // let the copies that were issued land before the CTA exits
         for (int i = max(0, sh.issued - a.stages); i < sh.issued; ++i)
-            mbar_wait_bounded(smem_u32(&sh.full[i % a.stages]), (uint32_t)(i / a.stages) & 1u, nullptr);
+            mbar_wait_near(smem_u32(&sh.full[i % a.stages]), (uint32_t)(i / a.stages) & 1u, &never);
     __syncthreads();
     if (warp == 1)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(2 * BN) : "memory");

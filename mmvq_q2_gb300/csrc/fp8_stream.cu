@@ -2,40 +2,43 @@
 // fp8_gemm for up to 32 rows, and fp8_moe, the routed experts of a few tokens.
 //
 // Bound by memory: each weight is read once and used for a handful of tokens.
-// A persistent CTA an SM walks items of 32 weight rows.  One warp copies the
-// rows, 512 values at a time, into a ring of shared-memory stages, a tensor
-// copy each (with a bulk copy a row, 73 cycles each, their issue was the
-// bound: 2.0 TB/s).  Two groups of four warps take turns at the stages; a
-// warp feeds its 128 values of all 32 rows to the tensor cores as they are
-// (mma.sync m16n8k32 on e4m3, weights as the 16 rows, tokens as the 8
-// columns), scales each block's sums in fp32 and adds them up.  Three more
-// warps join the eight through shared memory and store, while those go on
-// with the next item (with the eight doing it themselves, fp8_moe's second
-// launch, with its counters, took twice the time).  (The
-// 5th-generation tensor cores would want 128 weight rows or tokens a tile; at
-// these sizes the MMAs take a few percent of the time either way.)
+// So the weights' way is short: three warps copy tiles of 2 x 128 values of K by
+// up to 128 rows into a ring of shared-memory stages (tensor copies, 128-byte
+// swizzled; a warp takes 390 cycles from one stage's copy to the next's, so
+// one alone was the bound), another issues tcgen05.mma kind::f8f6f4 on them as
+// they are, weight rows as M = 128, tokens as N = 16 or 32 columns.  The scales
+// change every 128 values of K, so each block of a stage has an accumulator of
+// its own in tensor memory, and four warps read them back, scale them and add
+// them up in fp32, a thread a row; that frees the stage.  (mma.sync, eight warps at the same
+// ring: it is made of conversions to f16 and f16 MMAs here, and was bound by
+// its instructions' latency: 16 rows of 16384 x 16384 52 to 59 us, experts of
+// 8 tokens 278 us.  A bulk copy a row, 512 bytes, was bound by their issue, 73
+// cycles each.)
 //
-// A thread needs 4 values of a row for each MMA.  Since the order along K is
-// free as long as both operands share it, it takes 16 neighbouring bytes of
-// its row and feeds them to two MMAs: one 16-byte load a row and 64 values.
-// The copies swizzle lines of 128 bytes, so that the loads of two rows meet no
-// bank twice; rows that are no multiple of 128 bytes cannot be cut into such
-// lines and lie as they are (loads then take twice the cycles).
+// A persistent CTA an SM.  Rows are shared out evenly: a tile has as many
+// rows, up to 128, as make the tiles a whole number for each SM, or for each
+// cluster of 2 or 4 that then share a tile along K and join through distributed
+// shared memory (an MMA takes its 39 cycles whatever rows the tile has, so
+// tiles are kept large).  fp8_moe's first launch (gate and up) gives each CTA an equal
+// run of units of 16 + 16 rows, expert after expert, up to four units a tile;
+// its second (down) gives each cluster its rows of y, of every expert in
+// turn, so that the sum over a token's experts stays with the cluster.  (Joined
+// by whoever finished a tile last, the fences alone took 10000 cycles an item.)
 //
 // bf16 tokens (fp8_moe) enter as two columns of e4m3 each: with a power of
 // two that brings a block's largest below 256, the upper 4 bits of a value
 // are one e4m3 number and what is left, times 16, another.  Together they are
 // the bf16 value exactly, where it is within 2^-13 of the block's largest (and
-// off by less than 2^-20 of that below).  The weights need no conversion that
-// way: expanding them to bf16 costs 2 to 4 instructions a pair, more than the
-// streaming leaves room for.
+// off by less than 2^-20 of that below).  Four warps write them into the
+// stages, each its share of the blocks, the next one's values on their way.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
 #include <algorithm>
+#include <cmath>
 #include <mutex>
 
-#include "q2k_common.cuh"
+#include "fp8_common.cuh"
 #include "q2k_internal.h"
 
 namespace q2k {
@@ -44,52 +47,55 @@ __device__ int g_fp8_stream_error = 0;
 
 namespace {
 
-constexpr int kWarps = 8;                      // that compute, in two groups; one more copies
-constexpr int kEndWarps = 3;                   // that join and store
-constexpr int kThreads = (kWarps + 1 + kEndWarps) * 32;
-constexpr int kRows = 32;                      // weight rows of an item
-constexpr int kChunk = 512;                    // values of a row in a stage
-constexpr int kWStage = kRows * kChunk;
+constexpr int kRowsMax = 128;  // weight rows of a tile: the MMA's M
+constexpr int kBlock = 128;    // values of K that share a scale: a swizzle row
+constexpr int kPair = 2;       // such blocks in a stage
+constexpr int kUnit = 16;      // UP: rows of gate, and of up, in a unit
+constexpr int kMaxStages = 16;
+constexpr int kCopyWarps = 3, kSplitWarps = 4;
 constexpr int kMaxPairs = 1024, kMaxExperts = 1024;
 
 enum Mode : int { GEMM = 0, UP = 1, DOWN = 2 };
 
+// Warps: one for the MMAs, three for copies, four that add up (tensor memory lanes by warp % 4), four for columns.
+constexpr int threads_of(int mode) { return mode == GEMM ? 256 : 384; }
+
+// Stages that have their accumulators in tensor memory, 512 columns of it.
+constexpr int stages_of(int columns) { return 512 / (kPair * columns); }
+
 struct StreamArgs {
-    const uint8_t* W;
     const float* w_scales;
-    int K, blocks;      // blocks of 128 along K
-    int rows;           // weight rows: N; inter (UP); dim (DOWN)
-    int row_blocks;     // of w_scales
-    int tiles;          // items of one matrix
-    int stages, stage_bytes;  // stages: an even number, so that a stage is always the same group's
-    int swizzled;             // lines of 128 bytes
-    int k_step, block_step;   // coordinates of a chunk: (0, 4 blocks) swizzled, (128 words, 0) otherwise
+    int K, blocks, pairs;     // blocks of 128 along K, and pairs of them
+    int rows;                 // weight rows: N; inter (UP); dim (DOWN)
+    int row_blocks;           // of w_scales
+    int tile_rows, tiles;     // rows of a tile (UP: of a unit), tiles of one matrix
+    int box_bytes;            // of one copy of weights
+    int stages, w_bytes;      // of weights in a block of a stage
     int m;
     // GEMM
-    const uint8_t* x;
     const float* x_scales;
-    int64_t ldx, ld_xs;
+    int64_t ld_xs;
     // fp8_moe
-    const uint16_t* xb;     // bf16 rows: tokens (UP) or h of the pairs (DOWN)
+    const uint16_t* xb;       // bf16 rows: tokens (UP) or h of the pairs (DOWN)
+    int64_t ldx;
     const int32_t* ids;
     const float* route_w;
     int topk, E;
-    uint16_t* h;            // [pairs, inter]
-    float* part;            // [pairs, dim]
-    int* done;              // [tiles of dim]
-    int done_count;
+    uint16_t* h;              // [pairs, inter]
     // results
     void* y;
     int64_t ldy;
     int y_bf16;
 };
 
-__device__ __forceinline__ void mma_e4m3(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                         uint32_t b1)
+// 16 fp32 columns of this warp's 32 lanes; complete after settle().
+__device__ __forceinline__ void tmem_load16(uint32_t taddr, float* v)
 {
-    asm("mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]),
+          "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15])
+        : "r"(taddr));
 }
 
 // Two floats as e4m3, and back.
@@ -107,14 +113,26 @@ __device__ __forceinline__ float2 from_e4m3x2(uint32_t v)
     return make_float2(half_lo_f(h), half_hi_f(h));
 }
 
-// The computing warps among themselves, and those that end items.
-__device__ __forceinline__ void consumers_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kWarps * 32) : "memory"); }
-__device__ __forceinline__ void enders_sync() { asm volatile("bar.sync 6, %0;" ::"n"(kEndWarps * 32) : "memory"); }
-// Between the two: buffer `buf` is full, or free again; one side arrives, the other waits.
-constexpr int kBothSides = (kWarps + kEndWarps) * 32;
-__device__ __forceinline__ void pair_arrive(int id) { asm volatile("bar.arrive %0, %1;" ::"r"(id), "n"(kBothSides) : "memory"); }
-__device__ __forceinline__ void pair_sync(int id) { asm volatile("bar.sync %0, %1;" ::"r"(id), "n"(kBothSides) : "memory"); }
-constexpr int kBarFull = 2, kBarFree = 4;
+// A box of 128 bytes by rows, by gate and up, by expert.
+__device__ __forceinline__ void copy_box(uint32_t dst, const CUtensorMap* map, int k, int row, int expert, uint32_t bar,
+                                         uint64_t policy)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
+        " [%0], [%1, {%2, %3, %4, %5}], [%6], %7;" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(k), "r"(row), "r"(0), "r"(expert), "r"(bar), "l"(policy)
+        : "memory");
+}
+
+__device__ __forceinline__ float load_peer(uint32_t addr, uint32_t rank)
+{
+    float v;
+    asm volatile("{\n\t.reg .b32 p;\n\tmapa.shared::cluster.u32 p, %1, %2;\n\tld.shared::cluster.f32 %0, [p];\n\t}"
+                 : "=f"(v)
+                 : "r"(addr), "r"(rank)
+                 : "memory");
+    return v;
+}
 
 // The experts that have a token, as passes of up to CAP (token, choice) pairs.
 struct Lists {
@@ -126,6 +144,7 @@ struct Lists {
 };
 
 // By all threads; ends with a barrier.
+template <int kThreads>
 __device__ void build_lists(Lists& l, const StreamArgs& a, int cap)
 {
     const int pairs = a.m * a.topk, tid = threadIdx.x;
@@ -190,15 +209,18 @@ __device__ void build_lists(Lists& l, const StreamArgs& a, int cap)
     __syncthreads();
 }
 
-// A block of 128 bf16 values, 4 a lane, as two rows of e4m3 and their scale.
-__device__ __forceinline__ void split_block(const float (&v)[4], uint8_t* upper, uint8_t* lower, float* scale)
+// A block of 128 bf16 values, 4 a lane, as the two e4m3 rows of column pair t (128-byte swizzled), and its scale.
+__device__ __forceinline__ void split_block(uint2 raw, uint8_t* tile, int t, float* scale)
 {
+    const int lane = threadIdx.x & 31;
+    const float v[4] = {__uint_as_float(raw.x << 16), __uint_as_float(raw.x & 0xffff0000u), __uint_as_float(raw.y << 16),
+                        __uint_as_float(raw.y & 0xffff0000u)};
     const uint32_t top = __reduce_max_sync(
         0xffffffffu, max(max(__float_as_uint(v[0]) & 0x7fffffffu, __float_as_uint(v[1]) & 0x7fffffffu),
                          max(__float_as_uint(v[2]) & 0x7fffffffu, __float_as_uint(v[3]) & 0x7fffffffu)));
     // 2^(7 - e) of the largest's exponent e, within fp32's powers of two for it and its inverse
     const uint32_t e = min(max(top >> 23, 20u), 254u);
-    const float f = __uint_as_float((261u - e) << 23), inv = __uint_as_float((e - 7u) << 23);
+    const float f = __uint_as_float((261u - e) << 23);
     float w[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -210,374 +232,477 @@ __device__ __forceinline__ void split_block(const float (&v)[4], uint8_t* upper,
     const float2 r0 = from_e4m3x2(u0), r1 = from_e4m3x2(u1);
     const uint32_t l0 = e4m3x2((w[0] - r0.x) * 16.f, (w[1] - r0.y) * 16.f);
     const uint32_t l1 = e4m3x2((w[2] - r1.x) * 16.f, (w[3] - r1.y) * 16.f);
-    *reinterpret_cast<uint32_t*>(upper) = u0 | u1 << 16;
-    *reinterpret_cast<uint32_t*>(lower) = l0 | l1 << 16;
-    if ((threadIdx.x & 31) == 0)
-        *scale = inv;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int row = 2 * t + i;
+        *reinterpret_cast<uint32_t*>(tile + row * kBlock + (((lane >> 2) ^ (row & 7)) << 4) + ((lane & 3) << 2)) =
+            i ? l0 | l1 << 16 : u0 | u1 << 16;
+    }
+    if (lane == 0)
+        *scale = __uint_as_float((e - 7u) << 23);
 }
 
-// A box of 512 bytes by rows, by gate and up, by expert.
-__device__ __forceinline__ void copy_box(uint32_t dst, const CUtensorMap* map, int k, int block, int row, int expert, uint32_t bar,
-                                         uint64_t policy)
-{
-    asm volatile(
-        "cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
-        " [%0], [%1, {%2, %3, %4, %5, %6}], [%7], %8;" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(k), "r"(block), "r"(row), "r"(0), "r"(expert), "r"(bar), "l"(policy)
-        : "memory");
-}
-
-template <int MODE, int NT>
+template <int MODE, int NC>
 struct Shared {
-    static constexpr int kTok = MODE == GEMM ? 8 * NT : 4 * NT;  // tokens of a pass
-    uint64_t full[16], empty[16];
-    static constexpr int kBufs = MODE == GEMM && NT == 4 ? 1 : 2;
-    int abort_flag, issued, last;
-    float red[kBufs][2][kWarps][kTok * 20];  // [buffer][row tile][warp]: 16 rows of a token, 20 apart
+    uint64_t full[kMaxStages], done[kMaxStages], freed[kMaxStages];  // of a stage: copied; multiplied; added up
+    uint32_t tmem;
+    int abort_flag;
+    alignas(16) float scales[MODE == GEMM ? 1 : kMaxStages][kPair][NC / 2];  // of a stage's columns; read four at a time
     Lists lists[MODE == GEMM ? 0 : 1];
 };
 
-template <int MODE, int NT>
-__global__ void __launch_bounds__(kThreads, 1)
+// What a CTA works on: pieces of a tile and a run of blocks along K, one after another.
+template <int MODE, int S>
+struct Walk {
+    int tiles, pairs, passes, rank;
+    int at, end, tile_at;                 // UP: units; else pairs of blocks of all passes
+    int pass, tile, units, k, k_end;      // the piece, k in pairs of blocks
+    bool last;                            // of its tile
+
+    __device__ __forceinline__ Walk(const StreamArgs& a, int n_passes) : tiles(a.tiles), pairs(a.pairs), passes(n_passes)
+    {
+        rank = S > 1 ? (int)blockIdx.x % S : 0;
+        tile_at = (int)blockIdx.x / S;
+        if (MODE == UP) {
+            const int64_t total = (int64_t)passes * tiles;
+            at = (int)(blockIdx.x * total / gridDim.x);
+            end = (int)((blockIdx.x + 1) * total / gridDim.x);
+        } else {
+            range();
+        }
+        pass = tile = k = k_end = 0;
+        units = 1;
+        last = true;
+    }
+    __device__ __forceinline__ void range()
+    {
+        const int total = passes * pairs;  // at most 1024 * 64
+        at = rank * total / S;
+        end = (rank + 1) * total / S;
+    }
+    __device__ __forceinline__ bool next()
+    {
+        if (MODE == UP) {
+            if (at >= end)
+                return false;
+            pass = at / tiles;
+            tile = at - pass * tiles;
+            units = min(min(4, tiles - tile), end - at);
+            at += units;
+            k = 0;
+            k_end = pairs;
+            return true;
+        }
+        if (tile_at >= tiles || at >= end)
+            return false;
+        tile = tile_at;
+        pass = MODE == GEMM ? 0 : at / pairs;
+        k = at - pass * pairs;
+        k_end = min(pairs, k + end - at);
+        at += k_end - k;
+        last = at >= end;
+        if (last) {  // the next tile, if there is one
+            tile_at += (int)gridDim.x / S;
+            range();
+        }
+        return true;
+    }
+};
+
+template <int MODE, int NC, int S>
+__global__ void __launch_bounds__(threads_of(MODE), 1)
     fp8_stream_kernel(const StreamArgs a, const __grid_constant__ CUtensorMap tw, const __grid_constant__ CUtensorMap tx)
 {
-    using Sh = Shared<MODE, NT>;
-    constexpr int TOK = Sh::kTok;
+    using Sh = Shared<MODE, NC>;
+    constexpr int kThreads = threads_of(MODE);
+    constexpr int TOK = MODE == GEMM ? NC : NC / 2;  // tokens of a pass
+    constexpr uint32_t kXBytes = NC * kBlock;        // of tokens in a block of a stage
+    constexpr uint32_t kTmem = (uint32_t)(stages_of(NC) * kPair * NC);
     extern __shared__ __align__(1024) uint8_t smem[];
-    // the 128-byte swizzle repeats every 1024 bytes: stages start on 1024
+    // The 128-byte swizzle repeats every 1024 bytes: stages start on 1024.  (An MMA reads 128 rows of weights whatever
+    // the tile has: past them, and past the ring's end, lie other bytes of this CTA, whose sums nothing uses.)
     uint8_t* const ring = smem + ((1024u - (smem_u32(smem) & 1023u)) & 1023u);
-    Sh& sh = *reinterpret_cast<Sh*>(ring + (size_t)a.stages * a.stage_bytes);
-    constexpr int kFixed = ((int)sizeof(Sh) + 127) / 128 * 128;
-    float* const xs = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(&sh) + kFixed);  // [blocks][TOK]
-    uint8_t* const cols = reinterpret_cast<uint8_t*>(xs) + (a.blocks * TOK * 4 + 127) / 128 * 128;
-    const int col_pitch = a.blocks * 128 + 64;
+    uint8_t* const x_ring = ring + (size_t)a.stages * kPair * a.w_bytes;
+    Sh& sh = *reinterpret_cast<Sh*>(x_ring + (size_t)a.stages * kPair * kXBytes);
+    // [m][128] sums of a tile (not UP)
+    float* const y_sum = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(&sh) + (sizeof(Sh) + 127) / 128 * 128);
+    float* const xs = y_sum + (S > 1 ? a.m * kRowsMax : 0);  // GEMM: [2 pairs][NC]
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < a.stages; ++s) {
-            mbar_init(smem_u32(&sh.full[s]), 1);
-            mbar_init(smem_u32(&sh.empty[s]), kWarps / 2);
+            mbar_init(smem_u32(&sh.full[s]), MODE == GEMM ? 1 : 2);
+            mbar_init(smem_u32(&sh.done[s]), 1);
+            mbar_init(smem_u32(&sh.freed[s]), 4);
         }
         sh.abort_flag = 0;
-        sh.issued = 0;
         fence_mbar_init();
+    }
+    if (warp == 0) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&sh.tmem)),
+                     "r"(kTmem)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
     // UP lets DOWN start only once what came before is complete: DOWN reads ids
     // and weights before it waits for UP.
     if (MODE != DOWN)
         pdl_wait();
     pdl_launch_dependents();
+    if constexpr (MODE == GEMM)
+        for (int i = threadIdx.x; i < a.pairs * kPair * NC; i += kThreads) {
+            const int b = i / NC, t = i % NC;
+            xs[i] = t < a.m && b < a.blocks ? a.x_scales[t * a.ld_xs + b] : 0.f;
+        }
+    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
     int passes = 1;
     if constexpr (MODE != GEMM) {
-        build_lists(sh.lists[0], a, TOK);
+        build_lists<kThreads>(sh.lists[0], a, TOK);
         passes = sh.lists[0].passes;
     } else {
-        for (int i = threadIdx.x; i < a.blocks * TOK; i += kThreads) {
-            const int b = i / TOK, t = i % TOK;
-            xs[i] = t < a.m ? a.x_scales[t * a.ld_xs + b] : 0.f;
-        }
         __syncthreads();
     }
-    const int total = passes * a.tiles;
-    const int first = (int)((int64_t)blockIdx.x * total / gridDim.x);
-    const int end = (int)((int64_t)(blockIdx.x + 1) * total / gridDim.x);
-    const int n_chunks = (a.K + kChunk - 1) / kChunk;
+    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+    const uint32_t tmem = sh.tmem;
+    const Lists& l = sh.lists[0];
 
     volatile int* const abort_flag = &sh.abort_flag;
     auto give_up = [&]() {
         atomicOr(&g_fp8_stream_error, Q2K_ERR_BIT_WAIT_TIMEOUT);
         *abort_flag = 1;
     };
+    // by a whole warp
+    auto wait = [&](uint64_t* bar, int use) {
+        const bool ok = __all_sync(0xffffffffu, mbar_wait_near(smem_u32(bar), (uint32_t)use & 1u, abort_flag));
+        if (!ok && lane == 0)
+            give_up();
+        return ok;
+    };
+    auto store = [&](int64_t t, int row, float v) {
+        if (a.y_bf16)
+            static_cast<uint16_t*>(a.y)[t * a.ldy + row] = __bfloat16_as_ushort(__float2bfloat16_rn(v));
+        else
+            static_cast<float*>(a.y)[t * a.ldy + row] = v;
+    };
+    Walk<MODE, S> work(a, passes);
+    const int q = warp & 3;  // of the warps that add up: their lanes, 32 rows
 
-    if (warp == kWarps) {
-        if (lane == 0) {  // copies
+    if (warp == 0) {
+        // ---- MMAs
+        constexpr uint32_t idesc = instr_desc_e4m3(NC);
+        const uint32_t w_bytes = (uint32_t)a.w_bytes, ring_at = smem_u32(ring), x_at = smem_u32(x_ring);
+        int slot = 0, use = 0;
+        bool ok = true, ready = false;
+        while (ok && work.next())
+            for (int k = work.k; k < work.k_end; ++k) {
+                if (!ready && !wait(&sh.full[slot], use)) {
+                    ok = false;
+                    break;
+                }
+                const int slot1 = slot + 1 == a.stages ? 0 : slot + 1, use1 = use + (slot1 == 0);
+                const bool full1 = mbar_ready(smem_u32(&sh.full[slot1]), (uint32_t)use1 & 1u);
+                asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+                const uint32_t s0 = uniform((uint32_t)slot);
+                const uint32_t sa = ring_at + s0 * kPair * w_bytes, sb = x_at + s0 * kPair * kXBytes, d = tmem + s0 * kPair * NC;
+                if (elect_one()) {
+#pragma unroll
+                    for (int p = 0; p < kPair; ++p)
+#pragma unroll
+                        for (int i = 0; i < kBlock / 32; ++i)  // K = 32 an MMA: 32 bytes along the swizzled row
+                            umma_e4m3(d + p * NC, desc_at(sa + p * w_bytes + 32 * i), desc_at(sb + p * kXBytes + 32 * i), idesc, i > 0);
+                    umma_commit(smem_u32(&sh.done[0]) + 8 * s0);
+                }
+                ready = __all_sync(0xffffffffu, full1);
+                slot = slot1;
+                use = use1;
+            }
+    } else if (warp <= kCopyWarps) {
+        // ---- copies: of every third stage
+        if (lane == 0) {
             const uint64_t wpol = l2_policy_evict_first(), xpol = l2_policy_evict_last();
-            int slot = 0, use = 0;
+            int slot = 0, use = 0, turn = 0, last_slot = -1, last_use = 0;
             bool ok = true;
-            for (int it = first; it < end && ok; ++it) {
-                const int v = it / a.tiles, tile = it - v * a.tiles;
-                const int row = tile * (MODE == UP ? 16 : kRows);
-                const int expert = MODE == GEMM ? 0 : sh.lists[0].v_expert[v];
-                for (int c = 0; c < n_chunks; ++c) {
-                    if (use > 0 && !mbar_wait_bounded(smem_u32(&sh.empty[slot]), (uint32_t)(use - 1) & 1u, abort_flag)) {
-                        give_up();
-                        ok = false;
-                        break;
+            while (ok && work.next()) {
+                const int expert = MODE == GEMM ? 0 : l.v_expert[work.pass];
+                for (int k = work.k; k < work.k_end; ++k) {
+                    if (turn == warp - 1) {
+                        if (use > 0 && !mbar_wait_near(smem_u32(&sh.freed[slot]), (uint32_t)(use - 1) & 1u, abort_flag)) {
+                            give_up();
+                            ok = false;
+                            break;
+                        }
+                        const uint32_t bar = smem_u32(&sh.full[slot]);
+                        uint32_t dst = smem_u32(ring + (size_t)slot * kPair * a.w_bytes);
+                        mbar_arrive_expect_tx(bar, kPair * ((uint32_t)(work.units * a.box_bytes) + (MODE == GEMM ? kXBytes : 0u)));
+#pragma unroll
+                        for (int p = 0; p < kPair; ++p, dst += (uint32_t)a.w_bytes) {
+                            const int at = (k * kPair + p) * kBlock;
+                            for (int u = 0; u < work.units; ++u)
+                                copy_box(dst + u * a.box_bytes, &tw, at, (work.tile + u) * a.tile_rows, expert, bar, wpol);
+                            if (MODE == GEMM)
+                                copy_box(smem_u32(x_ring + (slot * kPair + p) * kXBytes), &tx, at, 0, 0, bar, xpol);
+                        }
+                        last_slot = slot;
+                        last_use = use;
                     }
-                    const uint32_t bar = smem_u32(&sh.full[slot]);
-                    const uint32_t dst = smem_u32(ring + (size_t)slot * a.stage_bytes);
-                    mbar_arrive_expect_tx(bar, (uint32_t)a.stage_bytes);
-                    copy_box(dst, &tw, c * a.k_step, c * a.block_step, row, expert, bar, wpol);
-                    if (MODE == GEMM)
-                        copy_box(dst + kWStage, &tx, c * a.k_step, c * a.block_step, 0, 0, bar, xpol);
-                    sh.issued = sh.issued + 1;
+                    if (++turn == kCopyWarps)
+                        turn = 0;
                     if (++slot == a.stages) {
                         slot = 0;
                         ++use;
                     }
                 }
             }
+            if (last_slot >= 0 && *abort_flag) {  // let the copies that were issued land before the CTA exits
+                const volatile int never = 0;
+                mbar_wait_near(smem_u32(&sh.full[last_slot]), (uint32_t)last_use & 1u, &never);
+            }
         }
         __syncwarp();
-    } else if (warp < kWarps) {
+    } else if (warp >= 4 && warp < 8) {
+        // ---- sums
         if (MODE == DOWN)
             pdl_wait();
-        const int kb = warp & 3, group = warp >> 2, g = lane >> 2, c4 = lane & 3;
-        int slot = group, use = 0, turn = 0, cur_v = -1, n_tok = a.m, buf = 0;
-        // where this thread's 16 bytes of a row's two halves lie
-        int at[2];
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-            at[h] = kb * 128 + 16 * (a.swizzled ? (4 * h + c4) ^ (kb | (g & 1) << 2) : 4 * h + c4);
-        // scale of this warp's block of chunk `lane`, fetched an item ahead
-        auto scale_of = [&](int it, int chunk, int part) {
-            const int b = chunk * 4 + kb;
-            if (it >= end || b >= a.blocks)
-                return 0.f;
-            const int v = it / a.tiles, tile = it - v * a.tiles;
-            int64_t row_block;
-            if (MODE == GEMM)
-                row_block = tile * kRows / 128;
-            else if (MODE == UP)
-                row_block = ((int64_t)sh.lists[0].v_expert[v] * 2 + part) * a.row_blocks + tile * 16 / 128;
-            else
-                row_block = (int64_t)sh.lists[0].v_expert[v] * a.row_blocks + tile * kRows / 128;
-            return a.w_scales[row_block * a.blocks + b];
+        const uint32_t t_addr = tmem + ((uint32_t)(32 * q) << 16);
+        const bool mine = 32 * q < a.tile_rows || MODE == UP;  // has rows
+        if (MODE == DOWN || S > 1)
+            for (int t = 0; t < a.m; ++t)
+                y_sum[t * kRowsMax + 32 * q + lane] = 0.f;
+        int slot = 0, use = 0;
+        // The scales of a piece's blocks, 32 at a time, a lane each: of rows before `cut` the first, else the second.
+        struct Scales {
+            float v[2];
+            int cut;
         };
-        // (gate and up have scales of their own; otherwise both row tiles share one)
-        float next_ws[2] = {scale_of(first, lane, 0), MODE == UP ? scale_of(first, lane, 1) : 0.f};
-        const int col_step = MODE == GEMM ? kChunk : col_pitch;
-        for (int it = first; it < end; ++it) {
-            const int v = it / a.tiles;
-            float ws_lane[2] = {next_ws[0], next_ws[1]};
-            next_ws[0] = scale_of(it + 1, lane, 0);
-            if (MODE == UP)
-                next_ws[1] = scale_of(it + 1, lane, 1);
-            if constexpr (MODE != GEMM) {
-                if (v != cur_v) {
-                    cur_v = v;
-                    consumers_sync();  // the columns are no longer read
-                    const Lists& l = sh.lists[0];
-                    n_tok = l.v_count[v];
-                    const uint16_t* pairs = l.list + l.v_first[v];
-                    const int64_t ld = MODE == UP ? a.ldx : a.K;
-                    const bool wide = (reinterpret_cast<uintptr_t>(a.xb) & 7u) == 0 && ld % 4 == 0;
-                    constexpr int U = 4;
-                    const int work = n_tok * a.blocks;
-                    for (int i0 = warp; i0 < work; i0 += U * kWarps) {
-                        float val[U][4];
-#pragma unroll
-                        for (int u = 0; u < U; ++u) {
-                            const int i = i0 + u * kWarps, t = i / a.blocks, k = (i - t * a.blocks) * 128 + lane * 4;
-                            val[u][0] = val[u][1] = val[u][2] = val[u][3] = 0.f;
-                            if (i < work && k < a.K) {
-                                const int pair = pairs[t];
-                                const uint16_t* p = a.xb + (int64_t)(MODE == UP ? pair / a.topk : pair) * ld + k;
-                                if (wide) {
-                                    const uint2 w = *reinterpret_cast<const uint2*>(p);
-                                    val[u][0] = __uint_as_float(w.x << 16);
-                                    val[u][1] = __uint_as_float(w.x & 0xffff0000u);
-                                    val[u][2] = __uint_as_float(w.y << 16);
-                                    val[u][3] = __uint_as_float(w.y & 0xffff0000u);
-                                } else {
-#pragma unroll
-                                    for (int j = 0; j < 4; ++j)
-                                        val[u][j] = bf16_bits_f(p[j]);
-                                }
-                            }
-                        }
-#pragma unroll
-                        for (int u = 0; u < U; ++u) {
-                            const int i = i0 + u * kWarps;
-                            if (i < work) {
-                                const int t = i / a.blocks, b = i - t * a.blocks;
-                                uint8_t* col = cols + (size_t)(2 * t) * col_pitch + b * 128 + lane * 4;
-                                split_block(val[u], col, col + col_pitch, &xs[b * TOK + t]);
-                            }
-                        }
-                    }
-                    consumers_sync();
-                }
+        auto scales_of = [&](int k0) {
+            Scales s{{0.f, 0.f}, 32};
+            int64_t first, second;
+            if (MODE == UP) {
+                first = (int64_t)l.v_expert[work.pass] * 2 * a.row_blocks + min((work.tile + q) * kUnit / 128, a.row_blocks - 1);
+                second = first + a.row_blocks;
+                s.cut = kUnit;
+            } else {
+                const int row = work.tile * a.tile_rows + 32 * q;
+                const int64_t e = MODE == DOWN ? (int64_t)l.v_expert[work.pass] * a.row_blocks : 0;
+                first = e + min(row / 128, a.row_blocks - 1);
+                second = e + min(row / 128 + 1, a.row_blocks - 1);
+                s.cut = (row / 128 + 1) * 128 - row;
             }
-            const int n_nt = MODE == GEMM ? NT : (n_tok + 3) / 4;
-            float acc[2][NT][4];
+            if (k0 + lane < min(a.blocks, work.k_end * kPair)) {
+                s.v[0] = a.w_scales[first * a.blocks + k0 + lane];
+                if (s.cut < 32)
+                    s.v[1] = a.w_scales[second * a.blocks + k0 + lane];
+            }
+            return s;
+        };
+        bool ready = false;
+        while (work.next()) {
+            const int n_tok = MODE == GEMM ? a.m : l.v_count[work.pass];
+            float acc[TOK];
 #pragma unroll
-            for (int i = 0; i < 2 * NT; ++i)
-                acc[i / NT][i % NT][0] = acc[i / NT][i % NT][1] = acc[i / NT][i % NT][2] = acc[i / NT][i % NT][3] = 0.f;
-            for (int c = 0; c < n_chunks; ++c, turn ^= 1) {
-                if (MODE == GEMM && c > 0 && (c & 31) == 0)
-                    ws_lane[0] = scale_of(it, c + lane, 0);
-                if (turn != group)
-                    continue;
-                const bool ok = __all_sync(0xffffffffu, mbar_wait_bounded(smem_u32(&sh.full[slot]), (uint32_t)use & 1u, abort_flag));
-                if (!ok) {
-                    if (lane == 0)
-                        give_up();
-                } else if (c * 4 + kb < a.blocks) {
-                    const uint8_t* st = ring + (size_t)slot * a.stage_bytes;
-                    uint4 w[2][2][2];  // [row tile][rows g and g + 8][half]
+            for (int t = 0; t < TOK; ++t)
+                acc[t] = 0.f;
+            Scales ws = scales_of(work.k * kPair);
+            for (int k = work.k; k < work.k_end; ++k) {
+                const int j = (k - work.k) * kPair & 31;
+                if (j == 0 && k > work.k)
+                    ws = scales_of(k * kPair);
+                float w[kPair];
 #pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        w[i >> 2][(i >> 1) & 1][i & 1] =
-                            *reinterpret_cast<const uint4*>(st + (g + (i >> 1) * 8) * kChunk + at[i & 1]);
-                    const float ws0 = __shfl_sync(0xffffffffu, ws_lane[0], c & 31);
-                    const float ws1 = MODE == UP ? __shfl_sync(0xffffffffu, ws_lane[1], c & 31) : ws0;
-                    const float* px = xs + (c * 4 + kb) * TOK;
-                    const uint8_t* pb = (MODE == GEMM ? st + kWStage : cols + c * kChunk + kb * 128 + c4 * 16) + g * col_step;
+                for (int p = 0; p < kPair; ++p) {
+                    const float w0 = __shfl_sync(0xffffffffu, ws.v[0], j + p), w1 = __shfl_sync(0xffffffffu, ws.v[1], j + p);
+                    w[p] = lane < ws.cut ? w0 : w1;
+                }
+                // (what filled the stage has the columns' scales with it)
+                if (!ready && !(wait(&sh.done[slot], use) && wait(&sh.full[slot], use)))
+                    break;
+                asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+                const int slot1 = slot + 1 == a.stages ? 0 : slot + 1, use1 = use + (slot1 == 0);
+                float d[kPair * NC], sx[kPair][TOK];
+                if (mine) {
 #pragma unroll
-                    for (int n = 0; n < NT; ++n) {
-                        if (MODE != GEMM && n >= n_nt)
-                            break;
-                        float d[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+                    for (int c = 0; c < kPair * NC; c += 16)
+                        tmem_load16(t_addr + slot * kPair * NC + c, d + c);
 #pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            const uint4 x = *reinterpret_cast<const uint4*>(pb + n * 8 * col_step + (MODE == GEMM ? at[h] : 64 * h));
+                    for (int p = 0; p < kPair; ++p) {
+                        const float* px = MODE == GEMM ? xs + (k * kPair + p) * NC : sh.scales[slot][p];
 #pragma unroll
-                            for (int t = 0; t < 2; ++t)
-                                mma_e4m3(d[t], w[t][0][h].x, w[t][1][h].x, w[t][0][h].y, w[t][1][h].y, x.x, x.y);
-#pragma unroll
-                            for (int t = 0; t < 2; ++t)
-                                mma_e4m3(d[t], w[t][0][h].z, w[t][1][h].z, w[t][0][h].w, w[t][1][h].w, x.z, x.w);
-                        }
-                        if (MODE == GEMM) {
-                            const float2 s = *reinterpret_cast<const float2*>(px + n * 8 + 2 * c4);
-                            const float s0 = ws0 * s.x, s1 = ws0 * s.y;
-#pragma unroll
-                            for (int t = 0; t < 2; ++t) {
-                                acc[t][n][0] = fmaf(d[t][0], s0, acc[t][n][0]);
-                                acc[t][n][1] = fmaf(d[t][1], s1, acc[t][n][1]);
-                                acc[t][n][2] = fmaf(d[t][2], s0, acc[t][n][2]);
-                                acc[t][n][3] = fmaf(d[t][3], s1, acc[t][n][3]);
-                            }
-                        } else {  // columns 2t and 2t + 1 are token t's upper and lower part
-                            const float sx = px[n * 4 + c4];
-#pragma unroll
-                            for (int t = 0; t < 2; ++t) {
-                                const float s = (t ? ws1 : ws0) * sx;
-                                acc[t][n][0] = fmaf(fmaf(d[t][1], 0.0625f, d[t][0]), s, acc[t][n][0]);
-                                acc[t][n][2] = fmaf(fmaf(d[t][3], 0.0625f, d[t][2]), s, acc[t][n][2]);
-                            }
+                        for (int t = 0; t < TOK; t += 4) {
+                            if (MODE != GEMM && t >= n_tok)
+                                break;
+                            const float4 v = *reinterpret_cast<const float4*>(px + t);
+                            sx[p][t] = v.x, sx[p][t + 1] = v.y, sx[p][t + 2] = v.z, sx[p][t + 3] = v.w;
                         }
                     }
                 }
-                __syncwarp();
+                const bool done1 = mbar_ready(smem_u32(&sh.done[slot1]), (uint32_t)use1 & 1u);
+                const bool full1 = mbar_ready(smem_u32(&sh.full[slot1]), (uint32_t)use1 & 1u);
+                settle(d);
+                asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+                ready = __all_sync(0xffffffffu, done1 && full1);
                 if (lane == 0)
-                    mbar_arrive(smem_u32(&sh.empty[slot]));
-                if ((slot += 2) >= a.stages) {
-                    slot = group;
-                    ++use;
+                    mbar_arrive(smem_u32(&sh.freed[slot]));
+                if (mine) {
+#pragma unroll
+                    for (int p = 0; p < kPair; ++p)
+#pragma unroll
+                        for (int t = 0; t < TOK; ++t) {
+                            if (MODE != GEMM && (t & 3) == 0 && t >= n_tok)
+                                break;
+                            if (MODE == GEMM)
+                                acc[t] = fmaf(d[p * NC + t], w[p] * sx[p][t], acc[t]);
+                            else  // columns 2t and 2t + 1 are token t's upper and lower part
+                                acc[t] = fmaf(fmaf(d[p * NC + 2 * t + 1], 0.0625f, d[p * NC + 2 * t]), w[p] * sx[p][t], acc[t]);
+                        }
                 }
+                slot = slot1;
+                use = use1;
             }
-            if (it - first >= Sh::kBufs)
-                pair_sync(kBarFree + buf);
-#pragma unroll
-            for (int t = 0; t < 2; ++t) {
-                float* red = sh.red[buf][t][warp];
-#pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    if (MODE == GEMM) {
-#pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            red[(n * 8 + 2 * c4 + (j & 1)) * 20 + g + (j >> 1) * 8] = acc[t][n][j];
-                    } else if (n < n_nt) {
-                        red[(n * 4 + c4) * 20 + g] = acc[t][n][0];
-                        red[(n * 4 + c4) * 20 + g + 8] = acc[t][n][2];
-                    }
-                }
-            }
-            pair_arrive(kBarFull + buf);
-            buf ^= Sh::kBufs - 1;
-        }
-    } else {
-        if (MODE == DOWN)
-            pdl_wait();
-        const int tid = (int)threadIdx.x - (kWarps + 1) * 32;
-        if (MODE == UP && blockIdx.x == 0)
-            for (int i = tid; i < a.done_count; i += kEndWarps * 32)
-                a.done[i] = 0;
-        int buf = 0;
-        for (int it = first; it < end; ++it) {
-            const int v = it / a.tiles, tile = it - v * a.tiles;
-            const int n_tok = MODE == GEMM ? a.m : sh.lists[0].v_count[v];
-            pair_sync(kBarFull + buf);
-            auto total_of = [&](int tile16, int t, int r) {
-                float v = 0.f;
-#pragma unroll
-                for (int w = 0; w < kWarps; ++w)
-                    v += sh.red[buf][tile16][w][t * 20 + r];
-                return v;
-            };
             if constexpr (MODE == GEMM) {
-                for (int o = tid; o < a.m * kRows; o += kEndWarps * 32) {
-                    const int t = o >> 5, r = o & 31, n = tile * kRows + r;
-                    if (n < a.rows) {
-                        const float yv = total_of(r >> 4, t, r & 15);
-                        if (a.y_bf16)
-                            static_cast<uint16_t*>(a.y)[t * a.ldy + n] = __bfloat16_as_ushort(__float2bfloat16_rn(yv));
-                        else
-                            static_cast<float*>(a.y)[t * a.ldy + n] = yv;
+                const int r = 32 * q + lane, row = work.tile * a.tile_rows + r;
+#pragma unroll
+                for (int t = 0; t < TOK; ++t)
+                    if (t < a.m) {
+                        if (S > 1)
+                            y_sum[t * kRowsMax + r] = acc[t];
+                        else if (r < a.tile_rows && row < a.rows && !*abort_flag)
+                            store(t, row, acc[t]);
                     }
-                }
             } else if constexpr (MODE == UP) {
-                const Lists& l = sh.lists[0];
-                for (int o = tid; o < n_tok * 16; o += kEndWarps * 32) {
-                    const int t = o >> 4, r = o & 15, row = tile * 16 + r;
-                    if (row < a.rows) {
-                        const float gate = total_of(0, t, r), up = total_of(1, t, r);
+                const int row = (work.tile + q) * kUnit + (lane & 15);
+#pragma unroll
+                for (int t = 0; t < TOK; ++t) {
+                    if (t >= n_tok)
+                        break;
+                    const float gate = acc[t], up = __shfl_down_sync(0xffffffffu, acc[t], 16);
+                    if (q < work.units && lane < 16 && row < a.rows) {
                         const float hv = __fdiv_rn(gate, 1.0f + expf(-gate)) * up;
-                        a.h[(int64_t)l.list[l.v_first[v] + t] * a.rows + row] = __bfloat16_as_ushort(__float2bfloat16_rn(hv));
+                        a.h[(int64_t)l.list[l.v_first[work.pass] + t] * a.rows + row] = __bfloat16_as_ushort(__float2bfloat16_rn(hv));
                     }
                 }
             } else {
-                const Lists& l = sh.lists[0];
-                for (int o = tid; o < n_tok * kRows; o += kEndWarps * 32) {
-                    const int t = o >> 5, r = o & 31, row = tile * kRows + r;
-                    if (row < a.rows)
-                        a.part[(int64_t)l.list[l.v_first[v] + t] * a.rows + row] = total_of(r >> 4, t, r & 15);
+                // (a row of y_sum's columns is this thread's alone)
+                const int r = 32 * q + lane, row = work.tile * a.tile_rows + r;
+#pragma unroll
+                for (int t = 0; t < TOK; ++t) {
+                    if (t >= n_tok)
+                        break;
+                    const int pair = l.list[l.v_first[work.pass] + t];
+                    float& to = y_sum[pair / a.topk * kRowsMax + r];
+                    to = fmaf(a.route_w[pair], acc[t], to);
                 }
-                // The pass that finishes a tile last adds up its tokens' choices, in their order.
-                __threadfence();
-                enders_sync();
-                if (tid == 0)
-                    sh.last = atomicAdd(&a.done[tile], 1) == passes - 1;
-                enders_sync();
-                if (sh.last) {
-                    __threadfence();
-                    for (int o = tid; o < a.m * kRows; o += kEndWarps * 32) {
-                        const int t = o >> 5, row = tile * kRows + (o & 31);
-                        if (row >= a.rows)
-                            continue;
-                        float yv = 0.f;
-                        for (int j = 0; j < a.topk; ++j) {
-                            const int p = t * a.topk + j, e = l.ids[p];
-                            if (e >= 0 && e < a.E)
-                                yv = fmaf(a.route_w[p], __ldcg(a.part + (int64_t)p * a.rows + row), yv);
-                        }
-                        if (a.y_bf16)
-                            static_cast<uint16_t*>(a.y)[t * a.ldy + row] = __bfloat16_as_ushort(__float2bfloat16_rn(yv));
-                        else
-                            static_cast<float*>(a.y)[t * a.ldy + row] = yv;
+                if (S == 1 && work.last)
+                    for (int t = 0; t < a.m; ++t) {
+                        if (r < a.tile_rows && row < a.rows && !*abort_flag)
+                            store(t, row, y_sum[t * kRowsMax + r]);
+                        y_sum[t * kRowsMax + r] = 0.f;
                     }
+            }
+        }
+        if (MODE == DOWN && S == 1 && passes == 0)  // no token has an expert
+            for (int tile = (int)blockIdx.x; tile < a.tiles; tile += (int)gridDim.x)
+                for (int t = 0; t < a.m; ++t) {
+                    const int r = 32 * q + lane, row = tile * a.tile_rows + r;
+                    if (r < a.tile_rows && row < a.rows)
+                        store(t, row, 0.f);
+                }
+    } else if constexpr (MODE != GEMM) {
+        // ---- columns
+        if (MODE == DOWN)
+            pdl_wait();
+        const int sw = warp - 8;
+        const int64_t ld = MODE == UP ? a.ldx : a.K;
+        const bool wide = (reinterpret_cast<uintptr_t>(a.xb) & 7u) == 0 && ld % 4 == 0;
+        auto value = [&](const Walk<MODE, S>& w, int t, int p) {
+            const int k = (w.k * kPair + p) * kBlock + lane * 4;
+            uint2 v = make_uint2(0u, 0u);
+            if (t < l.v_count[w.pass] && k < a.K) {
+                const int pair = l.list[l.v_first[w.pass] + t];
+                const uint16_t* p16 = a.xb + (int64_t)(MODE == UP ? pair / a.topk : pair) * ld + k;
+                v = wide ? *reinterpret_cast<const uint2*>(p16)
+                         : make_uint2(p16[0] | (uint32_t)p16[1] << 16, p16[2] | (uint32_t)p16[3] << 16);
+            }
+            return v;
+        };
+        auto advance = [&](Walk<MODE, S>& w, int n) {  // n stages further
+            for (; n > 0; --n)
+                if (++w.k >= w.k_end && !w.next())
+                    return false;
+            return true;
+        };
+        constexpr int G = 4;  // tokens fetched ahead
+        uint2 ahead[G][kPair];
+        bool live = work.next() && advance(work, sw);
+        if (live)
+#pragma unroll
+            for (int i = 0; i < G * kPair; ++i)
+                ahead[i / kPair][i % kPair] = value(work, i / kPair, i % kPair);
+        int slot = sw % a.stages, use = sw / a.stages;
+        while (live) {
+            uint2 now[G][kPair];
+#pragma unroll
+            for (int i = 0; i < G * kPair; ++i)
+                now[i / kPair][i % kPair] = ahead[i / kPair][i % kPair];
+            Walk<MODE, S> then = work;
+            live = advance(then, kSplitWarps);
+            if (live)
+#pragma unroll
+                for (int i = 0; i < G * kPair; ++i)
+                    ahead[i / kPair][i % kPair] = value(then, i / kPair, i % kPair);
+            if (use > 0 && !wait(&sh.freed[slot], use - 1))
+                break;
+            const int n_tok = l.v_count[work.pass];
+#pragma unroll
+            for (int p = 0; p < kPair; ++p) {
+                uint8_t* const tile = x_ring + (slot * kPair + p) * kXBytes;
+                float* const scale = sh.scales[slot][p];
+#pragma unroll
+                for (int t = 0; t < G; ++t)
+                    if (t < n_tok)
+                        split_block(now[t][p], tile, t, scale + t);
+                for (int t = G; t < n_tok; t += G) {
+                    uint2 more[G];
+#pragma unroll
+                    for (int i = 0; i < G; ++i)
+                        more[i] = value(work, t + i, p);
+#pragma unroll
+                    for (int i = 0; i < G; ++i)
+                        if (t + i < n_tok)
+                            split_block(more[i], tile, t + i, scale + t + i);
                 }
             }
-            if (it + Sh::kBufs < end)
-                pair_arrive(kBarFree + buf);
-            buf ^= Sh::kBufs - 1;
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(smem_u32(&sh.full[slot]));
+            work = then;
+            for (slot += kSplitWarps; slot >= a.stages; slot -= a.stages)
+                ++use;
         }
-        if (MODE == DOWN && passes == 0)  // no token has an expert
-            for (int64_t o = (int64_t)blockIdx.x * kEndWarps * 32 + tid; o < (int64_t)a.m * a.rows;
-                 o += (int64_t)gridDim.x * kEndWarps * 32) {
-                const int64_t at = o / a.rows * a.ldy + o % a.rows;
-                if (a.y_bf16)
-                    static_cast<uint16_t*>(a.y)[at] = 0;
-                else
-                    static_cast<float*>(a.y)[at] = 0.f;
-            }
     }
+    if constexpr (S > 1) {
+        __syncwarp();
+        cluster_sync();
+        const int rank = (int)blockIdx.x % S, tile = (int)blockIdx.x / S;
+        if (warp >= 4 && warp < 8) {
+            const int r = 32 * q + lane, row = tile * a.tile_rows + r;
+            if (r < a.tile_rows && row < a.rows && !*abort_flag)
+                for (int t = rank; t < a.m; t += S) {
+                    const uint32_t at = smem_u32(y_sum + t * kRowsMax + r);
+                    float v = 0.f;
+#pragma unroll
+                    for (int c = 0; c < S; ++c)  // in the order of K
+                        v += load_peer(at, c);
+                    store(t, row, v);
+                }
+        }
+        __syncwarp();
+        cluster_sync();  // nobody reads this CTA's sums any more
+    }
+    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
     __syncthreads();
-    if (sh.abort_flag && threadIdx.x == 0)  // let the copies that were issued land before the CTA exits
-        for (int i = max(0, sh.issued - a.stages); i < sh.issued; ++i)
-            mbar_wait_bounded(smem_u32(&sh.full[i % a.stages]), (uint32_t)(i / a.stages) & 1u, nullptr);
+    if (warp == 0)
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmem) : "memory");
 }
 
 PFN_cuTensorMapEncodeTiled_v12000 stream_encoder()
@@ -594,72 +719,130 @@ PFN_cuTensorMapEncodeTiled_v12000 stream_encoder()
     return fn;
 }
 
-// [experts, parts, rows, K] codes, rows ld bytes apart.  A box is 512 bytes of K, zeros past the edges: as lines of 128
-// bytes where K is cut into such, as words otherwise.
-bool encode_rows(CUtensorMap* map, const void* base, bool lines, int64_t K, int64_t rows, int64_t ld, int64_t parts,
-                 int64_t experts, int box_rows)
+// [experts, parts, rows, K] codes, rows ld bytes apart.  A box is 128 values of K by box_rows rows by all parts, zeros
+// past the edges.
+bool encode_rows(CUtensorMap* map, const void* base, int64_t K, int64_t rows, int64_t ld, int64_t parts, int64_t experts,
+                 int box_rows)
 {
     PFN_cuTensorMapEncodeTiled_v12000 enc = stream_encoder();
-    const cuuint64_t k = (cuuint64_t)K, l = (cuuint64_t)ld, r = (cuuint64_t)rows, p = (cuuint64_t)parts;
-    const cuuint64_t dims[5] = {lines ? 128 : k / 4, lines ? k / 128 : 1, r, p, (cuuint64_t)experts};
-    const cuuint64_t strides[4] = {lines ? 128 : l, l, l * r, l * r * p};
-    const cuuint32_t box[5] = {128, lines ? 4u : 1u, (cuuint32_t)box_rows, (cuuint32_t)parts, 1};
-    const cuuint32_t ones[5] = {1, 1, 1, 1, 1};
-    return enc && enc(map, lines ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_UINT32, 5, const_cast<void*>(base),
-                      dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                      lines ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+    const cuuint64_t l = (cuuint64_t)ld, r = (cuuint64_t)rows, p = (cuuint64_t)parts;
+    const cuuint64_t dims[4] = {(cuuint64_t)K, r, p, (cuuint64_t)experts};
+    const cuuint64_t strides[3] = {l, l * r, l * r * p};
+    const cuuint32_t box[4] = {kBlock, (cuuint32_t)box_rows, (cuuint32_t)parts, 1};
+    const cuuint32_t ones[4] = {1, 1, 1, 1};
+    return enc && enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void*>(base), dims, strides, box, ones,
+                      CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                       CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int MODE, int NT>
-cudaError_t launch_stream(StreamArgs a, int items, cudaStream_t s)
+// Rows a tile: as many, up to 128, as give each of `teams` the same number of tiles.
+int balanced_rows(int64_t rows, int teams)
 {
-    using Sh = Shared<MODE, NT>;
+    const int64_t rounds = (rows + (int64_t)kRowsMax * teams - 1) / ((int64_t)kRowsMax * teams);
+    return (int)((rows + rounds * teams - 1) / (rounds * teams));
+}
+
+// Clusters of S such CTAs that the device runs at once (the same on every device: the library runs on one kind).
+template <int MODE, int NC, int S>
+cudaError_t clusters_of(const DeviceInfo& di, int* n)
+{
+    static std::atomic<int> known{0};
+    *n = known.load(std::memory_order_relaxed);
+    if (*n > 0)
+        return cudaSuccess;
+    static std::atomic<unsigned long long> devs{0};
+    cudaError_t e = allow_max_smem(fp8_stream_kernel<MODE, NC, S>, devs);
+    if (e != cudaSuccess)
+        return e;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)(di.sm_count / S * S));
+    cfg.blockDim = dim3(threads_of(MODE));
+    cfg.dynamicSmemBytes = (size_t)di.smem_optin;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = S;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    e = cudaOccupancyMaxActiveClusters(n, fp8_stream_kernel<MODE, NC, S>, &cfg);
+    if (e != cudaSuccess)
+        return e;
+    if (*n < 1)
+        return cudaErrorInvalidConfiguration;
+    known.store(*n, std::memory_order_relaxed);
+    return cudaSuccess;
+}
+
+template <int MODE, int NC, int S>
+cudaError_t launch_stream(StreamArgs a, const void* W, const void* x, const DeviceInfo& di, cudaStream_t s)
+{
+    using Sh = Shared<MODE, NC>;
+    auto* kernel = fp8_stream_kernel<MODE, NC, S>;
+    static std::atomic<unsigned long long> devs{0};
+    cudaError_t e = allow_max_smem(kernel, devs);
+    if (e != cudaSuccess)
+        return e;
+    a.blocks = (a.K + kBlock - 1) / kBlock;
+    a.pairs = (a.blocks + kPair - 1) / kPair;
+    a.row_blocks = (a.rows + 127) / 128;
+    int teams = di.sm_count / S;
+    if (S > 2 && (e = clusters_of<MODE, NC, S>(di, &teams)) != cudaSuccess)
+        return e;
+    a.tile_rows = MODE == UP ? kUnit : balanced_rows(a.rows, teams);
+    a.tiles = (a.rows + a.tile_rows - 1) / a.tile_rows;
+    const int parts = MODE == UP ? 2 : 1;
+    a.box_bytes = a.tile_rows * parts * kBlock;
+    a.w_bytes = MODE == UP ? kRowsMax * kBlock : (a.box_bytes + 1023) / 1024 * 1024;
+    const size_t rest = (sizeof(Sh) + 127) / 128 * 128 + (MODE == DOWN || S > 1 ? (size_t)a.m * kRowsMax * 4 : 0) +
+                        (MODE == GEMM ? (size_t)a.pairs * kPair * NC * 4 : 0);
+    const size_t past = (size_t)(kRowsMax * kBlock - a.w_bytes);  // what an MMA may read behind the last stage
+    const size_t stage = (size_t)kPair * (a.w_bytes + NC * kBlock), room = (size_t)di.smem_optin - 1024;
+    a.stages = (int)std::min<size_t>(stages_of(NC), rest < room ? (room - rest) / stage : 0);
+    size_t bytes = (size_t)a.stages * stage + rest;
+    if ((size_t)a.stages * kPair * NC * kBlock + rest < past)
+        bytes = (size_t)a.stages * kPair * a.w_bytes + past;
+    if (a.stages < 2 || bytes > room)
+        return cudaErrorInvalidConfiguration;
+    CUtensorMap tw{}, tx{};
+    if (!encode_rows(&tw, W, a.K, a.rows, a.K, parts, std::max(a.E, 1), a.tile_rows) ||
+        (MODE == GEMM && !encode_rows(&tx, x, a.K, a.m, a.ldx, 1, 1, NC)))
+        return cudaErrorInvalidValue;
+    cudaLaunchConfig_t cfg{};
+    // (UP: the passes are known on the device alone, so a CTA on every SM)
+    cfg.gridDim = dim3((unsigned)(MODE == UP ? di.sm_count : std::min(a.tiles, teams) * S));
+    cfg.blockDim = dim3(threads_of(MODE));
+    cfg.dynamicSmemBytes = 1024 + bytes;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = S;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = S > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kernel, a, tw, tx);
+}
+
+template <int MODE, int NC>
+cudaError_t launch_stream(const StreamArgs& a, const void* W, const void* x, cudaStream_t s)
+{
     DeviceInfo di;
     cudaError_t e = device_info(&di);
     if (e != cudaSuccess)
         return e;
-    static std::atomic<unsigned long long> devs{0};
-    if ((e = allow_max_smem(fp8_stream_kernel<MODE, NT>, devs)) != cudaSuccess)
-        return e;
-    a.blocks = (a.K + 127) / 128;
-    a.stage_bytes = kWStage + (MODE == GEMM ? 8 * NT * kChunk : 0);
-    a.swizzled = a.K % 128 == 0;
-    a.k_step = a.swizzled ? 0 : kChunk / 4;
-    a.block_step = a.swizzled ? 4 : 0;
-    const int parts = MODE == UP ? 2 : 1;
-    CUtensorMap tw{}, tx{};
-    if (!encode_rows(&tw, a.W, a.swizzled, a.K, a.rows, a.K, parts, std::max(a.E, 1), kRows / parts) ||
-        (MODE == GEMM && !encode_rows(&tx, a.x, a.swizzled, a.K, a.m, a.ldx, 1, 1, 8 * NT)))
-        return cudaErrorInvalidValue;
-    const size_t fixed = 1024 + (sizeof(Sh) + 127) / 128 * 128 + (size_t)(a.blocks * Sh::kTok * 4 + 127) / 128 * 128 +
-                         (MODE == GEMM ? 0 : (size_t)(8 * NT) * (a.blocks * 128 + 64));
-    if (fixed + 2 * (size_t)a.stage_bytes > (size_t)di.smem_optin)
-        return cudaErrorInvalidConfiguration;
-    a.stages = (int)std::min<size_t>(16, ((size_t)di.smem_optin - fixed) / a.stage_bytes) & ~1;
-    return launch_pdl(fp8_stream_kernel<MODE, NT>, dim3((unsigned)std::min(items, di.sm_count)), dim3(kThreads),
-                      fixed + (size_t)a.stages * a.stage_bytes, s, a, tw, tx);
-}
-
-size_t part_bytes(size_t n) { return (n + 255) / 256 * 256; }
-
-// Columns of 8 that a pass of the experts has: 4 tokens each.
-int moe_columns(int64_t m, int64_t K)
-{
-    // 4 tiles of 8 columns where they leave room for a ring, fewer for few tokens or long rows
-    const int fit = K <= 2048 ? 4 : K <= 6144 ? 2 : 1;
-    const int want = m <= 4 ? 1 : m <= 8 ? 2 : 4;
-    return std::min(fit, want);
-}
-
-template <int MODE>
-cudaError_t launch_moe(const StreamArgs& a, int items, cudaStream_t s)
-{
-    switch (moe_columns(a.m, a.K)) {
-    case 1: return launch_stream<MODE, 1>(a, items, s);
-    case 2: return launch_stream<MODE, 2>(a, items, s);
-    default: return launch_stream<MODE, 4>(a, items, s);
+    // Clusters along K as long as the tiles of all of them at once cover the rows.  (With clusters of 4, 8 of 152 SMs are
+    // left out, which costs less than tiles of half the rows.)
+    if constexpr (MODE != UP) {
+        int teams = 0;
+        if ((e = clusters_of<MODE, NC, 4>(di, &teams)) != cudaSuccess)
+            return e;
+        if (a.rows <= kRowsMax * teams)
+            return launch_stream<MODE, NC, 4>(a, W, x, di, s);
+        if (a.rows <= kRowsMax * (di.sm_count / 2))
+            return launch_stream<MODE, NC, 2>(a, W, x, di, s);
     }
+    return launch_stream<MODE, NC, 1>(a, W, x, di, s);
 }
 
 }  // namespace
@@ -669,80 +852,64 @@ bool fp8_encoder_there() { return stream_encoder() != nullptr; }
 bool fp8_stream_supported(const Fp8Gemm& p)
 {
     // the scales of x lie in shared memory, 32 KB at most
-    return p.m <= 32 && (p.K + 127) / 128 * ((p.m + 7) / 8 * 8) <= 8192 && p.N <= (1 << 30);
+    const int64_t columns = p.m <= 16 ? 16 : 32;
+    return p.m <= 32 && (p.K + 127) / 128 * columns <= 8192;
 }
 
 cudaError_t launch_fp8_gemm_stream(const Fp8Gemm& p, cudaStream_t s)
 {
     StreamArgs a{};
-    a.W = p.W;
     a.w_scales = p.w_scales;
     a.K = (int)p.K;
     a.rows = (int)p.N;
-    a.tiles = (a.rows + kRows - 1) / kRows;
     a.m = (int)p.m;
-    a.x = p.x;
     a.x_scales = p.x_scales;
     a.ldx = p.ldx;
     a.ld_xs = p.ld_xs;
     a.y = p.y;
     a.ldy = p.ldy;
     a.y_bf16 = p.y_bf16;
-    if (a.m <= 8)
-        return launch_stream<GEMM, 1>(a, a.tiles, s);
-    return a.m <= 16 ? launch_stream<GEMM, 2>(a, a.tiles, s) : launch_stream<GEMM, 4>(a, a.tiles, s);
+    return a.m <= 16 ? launch_stream<GEMM, 16>(a, p.W, p.x, s) : launch_stream<GEMM, 32>(a, p.W, p.x, s);
 }
 
-size_t fp8_moe_workspace(int64_t m, int64_t topk, int64_t dim, int64_t inter)
+size_t fp8_moe_workspace(int64_t m, int64_t topk, int64_t inter)
 {
-    const size_t pairs = (size_t)(m * topk);
-    return part_bytes(pairs * inter * 2) + part_bytes(pairs * dim * 4) + part_bytes((size_t)(dim + kRows - 1) / kRows * 4);
+    return (size_t)(m * topk * inter * 2 + 255) / 256 * 256;
 }
 
 cudaError_t launch_fp8_moe(const Fp8Moe& p, cudaStream_t s)
 {
-    DeviceInfo di;
-    cudaError_t e = device_info(&di);
-    if (e != cudaSuccess)
-        return e;
-    const size_t pairs = (size_t)(p.m * p.topk);
-    uint8_t* ws = static_cast<uint8_t*>(p.workspace);
     StreamArgs a{};
     a.m = (int)p.m;
     a.ids = p.ids;
     a.route_w = p.route_w;
     a.topk = p.topk;
     a.E = p.E;
-    a.h = reinterpret_cast<uint16_t*>(ws);
-    a.part = reinterpret_cast<float*>(ws + part_bytes(pairs * p.inter * 2));
-    a.done = reinterpret_cast<int*>(ws + part_bytes(pairs * p.inter * 2) + part_bytes(pairs * p.dim * 4));
-    a.done_count = (int)((p.dim + kRows - 1) / kRows);
+    a.h = static_cast<uint16_t*>(p.workspace);
     a.y = p.y;
     a.ldy = p.ldy;
     a.y_bf16 = p.y_bf16;
 
     StreamArgs up = a;
-    up.W = p.gate_up;
     up.w_scales = p.gate_up_scales;
     up.K = (int)p.dim;
     up.rows = (int)p.inter;
-    up.row_blocks = (up.rows + 127) / 128;
-    up.tiles = (up.rows + 15) / 16;
     up.xb = p.x;
     up.ldx = p.ldx;
-    // passes are known on the device alone: a CTA on every SM
-    if ((e = launch_moe<UP>(up, di.sm_count, s)) != cudaSuccess)
-        return e;
 
     StreamArgs down = a;
-    down.W = p.down;
     down.w_scales = p.down_scales;
     down.K = (int)p.inter;
     down.rows = (int)p.dim;
-    down.row_blocks = (down.rows + 127) / 128;
-    down.tiles = a.done_count;
     down.xb = a.h;
-    return launch_moe<DOWN>(down, di.sm_count, s);
+
+    // 8 tokens a pass, 16 where experts, about evenly chosen, often have more
+    const double mean = (double)p.m * p.topk / p.E;
+    const bool many = std::min<double>((double)p.m, mean + 2 * std::sqrt(mean)) > 8;
+    cudaError_t e = many ? launch_stream<UP, 32>(up, p.gate_up, nullptr, s) : launch_stream<UP, 16>(up, p.gate_up, nullptr, s);
+    if (e != cudaSuccess)
+        return e;
+    return many ? launch_stream<DOWN, 32>(down, p.down, nullptr, s) : launch_stream<DOWN, 16>(down, p.down, nullptr, s);
 }
 
 cudaError_t fp8_stream_error_word(int32_t* out, bool clear)

@@ -1042,7 +1042,7 @@ size_t fp8_moe_workspace_bytes(int64_t m, int64_t topk, int64_t dim, int64_t int
 {
     if (!fp8_moe_shape_ok(m, topk, dim, inter))
         return 0;
-    return fp8_moe_workspace(m, topk, dim, inter);
+    return fp8_moe_workspace(m, topk, inter);
 }
 
 int fp8_moe(const uint16_t* x, int64_t m, int64_t dim, int64_t ldx, const int32_t* ids, const float* route_w,
@@ -1054,7 +1054,7 @@ int fp8_moe(const uint16_t* x, int64_t m, int64_t dim, int64_t ldx, const int32_
         return Q2K_ERR_NULL_ARG;
     if (!fp8_moe_shape_ok(m, topk, dim, inter) || !type_ok(y_type) || E < 1 || E > 1024 || ldx < dim || ldy < dim)
         return Q2K_ERR_BAD_SHAPE;
-    if (m != 0 && (!workspace || workspace_bytes < fp8_moe_workspace(m, topk, dim, inter)))
+    if (m != 0 && (!workspace || workspace_bytes < fp8_moe_workspace(m, topk, inter)))
         return Q2K_ERR_WORKSPACE;
     if (!aligned(x, 2) || !aligned(ids, 4) || !aligned(route_w, 4) || !aligned(gate_up, 16) || !aligned(down, 16) ||
         !aligned(gate_up_scales, 4) || !aligned(down_scales, 4) || !aligned(y, y_type == Q2K_BF16 ? 2 : 4) ||

@@ -295,7 +295,7 @@ struct Fp8Moe {
     int64_t ldy;
     void* workspace;
 };
-size_t fp8_moe_workspace(int64_t m, int64_t topk, int64_t dim, int64_t inter);
+size_t fp8_moe_workspace(int64_t m, int64_t topk, int64_t inter);
 cudaError_t launch_fp8_moe(const Fp8Moe& p, cudaStream_t s);
 
 // Read (and optionally clear) this translation unit's device error word.
