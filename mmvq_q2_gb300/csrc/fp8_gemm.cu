@@ -3,16 +3,20 @@
 // cores: tcgen05.mma kind::f8f6f4 on e4m3, fp32 accumulators in tensor memory.
 //
 // The scales change every 128 values along K, so an accumulator holds one such
-// block alone: four MMAs of K = 32 fill one of two accumulators while the
-// other is read back, multiplied by its rows' and its block's scale and added
+// block alone: four MMAs of K = 32 fill one of two to eight accumulators while
+// another is read back, multiplied by its rows' and its block's scale and added
 // to fp32 sums in registers.  A tile is 128 rows of x (a tensor memory lane
-// each, so a thread has one row and its scale is one number) by BN rows of W
-// (half of BN to a group of four warps; within one block of 128, so W's scale
-// is one number too):
-//   warp 0       copies tiles of 128 values of K (128-byte swizzled) into a
-//                ring of shared-memory stages;
+// each, so a thread has one row and its scale is one number) by BN rows of W,
+// half of BN to a group of four warps:
+//   warps 0,2,3  copy tiles of 128 values of K (128-byte swizzled) into a ring
+//                of shared-memory stages, a stage in turn;
 //   warp 1       issues the MMAs;
-//   warps 4..11  read back, scale, add; at the end store y.
+//   warps 4..11  read back, scale, add; at the end they leave y in shared
+//                memory for tensor copies to store.
+// What bounds a block of K is the way round its accumulator: MMAs, commit and
+// wait, read back, free, wait.  So the sums and what is read back have to fit
+// the registers together, and an accumulator is freed before anything is added:
+// BN is 192, not 256 (which had to read back in eight pieces).
 // CTAs walk the tiles, 16 tiles of x at a time, so that what runs together
 // shares operands in L2.  Where there are fewer tiles than SMs, the CTAs of a
 // cluster share a tile along K and add their sums through shared memory, in
@@ -45,30 +49,29 @@ struct GemmArgs {
     int64_t ld_xs, ldy;
     int m, N, blocks;  // blocks of 128 along K
     int tiles_m, tiles_n, stages;
+    int bulk_store;     // y by tensor copies
     int y_bf16, align;  // bytes that the start of every 32 values of y is aligned to: 32, 16 or less
 };
 
 struct GemmShared {
-    uint64_t full[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2];
+    uint64_t full[kMaxStages], done[kMaxStages];  // of a stage: copied; multiplied
+    uint64_t acc_empty[8];                        // of an accumulator: read back
     uint32_t tmem;
-    int abort_flag, issued;
+    int abort_flag;
 };
 
-// 32 fp32 columns of this warp's 32 lanes; complete after settle().
-__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&v)[32])
+// 16 fp32 columns of this warp's 32 lanes; complete after settle().
+__device__ __forceinline__ void tmem_load16(uint32_t taddr, float* v)
 {
     asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
-        "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
         : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]),
-          "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]), "=f"(v[16]),
-          "=f"(v[17]), "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]), "=f"(v[24]),
-          "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
+          "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15])
         : "r"(taddr));
 }
 
-// acc += v * f, two values an instruction.
-__device__ __forceinline__ void fma_pairs(float* acc, const float (&v)[32], float f)
+// acc += v * f of 32 values, two an instruction (one at a time 229 us for 8191 x 8192 x 4096 against 219).
+__device__ __forceinline__ void fma_pairs(float* acc, const float* v, float f)
 {
 #pragma unroll
     for (int i = 0; i < 32; i += 2)
@@ -137,6 +140,50 @@ __device__ __forceinline__ void store_row(const GemmArgs& a, int64_t row, int co
     }
 }
 
+// A box of 64 bytes by 32 rows of y from shared memory; lane 0 of the warp that has it.
+__device__ __forceinline__ void store_box(const CUtensorMap* map, int x, int y, uint32_t src)
+{
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];\n\t"
+                 "cp.async.bulk.commit_group;" ::"l"(reinterpret_cast<uint64_t>(map)),
+                 "r"(x), "r"(y), "r"(src)
+                 : "memory");
+}
+
+// n columns of a warp's 32 rows by such boxes, through its one buffer (two would cost a stage of the ring, and more time
+// than they save).
+template <int n, bool BF16>
+__device__ __forceinline__ void store_boxes(const GemmArgs& a, const CUtensorMap* map, uint8_t* buf, int row0, int col, const float* v)
+{
+    constexpr int kCols = BF16 ? 32 : 16;
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int b = 0; b < n / kCols; ++b) {
+        if (row0 >= a.m || col + b * kCols >= a.N)
+            break;  // nothing of the box, or of those after it, is in y
+        if (lane == 0)  // the buffer's last store has read it
+            asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+        __syncwarp();
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {  // 16 bytes of the row, where the 64-byte swizzle has them
+            uint32_t w[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if (BF16)
+                    asm("cvt.rn.bf16x2.f32 %0, %1, %2;"
+                        : "=r"(w[i])
+                        : "f"(v[b * kCols + 8 * j + 2 * i + 1]), "f"(v[b * kCols + 8 * j + 2 * i]));
+                else
+                    w[i] = __float_as_uint(v[b * kCols + 4 * j + i]);
+            }
+            *reinterpret_cast<uint4*>(buf + lane * 64 + ((j ^ (lane >> 1 & 3)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0)
+            store_box(map, col + b * kCols, row0, smem_u32(buf));
+    }
+}
+
 __device__ __forceinline__ void store_peer(uint32_t addr, uint32_t rank, float v)
 {
     asm volatile("{\n\t.reg .b32 p;\n\tmapa.shared::cluster.u32 p, %0, %1;\n\tst.shared::cluster.f32 [p], %2;\n\t}" ::"r"(addr),
@@ -144,38 +191,42 @@ __device__ __forceinline__ void store_peer(uint32_t addr, uint32_t rank, float v
                  : "memory");
 }
 
+constexpr int kBox = 64 * 32, kBoxes = 8 * kBox;  // of y, one a warp
+
 // S CTAs of a cluster share a tile along K.
 template <int BN, int S>
 __global__ void __launch_bounds__(kThreads, 1)
-    fp8_gemm_kernel(const GemmArgs a, const __grid_constant__ CUtensorMap tx, const __grid_constant__ CUtensorMap tw)
+    fp8_gemm_kernel(const GemmArgs a, const __grid_constant__ CUtensorMap tx, const __grid_constant__ CUtensorMap tw,
+                    const __grid_constant__ CUtensorMap ty)
 {
-    constexpr int WGC = BN / 2;  // columns of a group of four warps
+    constexpr int WGC = BN / 2;     // columns of a group of four warps
+    constexpr int kAccs = 512 / BN;  // accumulators in tensor memory
+    static_assert(WGC % 32 == 0, "32 columns share a scale");
     constexpr uint32_t kStage = (uint32_t)(kXTile + BN * kTK);
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     pdl_launch_dependents();
     // the 128-byte swizzle repeats every 1024 bytes: stages start on 1024
     uint8_t* const ring = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     float* const red = reinterpret_cast<float*>(ring + (size_t)a.stages * kStage);  // S > 1: [S][BN / S][128]
-    GemmShared& sh = *reinterpret_cast<GemmShared*>(red + (S > 1 ? BN * 128 : 0));
+    uint8_t* const boxes = reinterpret_cast<uint8_t*>(red);                         // S == 1
+    GemmShared& sh = *reinterpret_cast<GemmShared*>(boxes + (S > 1 ? BN * 512 : kBoxes));
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = S > 1 ? (int)blockIdx.x % S : 0;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < a.stages; ++s) {
             mbar_init(smem_u32(&sh.full[s]), 1);
-            mbar_init(smem_u32(&sh.empty[s]), 1);
+            mbar_init(smem_u32(&sh.done[s]), 1);
         }
-        for (int b = 0; b < 2; ++b) {
-            mbar_init(smem_u32(&sh.acc_full[b]), 1);
+        for (int b = 0; b < kAccs; ++b) {
             mbar_init(smem_u32(&sh.acc_empty[b]), 8);
         }
         sh.abort_flag = 0;
-        sh.issued = 0;
         fence_mbar_init();
     }
     if (warp == 1) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&sh.tmem)),
-                     "r"(2 * BN)
+                     "r"(512)
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
@@ -202,43 +253,56 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
 
     if (warp < 4) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
-        if (warp == 0) {
-            if (lane == 0) {  // copies
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+        if (warp != 1) {
+            if (lane == 0) {  // copies: of every third stage
                 const uint64_t pol = l2_policy_evict_last();
-                int slot = 0, use = 0;
+                const int me = warp == 0 ? 0 : warp - 1;
+                int slot = 0, use = 0, turn = 0, last_slot = -1, last_use = 0;
                 bool ok = true;
                 for (int t = tile0; t < tiles && ok; t += step) {
                     int m0, n0;
                     place(t, m0, n0);
                     for (int k = k_first; k < k_end; ++k) {
-                        if (use > 0 && !mbar_wait_near(smem_u32(&sh.empty[slot]), (uint32_t)(use - 1) & 1u, abort_flag)) {
-                            give_up();
-                            ok = false;
-                            break;
+                        if (turn == me) {
+                            if (use > 0 && !mbar_wait_near(smem_u32(&sh.done[slot]), (uint32_t)(use - 1) & 1u, abort_flag)) {
+                                give_up();
+                                ok = false;
+                                break;
+                            }
+                            const uint32_t bar = smem_u32(&sh.full[slot]), dst = smem_u32(ring + (size_t)slot * kStage);
+                            mbar_arrive_expect_tx(bar, kStage);
+                            tma_load_2d(dst, &tx, k * kTK, m0, bar, pol);
+                            tma_load_2d(dst + kXTile, &tw, k * kTK, n0, bar, pol);
+                            last_slot = slot;
+                            last_use = use;
                         }
-                        const uint32_t bar = smem_u32(&sh.full[slot]), dst = smem_u32(ring + (size_t)slot * kStage);
-                        mbar_arrive_expect_tx(bar, kStage);
-                        tma_load_2d(dst, &tx, k * kTK, m0, bar, pol);
-                        tma_load_2d(dst + kXTile, &tw, k * kTK, n0, bar, pol);
-                        sh.issued = sh.issued + 1;
+                        if (++turn == 3)
+                            turn = 0;
                         if (++slot == a.stages) {
                             slot = 0;
                             ++use;
                         }
                     }
                 }
+                if (last_slot >= 0 && *abort_flag) {  // let the copies that were issued land before the CTA exits
+                    const volatile int never = 0;
+                    mbar_wait_near(smem_u32(&sh.full[last_slot]), (uint32_t)last_use & 1u, &never);
+                }
             }
             __syncwarp();
-        } else if (warp == 1) {  // MMAs
+        } else {  // MMAs
             constexpr uint32_t idesc = instr_desc_e4m3(BN);
+            const uint32_t ring_at = smem_u32(ring);
             int slot = 0, use = 0, n = 0;
             bool ok = true;
             for (int t = tile0; t < tiles && ok; t += step)
                 for (int k = k_first; k < k_end; ++k, ++n) {
-                    const int buf = n & 1;
+                    const int b = n % kAccs;
+                    const uint32_t s0 = uniform((uint32_t)slot), b0 = uniform((uint32_t)b);
+                    const uint32_t sa = ring_at + s0 * kStage, d = tmem + b0 * BN;
                     if (!mbar_wait_near(smem_u32(&sh.full[slot]), (uint32_t)use & 1u, abort_flag) ||
-                        (n >= 2 && !mbar_wait_near(smem_u32(&sh.acc_empty[buf]), (uint32_t)((n >> 1) - 1) & 1u, abort_flag)))
+                        (n >= kAccs && !mbar_wait_near(smem_u32(&sh.acc_empty[b]), (uint32_t)(n / kAccs - 1) & 1u, abort_flag)))
                         ok = false;
                     ok = __all_sync(0xffffffffu, ok);
                     if (!ok) {
@@ -247,14 +311,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                         break;
                     }
                     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-                    const uint32_t sa = smem_u32(ring + (size_t)slot * kStage);
                     if (elect_one()) {
 #pragma unroll
                         for (int i = 0; i < kTK / 32; ++i)  // K = 32 an MMA: 32 bytes along the swizzled row
-                            umma_e4m3(tmem + buf * BN, smem_desc_sw128(sa + 32 * i), smem_desc_sw128(sa + kXTile + 32 * i),
-                                      idesc, i > 0);
-                        umma_commit(smem_u32(&sh.empty[slot]));
-                        umma_commit(smem_u32(&sh.acc_full[buf]));
+                            umma_e4m3(d, desc_at(sa + 32 * i), desc_at(sa + kXTile + 32 * i), idesc, i > 0);
+                        // (one commit, 115 cycles, tells both that the accumulator is full and that the stage is free)
+                        umma_commit(smem_u32(&sh.done[0]) + 8 * s0);
                     }
                     __syncwarp();
                     if (++slot == a.stages) {
@@ -264,51 +326,75 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
         }
     } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
         const int q = warp & 3, wg = (warp - 4) >> 2;
         const uint32_t t_addr = tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(wg * WGC);
-        int n = 0;
+        int n = 0, slot = 0, use = 0;
         for (int t = tile0; t < tiles; t += step) {
             int m0, n0;
             place(t, m0, n0);
             const int row = m0 + 32 * q + lane, col = n0 + wg * WGC;
             const float* xs = a.x_scales + (int64_t)min(row, a.m - 1) * a.ld_xs;
-            const float* ws = a.w_scales + (int64_t)(min(col, a.N - 1) / 128) * a.blocks;
+            // W's rows of one scale: 32 columns, at least, from a multiple of 128 on
+            const int turn = (col / 128 + 1) * 128 - col, last_block = (a.N - 1) / 128;
+            const float* ws = a.w_scales + (int64_t)min(col / 128, last_block) * a.blocks;
+            const float* ws2 = a.w_scales + (int64_t)min(col / 128 + 1, last_block) * a.blocks;
             float acc[WGC];
 #pragma unroll
             for (int i = 0; i < WGC; ++i)
                 acc[i] = 0.f;
-            float f = k_first < k_end ? xs[k_first] * ws[k_first] : 0.f;
+            // a block's scales, the next one's on their way
+            float fx = 0.f, fw = 0.f, fw2 = 0.f;
+            auto fetch = [&](int k) {
+                if (k < k_end) {
+                    fx = xs[k];
+                    fw = ws[k];
+                    if (WGC > 64)
+                        fw2 = ws2[k];
+                }
+            };
+            fetch(k_first);
             for (int k = k_first; k < k_end; ++k, ++n) {
-                const int buf = n & 1;
-                const float f_next = k + 1 < k_end ? xs[k + 1] * ws[k + 1] : 0.f;
+                const int buf = n % kAccs;
+                const float f = fx * fw, f2 = fx * fw2;
+                fetch(k + 1);
                 const bool ok = __all_sync(
-                    0xffffffffu, mbar_wait_near(smem_u32(&sh.acc_full[buf]), (uint32_t)(n >> 1) & 1u, abort_flag));
+                    0xffffffffu, mbar_wait_near(smem_u32(&sh.done[slot]), (uint32_t)use & 1u, abort_flag));
                 if (!ok) {
                     if (lane == 0)
                         give_up();
                     break;
                 }
                 asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-                float v[2][32];
-                tmem_ld32(t_addr + buf * BN, v[0]);
+                float v[WGC];
 #pragma unroll
-                for (int c = 0; c < WGC; c += 32) {
-                    settle(v[(c / 32) & 1]);
-                    if (c + 32 < WGC) {
-                        tmem_ld32(t_addr + buf * BN + c + 32, v[(c / 32 + 1) & 1]);
-                    } else {
-                        asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-                        if (lane == 0)
-                            mbar_arrive(smem_u32(&sh.acc_empty[buf]));
-                    }
-                    fma_pairs(acc + c, v[(c / 32) & 1], f);
+                for (int c = 0; c < WGC; c += 16)
+                    tmem_load16(t_addr + buf * BN + c, v + c);
+                settle(v);
+                asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(smem_u32(&sh.acc_empty[buf]));
+#pragma unroll
+                for (int c = 0; c < WGC; c += 32)
+                    fma_pairs(acc + c, v + c, WGC <= 64 || c < turn ? f : f2);
+                if (++slot == a.stages) {
+                    slot = 0;
+                    ++use;
                 }
-                f = f_next;
             }
             if constexpr (S == 1) {
-                if (row < a.m && !*abort_flag)
+                if (*abort_flag)
+                    continue;
+                if (a.bulk_store) {
+                    uint8_t* const mine = boxes + (warp - 4) * kBox;
+                    if (a.y_bf16)
+                        store_boxes<WGC, true>(a, &ty, mine, m0 + 32 * q, col, acc);
+                    else
+                        store_boxes<WGC, false>(a, &ty, mine, m0 + 32 * q, col, acc);
+                } else if (row < a.m) {
                     store_row<WGC>(a, row, col, acc);
+                }
             } else {
                 // slice r of the columns is added up and stored by CTA r
                 constexpr int SC = WGC / S;
@@ -319,6 +405,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
     }
+    if (S == 1 && warp >= 4 && lane == 0)
+        asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     if constexpr (S > 1) {
         cluster_sync();
         if (warp >= 4) {
@@ -341,13 +429,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
     __syncthreads();
-    const volatile int never = 0;
-    if (sh.abort_flag && threadIdx.x == 0)  // let the copies that were issued land before the CTA exits
-        for (int i = max(0, sh.issued - a.stages); i < sh.issued; ++i)
-            mbar_wait_near(smem_u32(&sh.full[i % a.stages]), (uint32_t)(i / a.stages) & 1u, &never);
-    __syncthreads();
     if (warp == 1)
-        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(2 * BN) : "memory");
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
 }
 
 PFN_cuTensorMapEncodeTiled_v12000 gemm_encoder()
@@ -364,16 +447,19 @@ PFN_cuTensorMapEncodeTiled_v12000 gemm_encoder()
     return fn;
 }
 
-// Codes [rows, K], rows ld apart; a box is 128 values by box_rows, 128-byte swizzled, zeros past the edges.
-bool encode_codes(CUtensorMap* map, const void* base, int64_t rows, int64_t K, int64_t ld, int box_rows)
+// [rows, cols] values of `size` bytes, rows ld apart; a box is box_bytes (64 or 128, and swizzled so) by box_rows, zeros
+// past the edges (stores are cut there).
+bool encode_boxes(CUtensorMap* map, CUtensorMapDataType type, int size, const void* base, int64_t rows, int64_t cols, int64_t ld,
+                  int box_rows, int box_bytes)
 {
     PFN_cuTensorMapEncodeTiled_v12000 enc = gemm_encoder();
-    const cuuint64_t dims[2] = {(cuuint64_t)K, (cuuint64_t)rows};
-    const cuuint64_t strides[1] = {(cuuint64_t)ld};
-    const cuuint32_t box[2] = {(cuuint32_t)kTK, (cuuint32_t)box_rows};
+    const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+    const cuuint64_t strides[1] = {(cuuint64_t)(ld * size)};
+    const cuuint32_t box[2] = {(cuuint32_t)(box_bytes / size), (cuuint32_t)box_rows};
     const cuuint32_t ones[2] = {1, 1};
-    return enc && enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, ones,
-                      CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+    return enc && enc(map, type, 2, const_cast<void*>(base), dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                      box_bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                      CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                       CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -388,10 +474,15 @@ cudaError_t launch_tiles(GemmArgs a, const Fp8Gemm& p, const DeviceInfo& di, cud
         return e;
     a.tiles_m = (a.m + kTM - 1) / kTM;
     a.tiles_n = (a.N + BN - 1) / BN;
-    const size_t extra = 1024 + sizeof(GemmShared) + (S > 1 ? (size_t)BN * 512 : 0);
+    const size_t extra = 1024 + sizeof(GemmShared) + (S > 1 ? (size_t)BN * 512 : (size_t)kBoxes);
     a.stages = (int)std::min<size_t>(kMaxStages, ((size_t)di.smem_optin - extra) / kStage);
-    CUtensorMap tx{}, tw{};
-    if (!encode_codes(&tx, p.x, p.m, p.K, p.ldx, kTM) || !encode_codes(&tw, p.W, p.N, p.K, p.K, BN))
+    CUtensorMap tx{}, tw{}, ty{};
+    if (!encode_boxes(&tx, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, p.x, p.m, p.K, p.ldx, kTM, 128) ||
+        !encode_boxes(&tw, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, p.W, p.N, p.K, p.K, BN, 128))
+        return cudaErrorInvalidValue;
+    a.bulk_store = S == 1 && a.align >= 16 && p.ldy < ((int64_t)1 << 36);
+    if (a.bulk_store && !(p.y_bf16 ? encode_boxes(&ty, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, p.y, p.m, p.N, p.ldy, 32, 64)
+                                   : encode_boxes(&ty, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, p.y, p.m, p.N, p.ldy, 32, 64)))
         return cudaErrorInvalidValue;
     const int64_t tiles = (int64_t)a.tiles_m * a.tiles_n;
     if (tiles * S > 0x7fffffff)
@@ -409,7 +500,7 @@ cudaError_t launch_tiles(GemmArgs a, const Fp8Gemm& p, const DeviceInfo& di, cud
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = S > 1 ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, kernel, a, tx, tw);
+    return cudaLaunchKernelEx(&cfg, kernel, a, tx, tw, ty);
 }
 
 }  // namespace
@@ -434,25 +525,26 @@ cudaError_t launch_fp8_gemm(const Fp8Gemm& p, cudaStream_t s)
     a.y_bf16 = p.y_bf16;
     const uintptr_t bits = reinterpret_cast<uintptr_t>(p.y) | (uintptr_t)(p.ldy * (p.y_bf16 ? 2 : 4));
     a.align = bits % 32 == 0 ? 32 : bits % 16 == 0 ? 16 : 1;
-    // What each choice of tile and split would take, in cycles: blocks of K one after another, each bound by the MMA, the
-    // read-back or its operands' way from L2.
+    // What each choice of tile and split would take, in cycles: blocks of K one after another, each as long as the way
+    // round an accumulator, the MMAs or the operands' way from L2; a tile's start and end; the join of a cluster.
     auto cost = [&](int bn, int split) {
-        const int64_t tiles = (int64_t)((a.m + kTM - 1) / kTM) * ((a.N + bn - 1) / bn) * split;
-        const int64_t waves = (tiles + di.sm_count - 1) / di.sm_count;
-        const int64_t block = std::max<int64_t>(2 * bn + 60, (std::min(a.m, kTM) + bn) * (int64_t)kTK / 48);
-        return waves * ((a.blocks + split - 1) / split * block + 1500 + 6 * bn) + (split > 1 ? 1500 : 0);
+        const int64_t tiles = (int64_t)((a.m + kTM - 1) / kTM) * ((a.N + bn - 1) / bn);
+        const int64_t at_once = split == 4 ? di.sm_count / 4 - 2 : di.sm_count / split;
+        const int64_t rounds = (tiles + at_once - 1) / at_once;
+        return rounds * ((a.blocks + split - 1) / split * (bn == 192 ? 720 : bn == 128 ? 600 : 560) + 2000 + 8 * bn) +
+               (split > 1 ? 800 + 400 * split : 0);
     };
     int best = 0;
-    const int options[5][2] = {{256, 1}, {128, 1}, {128, 2}, {64, 1}, {64, 4}};
+    const int options[5][2] = {{192, 1}, {128, 1}, {128, 2}, {128, 4}, {64, 2}};
     for (int i = 1; i < 5; ++i)
         if (options[i][1] <= a.blocks && cost(options[i][0], options[i][1]) < cost(options[best][0], options[best][1]))
             best = i;
     switch (best) {
-    case 0: return launch_tiles<256, 1>(a, p, di, s);
+    case 0: return launch_tiles<192, 1>(a, p, di, s);
     case 1: return launch_tiles<128, 1>(a, p, di, s);
     case 2: return launch_tiles<128, 2>(a, p, di, s);
-    case 3: return launch_tiles<64, 1>(a, p, di, s);
-    default: return launch_tiles<64, 4>(a, p, di, s);
+    case 3: return launch_tiles<128, 4>(a, p, di, s);
+    default: return launch_tiles<64, 2>(a, p, di, s);
     }
 }
 
