@@ -6,17 +6,19 @@
 // block alone: four MMAs of K = 32 fill one of two to eight accumulators while
 // another is read back, multiplied by its rows' and its block's scale and added
 // to fp32 sums in registers.  A tile is 128 rows of x (a tensor memory lane
-// each, so a thread has one row and its scale is one number) by BN rows of W,
-// half of BN to a group of four warps:
+// each, so a thread has one row and its scale is one number) by BN rows of W
+// (half of BN to a group of four warps; within one block of 128, so W's scale
+// is one number too):
 //   warps 0,2,3  copy tiles of 128 values of K (128-byte swizzled) into a ring
 //                of shared-memory stages, a stage in turn;
 //   warp 1       issues the MMAs;
 //   warps 4..11  read back, scale, add; at the end they leave y in shared
-//                memory for tensor copies to store.
-// What bounds a block of K is the way round its accumulator: MMAs, commit and
-// wait, read back, free, wait.  So the sums and what is read back have to fit
-// the registers together, and an accumulator is freed before anything is added:
-// BN is 192, not 256 (which had to read back in eight pieces).
+//                memory for tensor copies to store (8191 x 8192 x 4096 213 us;
+//                stored by the warps 222).
+// What bounds a block of K at BN = 256, 940 cycles where its MMAs take 510: the
+// operands go into shared memory and out of it, 96 KB at 128 bytes a cycle, and
+// the way round an accumulator (MMAs, commit and wait, read back, wait) is
+// longer than two blocks.  192 columns, read back at once, took 254 us.
 // CTAs walk the tiles, 16 tiles of x at a time, so that what runs together
 // shares operands in L2.  Where there are fewer tiles than SMs, the CTAs of a
 // cluster share a tile along K and add their sums through shared memory, in
@@ -70,11 +72,11 @@ __device__ __forceinline__ void tmem_load16(uint32_t taddr, float* v)
         : "r"(taddr));
 }
 
-// acc += v * f of 32 values, two an instruction (one at a time 229 us for 8191 x 8192 x 4096 against 219).
+// acc += v * f of 16 values, two an instruction (one at a time 229 us for 8191 x 8192 x 4096 against 219).
 __device__ __forceinline__ void fma_pairs(float* acc, const float* v, float f)
 {
 #pragma unroll
-    for (int i = 0; i < 32; i += 2)
+    for (int i = 0; i < 16; i += 2)
         asm("{\n\t.reg .b64 a, b, c;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %4};\n\tmov.b64 c, {%0, %1};\n\t"
             "fma.rn.f32x2 c, a, b, c;\n\tmov.b64 {%0, %1}, c;\n\t}"
             : "+f"(acc[i]), "+f"(acc[i + 1])
@@ -140,7 +142,7 @@ __device__ __forceinline__ void store_row(const GemmArgs& a, int64_t row, int co
     }
 }
 
-// A box of 64 bytes by 32 rows of y from shared memory; lane 0 of the warp that has it.
+// A box of 128 bytes by 32 rows of y from shared memory; lane 0 of the warp that has it.
 __device__ __forceinline__ void store_box(const CUtensorMap* map, int x, int y, uint32_t src)
 {
     asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];\n\t"
@@ -154,7 +156,7 @@ __device__ __forceinline__ void store_box(const CUtensorMap* map, int x, int y, 
 template <int n, bool BF16>
 __device__ __forceinline__ void store_boxes(const GemmArgs& a, const CUtensorMap* map, uint8_t* buf, int row0, int col, const float* v)
 {
-    constexpr int kCols = BF16 ? 32 : 16;
+    constexpr int kCols = BF16 ? 64 : 32;
     const int lane = threadIdx.x & 31;
 #pragma unroll
     for (int b = 0; b < n / kCols; ++b) {
@@ -164,7 +166,7 @@ __device__ __forceinline__ void store_boxes(const GemmArgs& a, const CUtensorMap
             asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
         __syncwarp();
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {  // 16 bytes of the row, where the 64-byte swizzle has them
+        for (int j = 0; j < 8; ++j) {  // 16 bytes of the row, where the swizzle has them
             uint32_t w[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -175,7 +177,7 @@ __device__ __forceinline__ void store_boxes(const GemmArgs& a, const CUtensorMap
                 else
                     w[i] = __float_as_uint(v[b * kCols + 4 * j + i]);
             }
-            *reinterpret_cast<uint4*>(buf + lane * 64 + ((j ^ (lane >> 1 & 3)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+            *reinterpret_cast<uint4*>(buf + lane * 128 + ((j ^ (lane & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
@@ -191,7 +193,7 @@ __device__ __forceinline__ void store_peer(uint32_t addr, uint32_t rank, float v
                  : "memory");
 }
 
-constexpr int kBox = 64 * 32, kBoxes = 8 * kBox;  // of y, one a warp
+constexpr int kBox = 128 * 32, kBoxes = 8 * kBox;  // of y, one a warp
 
 // S CTAs of a cluster share a tile along K.
 template <int BN, int S>
@@ -201,7 +203,6 @@ __global__ void __launch_bounds__(kThreads, 1)
 {
     constexpr int WGC = BN / 2;     // columns of a group of four warps
     constexpr int kAccs = 512 / BN;  // accumulators in tensor memory
-    static_assert(WGC % 32 == 0, "32 columns share a scale");
     constexpr uint32_t kStage = (uint32_t)(kXTile + BN * kTK);
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     pdl_launch_dependents();
@@ -335,29 +336,20 @@ __global__ void __launch_bounds__(kThreads, 1)
             place(t, m0, n0);
             const int row = m0 + 32 * q + lane, col = n0 + wg * WGC;
             const float* xs = a.x_scales + (int64_t)min(row, a.m - 1) * a.ld_xs;
-            // W's rows of one scale: 32 columns, at least, from a multiple of 128 on
-            const int turn = (col / 128 + 1) * 128 - col, last_block = (a.N - 1) / 128;
-            const float* ws = a.w_scales + (int64_t)min(col / 128, last_block) * a.blocks;
-            const float* ws2 = a.w_scales + (int64_t)min(col / 128 + 1, last_block) * a.blocks;
+            const float* ws = a.w_scales + (int64_t)(min(col, a.N - 1) / 128) * a.blocks;
             float acc[WGC];
 #pragma unroll
             for (int i = 0; i < WGC; ++i)
                 acc[i] = 0.f;
-            // a block's scales, the next one's on their way
-            float fx = 0.f, fw = 0.f, fw2 = 0.f;
-            auto fetch = [&](int k) {
-                if (k < k_end) {
-                    fx = xs[k];
-                    fw = ws[k];
-                    if (WGC > 64)
-                        fw2 = ws2[k];
-                }
-            };
-            fetch(k_first);
+            // a block's scale, the next one's on its way
+            float fx = k_first < k_end ? xs[k_first] : 0.f, fw = k_first < k_end ? ws[k_first] : 0.f;
             for (int k = k_first; k < k_end; ++k, ++n) {
                 const int buf = n % kAccs;
-                const float f = fx * fw, f2 = fx * fw2;
-                fetch(k + 1);
+                const float f = fx * fw;
+                if (k + 1 < k_end) {
+                    fx = xs[k + 1];
+                    fw = ws[k + 1];
+                }
                 const bool ok = __all_sync(
                     0xffffffffu, mbar_wait_near(smem_u32(&sh.done[slot]), (uint32_t)use & 1u, abort_flag));
                 if (!ok) {
@@ -366,18 +358,38 @@ __global__ void __launch_bounds__(kThreads, 1)
                     break;
                 }
                 asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-                float v[WGC];
+                // All columns at once as far as registers go, else 16 on their way while 16 are added up (with 32 they do
+                // not suffice: 256 us for 8191 x 8192 x 4096 against 219).  The accumulator is free once the last have
+                // landed.
+                auto free_it = [&]() {
+                    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive(smem_u32(&sh.acc_empty[buf]));
+                };
+                if constexpr (WGC <= 64) {
+                    float v[WGC];
 #pragma unroll
-                for (int c = 0; c < WGC; c += 16)
-                    tmem_load16(t_addr + buf * BN + c, v + c);
-                settle(v);
-                asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-                __syncwarp();
-                if (lane == 0)
-                    mbar_arrive(smem_u32(&sh.acc_empty[buf]));
+                    for (int c = 0; c < WGC; c += 16)
+                        tmem_load16(t_addr + buf * BN + c, v + c);
+                    settle(v);
+                    free_it();
 #pragma unroll
-                for (int c = 0; c < WGC; c += 32)
-                    fma_pairs(acc + c, v + c, WGC <= 64 || c < turn ? f : f2);
+                    for (int c = 0; c < WGC; c += 16)
+                        fma_pairs(acc + c, v + c, f);
+                } else {
+                    float v[2][16];
+                    tmem_load16(t_addr + buf * BN, v[0]);
+#pragma unroll
+                    for (int c = 0; c < WGC; c += 16) {
+                        settle(v[c / 16 & 1]);
+                        if (c + 16 < WGC)
+                            tmem_load16(t_addr + buf * BN + c + 16, v[(c / 16 + 1) & 1]);
+                        else
+                            free_it();
+                        fma_pairs(acc + c, v[c / 16 & 1], f);
+                    }
+                }
                 if (++slot == a.stages) {
                     slot = 0;
                     ++use;
@@ -447,19 +459,18 @@ PFN_cuTensorMapEncodeTiled_v12000 gemm_encoder()
     return fn;
 }
 
-// [rows, cols] values of `size` bytes, rows ld apart; a box is box_bytes (64 or 128, and swizzled so) by box_rows, zeros
-// past the edges (stores are cut there).
+// [rows, cols] values of `size` bytes, rows ld apart; a box is 128 bytes by box_rows, 128-byte swizzled, zeros past the
+// edges (stores are cut there).
 bool encode_boxes(CUtensorMap* map, CUtensorMapDataType type, int size, const void* base, int64_t rows, int64_t cols, int64_t ld,
-                  int box_rows, int box_bytes)
+                  int box_rows)
 {
     PFN_cuTensorMapEncodeTiled_v12000 enc = gemm_encoder();
     const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
     const cuuint64_t strides[1] = {(cuuint64_t)(ld * size)};
-    const cuuint32_t box[2] = {(cuuint32_t)(box_bytes / size), (cuuint32_t)box_rows};
+    const cuuint32_t box[2] = {(cuuint32_t)(128 / size), (cuuint32_t)box_rows};
     const cuuint32_t ones[2] = {1, 1};
     return enc && enc(map, type, 2, const_cast<void*>(base), dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                      box_bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
-                      CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                      CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                       CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -477,12 +488,12 @@ cudaError_t launch_tiles(GemmArgs a, const Fp8Gemm& p, const DeviceInfo& di, cud
     const size_t extra = 1024 + sizeof(GemmShared) + (S > 1 ? (size_t)BN * 512 : (size_t)kBoxes);
     a.stages = (int)std::min<size_t>(kMaxStages, ((size_t)di.smem_optin - extra) / kStage);
     CUtensorMap tx{}, tw{}, ty{};
-    if (!encode_boxes(&tx, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, p.x, p.m, p.K, p.ldx, kTM, 128) ||
-        !encode_boxes(&tw, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, p.W, p.N, p.K, p.K, BN, 128))
+    if (!encode_boxes(&tx, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, p.x, p.m, p.K, p.ldx, kTM) ||
+        !encode_boxes(&tw, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, p.W, p.N, p.K, p.K, BN))
         return cudaErrorInvalidValue;
     a.bulk_store = S == 1 && a.align >= 16 && p.ldy < ((int64_t)1 << 36);
-    if (a.bulk_store && !(p.y_bf16 ? encode_boxes(&ty, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, p.y, p.m, p.N, p.ldy, 32, 64)
-                                   : encode_boxes(&ty, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, p.y, p.m, p.N, p.ldy, 32, 64)))
+    if (a.bulk_store && !(p.y_bf16 ? encode_boxes(&ty, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, p.y, p.m, p.N, p.ldy, 32)
+                                   : encode_boxes(&ty, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, p.y, p.m, p.N, p.ldy, 32)))
         return cudaErrorInvalidValue;
     const int64_t tiles = (int64_t)a.tiles_m * a.tiles_n;
     if (tiles * S > 0x7fffffff)
@@ -525,22 +536,26 @@ cudaError_t launch_fp8_gemm(const Fp8Gemm& p, cudaStream_t s)
     a.y_bf16 = p.y_bf16;
     const uintptr_t bits = reinterpret_cast<uintptr_t>(p.y) | (uintptr_t)(p.ldy * (p.y_bf16 ? 2 : 4));
     a.align = bits % 32 == 0 ? 32 : bits % 16 == 0 ? 16 : 1;
-    // What each choice of tile and split would take, in cycles: blocks of K one after another, each as long as the way
-    // round an accumulator, the MMAs or the operands' way from L2; a tile's start and end; the join of a cluster.
-    auto cost = [&](int bn, int split) {
-        const int64_t tiles = (int64_t)((a.m + kTM - 1) / kTM) * ((a.N + bn - 1) / bn);
-        const int64_t at_once = split == 4 ? di.sm_count / 4 - 2 : di.sm_count / split;
+    // What each choice of tile and split takes, in cycles, as measured at 48 to 1024 rows of 512 to 16384 x 2048 to 4096:
+    // once, and for each block of K of a tile.  (128 columns over 4 CTAs, 128 rows of 4096 x 4096: 8.4 us against 12.6
+    // alone; 128 over 2, 5000 x 4112: 11.8 against 15.4; 64 over 2, 2048 x 2048: 5.9 against 6.7 for 128 over 4; 256
+    // alone, 203 rows of 16384 x 4096: 19.6 against 24.0 for 128.)
+    struct Option {
+        int bn, split, once, block;
+    };
+    constexpr Option options[5] = {{256, 1, 5700, 800}, {128, 1, 6000, 540}, {128, 2, 9200, 560}, {128, 4, 11000, 330}, {64, 2, 7400, 475}};
+    auto cost = [&](const Option& o) {
+        const int64_t tiles = (int64_t)((a.m + kTM - 1) / kTM) * ((a.N + o.bn - 1) / o.bn);
+        const int64_t at_once = o.split == 4 ? di.sm_count / 4 - 2 : di.sm_count / o.split;  // (some SMs are left out)
         const int64_t rounds = (tiles + at_once - 1) / at_once;
-        return rounds * ((a.blocks + split - 1) / split * (bn == 192 ? 720 : bn == 128 ? 600 : 560) + 2000 + 8 * bn) +
-               (split > 1 ? 800 + 400 * split : 0);
+        return o.once + rounds * ((a.blocks + o.split - 1) / o.split) * o.block + (rounds - 1) * 2000;
     };
     int best = 0;
-    const int options[5][2] = {{192, 1}, {128, 1}, {128, 2}, {128, 4}, {64, 2}};
     for (int i = 1; i < 5; ++i)
-        if (options[i][1] <= a.blocks && cost(options[i][0], options[i][1]) < cost(options[best][0], options[best][1]))
+        if (options[i].split <= a.blocks && cost(options[i]) < cost(options[best]))
             best = i;
     switch (best) {
-    case 0: return launch_tiles<192, 1>(a, p, di, s);
+    case 0: return launch_tiles<256, 1>(a, p, di, s);
     case 1: return launch_tiles<128, 1>(a, p, di, s);
     case 2: return launch_tiles<128, 2>(a, p, di, s);
     case 3: return launch_tiles<128, 4>(a, p, di, s);
