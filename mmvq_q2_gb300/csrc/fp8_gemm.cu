@@ -491,7 +491,8 @@ cudaError_t launch_tiles(GemmArgs a, const Fp8Gemm& p, const DeviceInfo& di, cud
     if (!encode_boxes(&tx, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, p.x, p.m, p.K, p.ldx, kTM) ||
         !encode_boxes(&tw, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, p.W, p.N, p.K, p.K, BN))
         return cudaErrorInvalidValue;
-    a.bulk_store = S == 1 && a.align >= 16 && p.ldy < ((int64_t)1 << 36);
+    // (a tensor copy stores 16 bytes at a time: a row that ends inside them would have what follows it overwritten)
+    a.bulk_store = S == 1 && a.align >= 16 && p.N * (p.y_bf16 ? 2 : 4) % 16 == 0 && p.ldy < ((int64_t)1 << 36);
     if (a.bulk_store && !(p.y_bf16 ? encode_boxes(&ty, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, p.y, p.m, p.N, p.ldy, 32)
                                    : encode_boxes(&ty, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, p.y, p.m, p.N, p.ldy, 32)))
         return cudaErrorInvalidValue;

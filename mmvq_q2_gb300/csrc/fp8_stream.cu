@@ -124,6 +124,18 @@ __device__ __forceinline__ void copy_box(uint32_t dst, const CUtensorMap* map, i
         : "memory");
 }
 
+__device__ __forceinline__ void prefetch_map(const CUtensorMap* map)
+{
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
+}
+
+__device__ __forceinline__ void store_peer(uint32_t addr, uint32_t rank, float v)
+{
+    asm volatile("{\n\t.reg .b32 p;\n\tmapa.shared::cluster.u32 p, %0, %1;\n\tst.shared::cluster.f32 [p], %2;\n\t}" ::"r"(addr),
+                 "r"(rank), "f"(v)
+                 : "memory");
+}
+
 __device__ __forceinline__ float load_peer(uint32_t addr, uint32_t rank)
 {
     float v;
@@ -136,18 +148,76 @@ __device__ __forceinline__ float load_peer(uint32_t addr, uint32_t rank)
 
 // The experts that have a token, as passes of up to CAP (token, choice) pairs.
 struct Lists {
-    int ids[kMaxPairs];
+    alignas(16) int ids[kMaxPairs];
     uint16_t rank[kMaxPairs], list[kMaxPairs];                         // pairs by expert, in order
     uint16_t v_expert[kMaxPairs], v_first[kMaxPairs], v_count[kMaxPairs];  // passes
-    uint16_t count[kMaxExperts];
+    alignas(16) uint16_t count[kMaxExperts];
     int passes;
 };
+
+constexpr int kFewPairs = 256;
+
+// The lists of up to 256 pairs: a pair's place is the number of pairs before it, by expert and then by pair, which each
+// thread counts for itself; likewise a pass's.  (2.2 us with the other way, for 8 pairs of 256 experts.)
+template <int kThreads>
+__device__ __forceinline__ void build_few_lists(Lists& l, const StreamArgs& a, int cap)
+{
+    static_assert(kThreads >= kFewPairs, "a thread a pair");
+    constexpr int kNone = 0x7fffffff;
+    int* const starts = reinterpret_cast<int*>(l.count);  // the expert where a pair starts a pass
+    const int pairs = a.m * a.topk, i = threadIdx.x, whole = (pairs + 3) & ~3;
+    int e = kNone;
+    if (i < whole) {
+        if (i < pairs)
+            e = a.ids[i];
+        e = e >= 0 && e < a.E ? e : kNone;
+        l.ids[i] = e;
+    }
+    __syncthreads();
+    int place = 0, before = 0, same = 0;
+    if (i < whole) {
+        for (int j = 0; j < whole; j += 4) {
+            const int4 v = *reinterpret_cast<const int4*>(l.ids + j);
+            const int o[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const bool eq = o[u] == e, first = eq && j + u < i;
+                place += o[u] < e || first;
+                before += first;
+                same += eq;
+            }
+        }
+        starts[i] = e != kNone && before % cap == 0 ? e : kNone;
+        if (e != kNone)
+            l.list[place] = (uint16_t)i;
+    }
+    const bool start = i < whole && e != kNone && before % cap == 0;
+    const int passes = __syncthreads_count(start);
+    if (start) {
+        int v = 0;
+        for (int j = 0; j < whole; j += 4) {
+            const int4 w = *reinterpret_cast<const int4*>(starts + j);
+            const int o[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+                v += o[u] < e || (o[u] == e && j + u < i);
+        }
+        l.v_expert[v] = (uint16_t)e;
+        l.v_first[v] = (uint16_t)place;
+        l.v_count[v] = (uint16_t)min(cap, same - before);
+    }
+    if (i == 0)
+        l.passes = passes;
+    __syncthreads();
+}
 
 // By all threads; ends with a barrier.
 template <int kThreads>
 __device__ void build_lists(Lists& l, const StreamArgs& a, int cap)
 {
     const int pairs = a.m * a.topk, tid = threadIdx.x;
+    if (pairs <= kFewPairs)
+        return build_few_lists<kThreads>(l, a, cap);
     for (int i = tid; i < a.E; i += kThreads)
         l.count[i] = 0;
     for (int i = tid; i < pairs; i += kThreads)
@@ -324,9 +394,9 @@ __global__ void __launch_bounds__(threads_of(MODE), 1)
     uint8_t* const ring = smem + ((1024u - (smem_u32(smem) & 1023u)) & 1023u);
     uint8_t* const x_ring = ring + (size_t)a.stages * kPair * a.w_bytes;
     Sh& sh = *reinterpret_cast<Sh*>(x_ring + (size_t)a.stages * kPair * kXBytes);
-    // [m][128] sums of a tile (not UP)
+    // [m][128] sums of a tile (DOWN), or the cluster's of the tokens that are this CTA's (GEMM): [S][m / S][128]
     float* const y_sum = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(&sh) + (sizeof(Sh) + 127) / 128 * 128);
-    float* const xs = y_sum + (S > 1 ? a.m * kRowsMax : 0);  // GEMM: [2 pairs][NC]
+    float* const xs = y_sum + (S > 1 ? (a.m + S - 1) * kRowsMax : 0);  // GEMM: [2 pairs][NC]
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
@@ -338,6 +408,14 @@ __global__ void __launch_bounds__(threads_of(MODE), 1)
         sh.abort_flag = 0;
         fence_mbar_init();
     }
+    if (threadIdx.x == 32) {
+        prefetch_map(&tw);
+        if (MODE == GEMM)
+            prefetch_map(&tx);
+    }
+    __syncwarp();
+    if (S > 1)
+        cluster_arrive();  // this CTA has started
     if (warp == 0) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&sh.tmem)),
                      "r"(kTmem)
@@ -349,11 +427,6 @@ __global__ void __launch_bounds__(threads_of(MODE), 1)
     if (MODE != DOWN)
         pdl_wait();
     pdl_launch_dependents();
-    if constexpr (MODE == GEMM)
-        for (int i = threadIdx.x; i < a.pairs * kPair * NC; i += kThreads) {
-            const int b = i / NC, t = i % NC;
-            xs[i] = t < a.m && b < a.blocks ? a.x_scales[t * a.ld_xs + b] : 0.f;
-        }
     asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
     int passes = 1;
     if constexpr (MODE != GEMM) {
@@ -386,6 +459,7 @@ __global__ void __launch_bounds__(threads_of(MODE), 1)
     };
     Walk<MODE, S> work(a, passes);
     const int q = warp & 3;  // of the warps that add up: their lanes, 32 rows
+    const int rank = S > 1 ? (int)blockIdx.x % S : 0, share = (a.m + S - 1) / S;
 
     if (warp == 0) {
         // ---- MMAs
@@ -465,9 +539,16 @@ __global__ void __launch_bounds__(threads_of(MODE), 1)
             pdl_wait();
         const uint32_t t_addr = tmem + ((uint32_t)(32 * q) << 16);
         const bool mine = 32 * q < a.tile_rows || MODE == UP;  // has rows
-        if (MODE == DOWN || S > 1)
+        if (MODE == DOWN)
             for (int t = 0; t < a.m; ++t)
                 y_sum[t * kRowsMax + 32 * q + lane] = 0.f;
+        if constexpr (MODE == GEMM) {
+            for (int i = (int)threadIdx.x - 128; i < a.pairs * kPair * NC; i += 128) {
+                const int b = i / NC, t = i % NC;
+                xs[i] = t < a.m && b < a.blocks ? a.x_scales[t * a.ld_xs + b] : 0.f;
+            }
+            asm volatile("bar.sync 1, 128;" ::: "memory");
+        }
         int slot = 0, use = 0;
         // The scales of a piece's blocks, 32 at a time, a lane each: of rows before `cut` the first, else the second.
         struct Scales {
@@ -494,6 +575,19 @@ __global__ void __launch_bounds__(threads_of(MODE), 1)
                     s.v[1] = a.w_scales[second * a.blocks + k0 + lane];
             }
             return s;
+        };
+        // GEMM, S > 1: token t's sums go to CTA t % S, into the place that it has for this CTA's
+        bool pushed = false;
+        auto push = [&](const float (&v)[TOK]) {
+            __syncwarp();
+            if (!pushed)
+                cluster_wait();  // all have started
+            pushed = true;
+            const uint32_t at = smem_u32(y_sum + rank * share * kRowsMax + 32 * q + lane);
+#pragma unroll
+            for (int t = 0; t < TOK; ++t)
+                if (t < a.m)
+                    store_peer(at + (uint32_t)(t / S) * (kRowsMax * 4), t % S, v[t]);
         };
         bool ready = false;
         while (work.next()) {
@@ -560,14 +654,14 @@ __global__ void __launch_bounds__(threads_of(MODE), 1)
             }
             if constexpr (MODE == GEMM) {
                 const int r = 32 * q + lane, row = work.tile * a.tile_rows + r;
+                if (S > 1) {
+                    push(acc);
+                } else if (r < a.tile_rows && row < a.rows && !*abort_flag) {
 #pragma unroll
-                for (int t = 0; t < TOK; ++t)
-                    if (t < a.m) {
-                        if (S > 1)
-                            y_sum[t * kRowsMax + r] = acc[t];
-                        else if (r < a.tile_rows && row < a.rows && !*abort_flag)
+                    for (int t = 0; t < TOK; ++t)
+                        if (t < a.m)
                             store(t, row, acc[t]);
-                    }
+                }
             } else if constexpr (MODE == UP) {
                 const int row = (work.tile + q) * kUnit + (lane & 15);
 #pragma unroll
@@ -599,6 +693,10 @@ __global__ void __launch_bounds__(threads_of(MODE), 1)
                     }
             }
         }
+        if (MODE == GEMM && S > 1 && !pushed) {  // fewer pairs of blocks than CTAs
+            const float none[TOK] = {};
+            push(none);
+        }
         if (MODE == DOWN && S == 1 && passes == 0)  // no token has an expert
             for (int tile = (int)blockIdx.x; tile < a.tiles; tile += (int)gridDim.x)
                 for (int t = 0; t < a.m; ++t) {
@@ -613,16 +711,16 @@ __global__ void __launch_bounds__(threads_of(MODE), 1)
         const int sw = warp - 8;
         const int64_t ld = MODE == UP ? a.ldx : a.K;
         const bool wide = (reinterpret_cast<uintptr_t>(a.xb) & 7u) == 0 && ld % 4 == 0;
-        auto value = [&](const Walk<MODE, S>& w, int t, int p) {
-            const int k = (w.k * kPair + p) * kBlock + lane * 4;
-            uint2 v = make_uint2(0u, 0u);
-            if (t < l.v_count[w.pass] && k < a.K) {
-                const int pair = l.list[l.v_first[w.pass] + t];
-                const uint16_t* p16 = a.xb + (int64_t)(MODE == UP ? pair / a.topk : pair) * ld + k;
-                v = wide ? *reinterpret_cast<const uint2*>(p16)
-                         : make_uint2(p16[0] | (uint32_t)p16[1] << 16, p16[2] | (uint32_t)p16[3] << 16);
-            }
-            return v;
+        auto row_of = [&](int pass, int t) {
+            const int pair = l.list[l.v_first[pass] + t];
+            return a.xb + (int64_t)(MODE == UP ? pair / a.topk : pair) * ld + lane * 4;
+        };
+        auto load4 = [&](const uint16_t* row, int k) {  // four values from lane * 4 on; zeros past K
+            if (k + lane * 4 >= a.K)
+                return make_uint2(0u, 0u);
+            const uint16_t* const v = row + k;
+            return wide ? *reinterpret_cast<const uint2*>(v)
+                        : make_uint2(v[0] | (uint32_t)v[1] << 16, v[2] | (uint32_t)v[3] << 16);
         };
         auto advance = [&](Walk<MODE, S>& w, int n) {  // n stages further
             for (; n > 0; --n)
@@ -631,43 +729,57 @@ __global__ void __launch_bounds__(threads_of(MODE), 1)
             return true;
         };
         constexpr int G = 4;  // tokens fetched ahead
+        const uint16_t* row[G] = {};
         uint2 ahead[G][kPair];
+        int pass = -1, n_tok = 0;
+        auto fetch = [&]() {
+            if (work.pass != pass) {
+                pass = work.pass;
+                n_tok = l.v_count[pass];
+#pragma unroll
+                for (int t = 0; t < G; ++t)
+                    if (t < n_tok)
+                        row[t] = row_of(pass, t);
+            }
+#pragma unroll
+            for (int t = 0; t < G; ++t)
+                if (t < n_tok)
+#pragma unroll
+                    for (int p = 0; p < kPair; ++p)
+                        ahead[t][p] = load4(row[t], (work.k * kPair + p) * kBlock);
+        };
         bool live = work.next() && advance(work, sw);
         if (live)
-#pragma unroll
-            for (int i = 0; i < G * kPair; ++i)
-                ahead[i / kPair][i % kPair] = value(work, i / kPair, i % kPair);
+            fetch();
         int slot = sw % a.stages, use = sw / a.stages;
         while (live) {
             uint2 now[G][kPair];
 #pragma unroll
             for (int i = 0; i < G * kPair; ++i)
                 now[i / kPair][i % kPair] = ahead[i / kPair][i % kPair];
-            Walk<MODE, S> then = work;
-            live = advance(then, kSplitWarps);
+            const int now_pass = pass, now_tok = n_tok, now_k = work.k;
+            live = advance(work, kSplitWarps);
             if (live)
-#pragma unroll
-                for (int i = 0; i < G * kPair; ++i)
-                    ahead[i / kPair][i % kPair] = value(then, i / kPair, i % kPair);
+                fetch();
             if (use > 0 && !wait(&sh.freed[slot], use - 1))
                 break;
-            const int n_tok = l.v_count[work.pass];
 #pragma unroll
             for (int p = 0; p < kPair; ++p) {
                 uint8_t* const tile = x_ring + (slot * kPair + p) * kXBytes;
                 float* const scale = sh.scales[slot][p];
 #pragma unroll
                 for (int t = 0; t < G; ++t)
-                    if (t < n_tok)
+                    if (t < now_tok)
                         split_block(now[t][p], tile, t, scale + t);
-                for (int t = G; t < n_tok; t += G) {
+                for (int t = G; t < now_tok; t += G) {
                     uint2 more[G];
 #pragma unroll
                     for (int i = 0; i < G; ++i)
-                        more[i] = value(work, t + i, p);
+                        if (t + i < now_tok)
+                            more[i] = load4(row_of(now_pass, t + i), (now_k * kPair + p) * kBlock);
 #pragma unroll
                     for (int i = 0; i < G; ++i)
-                        if (t + i < n_tok)
+                        if (t + i < now_tok)
                             split_block(more[i], tile, t + i, scale + t + i);
                 }
             }
@@ -675,29 +787,31 @@ __global__ void __launch_bounds__(threads_of(MODE), 1)
             __syncwarp();
             if (lane == 0)
                 mbar_arrive(smem_u32(&sh.full[slot]));
-            work = then;
             for (slot += kSplitWarps; slot >= a.stages; slot -= a.stages)
                 ++use;
         }
     }
     if constexpr (S > 1) {
+        const bool adds = warp >= 4 && warp < 8;
         __syncwarp();
-        cluster_sync();
-        const int rank = (int)blockIdx.x % S, tile = (int)blockIdx.x / S;
-        if (warp >= 4 && warp < 8) {
-            const int r = 32 * q + lane, row = tile * a.tile_rows + r;
-            if (r < a.tile_rows && row < a.rows && !*abort_flag)
-                for (int t = rank; t < a.m; t += S) {
-                    const uint32_t at = smem_u32(y_sum + t * kRowsMax + r);
-                    float v = 0.f;
+        if (MODE != GEMM || !adds)
+            cluster_wait();  // (the pushing warps have)
+        __syncwarp();
+        cluster_arrive();
+        cluster_wait();
+        const int r = 32 * q + lane, row = (int)blockIdx.x / S * a.tile_rows + r;
+        if (adds && r < a.tile_rows && row < a.rows && !*abort_flag)
+            for (int t = rank; t < a.m; t += S) {
+                float v = 0.f;
 #pragma unroll
-                    for (int c = 0; c < S; ++c)  // in the order of K
-                        v += load_peer(at, c);
-                    store(t, row, v);
-                }
-        }
+                for (int c = 0; c < S; ++c)  // in the order of K
+                    v += MODE == GEMM ? y_sum[(c * share + t / S) * kRowsMax + r] : load_peer(smem_u32(y_sum + t * kRowsMax + r), c);
+                store(t, row, v);
+            }
         __syncwarp();
-        cluster_sync();  // nobody reads this CTA's sums any more
+        if (MODE != GEMM) {
+            cluster_sync();  // nobody reads this CTA's sums any more
+        }
     }
     asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
     __syncthreads();
@@ -793,7 +907,7 @@ cudaError_t launch_stream(StreamArgs a, const void* W, const void* x, const Devi
     const int parts = MODE == UP ? 2 : 1;
     a.box_bytes = a.tile_rows * parts * kBlock;
     a.w_bytes = MODE == UP ? kRowsMax * kBlock : (a.box_bytes + 1023) / 1024 * 1024;
-    const size_t rest = (sizeof(Sh) + 127) / 128 * 128 + (MODE == DOWN || S > 1 ? (size_t)a.m * kRowsMax * 4 : 0) +
+    const size_t rest = (sizeof(Sh) + 127) / 128 * 128 + (MODE == DOWN || S > 1 ? (size_t)(a.m + S - 1) * kRowsMax * 4 : 0) +
                         (MODE == GEMM ? (size_t)a.pairs * kPair * NC * 4 : 0);
     const size_t past = (size_t)(kRowsMax * kBlock - a.w_bytes);  // what an MMA may read behind the last stage
     const size_t stage = (size_t)kPair * (a.w_bytes + NC * kBlock), room = (size_t)di.smem_optin - 1024;

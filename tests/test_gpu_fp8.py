@@ -496,3 +496,17 @@ def test_calls_on_streams_of_their_own(lib):
         got = [lib.fp8_moe(*s, stream=st) for s, st in zip(sets, streams)]
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("m,N,extra", [(40, 133, 3), (40, 130, 6), (200, 257, 7), (300, 1001, 7), (300, 1002, 2), (130, 1000, 8), (513, 127, 1)])
+def test_gemm_leaves_what_follows_a_row(lib, dtype, m, N, extra):
+    """Rows of y that end inside 16 bytes, with aligned row starts."""
+    g = gen(N)
+    K = 256
+    x, xs, w, ws = codes(g, m, K), scales(g, m, 2), codes(g, N, K), scales(g, blocks(N), 2)
+    out, untouched = guarded(m, N, dtype, extra=extra)
+    y = lib.fp8_gemm(x, xs, w, ws, out=out)
+    want, size = gemm_want(x, xs, w, ws)
+    within(y, want, gemm_tol(want, size, K, dtype))
+    untouched()
