@@ -30,13 +30,14 @@
 // are one e4m3 number and what is left, times 16, another.  Together they are
 // the bf16 value exactly, where it is within 2^-13 of the block's largest (and
 // off by less than 2^-20 of that below).  Four warps write them into the
-// stages, each its share of the blocks, the next one's values on their way.
+// stages, every fourth token each, the next stage's values on their way.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
 #include <algorithm>
 #include <cmath>
 #include <mutex>
+#include <type_traits>
 
 #include "fp8_common.cuh"
 #include "q2k_internal.h"
@@ -279,37 +280,49 @@ __device__ void build_lists(Lists& l, const StreamArgs& a, int cap)
     __syncthreads();
 }
 
-// A block of 128 bf16 values, 4 a lane, as the two e4m3 rows of column pair t (128-byte swizzled), and its scale.
-__device__ __forceinline__ void split_block(uint2 raw, uint8_t* tile, int t, float* scale)
+// N blocks of 128 bf16 values, 4 a lane, each as two e4m3 rows (128-byte swizzled: 2 * t[n] and the next one of its
+// tile), and its scale.  All at once: each is a chain of its own.
+template <int N>
+__device__ __forceinline__ void split_blocks(const uint2 (&raw)[N], uint8_t* const (&tile)[N], const int (&t)[N], float* const (&scale)[N])
 {
     const int lane = threadIdx.x & 31;
-    const float v[4] = {__uint_as_float(raw.x << 16), __uint_as_float(raw.x & 0xffff0000u), __uint_as_float(raw.y << 16),
-                        __uint_as_float(raw.y & 0xffff0000u)};
-    const uint32_t top = __reduce_max_sync(
-        0xffffffffu, max(max(__float_as_uint(v[0]) & 0x7fffffffu, __float_as_uint(v[1]) & 0x7fffffffu),
-                         max(__float_as_uint(v[2]) & 0x7fffffffu, __float_as_uint(v[3]) & 0x7fffffffu)));
-    // 2^(7 - e) of the largest's exponent e, within fp32's powers of two for it and its inverse
-    const uint32_t e = min(max(top >> 23, 20u), 254u);
-    const float f = __uint_as_float((261u - e) << 23);
-    float w[4];
+    uint32_t top[N];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        w[j] = v[j] * f;
-        if ((__float_as_uint(v[j]) & 0x7fffffffu) >= 0x7f800000u)
-            w[j] = __uint_as_float(0x7fffffffu);  // infinity too: e4m3 has none
+    for (int n = 0; n < N; ++n) {
+        // the larger of two magnitudes, as whole numbers: NaN above infinity above the others
+        const uint32_t a = raw[n].x & 0x7fff7fffu, b = raw[n].y & 0x7fff7fffu;
+        top[n] = max(max(a & 0xffffu, a >> 16), max(b & 0xffffu, b >> 16));
     }
-    const uint32_t u0 = e4m3x2(w[0], w[1]), u1 = e4m3x2(w[2], w[3]);
-    const float2 r0 = from_e4m3x2(u0), r1 = from_e4m3x2(u1);
-    const uint32_t l0 = e4m3x2((w[0] - r0.x) * 16.f, (w[1] - r0.y) * 16.f);
-    const uint32_t l1 = e4m3x2((w[2] - r1.x) * 16.f, (w[3] - r1.y) * 16.f);
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const int row = 2 * t + i;
-        *reinterpret_cast<uint32_t*>(tile + row * kBlock + (((lane >> 2) ^ (row & 7)) << 4) + ((lane & 3) << 2)) =
-            i ? l0 | l1 << 16 : u0 | u1 << 16;
+    for (int n = 0; n < N; ++n)
+        top[n] = __reduce_max_sync(0xffffffffu, top[n]);
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+        // 2^(7 - e) of the largest's exponent e, within fp32's powers of two for it and its inverse
+        const uint32_t e = min(max(top[n] >> 7, 20u), 254u);
+        const float f = __uint_as_float((261u - e) << 23);
+        float w[4] = {__uint_as_float(raw[n].x << 16), __uint_as_float(raw[n].x & 0xffff0000u), __uint_as_float(raw[n].y << 16),
+                      __uint_as_float(raw[n].y & 0xffff0000u)};
+        if (top[n] >= 0x7f80u) {  // infinity as NaN: e4m3 has none
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if ((__float_as_uint(w[j]) & 0x7fffffffu) >= 0x7f800000u)
+                    w[j] = __uint_as_float(0x7fffffffu);
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            w[j] *= f;
+        const uint32_t u0 = e4m3x2(w[0], w[1]), u1 = e4m3x2(w[2], w[3]);
+        const float2 r0 = from_e4m3x2(u0), r1 = from_e4m3x2(u1);
+        const uint32_t l0 = e4m3x2((w[0] - r0.x) * 16.f, (w[1] - r0.y) * 16.f);
+        const uint32_t l1 = e4m3x2((w[2] - r1.x) * 16.f, (w[3] - r1.y) * 16.f);
+        uint8_t* const at = tile[n] + 2 * t[n] * kBlock + ((lane & 3) << 2);
+        const int chunk = lane >> 2, swizzle = 2 * t[n] & 7;
+        *reinterpret_cast<uint32_t*>(at + ((chunk ^ swizzle) << 4)) = u0 | u1 << 16;
+        *reinterpret_cast<uint32_t*>(at + kBlock + ((chunk ^ (swizzle + 1)) << 4)) = l0 | l1 << 16;
+        if (lane == 0)
+            *scale[n] = __uint_as_float((e - 7u) << 23);
     }
-    if (lane == 0)
-        *scale = __uint_as_float((e - 7u) << 23);
 }
 
 template <int MODE, int NC>
@@ -401,7 +414,7 @@ __global__ void __launch_bounds__(threads_of(MODE), 1)
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < a.stages; ++s) {
-            mbar_init(smem_u32(&sh.full[s]), MODE == GEMM ? 1 : 2);
+            mbar_init(smem_u32(&sh.full[s]), MODE == GEMM ? 1 : 1 + kSplitWarps);
             mbar_init(smem_u32(&sh.done[s]), 1);
             mbar_init(smem_u32(&sh.freed[s]), 4);
         }
@@ -711,10 +724,6 @@ __global__ void __launch_bounds__(threads_of(MODE), 1)
         const int sw = warp - 8;
         const int64_t ld = MODE == UP ? a.ldx : a.K;
         const bool wide = (reinterpret_cast<uintptr_t>(a.xb) & 7u) == 0 && ld % 4 == 0;
-        auto row_of = [&](int pass, int t) {
-            const int pair = l.list[l.v_first[pass] + t];
-            return a.xb + (int64_t)(MODE == UP ? pair / a.topk : pair) * ld + lane * 4;
-        };
         auto load4 = [&](const uint16_t* row, int k) {  // four values from lane * 4 on; zeros past K
             if (k + lane * 4 >= a.K)
                 return make_uint2(0u, 0u);
@@ -722,73 +731,71 @@ __global__ void __launch_bounds__(threads_of(MODE), 1)
             return wide ? *reinterpret_cast<const uint2*>(v)
                         : make_uint2(v[0] | (uint32_t)v[1] << 16, v[2] | (uint32_t)v[3] << 16);
         };
-        auto advance = [&](Walk<MODE, S>& w, int n) {  // n stages further
-            for (; n > 0; --n)
-                if (++w.k >= w.k_end && !w.next())
-                    return false;
-            return true;
-        };
-        constexpr int G = 4;  // tokens fetched ahead
+        // Every fourth token of a stage is this warp's; the next stage's values are on their way.
+        constexpr int G = TOK / kSplitWarps;
         const uint16_t* row[G] = {};
         uint2 ahead[G][kPair];
-        int pass = -1, n_tok = 0;
+        int pass = -1, count = 0;
         auto fetch = [&]() {
             if (work.pass != pass) {
                 pass = work.pass;
-                n_tok = l.v_count[pass];
+                count = (l.v_count[pass] - sw + kSplitWarps - 1) / kSplitWarps;
 #pragma unroll
-                for (int t = 0; t < G; ++t)
-                    if (t < n_tok)
-                        row[t] = row_of(pass, t);
+                for (int g = 0; g < G; ++g)
+                    if (g < count) {
+                        const int pair = l.list[l.v_first[pass] + sw + g * kSplitWarps];
+                        row[g] = a.xb + (int64_t)(MODE == UP ? pair / a.topk : pair) * ld + lane * 4;
+                    }
             }
 #pragma unroll
-            for (int t = 0; t < G; ++t)
-                if (t < n_tok)
+            for (int g = 0; g < G; ++g)
 #pragma unroll
-                    for (int p = 0; p < kPair; ++p)
-                        ahead[t][p] = load4(row[t], (work.k * kPair + p) * kBlock);
+                for (int p = 0; p < kPair; ++p)
+                    ahead[g][p] = g < count ? load4(row[g], (work.k * kPair + p) * kBlock) : make_uint2(0u, 0u);
         };
-        bool live = work.next() && advance(work, sw);
+        bool live = work.next();
         if (live)
             fetch();
-        int slot = sw % a.stages, use = sw / a.stages;
+        int slot = 0, use = 0;
         while (live) {
             uint2 now[G][kPair];
 #pragma unroll
             for (int i = 0; i < G * kPair; ++i)
                 now[i / kPair][i % kPair] = ahead[i / kPair][i % kPair];
-            const int now_pass = pass, now_tok = n_tok, now_k = work.k;
-            live = advance(work, kSplitWarps);
+            const int n_now = count;
+            live = ++work.k < work.k_end || work.next();
             if (live)
                 fetch();
             if (use > 0 && !wait(&sh.freed[slot], use - 1))
                 break;
+            uint8_t* const tile = x_ring + slot * kPair * kXBytes;
+            auto split = [&](auto tokens) {  // of so many tokens
+                constexpr int N = decltype(tokens)::value;
+                uint2 raw[N * kPair];
+                uint8_t* tiles[N * kPair];
+                int t[N * kPair];
+                float* scale[N * kPair];
 #pragma unroll
-            for (int p = 0; p < kPair; ++p) {
-                uint8_t* const tile = x_ring + (slot * kPair + p) * kXBytes;
-                float* const scale = sh.scales[slot][p];
-#pragma unroll
-                for (int t = 0; t < G; ++t)
-                    if (t < now_tok)
-                        split_block(now[t][p], tile, t, scale + t);
-                for (int t = G; t < now_tok; t += G) {
-                    uint2 more[G];
-#pragma unroll
-                    for (int i = 0; i < G; ++i)
-                        if (t + i < now_tok)
-                            more[i] = load4(row_of(now_pass, t + i), (now_k * kPair + p) * kBlock);
-#pragma unroll
-                    for (int i = 0; i < G; ++i)
-                        if (t + i < now_tok)
-                            split_block(more[i], tile, t + i, scale + t + i);
+                for (int i = 0; i < N * kPair; ++i) {
+                    raw[i] = now[i / kPair][i % kPair];
+                    tiles[i] = tile + i % kPair * kXBytes;
+                    t[i] = sw + i / kPair * kSplitWarps;
+                    scale[i] = &sh.scales[slot][i % kPair][t[i]];
                 }
-            }
+                split_blocks<N * kPair>(raw, tiles, t, scale);
+            };
+            if (n_now == 1)
+                split(std::integral_constant<int, 1>{});
+            else if (n_now > 1)
+                split(std::integral_constant<int, G>{});
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
             if (lane == 0)
                 mbar_arrive(smem_u32(&sh.full[slot]));
-            for (slot += kSplitWarps; slot >= a.stages; slot -= a.stages)
+            if (++slot == a.stages) {
+                slot = 0;
                 ++use;
+            }
         }
     }
     if constexpr (S > 1) {
