@@ -153,7 +153,16 @@ struct Lists {
     uint16_t rank[kMaxPairs], list[kMaxPairs];                         // pairs by expert, in order
     uint16_t v_expert[kMaxPairs], v_first[kMaxPairs], v_count[kMaxPairs];  // passes
     alignas(16) uint16_t count[kMaxExperts];
+    uint16_t token[kMaxPairs];  // of list's entries, and their weights
+    float weight[kMaxPairs];
     int passes;
+
+    __device__ __forceinline__ void put(const StreamArgs& a, int place, int pair)
+    {
+        list[place] = (uint16_t)pair;
+        token[place] = (uint16_t)(pair / a.topk);
+        weight[place] = a.route_w[pair];
+    }
 };
 
 constexpr int kFewPairs = 256;
@@ -190,7 +199,7 @@ __device__ __forceinline__ void build_few_lists(Lists& l, const StreamArgs& a, i
         }
         starts[i] = e != kNone && before % cap == 0 ? e : kNone;
         if (e != kNone)
-            l.list[place] = (uint16_t)i;
+            l.put(a, place, i);
     }
     const bool start = i < whole && e != kNone && before % cap == 0;
     const int passes = __syncthreads_count(start);
@@ -275,7 +284,7 @@ __device__ void build_lists(Lists& l, const StreamArgs& a, int cap)
     for (int i = tid; i < pairs; i += kThreads) {
         const int e = l.ids[i];
         if (e >= 0 && e < a.E)
-            l.list[l.count[e] + l.rank[i]] = (uint16_t)i;
+            l.put(a, l.count[e] + l.rank[i], i);
     }
     __syncthreads();
 }
@@ -568,21 +577,21 @@ __global__ void __launch_bounds__(threads_of(MODE), 1)
             float v[2];
             int cut;
         };
-        auto scales_of = [&](int k0) {
+        auto scales_of = [&](const Walk<MODE, S>& w, int k0) {
             Scales s{{0.f, 0.f}, 32};
             int64_t first, second;
             if (MODE == UP) {
-                first = (int64_t)l.v_expert[work.pass] * 2 * a.row_blocks + min((work.tile + q) * kUnit / 128, a.row_blocks - 1);
+                first = (int64_t)l.v_expert[w.pass] * 2 * a.row_blocks + min((w.tile + q) * kUnit / 128, a.row_blocks - 1);
                 second = first + a.row_blocks;
                 s.cut = kUnit;
             } else {
-                const int row = work.tile * a.tile_rows + 32 * q;
-                const int64_t e = MODE == DOWN ? (int64_t)l.v_expert[work.pass] * a.row_blocks : 0;
+                const int row = w.tile * a.tile_rows + 32 * q;
+                const int64_t e = MODE == DOWN ? (int64_t)l.v_expert[w.pass] * a.row_blocks : 0;
                 first = e + min(row / 128, a.row_blocks - 1);
                 second = e + min(row / 128 + 1, a.row_blocks - 1);
                 s.cut = (row / 128 + 1) * 128 - row;
             }
-            if (k0 + lane < min(a.blocks, work.k_end * kPair)) {
+            if (k0 + lane < min(a.blocks, w.k_end * kPair)) {
                 s.v[0] = a.w_scales[first * a.blocks + k0 + lane];
                 if (s.cut < 32)
                     s.v[1] = a.w_scales[second * a.blocks + k0 + lane];
@@ -603,17 +612,24 @@ __global__ void __launch_bounds__(threads_of(MODE), 1)
                     store_peer(at + (uint32_t)(t / S) * (kRowsMax * 4), t % S, v[t]);
         };
         bool ready = false;
-        while (work.next()) {
-            const int n_tok = MODE == GEMM ? a.m : l.v_count[work.pass];
+        bool more = work.next();
+        Scales next{{0.f, 0.f}, 32};
+        if (more)
+            next = scales_of(work, work.k * kPair);
+        while (more) {
+            const Walk<MODE, S> piece = work;
+            Scales ws = next;
+            if ((more = work.next()))
+                next = scales_of(work, work.k * kPair);  // (a piece ahead)
+            const int n_tok = MODE == GEMM ? a.m : l.v_count[piece.pass];
             float acc[TOK];
 #pragma unroll
             for (int t = 0; t < TOK; ++t)
                 acc[t] = 0.f;
-            Scales ws = scales_of(work.k * kPair);
-            for (int k = work.k; k < work.k_end; ++k) {
-                const int j = (k - work.k) * kPair & 31;
-                if (j == 0 && k > work.k)
-                    ws = scales_of(k * kPair);
+            for (int k = piece.k; k < piece.k_end; ++k) {
+                const int j = (k - piece.k) * kPair & 31;
+                if (j == 0 && k > piece.k)
+                    ws = scales_of(piece, k * kPair);
                 float w[kPair];
 #pragma unroll
                 for (int p = 0; p < kPair; ++p) {
@@ -666,7 +682,7 @@ __global__ void __launch_bounds__(threads_of(MODE), 1)
                 use = use1;
             }
             if constexpr (MODE == GEMM) {
-                const int r = 32 * q + lane, row = work.tile * a.tile_rows + r;
+                const int r = 32 * q + lane, row = piece.tile * a.tile_rows + r;
                 if (S > 1) {
                     push(acc);
                 } else if (r < a.tile_rows && row < a.rows && !*abort_flag) {
@@ -676,29 +692,29 @@ __global__ void __launch_bounds__(threads_of(MODE), 1)
                             store(t, row, acc[t]);
                 }
             } else if constexpr (MODE == UP) {
-                const int row = (work.tile + q) * kUnit + (lane & 15);
+                const int row = (piece.tile + q) * kUnit + (lane & 15);
 #pragma unroll
                 for (int t = 0; t < TOK; ++t) {
                     if (t >= n_tok)
                         break;
                     const float gate = acc[t], up = __shfl_down_sync(0xffffffffu, acc[t], 16);
-                    if (q < work.units && lane < 16 && row < a.rows) {
+                    if (q < piece.units && lane < 16 && row < a.rows) {
                         const float hv = __fdiv_rn(gate, 1.0f + expf(-gate)) * up;
-                        a.h[(int64_t)l.list[l.v_first[work.pass] + t] * a.rows + row] = __bfloat16_as_ushort(__float2bfloat16_rn(hv));
+                        a.h[(int64_t)l.list[l.v_first[piece.pass] + t] * a.rows + row] = __bfloat16_as_ushort(__float2bfloat16_rn(hv));
                     }
                 }
             } else {
                 // (a row of y_sum's columns is this thread's alone)
-                const int r = 32 * q + lane, row = work.tile * a.tile_rows + r;
+                const int r = 32 * q + lane, row = piece.tile * a.tile_rows + r;
 #pragma unroll
                 for (int t = 0; t < TOK; ++t) {
                     if (t >= n_tok)
                         break;
-                    const int pair = l.list[l.v_first[work.pass] + t];
-                    float& to = y_sum[pair / a.topk * kRowsMax + r];
-                    to = fmaf(a.route_w[pair], acc[t], to);
+                    const int at = l.v_first[piece.pass] + t;
+                    float& to = y_sum[l.token[at] * kRowsMax + r];
+                    to = fmaf(l.weight[at], acc[t], to);
                 }
-                if (S == 1 && work.last)
+                if (S == 1 && piece.last)
                     for (int t = 0; t < a.m; ++t) {
                         if (r < a.tile_rows && row < a.rows && !*abort_flag)
                             store(t, row, y_sum[t * kRowsMax + r]);
@@ -743,8 +759,8 @@ __global__ void __launch_bounds__(threads_of(MODE), 1)
 #pragma unroll
                 for (int g = 0; g < G; ++g)
                     if (g < count) {
-                        const int pair = l.list[l.v_first[pass] + sw + g * kSplitWarps];
-                        row[g] = a.xb + (int64_t)(MODE == UP ? pair / a.topk : pair) * ld + lane * 4;
+                        const int at = l.v_first[pass] + sw + g * kSplitWarps;
+                        row[g] = a.xb + (int64_t)(MODE == UP ? l.token[at] : l.list[at]) * ld + lane * 4;
                     }
             }
 #pragma unroll
