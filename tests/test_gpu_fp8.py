@@ -206,7 +206,7 @@ GEMM_SIZES = [
     *[(m, 96, 256) for m in (1, 2, 3, 7, 8, 9, 15, 16, 17, 24, 31, 32, 33, 48, 63, 64, 65, 100, 127, 128, 129, 200, 255, 256, 257, 300, 513)],
     *[(m, N, 384) for m in (1, 9, 40, 130) for N in (1, 2, 5, 15, 16, 17, 31, 33, 63, 64, 65, 127, 128, 129, 255, 257, 500, 1000)],
     *[(m, 160, K) for m in (1, 12, 30, 70, 256) for K in (16, 32, 48, 64, 112, 128, 144, 240, 256, 272, 512, 528, 640, 1024, 1040, 2064, 4096, 4112)],
-    (1, 4096, 4096), (16, 2048, 16384), (8, 1024, 20480), (203, 5000, 4112), (1500, 1300, 1536), (32, 6000, 1040), (700, 128, 16400),
+    (8, 64, 131072), (20, 33, 65552), (3, 16, 65536), (1, 4096, 4096), (16, 2048, 16384), (8, 1024, 20480), (203, 5000, 4112), (1500, 1300, 1536), (32, 6000, 1040), (700, 128, 16400),
 ]
 
 
@@ -357,7 +357,8 @@ def moe_check(lib, args, dtype, what=""):
     (4, 8, 8, 512, 384), (5, 8, 2, 1040, 528), (8, 32, 4, 640, 768), (9, 4, 2, 384, 256), (16, 64, 6, 1024, 512),
     (17, 3, 2, 400, 208), (33, 8, 2, 256, 640), (64, 16, 4, 128, 128), (128, 8, 8, 256, 256), (40, 1, 1, 528, 272),
     (128, 1, 1, 256, 256), (32, 64, 32, 128, 128), (7, 1024, 8, 64, 32), (1, 4, 2, 4096, 2048), (6, 16, 4, 2880, 1520),
-    (2, 2, 1, 16384, 128), (2, 2, 1, 128, 16384), (20, 2, 1, 16384, 32), (20, 2, 1, 32, 16384), (3, 4, 2, 32, 48)])
+    (2, 2, 1, 16384, 128), (2, 2, 1, 128, 16384), (20, 2, 1, 16384, 32), (20, 2, 1, 32, 16384), (3, 4, 2, 32, 48),
+    (128, 2, 1, 16384, 64), (3, 4, 2, 9744, 160), (32, 8, 8, 256, 256), (33, 8, 8, 256, 128), (43, 16, 6, 144, 272)])
 def test_moe(lib, dtype, m, E, topk, dim, inter):
     args = moe_inputs(m * 31 + E, m, E, topk, dim, inter)
     y = moe_check(lib, args, dtype)
@@ -510,3 +511,50 @@ def test_gemm_leaves_what_follows_a_row(lib, dtype, m, N, extra):
     want, size = gemm_want(x, xs, w, ws)
     within(y, want, gemm_tol(want, size, K, dtype))
     untouched()
+
+
+def test_two_captured_steps_with_workspaces_of_their_own(lib):
+    """Replayed one after another and at once."""
+    sets = [moe_inputs(20 + i, 6, 8, 3, 512, 384) for i in range(2)]
+    want = [lib.fp8_moe(*s) for s in sets]
+    graphs, outs, streams = [], [], [torch.cuda.Stream() for _ in sets]
+    for s, st in zip(sets, streams):
+        work = torch.empty(lib.fp8_moe_workspace_bytes(6, 3, 512, 384), dtype=torch.uint8, device=DEV)
+        st.wait_stream(torch.cuda.current_stream())
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=st):
+            outs.append(lib.fp8_moe(*s, workspace=work))
+        graphs.append((graph, work))
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for o in outs:
+            o.zero_()
+        torch.cuda.synchronize()
+        for (graph, _), st in zip(graphs, streams):
+            with torch.cuda.stream(st):
+                graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(outs, want))
+
+
+def test_ids_written_by_the_launch_before(lib):
+    """The second launch reads ids and weights before it waits for the first: what came before has to be complete."""
+    args = moe_inputs(31, 4, 16, 2, 256, 256)
+    good = lib.fp8_moe(*args)
+    ids, w = args[1].clone(), args[2].clone()
+    for _ in range(50):
+        ids.fill_(-1)
+        w.fill_(0)
+        ids.copy_(args[1])
+        w.copy_(args[2])
+        assert torch.equal(lib.fp8_moe(args[0], ids, w, *args[3:]), good)
+
+
+def test_repeated_calls_give_the_same_bits(lib):
+    args = moe_inputs(77, 19, 12, 4, 640, 528)
+    x, xs, w, ws = codes(gen(1), 77, 1168), scales(gen(2), 77, 10), codes(gen(3), 900, 1168), scales(gen(4), 8, 10)
+    moe, gemm = lib.fp8_moe(*args), lib.fp8_gemm(x, xs, w, ws)
+    few = lib.fp8_gemm(x[:9], xs[:9], w, ws)
+    for _ in range(20):
+        assert torch.equal(lib.fp8_moe(*args), moe) and torch.equal(lib.fp8_gemm(x, xs, w, ws), gemm)
+        assert torch.equal(lib.fp8_gemm(x[:9], xs[:9], w, ws), few)
