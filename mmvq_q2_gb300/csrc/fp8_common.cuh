@@ -36,6 +36,16 @@ __device__ __forceinline__ bool mbar_ready(uint32_t bar, uint32_t parity) { retu
 // MMA that are computed from it need no moves to uniform registers.
 __device__ __forceinline__ uint32_t uniform(uint32_t v) { return __shfl_sync(0xffffffffu, v, 0); }
 
+// The shared memory to launch with: all but 8 KB of what a block may have.  These kernels take all of tensor memory, and
+// a block that finds it taken waits until it is given back.  Two clusters that each had one block waiting for the
+// other's would wait for ever, as would a block whose tensor memory is held by a launch that waits for it; so no second
+// block that works in tensor memory (none does with less than 8 KB for its operands) may fit on an SM beside one of these.
+inline size_t alone_on_sm(size_t bytes, size_t most)
+{
+    const size_t least = most - 8192;
+    return bytes < least ? least : bytes;
+}
+
 // The low and high word of smem_desc_sw128(), the address in the low one.
 __device__ __forceinline__ uint64_t desc_at(uint32_t addr)
 {

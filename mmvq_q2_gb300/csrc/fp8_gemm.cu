@@ -502,7 +502,7 @@ cudaError_t launch_tiles(GemmArgs a, const Fp8Gemm& p, const DeviceInfo& di, cud
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)(S > 1 ? tiles * S : std::min<int64_t>(tiles, di.sm_count)));
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = extra + (size_t)a.stages * kStage;
+    cfg.dynamicSmemBytes = alone_on_sm(extra + (size_t)a.stages * kStage, (size_t)di.smem_optin);
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -948,7 +948,7 @@ cudaError_t launch_stream(StreamArgs a, const void* W, const void* x, const Devi
     // (UP: the passes are known on the device alone, so a CTA on every SM)
     cfg.gridDim = dim3((unsigned)(MODE == UP ? di.sm_count : std::min(a.tiles, teams) * S));
     cfg.blockDim = dim3(threads_of(MODE));
-    cfg.dynamicSmemBytes = 1024 + bytes;
+    cfg.dynamicSmemBytes = alone_on_sm(1024 + bytes, (size_t)di.smem_optin);
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -51,3 +51,14 @@ def test_registers_moved_between_warps_add_up():
     threads = int(re.search(r"kThreads = (\d+)", text).group(1))
     launched = 65536 // threads // 8 * 8
     assert 128 * down + (threads - 128) * up <= threads * launched
+
+
+def test_no_second_block_with_tensor_memory_fits_beside_one():
+    """Every launch of a kernel that takes all of tensor memory asks for all but 8 KB of shared memory: two blocks on one
+    SM would wait for each other's tensor memory, and across two clusters for ever."""
+    for name in ("fp8_gemm.cu", "fp8_stream.cu"):
+        asked = re.findall(r"dynamicSmemBytes = ([^;]+);", source(name))
+        assert asked
+        for size in asked:
+            assert size.startswith("alone_on_sm(") or size == "(size_t)di.smem_optin", (name, size)
+    assert "most - 8192;" in source("fp8_common.cuh")

@@ -558,3 +558,20 @@ def test_repeated_calls_give_the_same_bits(lib):
     for _ in range(20):
         assert torch.equal(lib.fp8_moe(*args), moe) and torch.equal(lib.fp8_gemm(x, xs, w, ws), gemm)
         assert torch.equal(lib.fp8_gemm(x[:9], xs[:9], w, ws), few)
+
+
+def test_small_products_on_two_streams_at_once(lib):
+    """Products of few tiles, whose clusters could share SMs: none waits for another's tensor memory."""
+    g, sides = gen(43), (torch.cuda.Stream(), torch.cuda.Stream())
+    inputs = []
+    for m, N in ((1, 144), (16, 272), (24, 512), (48, 256)):
+        x, w = codes(g, m, 1024), codes(g, N, 1024)
+        inputs.append((x, scales(g, m, 8), w, scales(g, blocks(N), 8)))
+    alone = [lib.fp8_gemm(*i) for i in inputs]
+    torch.cuda.synchronize()
+    got = []
+    for turn in range(50):
+        for side in sides:
+            got += [(n, lib.fp8_gemm(*inputs[n], stream=side)) for n in range(len(inputs))]
+    torch.cuda.synchronize()
+    assert all(torch.equal(alone[n], y) for n, y in got)
