@@ -175,8 +175,8 @@ def test_swiglu(lib, dtype, rows, N, extra):
     g, u = x.double().chunk(2, -1)
     h = g * torch.sigmoid(g) * u
     up = s.double().repeat_interleave(128, 1)[:, :N]
-    # h in fp32: expf is off by 2 ulp, the sum, the division and the product by half of one each (2^-21 in all); the
-    # scale follows h's largest, then the two divisions
+    # h in fp32: 2^-22 for the power of two, 2^-23 for the reciprocal, 2^-24 for each of five roundings, 11 * 2^-24 in all;
+    # the scale follows h's largest, then the division: 12 of the 16 * 2^-24 allowed
     pad = torch.nn.functional.pad(h.abs(), (0, -N % 128)).view(rows, -1, 128).amax(-1)
     within(s, pad / 448, pad / 448 * 2.0 ** -20)
     within(q.double() * up, h, (h.abs() * 2.0 ** -4).maximum(up * 2.0 ** -10) * (1 + 2.0 ** -10))
@@ -188,6 +188,18 @@ def test_swiglu_far_ends(lib):
     h = (q.double() * s.double())[0]
     # the largest gets code 448 and reads as 448 times a scale of 6e4 / 448 that is rounded once
     assert torch.isfinite(h).all() and abs(h[5] - 6e4) <= 6e4 * 2.0 ** -24 and (h[[0, 1, 3, 6]] == 0).all()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("N", [16, 13])
+def test_swiglu_of_small_gates_and_large_ups(lib, dtype, N):
+    """e^-g near fp32's largest, up large: what is left is far from zero."""
+    x = torch.cat([torch.linspace(-88.6, -86.0, N, device=DEV), torch.full((N,), 1e30, device=DEV)]).to(dtype)[None]
+    q, s = lib.swiglu_fp8_rows(x)
+    g, u = x.double().chunk(2, -1)
+    h = g * torch.exp(g) / (1 + torch.exp(g)) * u
+    # e^g may be below fp32's normal values, off by 2 units of 2^-149 of at least 2^-129 there: 2^-19
+    within(q.double() * s.double(), h, (h.abs() * 2.0 ** -4).maximum(s.double() * 2.0 ** -10) * (1 + 2.0 ** -10))
 
 
 # ---- fp8_gemm ----------------------------------------------------------------------
