@@ -560,7 +560,8 @@ int moe_route_topk(const void* logits, int type, int64_t m, int64_t E, int64_t l
  * a matrix [N, K] has a scale for each 128 x 128 values, [ceil(N / 128),
  * ceil(K / 128)]; activation rows [m, K] have one for each 128 values,
  * [m, ceil(K / 128)].  The last block of a row or column may be short.  A
- * value stands for code * scale. */
+ * value stands for code * scale.  No output may overlap an input or another
+ * output. */
 
 /* Encode rows or a matrix.
  *   x       x_type [rows, K], rows ldx apart
@@ -626,7 +627,8 @@ size_t fp8_moe_workspace_bytes(int64_t m, int64_t topk, int64_t dim, int64_t int
  * Products accumulate in fp32 as in fp8_gemm; x enters as it is (bf16), h
  * is rounded to bf16 (as the buffers of the other expert calls are); the sum
  * over j is fp32, by rising expert; rounded once to bf16 where y is bf16.  A call
- * repeats bit for bit.  A token with a NaN or an infinity gives NaN.
+ * repeats bit for bit.  A token with a NaN or an infinity, or whose h
+ * is past bf16's range, gives NaN.
  *   workspace  at least fp8_moe_workspace_bytes(m, topk, dim, inter) bytes,
  *              256-byte aligned; calls that overlap need one each
  * 0 <= m <= 128, 1 <= topk <= 32, m * topk <= 1024, 1 <= E <= 1024, dim and
