@@ -15,10 +15,10 @@
 //   warps 4..11  read back, scale, add; at the end they leave y in shared
 //                memory for tensor copies to store (8191 x 8192 x 4096 213 us;
 //                stored by the warps 222).
-// What bounds a block of K at BN = 256, 940 cycles where its MMAs take 510: the
-// operands go into shared memory and out of it, 96 KB at 128 bytes a cycle, and
-// the way round an accumulator (MMAs, commit and wait, read back, wait) is
-// longer than two blocks.  192 columns, read back at once, took 254 us.
+// What bounds a block of K at BN = 256, 920 to 940 cycles where its MMAs take 510:
+// the way round an accumulator (until the adding warps are awake 1121, read back
+// 487, until the next issue 246) is two blocks, for two accumulators.  192
+// columns, read back at once, took 254 us; pairs of SMs on one tile 220.
 // CTAs walk the tiles, 16 tiles of x at a time, so that what runs together
 // shares operands in L2.  Where there are fewer tiles than SMs, the CTAs of a
 // cluster share a tile along K and add their sums through shared memory, in
