@@ -53,14 +53,16 @@ __device__ __forceinline__ uint32_t enc4(float a, float b, float c, float d)
 }
 
 // g / (1 + e^-g) * u, within 8 units of the last place of h.  e^-g is the hardware's 2^t (2^-22 off) of t = -g log2(e) as
-// a product, and what its rounding and log2(e)'s left as a factor 1 + t' ln 2.  The division is one of a quarter by a
-// quarter, by the hardware's reciprocal (2^-23 off), which past 2^126 would be 0 and lose what a large u shows; so h is
-// right to g = -88.7, below which e^-g is past fp32's range.  (8191 rows of 2048 16.5 us; with expf and a quick division
+// a product, and what its rounding and log2(e)'s left as a factor 1 + t' ln 2.  Both are taken of a gate cut at 128, where
+// e^-g no longer counts: past 2.36e38 the product is infinite and what it left is, too.  The division is one of a quarter
+// by a quarter, by the hardware's reciprocal (2^-23 off), which past 2^126 would be 0 and lose what a large u shows; so h
+// is right to g = -88.7, below which e^-g is past fp32's range.  (8191 rows of 2048 16.5 us; with expf and a quick division
 // 19.8, with a rounded one 28.)
 __device__ __forceinline__ float swiglu1(float g, float u)
 {
-    const float hi = __fmul_rn(g, -0x1.715476p+0f);
-    const float lo = fmaf(g, -0x1.4ae0cp-26f, fmaf(g, -0x1.715476p+0f, -hi));
+    const float c = fminf(g, 128.0f);  // (128 for NaN, which the products keep)
+    const float hi = __fmul_rn(c, -0x1.715476p+0f);
+    const float lo = fmaf(c, -0x1.4ae0cp-26f, fmaf(c, -0x1.715476p+0f, -hi));
     float e, r;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(hi));
     e *= fmaf(lo, 0x1.62e43p-1f, 1.0f);
