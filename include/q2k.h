@@ -582,9 +582,10 @@ int fp8_quantize(const void* x, int x_type, int64_t rows, int64_t K, int64_t ldx
 /* SwiGLU and the encoding of its rows (the twin of swiglu_q8_1_rows).
  *   gate_up  type [rows, 2 N], rows ld apart: N gate values, then N up values
  *   q, ldq, scales, ld_scales   as for fp8_quantize of [rows, N], block_rows 1
- * h = g / (1 + e^-g) * u in fp32, within 8 units of the last place (zero
- * where e^-g is past fp32's range), not rounded to fewer bits before it is
- * encoded.
+ * h = g / (1 + e^-g) * u in fp32, within 2^-20 of its value (zero where e^-g
+ * is past fp32's range, g < -88.7), not rounded to fewer bits before it is
+ * encoded; a product u / (1 + e^-g) below fp32's normal range keeps what fp32
+ * holds of it.
  * 0 <= rows, 1 <= N <= 2^19.  One launch. */
 int swiglu_fp8_rows(const void* gate_up, int type, int64_t rows, int64_t N, int64_t ld, uint8_t* q, int64_t ldq,
                     float* scales, int64_t ld_scales, q2k_stream_t stream);

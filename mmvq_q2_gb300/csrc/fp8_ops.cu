@@ -53,11 +53,13 @@ __device__ __forceinline__ uint32_t enc4(float a, float b, float c, float d)
 }
 
 // g / (1 + e^-g) * u, within 8 units of the last place of h.  e^-g is the hardware's 2^t (2^-22 off) of t = -g log2(e) as
-// a product, and what its rounding and log2(e)'s left as a factor 1 + t' ln 2.  Both are taken of a gate cut at 128, where
-// e^-g no longer counts: past 2.36e38 the product is infinite and what it left is, too.  The division is one of a quarter
-// by a quarter, by the hardware's reciprocal (2^-23 off), which past 2^126 would be 0 and lose what a large u shows; so h
-// is right to g = -88.7, below which e^-g is past fp32's range.  (8191 rows of 2048 16.5 us; with expf and a quick division
-// 19.8, with a rounded one 28.)
+// a product, and what its rounding and log2(e)'s left as a factor 1 + t' ln 2, a quarter of it here.  Both are taken of a
+// gate cut at 128, where e^-g no longer counts: past 2.36e38 the product is infinite and what it left is, too.  The
+// division is one of a quarter by a quarter, by the hardware's reciprocal (2^-23 off), which past 2^126 would be 0 and
+// lose what a large u shows; so h is right to g = -88.7, below which e^-g is past fp32's range.  The sigmoid meets u
+// before g, so that a gate near or below fp32's smallest normal value loses no bits to a factor below 1: 1 + e^-g of a gate
+// so small is 2, and u is large where h is not lost in any case.  (8191 rows of 2048 16.7 us; with expf and a quick
+// division 19.8, with a rounded one 28.)
 __device__ __forceinline__ float swiglu1(float g, float u)
 {
     const float c = fminf(g, 128.0f);  // (128 for NaN, which the products keep)
@@ -65,9 +67,8 @@ __device__ __forceinline__ float swiglu1(float g, float u)
     const float lo = fmaf(c, -0x1.4ae0cp-26f, fmaf(c, -0x1.715476p+0f, -hi));
     float e, r;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(hi));
-    e *= fmaf(lo, 0x1.62e43p-1f, 1.0f);
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(fmaf(e, 0.25f, 0.25f)));
-    return 0.25f * g * r * u;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(fmaf(e, fmaf(lo, 0x1.62e43p-3f, 0.25f), 0.25f)));
+    return 0.25f * r * u * g;
 }
 
 // 8 values as they lie in memory, and as numbers.
