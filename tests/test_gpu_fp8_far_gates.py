@@ -12,6 +12,8 @@ import torch
 
 from test_gpu_fp8 import BF16, DEV, F32, gen, lib  # noqa: F401
 
+pytestmark = pytest.mark.gpu
+
 
 def rows_of(gates, ups, N, dtype):
     """[n, 2 N]: a gate and an up a row, N times each, as they are in `dtype`."""
