@@ -55,6 +55,7 @@ __device__ __forceinline__ uint64_t desc_at(uint32_t addr)
 
 // Instruction descriptor: D fp32, A and B e4m3, both K-major, M = 128.
 constexpr uint32_t instr_desc_e4m3(int n) { return (1u << 4) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(128 >> 4) << 24); }
+constexpr uint32_t kBIsE5m2 = 1u << 10;  // (each operand of kind::f8f6f4 has a type of its own)
 
 __device__ __forceinline__ void umma_e4m3(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc, bool acc)
 {

@@ -6,7 +6,7 @@
 // up to 128 rows into a ring of shared-memory stages (tensor copies, 128-byte
 // swizzled; a warp takes 390 cycles from one stage's copy to the next's, so
 // one alone was the bound), another issues tcgen05.mma kind::f8f6f4 on them as
-// they are, weight rows as M = 128, tokens as N = 16 or 32 columns.  The scales
+// they are, weight rows as M = 128, tokens as N = 16 to 48 columns.  The scales
 // change every 128 values of K, so each block of a stage has an accumulator of
 // its own in tensor memory, and four warps read them back, scale them and add
 // them up in fp32, a thread a row; that frees the stage.  (mma.sync, eight warps at the same
@@ -25,12 +25,15 @@
 // turn, so that the sum over a token's experts stays with the cluster.  (Joined
 // by whoever finished a tile last, the fences alone took 10000 cycles an item.)
 //
-// bf16 tokens (fp8_moe) enter as two columns of e4m3 each: with a power of
-// two that brings a block's largest below 256, the upper 4 bits of a value
-// are one e4m3 number and what is left, times 16, another.  Together they are
-// the bf16 value exactly, where it is within 2^-13 of the block's largest (and
-// off by less than 2^-20 of that below).  Four warps write them into the
-// stages, every fourth token each, the next stage's values on their way.
+// bf16 tokens (fp8_moe) enter as three columns of e5m2 each: with a power of
+// two that brings a block's largest below 2^16, a value is an fp16 number,
+// whose upper byte is an e5m2 one; what is left, times 8, is the next, and
+// once more.  Together they are the bf16 value exactly, where it is within
+// 2^-30 of the block's largest (and off by less than 2^-37 of that below).
+// (Two columns of e4m3 are exact within 2^-13 alone; with two more for the
+// blocks that need them, as many of h's do, 32 tokens of 8 experts took 117 us
+// where these take 61.)  Four warps write them into the stages, every fourth
+// token each, the next stage's values on their way.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -54,6 +57,7 @@ constexpr int kPair = 2;       // such blocks in a stage
 constexpr int kUnit = 16;      // UP: rows of gate, and of up, in a unit
 constexpr int kMaxStages = 16;
 constexpr int kCopyWarps = 3, kSplitWarps = 4;
+constexpr int kPlanes = 3;     // columns that a bf16 token enters as
 constexpr int kMaxPairs = 1024, kMaxExperts = 1024;
 
 enum Mode : int { GEMM = 0, UP = 1, DOWN = 2 };
@@ -61,8 +65,13 @@ enum Mode : int { GEMM = 0, UP = 1, DOWN = 2 };
 // Warps: one for the MMAs, three for copies, four that add up (tensor memory lanes by warp % 4), four for columns.
 constexpr int threads_of(int mode) { return mode == GEMM ? 256 : 384; }
 
-// Stages that have their accumulators in tensor memory, 512 columns of it.
-constexpr int stages_of(int columns) { return 512 / (kPair * columns); }
+// Tokens of a pass, and rows of them in a block of a stage.
+constexpr int tokens_of(int mode, int columns) { return mode == GEMM ? columns : columns / kPlanes / 8 * 8; }
+constexpr int x_rows_of(int mode, int columns) { return mode == GEMM ? columns : kPlanes * tokens_of(mode, columns); }
+
+// Columns of tensor memory that an accumulator is given, and stages that have theirs in its 512.
+constexpr int acc_columns(int columns) { return columns <= 32 ? columns : 64; }
+constexpr int stages_of(int columns) { return 512 / (kPair * acc_columns(columns)); }
 
 struct StreamArgs {
     const float* w_scales;
@@ -99,19 +108,30 @@ __device__ __forceinline__ void tmem_load16(uint32_t taddr, float* v)
         : "r"(taddr));
 }
 
-// Two floats as e4m3, and back.
-__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi)
+// 8 of them.
+__device__ __forceinline__ void tmem_load8(uint32_t taddr, float* v)
 {
-    uint16_t r;
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7])
+                 : "r"(taddr));
+}
+
+// Two floats as fp16.
+__device__ __forceinline__ uint32_t f16x2(float lo, float hi)
+{
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
 }
 
-__device__ __forceinline__ float2 from_e4m3x2(uint32_t v)
+// What is left of two fp16 numbers without their upper bytes, times 8: exact.
+__device__ __forceinline__ uint32_t left8(uint32_t h)
 {
-    uint32_t h;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)v));
-    return make_float2(half_lo_f(h), half_hi_f(h));
+    uint32_t r;
+    asm("{\n\t.reg .b32 u;\n\tand.b32 u, %1, 0xff00ff00;\n\tsub.rn.f16x2 u, %1, u;\n\tmul.rn.f16x2 %0, u, %2;\n\t}"
+        : "=r"(r)
+        : "r"(h), "r"(0x48004800u));
+    return r;
 }
 
 // A box of 128 bytes by rows, by gate and up, by expert.
@@ -289,16 +309,17 @@ __device__ void build_lists(Lists& l, const StreamArgs& a, int cap)
     __syncthreads();
 }
 
-// N blocks of 128 bf16 values, 4 a lane, each as two e4m3 rows (128-byte swizzled: 2 * t[n] and the next one of its
-// tile), and its scale.  All at once: each is a chain of its own.
-template <int N>
+// N blocks of 128 bf16 values, 4 a lane, each as kPlanes e5m2 rows (128-byte swizzled: t[n] of the block's first 8 or 16
+// rows, of those after them, ...), and its scale.  All at once: each is a chain of its own.  A NaN or an infinity leaves
+// NaN.
+template <int N, int TOK>
 __device__ __forceinline__ void split_blocks(const uint2 (&raw)[N], uint8_t* const (&tile)[N], const int (&t)[N], float* const (&scale)[N])
 {
     const int lane = threadIdx.x & 31;
     uint32_t top[N];
 #pragma unroll
     for (int n = 0; n < N; ++n) {
-        // the larger of two magnitudes, as whole numbers: NaN above infinity above the others
+        // the larger of two magnitudes, as whole numbers
         const uint32_t a = raw[n].x & 0x7fff7fffu, b = raw[n].y & 0x7fff7fffu;
         top[n] = max(max(a & 0xffffu, a >> 16), max(b & 0xffffu, b >> 16));
     }
@@ -307,30 +328,22 @@ __device__ __forceinline__ void split_blocks(const uint2 (&raw)[N], uint8_t* con
         top[n] = __reduce_max_sync(0xffffffffu, top[n]);
 #pragma unroll
     for (int n = 0; n < N; ++n) {
-        // 2^(7 - e) of the largest's exponent e, within fp32's powers of two for it and its inverse
+        // 2^(15 - e) of the largest's exponent e, within fp32's powers of two for it and its inverse
         const uint32_t e = min(max(top[n] >> 7, 20u), 254u);
-        const float f = __uint_as_float((261u - e) << 23);
-        float w[4] = {__uint_as_float(raw[n].x << 16), __uint_as_float(raw[n].x & 0xffff0000u), __uint_as_float(raw[n].y << 16),
-                      __uint_as_float(raw[n].y & 0xffff0000u)};
-        if (top[n] >= 0x7f80u) {  // infinity as NaN: e4m3 has none
+        const float f = __uint_as_float((269u - e) << 23);
+        uint32_t h0 = f16x2(__uint_as_float(raw[n].x << 16) * f, __uint_as_float(raw[n].x & 0xffff0000u) * f);
+        uint32_t h1 = f16x2(__uint_as_float(raw[n].y << 16) * f, __uint_as_float(raw[n].y & 0xffff0000u) * f);
+        uint8_t* const at = tile[n] + t[n] * kBlock + (((lane >> 2) ^ (t[n] & 7)) << 4) + ((lane & 3) << 2);
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                if ((__float_as_uint(w[j]) & 0x7fffffffu) >= 0x7f800000u)
-                    w[j] = __uint_as_float(0x7fffffffu);
+        for (int p = 0; p < kPlanes; ++p) {
+            *reinterpret_cast<uint32_t*>(at + p * TOK * kBlock) = __byte_perm(h0, h1, 0x7531);  // the upper bytes
+            if (p + 1 < kPlanes) {
+                h0 = left8(h0);
+                h1 = left8(h1);
+            }
         }
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            w[j] *= f;
-        const uint32_t u0 = e4m3x2(w[0], w[1]), u1 = e4m3x2(w[2], w[3]);
-        const float2 r0 = from_e4m3x2(u0), r1 = from_e4m3x2(u1);
-        const uint32_t l0 = e4m3x2((w[0] - r0.x) * 16.f, (w[1] - r0.y) * 16.f);
-        const uint32_t l1 = e4m3x2((w[2] - r1.x) * 16.f, (w[3] - r1.y) * 16.f);
-        uint8_t* const at = tile[n] + 2 * t[n] * kBlock + ((lane & 3) << 2);
-        const int chunk = lane >> 2, swizzle = 2 * t[n] & 7;
-        *reinterpret_cast<uint32_t*>(at + ((chunk ^ swizzle) << 4)) = u0 | u1 << 16;
-        *reinterpret_cast<uint32_t*>(at + kBlock + ((chunk ^ (swizzle + 1)) << 4)) = l0 | l1 << 16;
         if (lane == 0)
-            *scale[n] = __uint_as_float((e - 7u) << 23);
+            *scale[n] = __uint_as_float((e - 15u) << 23);
     }
 }
 
@@ -339,7 +352,7 @@ struct Shared {
     uint64_t full[kMaxStages], done[kMaxStages], freed[kMaxStages];  // of a stage: copied; multiplied; added up
     uint32_t tmem;
     int abort_flag;
-    alignas(16) float scales[MODE == GEMM ? 1 : kMaxStages][kPair][NC / 2];  // of a stage's columns; read four at a time
+    alignas(16) float scales[MODE == GEMM ? 1 : kMaxStages][kPair][tokens_of(MODE, NC)];  // of a stage's columns; read four at a time
     Lists lists[MODE == GEMM ? 0 : 1];
 };
 
@@ -407,12 +420,14 @@ __global__ void __launch_bounds__(threads_of(MODE), 1)
 {
     using Sh = Shared<MODE, NC>;
     constexpr int kThreads = threads_of(MODE);
-    constexpr int TOK = MODE == GEMM ? NC : NC / 2;  // tokens of a pass
-    constexpr uint32_t kXBytes = NC * kBlock;        // of tokens in a block of a stage
-    constexpr uint32_t kTmem = (uint32_t)(stages_of(NC) * kPair * NC);
+    constexpr int TOK = tokens_of(MODE, NC), kPlane = MODE == GEMM ? 1 : kPlanes;
+    constexpr uint32_t kXBytes = x_rows_of(MODE, NC) * kBlock;  // of tokens in a block of a stage
+    constexpr int kAcc = acc_columns(NC);
+    constexpr uint32_t kTmem = 512;
     extern __shared__ __align__(1024) uint8_t smem[];
     // The 128-byte swizzle repeats every 1024 bytes: stages start on 1024.  (An MMA reads 128 rows of weights whatever
-    // the tile has: past them, and past the ring's end, lie other bytes of this CTA, whose sums nothing uses.)
+    // the tile has, and NC of tokens: past them, and past the rings' ends, lie other bytes of this CTA, whose sums
+    // nothing uses.)
     uint8_t* const ring = smem + ((1024u - (smem_u32(smem) & 1023u)) & 1023u);
     uint8_t* const x_ring = ring + (size_t)a.stages * kPair * a.w_bytes;
     Sh& sh = *reinterpret_cast<Sh*>(x_ring + (size_t)a.stages * kPair * kXBytes);
@@ -485,7 +500,7 @@ __global__ void __launch_bounds__(threads_of(MODE), 1)
 
     if (warp == 0) {
         // ---- MMAs
-        constexpr uint32_t idesc = instr_desc_e4m3(NC);
+        constexpr uint32_t idesc = instr_desc_e4m3(NC) | (MODE == GEMM ? 0u : kBIsE5m2);
         const uint32_t w_bytes = (uint32_t)a.w_bytes, ring_at = smem_u32(ring), x_at = smem_u32(x_ring);
         int slot = 0, use = 0;
         bool ok = true, ready = false;
@@ -499,13 +514,13 @@ __global__ void __launch_bounds__(threads_of(MODE), 1)
                 const bool full1 = mbar_ready(smem_u32(&sh.full[slot1]), (uint32_t)use1 & 1u);
                 asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
                 const uint32_t s0 = uniform((uint32_t)slot);
-                const uint32_t sa = ring_at + s0 * kPair * w_bytes, sb = x_at + s0 * kPair * kXBytes, d = tmem + s0 * kPair * NC;
+                const uint32_t sa = ring_at + s0 * kPair * w_bytes, sb = x_at + s0 * kPair * kXBytes, d = tmem + s0 * kPair * kAcc;
                 if (elect_one()) {
 #pragma unroll
                     for (int p = 0; p < kPair; ++p)
 #pragma unroll
                         for (int i = 0; i < kBlock / 32; ++i)  // K = 32 an MMA: 32 bytes along the swizzled row
-                            umma_e4m3(d + p * NC, desc_at(sa + p * w_bytes + 32 * i), desc_at(sb + p * kXBytes + 32 * i), idesc, i > 0);
+                            umma_e4m3(d + p * kAcc, desc_at(sa + p * w_bytes + 32 * i), desc_at(sb + p * kXBytes + 32 * i), idesc, i > 0);
                     umma_commit(smem_u32(&sh.done[0]) + 8 * s0);
                 }
                 ready = __all_sync(0xffffffffu, full1);
@@ -641,42 +656,60 @@ __global__ void __launch_bounds__(threads_of(MODE), 1)
                     break;
                 asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
                 const int slot1 = slot + 1 == a.stages ? 0 : slot + 1, use1 = use + (slot1 == 0);
-                float d[kPair * NC], sx[kPair][TOK];
-                if (mine) {
+                // Both blocks at once or, where registers do not suffice (16 tokens of fp8_moe), one after the other.
+                constexpr int R = TOK * kPlane, kAtOnce = kPair * R <= 64 ? kPair : 1;
 #pragma unroll
-                    for (int c = 0; c < kPair * NC; c += 16)
-                        tmem_load16(t_addr + slot * kPair * NC + c, d + c);
+                for (int p0 = 0; p0 < kPair; p0 += kAtOnce) {
+                    float d[kAtOnce * R], sx[kAtOnce][TOK];
+                    if (mine) {
 #pragma unroll
-                    for (int p = 0; p < kPair; ++p) {
-                        const float* px = MODE == GEMM ? xs + (k * kPair + p) * NC : sh.scales[slot][p];
+                        for (int p = 0; p < kAtOnce; ++p) {
+                            const uint32_t from = t_addr + slot * kPair * kAcc + (p0 + p) * kAcc;
 #pragma unroll
-                        for (int t = 0; t < TOK; t += 4) {
-                            if (MODE != GEMM && t >= n_tok)
-                                break;
-                            const float4 v = *reinterpret_cast<const float4*>(px + t);
-                            sx[p][t] = v.x, sx[p][t + 1] = v.y, sx[p][t + 2] = v.z, sx[p][t + 3] = v.w;
+                            for (int c = 0; c < R; c += 16)
+                                if (c + 16 <= R)
+                                    tmem_load16(from + c, d + p * R + c);
+                                else
+                                    tmem_load8(from + c, d + p * R + c);
+                        }
+#pragma unroll
+                        for (int p = 0; p < kAtOnce; ++p) {
+                            const float* px = MODE == GEMM ? xs + (k * kPair + p0 + p) * NC : sh.scales[slot][p0 + p];
+#pragma unroll
+                            for (int t = 0; t < TOK; t += 4) {
+                                if (MODE != GEMM && t >= n_tok)
+                                    break;
+                                const float4 v = *reinterpret_cast<const float4*>(px + t);
+                                sx[p][t] = v.x, sx[p][t + 1] = v.y, sx[p][t + 2] = v.z, sx[p][t + 3] = v.w;
+                            }
                         }
                     }
-                }
-                const bool done1 = mbar_ready(smem_u32(&sh.done[slot1]), (uint32_t)use1 & 1u);
-                const bool full1 = mbar_ready(smem_u32(&sh.full[slot1]), (uint32_t)use1 & 1u);
-                settle(d);
-                asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-                ready = __all_sync(0xffffffffu, done1 && full1);
-                if (lane == 0)
-                    mbar_arrive(smem_u32(&sh.freed[slot]));
-                if (mine) {
+                    bool done1 = false, full1 = false;
+                    if (p0 + kAtOnce == kPair) {
+                        done1 = mbar_ready(smem_u32(&sh.done[slot1]), (uint32_t)use1 & 1u);
+                        full1 = mbar_ready(smem_u32(&sh.full[slot1]), (uint32_t)use1 & 1u);
+                    }
+                    settle(d);
+                    if (p0 + kAtOnce == kPair) {
+                        asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+                        ready = __all_sync(0xffffffffu, done1 && full1);
+                        if (lane == 0)
+                            mbar_arrive(smem_u32(&sh.freed[slot]));
+                    }
+                    if (mine) {
 #pragma unroll
-                    for (int p = 0; p < kPair; ++p)
+                        for (int p = 0; p < kAtOnce; ++p)
 #pragma unroll
-                        for (int t = 0; t < TOK; ++t) {
-                            if (MODE != GEMM && (t & 3) == 0 && t >= n_tok)
-                                break;
-                            if (MODE == GEMM)
-                                acc[t] = fmaf(d[p * NC + t], w[p] * sx[p][t], acc[t]);
-                            else  // columns 2t and 2t + 1 are token t's upper and lower part
-                                acc[t] = fmaf(fmaf(d[p * NC + 2 * t + 1], 0.0625f, d[p * NC + 2 * t]), w[p] * sx[p][t], acc[t]);
-                        }
+                            for (int t = 0; t < TOK; ++t) {
+                                if (MODE != GEMM && (t & 3) == 0 && t >= n_tok)
+                                    break;
+                                const float f = w[p0 + p] * sx[p][t], *v = d + p * R + t;
+                                if (MODE == GEMM)
+                                    acc[t] = fmaf(v[0], f, acc[t]);
+                                else
+                                    acc[t] = fmaf(fmaf(fmaf(v[MODE == GEMM ? 0 : 2 * TOK], 0.125f, v[MODE == GEMM ? 0 : TOK]), 0.125f, v[0]), f, acc[t]);
+                            }
+                    }
                 }
                 slot = slot1;
                 use = use1;
@@ -798,7 +831,7 @@ __global__ void __launch_bounds__(threads_of(MODE), 1)
                     t[i] = sw + i / kPair * kSplitWarps;
                     scale[i] = &sh.scales[slot][i % kPair][t[i]];
                 }
-                split_blocks<N * kPair>(raw, tiles, t, scale);
+                split_blocks<N * kPair, TOK>(raw, tiles, t, scale);
             };
             if (n_now == 1)
                 split(std::integral_constant<int, 1>{});
@@ -933,10 +966,12 @@ cudaError_t launch_stream(StreamArgs a, const void* W, const void* x, const Devi
     const size_t rest = (sizeof(Sh) + 127) / 128 * 128 + (MODE == DOWN || S > 1 ? (size_t)(a.m + S - 1) * kRowsMax * 4 : 0) +
                         (MODE == GEMM ? (size_t)a.pairs * kPair * NC * 4 : 0);
     const size_t past = (size_t)(kRowsMax * kBlock - a.w_bytes);  // what an MMA may read behind the last stage
-    const size_t stage = (size_t)kPair * (a.w_bytes + NC * kBlock), room = (size_t)di.smem_optin - 1024;
+    constexpr size_t kXBytes = (size_t)x_rows_of(MODE, NC) * kBlock;
+    static_assert(sizeof(Sh) >= NC * kBlock - kXBytes, "an MMA reads so much behind the last stage's tokens");
+    const size_t stage = kPair * (a.w_bytes + kXBytes), room = (size_t)di.smem_optin - 1024;
     a.stages = (int)std::min<size_t>(stages_of(NC), rest < room ? (room - rest) / stage : 0);
     size_t bytes = (size_t)a.stages * stage + rest;
-    if ((size_t)a.stages * kPair * NC * kBlock + rest < past)
+    if (a.stages * kPair * kXBytes + rest < past)
         bytes = (size_t)a.stages * kPair * a.w_bytes + past;
     if (a.stages < 2 || bytes > room)
         return cudaErrorInvalidConfiguration;
@@ -1043,10 +1078,10 @@ cudaError_t launch_fp8_moe(const Fp8Moe& p, cudaStream_t s)
     // 8 tokens a pass, 16 where experts, about evenly chosen, often have more
     const double mean = (double)p.m * p.topk / p.E;
     const bool many = std::min<double>((double)p.m, mean + 2 * std::sqrt(mean)) > 8;
-    cudaError_t e = many ? launch_stream<UP, 32>(up, p.gate_up, nullptr, s) : launch_stream<UP, 16>(up, p.gate_up, nullptr, s);
+    cudaError_t e = many ? launch_stream<UP, 48>(up, p.gate_up, nullptr, s) : launch_stream<UP, 32>(up, p.gate_up, nullptr, s);
     if (e != cudaSuccess)
         return e;
-    return many ? launch_stream<DOWN, 32>(down, p.down, nullptr, s) : launch_stream<DOWN, 16>(down, p.down, nullptr, s);
+    return many ? launch_stream<DOWN, 48>(down, p.down, nullptr, s) : launch_stream<DOWN, 32>(down, p.down, nullptr, s);
 }
 
 cudaError_t fp8_stream_error_word(int32_t* out, bool clear)
