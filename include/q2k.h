@@ -625,13 +625,15 @@ size_t fp8_moe_workspace_bytes(int64_t m, int64_t topk, int64_t dim, int64_t int
  *   y         y_type [m, dim], rows ldy apart:  y[t] = sum over j of
  *             route_w[t, j] * (down_e h),  h = g / (1 + e^-g) * u,
  *             g = gate_e x_t,  u = up_e x_t,  e = ids[t, j]
- * Products accumulate in fp32 as in fp8_gemm.  x enters as it is (bf16), h
- * rounded to bf16: both are split into e5m2 numbers beside a power of two for
- * each 128 values, exact where a value is within 2^-30 of the largest of its
- * 128, and off by less than 2^-37 of that largest below.  The sum over j is
- * fp32, by rising expert; rounded once to bf16 where y is bf16.  A call
- * repeats bit for bit.  A token with a NaN or an infinity, or whose h
- * is past bf16's range, gives NaN.
+ * Products accumulate in fp32 as in fp8_gemm.  x enters as it is (bf16)
+ * where it is within 2^-30 of the largest of its 128 values, and off by less
+ * than 2^-37 of that largest below.  h is fp32 up to the second product, which
+ * it enters rounded to fp16 beside a power of two for each 128 values: 11 bits
+ * where it is within 2^-28 of the largest of them, off by at most 2^-39 of that
+ * largest below; h is zero where e^-g is past fp32's range.  The sum over j is
+ * fp32, by rising expert; rounded once to bf16 where y is bf16.  A call repeats
+ * bit for bit.  A token with a NaN or an infinity, or whose h is past fp32's
+ * range, gives NaN.
  *   workspace  at least fp8_moe_workspace_bytes(m, topk, dim, inter) bytes,
  *              256-byte aligned; calls that overlap need one each
  * 0 <= m <= 128, 1 <= topk <= 32, m * topk <= 1024, 1 <= E <= 1024, dim and

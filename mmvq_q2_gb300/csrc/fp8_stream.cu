@@ -6,7 +6,7 @@
 // up to 128 rows into a ring of shared-memory stages (tensor copies, 128-byte
 // swizzled; a warp takes 390 cycles from one stage's copy to the next's, so
 // one alone was the bound), another issues tcgen05.mma kind::f8f6f4 on them as
-// they are, weight rows as M = 128, tokens as N = 16 to 48 columns.  The scales
+// they are, weight rows as M = 128, tokens as N = 16 to 64 columns.  The scales
 // change every 128 values of K, so each block of a stage has an accumulator of
 // its own in tensor memory, and four warps read them back, scale them and add
 // them up in fp32, a thread a row; that frees the stage.  (mma.sync, eight warps at the same
@@ -25,15 +25,18 @@
 // turn, so that the sum over a token's experts stays with the cluster.  (Joined
 // by whoever finished a tile last, the fences alone took 10000 cycles an item.)
 //
-// bf16 tokens (fp8_moe) enter as three columns of e5m2 each: with a power of
-// two that brings a block's largest below 2^16, a value is an fp16 number,
-// whose upper byte is an e5m2 one; what is left, times 8, is the next, and
-// once more.  Together they are the bf16 value exactly, where it is within
-// 2^-30 of the block's largest (and off by less than 2^-37 of that below).
-// (Two columns of e4m3 are exact within 2^-13 alone; with two more for the
-// blocks that need them, as many of h's do, 32 tokens of 8 experts took 117 us
-// where these take 61.)  Four warps write them into the stages, every fourth
-// token each, the next stage's values on their way.
+// Tokens of fp8_moe enter as columns of e5m2: with a power of two that brings
+// a block's largest below 2^16, a bf16 value is an fp16 number, whose upper
+// byte is an e5m2 one; what is left, times 8, is the next, and once more.
+// Together the three are the bf16 value exactly, where it is within 2^-30 of
+// the block's largest (and off by less than 2^-37 of that below).  (Two columns
+// of e4m3 are exact within 2^-13 alone; with two more for the blocks that need
+// them, as many of h's do, 32 tokens of 8 experts took 117 us where these take
+// 61.)  h, which is fp32 between the launches, enters as four: rounded to fp16
+// beside the power of two, that number exactly.  (In bf16 and three, as x, its
+// rounding was off as far as that of y to bf16 is, and the experts of one token
+// took 40.6 us where they take 40.0.)  Four warps write the columns into the
+// stages, every fourth token each, the next stage's values on their way.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -57,7 +60,6 @@ constexpr int kPair = 2;       // such blocks in a stage
 constexpr int kUnit = 16;      // UP: rows of gate, and of up, in a unit
 constexpr int kMaxStages = 16;
 constexpr int kCopyWarps = 3, kSplitWarps = 4;
-constexpr int kPlanes = 3;     // columns that a bf16 token enters as
 constexpr int kMaxPairs = 1024, kMaxExperts = 1024;
 
 enum Mode : int { GEMM = 0, UP = 1, DOWN = 2 };
@@ -65,9 +67,10 @@ enum Mode : int { GEMM = 0, UP = 1, DOWN = 2 };
 // Warps: one for the MMAs, three for copies, four that add up (tensor memory lanes by warp % 4), four for columns.
 constexpr int threads_of(int mode) { return mode == GEMM ? 256 : 384; }
 
-// Tokens of a pass, and rows of them in a block of a stage.
-constexpr int tokens_of(int mode, int columns) { return mode == GEMM ? columns : columns / kPlanes / 8 * 8; }
-constexpr int x_rows_of(int mode, int columns) { return mode == GEMM ? columns : kPlanes * tokens_of(mode, columns); }
+// Columns that a token enters as; tokens of a pass, and rows of them in a block of a stage.
+constexpr int planes_of(int mode) { return mode == GEMM ? 1 : mode == UP ? 3 : 4; }
+constexpr int tokens_of(int mode, int columns) { return mode == GEMM ? columns : columns / planes_of(mode) / 8 * 8; }
+constexpr int x_rows_of(int mode, int columns) { return planes_of(mode) * tokens_of(mode, columns); }
 
 // Columns of tensor memory that an accumulator is given, and stages that have theirs in its 512.
 constexpr int acc_columns(int columns) { return columns <= 32 ? columns : 64; }
@@ -86,12 +89,12 @@ struct StreamArgs {
     const float* x_scales;
     int64_t ld_xs;
     // fp8_moe
-    const uint16_t* xb;       // bf16 rows: tokens (UP) or h of the pairs (DOWN)
+    const uint16_t* xb;       // UP: tokens, bf16 rows
     int64_t ldx;
     const int32_t* ids;
     const float* route_w;
     int topk, E;
-    uint16_t* h;              // [pairs, inter]
+    float* h;                 // [pairs, inter]
     // results
     void* y;
     int64_t ldy;
@@ -169,10 +172,8 @@ __device__ __forceinline__ float load_peer(uint32_t addr, uint32_t rank)
 
 // The experts that have a token, as passes of up to CAP (token, choice) pairs.
 struct Lists {
-    alignas(16) int ids[kMaxPairs];
-    uint16_t rank[kMaxPairs], list[kMaxPairs];                         // pairs by expert, in order
+    uint16_t list[kMaxPairs];                                              // pairs by expert, in order
     uint16_t v_expert[kMaxPairs], v_first[kMaxPairs], v_count[kMaxPairs];  // passes
-    alignas(16) uint16_t count[kMaxExperts];
     uint16_t token[kMaxPairs];  // of list's entries, and their weights
     float weight[kMaxPairs];
     int passes;
@@ -185,29 +186,36 @@ struct Lists {
     }
 };
 
+// What they are made with, where the first stage's columns are written later.
+struct ListScratch {
+    alignas(16) int ids[kMaxPairs];
+    alignas(16) uint16_t count[kMaxExperts];
+    uint16_t rank[kMaxPairs];
+};
+
 constexpr int kFewPairs = 256;
 
 // The lists of up to 256 pairs: a pair's place is the number of pairs before it, by expert and then by pair, which each
 // thread counts for itself; likewise a pass's.  (2.2 us with the other way, for 8 pairs of 256 experts.)
 template <int kThreads>
-__device__ __forceinline__ void build_few_lists(Lists& l, const StreamArgs& a, int cap)
+__device__ __forceinline__ void build_few_lists(Lists& l, ListScratch& s, const StreamArgs& a, int cap)
 {
     static_assert(kThreads >= kFewPairs, "a thread a pair");
     constexpr int kNone = 0x7fffffff;
-    int* const starts = reinterpret_cast<int*>(l.count);  // the expert where a pair starts a pass
+    int* const starts = reinterpret_cast<int*>(s.count);  // the expert where a pair starts a pass
     const int pairs = a.m * a.topk, i = threadIdx.x, whole = (pairs + 3) & ~3;
     int e = kNone;
     if (i < whole) {
         if (i < pairs)
             e = a.ids[i];
         e = e >= 0 && e < a.E ? e : kNone;
-        l.ids[i] = e;
+        s.ids[i] = e;
     }
     __syncthreads();
     int place = 0, before = 0, same = 0;
     if (i < whole) {
         for (int j = 0; j < whole; j += 4) {
-            const int4 v = *reinterpret_cast<const int4*>(l.ids + j);
+            const int4 v = *reinterpret_cast<const int4*>(s.ids + j);
             const int o[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
@@ -243,29 +251,29 @@ __device__ __forceinline__ void build_few_lists(Lists& l, const StreamArgs& a, i
 
 // By all threads; ends with a barrier.
 template <int kThreads>
-__device__ void build_lists(Lists& l, const StreamArgs& a, int cap)
+__device__ void build_lists(Lists& l, ListScratch& s, const StreamArgs& a, int cap)
 {
     const int pairs = a.m * a.topk, tid = threadIdx.x;
     if (pairs <= kFewPairs)
-        return build_few_lists<kThreads>(l, a, cap);
+        return build_few_lists<kThreads>(l, s, a, cap);
     for (int i = tid; i < a.E; i += kThreads)
-        l.count[i] = 0;
+        s.count[i] = 0;
     for (int i = tid; i < pairs; i += kThreads)
-        l.ids[i] = a.ids[i];
+        s.ids[i] = a.ids[i];
     __syncthreads();
     if (tid < 32) {
         // a pair's place among those of its expert, 32 pairs at a time
         for (int i0 = 0; i0 < pairs; i0 += 32) {
             const int i = i0 + tid;
-            const int e = i < pairs ? l.ids[i] : -1;
+            const int e = i < pairs ? s.ids[i] : -1;
             const bool valid = e >= 0 && e < a.E;
             const uint32_t same = __match_any_sync(0xffffffffu, valid ? e : -1);
-            const int before = valid ? l.count[e] : 0;
+            const int before = valid ? s.count[e] : 0;
             __syncwarp();
             if (valid) {
-                l.rank[i] = (uint16_t)(before + __popc(same & ((1u << tid) - 1u)));
+                s.rank[i] = (uint16_t)(before + __popc(same & ((1u << tid) - 1u)));
                 if ((same >> tid) == 1u)  // the last of them
-                    l.count[e] = (uint16_t)(before + __popc(same));
+                    s.count[e] = (uint16_t)(before + __popc(same));
             }
             __syncwarp();
         }
@@ -273,8 +281,8 @@ __device__ void build_lists(Lists& l, const StreamArgs& a, int cap)
         const int run = (a.E + 31) / 32, e0 = tid * run, e1 = min(a.E, e0 + run);
         int n = 0, v = 0;
         for (int e = e0; e < e1; ++e) {
-            n += l.count[e];
-            v += (l.count[e] + cap - 1) / cap;
+            n += s.count[e];
+            v += (s.count[e] + cap - 1) / cap;
         }
         int n_at = n, v_at = v;
 #pragma unroll
@@ -290,8 +298,8 @@ __device__ void build_lists(Lists& l, const StreamArgs& a, int cap)
         n_at -= n;
         v_at -= v;
         for (int e = e0; e < e1; ++e) {
-            const int c = l.count[e];
-            l.count[e] = (uint16_t)n_at;  // from here on the expert's first place
+            const int c = s.count[e];
+            s.count[e] = (uint16_t)n_at;  // from here on the expert's first place
             for (int at = 0; at < c; at += cap, ++v_at) {
                 l.v_expert[v_at] = (uint16_t)e;
                 l.v_first[v_at] = (uint16_t)(n_at + at);
@@ -302,48 +310,63 @@ __device__ void build_lists(Lists& l, const StreamArgs& a, int cap)
     }
     __syncthreads();
     for (int i = tid; i < pairs; i += kThreads) {
-        const int e = l.ids[i];
+        const int e = s.ids[i];
         if (e >= 0 && e < a.E)
-            l.put(a, l.count[e] + l.rank[i], i);
+            l.put(a, s.count[e] + s.rank[i], i);
     }
     __syncthreads();
 }
 
-// N blocks of 128 bf16 values, 4 a lane, each as kPlanes e5m2 rows (128-byte swizzled: t[n] of the block's first 8 or 16
-// rows, of those after them, ...), and its scale.  All at once: each is a chain of its own.  A NaN or an infinity leaves
-// NaN.
-template <int N, int TOK>
-__device__ __forceinline__ void split_blocks(const uint2 (&raw)[N], uint8_t* const (&tile)[N], const int (&t)[N], float* const (&scale)[N])
+// A lane's four values of a block: bf16 of a token, fp32 of h.
+template <int MODE>
+using Raw = std::conditional_t<MODE == DOWN, uint4, uint2>;
+
+// N blocks of 128 values, 4 a lane, each as e5m2 rows (128-byte swizzled: t[n] of the block's first TOK rows, of those after
+// them, ...), and its scale.  All at once: each is a chain of its own.  A NaN or an infinity leaves NaN.
+template <int MODE, int N, int TOK>
+__device__ __forceinline__ void split_blocks(const Raw<MODE> (&raw)[N], uint8_t* const (&tile)[N], const int (&t)[N], float* const (&scale)[N])
 {
     const int lane = threadIdx.x & 31;
+    // The exponent that the block's largest has at most: h's rounding to fp16 may carry into the next.
+    constexpr uint32_t kTop = MODE == DOWN ? 14 : 15;
     uint32_t top[N];
 #pragma unroll
     for (int n = 0; n < N; ++n) {
-        // the larger of two magnitudes, as whole numbers
-        const uint32_t a = raw[n].x & 0x7fff7fffu, b = raw[n].y & 0x7fff7fffu;
-        top[n] = max(max(a & 0xffffu, a >> 16), max(b & 0xffffu, b >> 16));
+        // the largest magnitude, as a whole number
+        if constexpr (MODE == DOWN) {
+            top[n] = max(max(raw[n].x & 0x7fffffffu, raw[n].y & 0x7fffffffu), max(raw[n].z & 0x7fffffffu, raw[n].w & 0x7fffffffu));
+        } else {
+            const uint32_t a = raw[n].x & 0x7fff7fffu, b = raw[n].y & 0x7fff7fffu;
+            top[n] = max(max(a & 0xffffu, a >> 16), max(b & 0xffffu, b >> 16)) << 16;
+        }
     }
 #pragma unroll
     for (int n = 0; n < N; ++n)
         top[n] = __reduce_max_sync(0xffffffffu, top[n]);
 #pragma unroll
     for (int n = 0; n < N; ++n) {
-        // 2^(15 - e) of the largest's exponent e, within fp32's powers of two for it and its inverse
-        const uint32_t e = min(max(top[n] >> 7, 20u), 254u);
-        const float f = __uint_as_float((269u - e) << 23);
-        uint32_t h0 = f16x2(__uint_as_float(raw[n].x << 16) * f, __uint_as_float(raw[n].x & 0xffff0000u) * f);
-        uint32_t h1 = f16x2(__uint_as_float(raw[n].y << 16) * f, __uint_as_float(raw[n].y & 0xffff0000u) * f);
+        // 2^(kTop - e) of the largest's exponent e, within fp32's powers of two for it and its inverse
+        const uint32_t e = min(max(top[n] >> 23, 20u), 254u);
+        const float f = __uint_as_float((254u + kTop - e) << 23);
+        uint32_t h0, h1;
+        if constexpr (MODE == DOWN) {
+            h0 = f16x2(__uint_as_float(raw[n].x) * f, __uint_as_float(raw[n].y) * f);
+            h1 = f16x2(__uint_as_float(raw[n].z) * f, __uint_as_float(raw[n].w) * f);
+        } else {
+            h0 = f16x2(__uint_as_float(raw[n].x << 16) * f, __uint_as_float(raw[n].x & 0xffff0000u) * f);
+            h1 = f16x2(__uint_as_float(raw[n].y << 16) * f, __uint_as_float(raw[n].y & 0xffff0000u) * f);
+        }
         uint8_t* const at = tile[n] + t[n] * kBlock + (((lane >> 2) ^ (t[n] & 7)) << 4) + ((lane & 3) << 2);
 #pragma unroll
-        for (int p = 0; p < kPlanes; ++p) {
+        for (int p = 0; p < planes_of(MODE); ++p) {
             *reinterpret_cast<uint32_t*>(at + p * TOK * kBlock) = __byte_perm(h0, h1, 0x7531);  // the upper bytes
-            if (p + 1 < kPlanes) {
+            if (p + 1 < planes_of(MODE)) {
                 h0 = left8(h0);
                 h1 = left8(h1);
             }
         }
         if (lane == 0)
-            *scale[n] = __uint_as_float((e - 15u) << 23);
+            *scale[n] = __uint_as_float((e - kTop) << 23);
     }
 }
 
@@ -420,7 +443,7 @@ __global__ void __launch_bounds__(threads_of(MODE), 1)
 {
     using Sh = Shared<MODE, NC>;
     constexpr int kThreads = threads_of(MODE);
-    constexpr int TOK = tokens_of(MODE, NC), kPlane = MODE == GEMM ? 1 : kPlanes;
+    constexpr int TOK = tokens_of(MODE, NC), kPlane = planes_of(MODE);
     constexpr uint32_t kXBytes = x_rows_of(MODE, NC) * kBlock;  // of tokens in a block of a stage
     constexpr int kAcc = acc_columns(NC);
     constexpr uint32_t kTmem = 512;
@@ -467,7 +490,7 @@ __global__ void __launch_bounds__(threads_of(MODE), 1)
     asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
     int passes = 1;
     if constexpr (MODE != GEMM) {
-        build_lists<kThreads>(sh.lists[0], a, TOK);
+        build_lists<kThreads>(sh.lists[0], *reinterpret_cast<ListScratch*>(x_ring), a, TOK);
         passes = sh.lists[0].passes;
     } else {
         __syncthreads();
@@ -704,10 +727,11 @@ __global__ void __launch_bounds__(threads_of(MODE), 1)
                                 if (MODE != GEMM && (t & 3) == 0 && t >= n_tok)
                                     break;
                                 const float f = w[p0 + p] * sx[p][t], *v = d + p * R + t;
-                                if (MODE == GEMM)
-                                    acc[t] = fmaf(v[0], f, acc[t]);
-                                else
-                                    acc[t] = fmaf(fmaf(fmaf(v[MODE == GEMM ? 0 : 2 * TOK], 0.125f, v[MODE == GEMM ? 0 : TOK]), 0.125f, v[0]), f, acc[t]);
+                                float all = v[(kPlane - 1) * TOK];
+#pragma unroll
+                                for (int c = kPlane - 2; c >= 0; --c)
+                                    all = fmaf(all, 0.125f, v[c * TOK]);
+                                acc[t] = fmaf(all, f, acc[t]);
                             }
                     }
                 }
@@ -733,7 +757,7 @@ __global__ void __launch_bounds__(threads_of(MODE), 1)
                     const float gate = acc[t], up = __shfl_down_sync(0xffffffffu, acc[t], 16);
                     if (q < piece.units && lane < 16 && row < a.rows) {
                         const float hv = __fdiv_rn(gate, 1.0f + expf(-gate)) * up;
-                        a.h[(int64_t)l.list[l.v_first[piece.pass] + t] * a.rows + row] = __bfloat16_as_ushort(__float2bfloat16_rn(hv));
+                        a.h[(int64_t)l.list[l.v_first[piece.pass] + t] * a.rows + row] = hv;
                     }
                 }
             } else {
@@ -771,19 +795,26 @@ __global__ void __launch_bounds__(threads_of(MODE), 1)
         if (MODE == DOWN)
             pdl_wait();
         const int sw = warp - 8;
-        const int64_t ld = MODE == UP ? a.ldx : a.K;
-        const bool wide = (reinterpret_cast<uintptr_t>(a.xb) & 7u) == 0 && ld % 4 == 0;
-        auto load4 = [&](const uint16_t* row, int k) {  // four values from lane * 4 on; zeros past K
+        const bool wide = (reinterpret_cast<uintptr_t>(a.xb) & 7u) == 0 && a.ldx % 4 == 0;
+        using R4 = Raw<MODE>;
+        using Value = std::conditional_t<MODE == UP, uint16_t, float>;
+        auto load4 = [&](const Value* row, int k) {  // four values from lane * 4 on; zeros past K
+            R4 r{};
             if (k + lane * 4 >= a.K)
-                return make_uint2(0u, 0u);
-            const uint16_t* const v = row + k;
-            return wide ? *reinterpret_cast<const uint2*>(v)
-                        : make_uint2(v[0] | (uint32_t)v[1] << 16, v[2] | (uint32_t)v[3] << 16);
+                return r;
+            const Value* const v = row + k;
+            if constexpr (MODE == DOWN)  // (rows of h are whole 64 bytes)
+                r = *reinterpret_cast<const uint4*>(v);
+            else if (wide)
+                r = *reinterpret_cast<const uint2*>(v);
+            else
+                r = make_uint2(v[0] | (uint32_t)v[1] << 16, v[2] | (uint32_t)v[3] << 16);
+            return r;
         };
         // Every fourth token of a stage is this warp's; the next stage's values are on their way.
         constexpr int G = TOK / kSplitWarps;
-        const uint16_t* row[G] = {};
-        uint2 ahead[G][kPair];
+        const Value* row[G] = {};
+        R4 ahead[G][kPair];
         int pass = -1, count = 0;
         auto fetch = [&]() {
             if (work.pass != pass) {
@@ -793,21 +824,24 @@ __global__ void __launch_bounds__(threads_of(MODE), 1)
                 for (int g = 0; g < G; ++g)
                     if (g < count) {
                         const int at = l.v_first[pass] + sw + g * kSplitWarps;
-                        row[g] = a.xb + (int64_t)(MODE == UP ? l.token[at] : l.list[at]) * ld + lane * 4;
+                        if constexpr (MODE == UP)
+                            row[g] = a.xb + (int64_t)l.token[at] * a.ldx + lane * 4;
+                        else
+                            row[g] = a.h + (int64_t)l.list[at] * a.K + lane * 4;
                     }
             }
 #pragma unroll
             for (int g = 0; g < G; ++g)
 #pragma unroll
                 for (int p = 0; p < kPair; ++p)
-                    ahead[g][p] = g < count ? load4(row[g], (work.k * kPair + p) * kBlock) : make_uint2(0u, 0u);
+                    ahead[g][p] = g < count ? load4(row[g], (work.k * kPair + p) * kBlock) : R4{};
         };
         bool live = work.next();
         if (live)
             fetch();
         int slot = 0, use = 0;
         while (live) {
-            uint2 now[G][kPair];
+            R4 now[G][kPair];
 #pragma unroll
             for (int i = 0; i < G * kPair; ++i)
                 now[i / kPair][i % kPair] = ahead[i / kPair][i % kPair];
@@ -820,7 +854,7 @@ __global__ void __launch_bounds__(threads_of(MODE), 1)
             uint8_t* const tile = x_ring + slot * kPair * kXBytes;
             auto split = [&](auto tokens) {  // of so many tokens
                 constexpr int N = decltype(tokens)::value;
-                uint2 raw[N * kPair];
+                R4 raw[N * kPair];
                 uint8_t* tiles[N * kPair];
                 int t[N * kPair];
                 float* scale[N * kPair];
@@ -831,7 +865,7 @@ __global__ void __launch_bounds__(threads_of(MODE), 1)
                     t[i] = sw + i / kPair * kSplitWarps;
                     scale[i] = &sh.scales[slot][i % kPair][t[i]];
                 }
-                split_blocks<N * kPair, TOK>(raw, tiles, t, scale);
+                split_blocks<MODE, N * kPair, TOK>(raw, tiles, t, scale);
             };
             if (n_now == 1)
                 split(std::integral_constant<int, 1>{});
@@ -1046,7 +1080,7 @@ cudaError_t launch_fp8_gemm_stream(const Fp8Gemm& p, cudaStream_t s)
 
 size_t fp8_moe_workspace(int64_t m, int64_t topk, int64_t inter)
 {
-    return (size_t)(m * topk * inter * 2 + 255) / 256 * 256;
+    return (size_t)(m * topk * inter * 4 + 255) / 256 * 256;
 }
 
 cudaError_t launch_fp8_moe(const Fp8Moe& p, cudaStream_t s)
@@ -1057,7 +1091,7 @@ cudaError_t launch_fp8_moe(const Fp8Moe& p, cudaStream_t s)
     a.route_w = p.route_w;
     a.topk = p.topk;
     a.E = p.E;
-    a.h = static_cast<uint16_t*>(p.workspace);
+    a.h = static_cast<float*>(p.workspace);
     a.y = p.y;
     a.ldy = p.ldy;
     a.y_bf16 = p.y_bf16;
@@ -1073,7 +1107,6 @@ cudaError_t launch_fp8_moe(const Fp8Moe& p, cudaStream_t s)
     down.w_scales = p.down_scales;
     down.K = (int)p.inter;
     down.rows = (int)p.dim;
-    down.xb = a.h;
 
     // 8 tokens a pass, 16 where experts, about evenly chosen, often have more
     const double mean = (double)p.m * p.topk / p.E;
@@ -1081,7 +1114,7 @@ cudaError_t launch_fp8_moe(const Fp8Moe& p, cudaStream_t s)
     cudaError_t e = many ? launch_stream<UP, 48>(up, p.gate_up, nullptr, s) : launch_stream<UP, 32>(up, p.gate_up, nullptr, s);
     if (e != cudaSuccess)
         return e;
-    return many ? launch_stream<DOWN, 48>(down, p.down, nullptr, s) : launch_stream<DOWN, 32>(down, p.down, nullptr, s);
+    return many ? launch_stream<DOWN, 64>(down, p.down, nullptr, s) : launch_stream<DOWN, 32>(down, p.down, nullptr, s);
 }
 
 cudaError_t fp8_stream_error_word(int32_t* out, bool clear)

@@ -21,7 +21,7 @@ def largest(v):
     return top.repeat_interleave(128, 1)[:, :n]
 
 
-def want_of(x, ids, route_w, gate_up, gs, down, ds):
+def want_of(x, ids, route_w, gate_up, gs, down, ds, rounded=2.0 ** -8):
     E, _, inter, dim = gate_up.shape
     want, tol, size = (torch.zeros(x.shape, dtype=torch.float64, device=DEV) for _ in range(3))
     per_up, per_down = (128 + blocks(dim) + 8) * U, (128 + blocks(inter) + 8) * U
@@ -36,7 +36,7 @@ def want_of(x, ids, route_w, gate_up, gs, down, ds):
         s = g * torch.sigmoid(g)
         h = s * u
         dh = 1.1 * dg * u.abs() + s.abs() * du + 1.1 * dg * du
-        dh = dh + (h.abs() + dh) * (2.0 ** -8 + 2.0 ** -20) + TINY
+        dh = dh + (h.abs() + dh) * (rounded + 2.0 ** -20) + TINY
         w = down[e].double() * spread(ds[e], dim, inter)
         r = route_w[t, j].double()[:, None]
         want.index_add_(0, t, r * (h @ w.t()))
@@ -121,3 +121,14 @@ def test_moe_of_a_wide_block_beside_nan(lib):  # noqa: F811
     y = lib.fp8_moe(*args)
     assert torch.isnan(y[:2]).all()
     within(y[2:], want, tol)
+
+
+@pytest.mark.parametrize("m,E,topk,dim,inter", [(1, 1, 1, 256, 16), (5, 4, 2, 144, 16), (3, 2, 1, 512, 32), (20, 2, 2, 272, 16), (40, 1, 1, 128, 48),
+                                                (6, 8, 4, 1040, 16), (32, 64, 8, 4096, 16)])
+def test_moe_keeps_eleven_bits_of_h(lib, m, E, topk, dim, inter):  # noqa: F811
+    """Few h, so that what their rounding leaves does not average out."""
+    args = inputs(m + 7 * dim, m, E, topk, dim, inter)
+    args[4] /= dim ** 0.5
+    args[6] /= inter ** 0.5
+    want, tol = want_of(*args, rounded=2.0 ** -11)
+    within(lib.fp8_moe(*args), want, tol)
