@@ -316,7 +316,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                         for (int i = 0; i < kTK / 32; ++i)  // K = 32 an MMA: 32 bytes along the swizzled row
                             umma_e4m3(d, desc_at(sa + 32 * i), desc_at(sa + kXTile + 32 * i), idesc, i > 0);
-                        // (one commit, 115 cycles, tells both that the accumulator is full and that the stage is free)
+                        // One commit, 115 cycles, tells both that the accumulator is full and that the stage is free.
+                        // So there have to be as many stages as accumulators: block n + stages then waits for the
+                        // accumulator of block n or a later one to be read back, hence until all who add have seen
+                        // this stage's barrier turn; with fewer it could turn twice before they look.
                         umma_commit(smem_u32(&sh.done[0]) + 8 * s0);
                     }
                     __syncwarp();
@@ -474,6 +477,21 @@ bool encode_boxes(CUtensorMap* map, CUtensorMapDataType type, int size, const vo
                       CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// The shared memory that a block may have on the one kind of device that this library runs on.
+constexpr size_t kSharedBytes = 232448;
+
+constexpr size_t extra_bytes(int bn, int split)
+{
+    return 1024 + sizeof(GemmShared) + (split > 1 ? (size_t)bn * 512 : (size_t)kBoxes);
+}
+
+// Stages that fit into `bytes` of shared memory; 0 where they are fewer than the accumulators.
+constexpr int stages_in(size_t bytes, int bn, int split)
+{
+    const size_t extra = extra_bytes(bn, split), n = bytes < extra ? 0 : (bytes - extra) / (size_t)(kXTile + bn * kTK);
+    return n < (size_t)(512 / bn) ? 0 : n < (size_t)kMaxStages ? (int)n : kMaxStages;
+}
+
 template <int BN, int S>
 cudaError_t launch_tiles(GemmArgs a, const Fp8Gemm& p, const DeviceInfo& di, cudaStream_t s)
 {
@@ -485,8 +503,10 @@ cudaError_t launch_tiles(GemmArgs a, const Fp8Gemm& p, const DeviceInfo& di, cud
         return e;
     a.tiles_m = (a.m + kTM - 1) / kTM;
     a.tiles_n = (a.N + BN - 1) / BN;
-    const size_t extra = 1024 + sizeof(GemmShared) + (S > 1 ? (size_t)BN * 512 : (size_t)kBoxes);
-    a.stages = (int)std::min<size_t>(kMaxStages, ((size_t)di.smem_optin - extra) / kStage);
+    static_assert(stages_in(kSharedBytes, BN, S) > 0, "fewer stages than accumulators");
+    a.stages = stages_in((size_t)di.smem_optin, BN, S);
+    if (a.stages == 0)
+        return cudaErrorInvalidConfiguration;
     CUtensorMap tx{}, tw{}, ty{};
     if (!encode_boxes(&tx, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, p.x, p.m, p.K, p.ldx, kTM) ||
         !encode_boxes(&tw, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, p.W, p.N, p.K, p.K, BN))
@@ -502,7 +522,7 @@ cudaError_t launch_tiles(GemmArgs a, const Fp8Gemm& p, const DeviceInfo& di, cud
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)(S > 1 ? tiles * S : std::min<int64_t>(tiles, di.sm_count)));
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = alone_on_sm(extra + (size_t)a.stages * kStage, (size_t)di.smem_optin);
+    cfg.dynamicSmemBytes = alone_on_sm(extra_bytes(BN, S) + (size_t)a.stages * kStage, (size_t)di.smem_optin);
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
