@@ -575,7 +575,7 @@ int moe_route_topk(const void* logits, int type, int64_t m, int64_t E, int64_t l
  * these operations in fp32 and rounded.  (Values below 2^-111 share the scale
  * of that size.)  A block with a NaN or an infinity gets scale NaN and codes
  * NaN.
- * 0 <= rows, 1 <= K <= 2^20.  One launch. */
+ * 0 <= rows <= 2^30, 1 <= K <= 2^20.  One launch. */
 int fp8_quantize(const void* x, int x_type, int64_t rows, int64_t K, int64_t ldx, int64_t block_rows, uint8_t* q,
                  int64_t ldq, float* scales, int64_t ld_scales, q2k_stream_t stream);
 
@@ -586,7 +586,7 @@ int fp8_quantize(const void* x, int x_type, int64_t rows, int64_t K, int64_t ldx
  * is past fp32's range, g < -88.7), not rounded to fewer bits before it is
  * encoded; a product u / (1 + e^-g) below fp32's normal range keeps what fp32
  * holds of it.
- * 0 <= rows, 1 <= N <= 2^19.  One launch. */
+ * 0 <= rows <= 2^30, 1 <= N <= 2^19.  One launch. */
 int swiglu_fp8_rows(const void* gate_up, int type, int64_t rows, int64_t N, int64_t ld, uint8_t* q, int64_t ldq,
                     float* scales, int64_t ld_scales, q2k_stream_t stream);
 
@@ -599,7 +599,9 @@ int swiglu_fp8_rows(const void* gate_up, int type, int64_t rows, int64_t N, int6
  * y[t, n] = sum over blocks b of x_scales[t, b] * w_scales[n / 128, b] *
  * (sum over k in b of x[t, k] w[n, k]): the inner sums on the tensor cores
  * with fp32 accumulation, scaled and added in fp32, rounded once to bf16
- * where y is bf16.  A call repeats bit for bit.
+ * where y is bf16.  The two scales are multiplied first: where their product
+ * is below 2^-126 or past fp32's range, what it loses is lost to y.  A call
+ * repeats bit for bit.
  * 0 <= m, 1 <= N, m and N below 2^30, K % 16 == 0, 16 <= K <= 2^20.  One launch.
  * Q2K_ERR_UNSUPPORTED when the CUDA driver offers no tensor-map encoder. */
 int fp8_gemm(const uint8_t* x, int64_t m, int64_t K, int64_t ldx, const float* x_scales, int64_t ld_xs,
@@ -610,8 +612,9 @@ int fp8_gemm(const uint8_t* x, int64_t m, int64_t K, int64_t ldx, const float* x
 size_t fp8_moe_workspace_bytes(int64_t m, int64_t topk, int64_t dim, int64_t inter);
 
 /* The routed experts of a few tokens as one call: gate and up, SwiGLU, down,
- * the route-weighted sum, every expert that a token chose read once for all
- * its tokens (up to the 16 that one pass takes).
+ * the route-weighted sum.  An expert that tokens chose is read once for each 8
+ * of them, or for each 16 where a mean of m * topk / E tokens, evenly spread,
+ * would often mean more than 8 (min(m, mean + 2 sqrt(mean)) > 8).
  *   x         bf16 [m, dim], rows ldx apart
  *   ids       int32 [m, topk]: experts; one outside [0, E) counts nothing
  *             (a step of fixed size can be padded with -1), one that a token
