@@ -132,3 +132,19 @@ def test_moe_keeps_eleven_bits_of_h(lib, m, E, topk, dim, inter):  # noqa: F811
     args[6] /= inter ** 0.5
     want, tol = want_of(*args, rounded=2.0 ** -11)
     within(lib.fp8_moe(*args), want, tol)
+
+
+@pytest.mark.parametrize("gate_scale,down_scale", [(2.0 ** -118, 2.0 ** -40), (2.0 ** -78, 2.0 ** -120), (2.0 ** -76, 2.0 ** -126)])
+@pytest.mark.parametrize("m,E,topk,dim,inter", [(1, 1, 1, 256, 128), (3, 4, 2, 144, 272), (20, 2, 2, 272, 128)])
+def test_moe_of_the_largest_tokens_and_h(lib, m, E, topk, dim, inter, gate_scale, down_scale):  # noqa: F811
+    """x up to bf16's largest value, h up to 2^120 and beyond: the powers of two beside them stay in range."""
+    args = inputs(m + inter, m, E, topk, dim, inter)
+    g = gen(m)
+    size = 0.5 + 0.5 * torch.rand(m, dim, generator=g, device=DEV)
+    args[0].copy_(torch.sign(args[0].float()) * size * 3.38e38)
+    args[0][0, 0] = torch.finfo(BF16).max
+    args[4].fill_(gate_scale / dim ** 0.5)
+    args[6].fill_(down_scale / inter ** 0.5)
+    want, tol = want_of(*args, rounded=2.0 ** -11)
+    assert torch.isfinite(want).all() and want.abs().max() < 3e38
+    within(lib.fp8_moe(*args), want, tol)
