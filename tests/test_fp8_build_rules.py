@@ -10,7 +10,7 @@ CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))),
 
 
 def front_end(tmp_path, change):
-    """The compiler's verdict on a changed copy of fp8_gemm.cu, without code for the device."""
+    """What the compiler says to a changed copy of fp8_gemm.cu, without code for the device."""
     from mmvq_q2_gb300 import build
     root = tmp_path / "pkg" / "csrc"
     shutil.copytree(CSRC, root)
